@@ -430,6 +430,132 @@ ar_status_t ar_debug_get_epoch(ar_handle_t h, uint32_t* epoch);
 ar_status_t ar_allreduce_fused_noalloc(int R, const void* const* d_in_tbl,
                                        void* const* d_out_tbl, size_t count, void* stream);
 
+/* ---- feed-forward operators around the sum ------------------------------
+ *
+ * A tensor-parallel layer's feed-forward block stands on both sides of the
+ * allreduce: before it every rank computes its shard of the gated
+ * projections and its partial down projection, whose R partial results
+ * ar_allreduce sums; after it come dropout and the residual.  The calls
+ * below are those steps for ONE rank's buffers (R virtual ranks: R calls).
+ * The pages have no counterpart to them.
+ *
+ * Matrices are row-major device arrays: element (i, j) of a matrix with
+ * leading dimension ld is at [i * ld + j], ld >= its columns, in elements.
+ * Any ld and any element-aligned base address is accepted; rows that start
+ * on 16 bytes (base and ld) take the tensor cores' fast path.  All calls are
+ * asynchronous on `stream`, allocate nothing, synchronise nothing, and can be
+ * captured into a CUDA graph.  Outputs must not overlap inputs or one another
+ * unless a call says so.
+ */
+typedef enum {
+  AR_ACT_SILU = 0,      /* v / (1 + exp(-v)) */
+  AR_ACT_GELU_TANH = 1  /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+} ar_activation_t;
+
+typedef struct ar_ffn_ctx* ar_ffn_t;
+
+/* ar_ffn_create -- a handle for one rank's gated feed-forward shard on the
+ * current CUDA device.
+ *   max_tokens  >= 1: bounds `tokens` of ar_ffn_backward and sizes its workspace
+ *               (ar_ffn_forward needs none and takes any number of tokens).
+ *   hidden      >= 1: columns of x and of the weights (K below).
+ *   width       >= 1: rows of each weight matrix, this rank's part of the
+ *               block's inner width (F below).
+ *   dtype       AR_BF16 or AR_FP16; AR_FP32 is AR_ERR_UNSUPPORTED (the
+ *               products run on 16-bit tensor-core operands).
+ *   activation  ar_activation_t.
+ *   train       non-zero: allocate the workspace of ar_ffn_backward (two
+ *               max_tokens x width matrices of dtype); zero: allocate nothing,
+ *               and ar_ffn_backward returns AR_ERR_UNSUPPORTED.
+ * ar_ffn_backward calls on one handle share the workspace: order them on one
+ * stream.  ar_ffn_forward calls share nothing.
+ * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (dtype, or the device is not
+ * compute capability 10.3), AR_ERR_OOM, AR_ERR_CUDA. */
+ar_status_t ar_ffn_create(size_t max_tokens, size_t hidden, size_t width, int dtype,
+                          int activation, int train, ar_ffn_t* out);
+
+/* ar_ffn_destroy -- synchronise the device and free the handle.  NULL is accepted. */
+ar_status_t ar_ffn_destroy(ar_ffn_t h);
+
+/* ar_ffn_forward -- out = act(x Wgate^T) * (x Wup^T), in one kernel.
+ *   x             [tokens, hidden], leading dimension ldx
+ *   w_gate, w_up  [width, hidden], both with leading dimension ldw
+ *   out           [tokens, width], leading dimension ldo
+ *   gate, up      NULL, or [tokens, width] with ldo: receive the two products
+ *                 before the activation, rounded to dtype, which
+ *                 ar_ffn_backward takes.  Both or neither.
+ * Sums are held in fp32; the activation and the product are taken in fp32
+ * from the unrounded sums; each output is rounded once, to nearest even.
+ * tokens = 0 returns AR_OK without a launch. */
+ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
+                           const void* w_up, size_t ldw, void* out, void* gate, void* up,
+                           size_t ldo, size_t tokens, void* stream);
+
+/* ar_ffn_backward -- the gradients of ar_ffn_forward:
+ *   dgate = dout * up * act'(gate),  dup = dout * act(gate)
+ *   dx      = dgate Wgate + dup Wup      [tokens, hidden], leading dimension lddx
+ *   dw_gate = dgate^T x,  dw_up = dup^T x   [width, hidden] each, lddw
+ *   gate, up, dout   [tokens, width], all with leading dimension ldo
+ *   dx           NULL: not computed
+ *   dw_gate, dw_up   both NULL: not computed
+ * Sums in fp32, outputs rounded once.  dgate and dup are rounded to dtype
+ * between the two steps, since they are operands of 16-bit tensor-core
+ * products.  The gradients are written, not added to what the outputs held.
+ * tokens = 0 writes zeros to dw_gate and dw_up.
+ * Errors: AR_ERR_INVALID_ARG (also tokens > max_tokens), AR_ERR_UNSUPPORTED
+ * (handle made with train = 0), AR_ERR_CUDA. */
+ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
+                            const void* w_up, size_t ldw, const void* gate, const void* up,
+                            const void* dout, size_t ldo, void* dx, size_t lddx, void* dw_gate,
+                            void* dw_up, size_t lddw, size_t tokens, void* stream);
+
+/* ar_dropout -- out = residual + (keep ? x / (1 - p) : 0).
+ *   x, residual, out  [rows, cols] of dtype (AR_BF16, AR_FP16, AR_FP32);
+ *             residual may be NULL (taken as 0); out may be exactly x or
+ *             residual (same address and leading dimension).
+ *   p         in [0, 1]: keep where draw >= rint(p 2^32); p = 1 drops all.
+ *   seed, sequence, offset   element (i, j) draws word n mod 4 of
+ *             Philox4x32-10 with key `seed` on the 128-bit counter
+ *             {n / 4, sequence}, n = offset + i * cols + j.  Use a sequence
+ *             for each layer and step; offset is the place of a block (a
+ *             rank's part of a reduce-scatter) in the whole tensor.
+ * The mask depends on (seed, sequence, n) alone and is never stored: ranks
+ * with equal arguments draw equal masks, and ar_dropout_backward (dx = keep ?
+ * dy / (1 - p) : 0; the residual's gradient is dy) draws it again.
+ * x * (1 / (1 - p)) and the sum are fp32 steps, rounded once to dtype.  A
+ * dropped element counts as 0 whatever it holds, infinities and NaN included.
+ * Errors: AR_ERR_INVALID_ARG (NULL x or out, ld < cols, p outside [0, 1] or
+ * NaN, offset + rows * cols past 2^64), AR_ERR_UNSUPPORTED (dtype). */
+ar_status_t ar_dropout(const void* x, size_t ldx, const void* residual, size_t ldr, void* out,
+                       size_t ldo, size_t rows, size_t cols, int dtype, double p, uint64_t seed,
+                       uint64_t sequence, uint64_t offset, void* stream);
+ar_status_t ar_dropout_backward(const void* dy, size_t lddy, void* dx, size_t lddx, size_t rows,
+                                size_t cols, int dtype, double p, uint64_t seed,
+                                uint64_t sequence, uint64_t offset, void* stream);
+
+/* ar_quantize_rows -- 8-bit integers and one scale for each row (token):
+ *   scale[i] = max_j |x[i, j]| / 127,  q[i, j] = rint(x[i, j] / scale[i])
+ * with IEEE fp32 divisions and ties to even; q is in [-127, 127].  A row of
+ * zeros gets scale 0 and zeros.  A row that holds an infinity or a NaN gets
+ * that as its scale, and zeros, so that its products come out as NaN.
+ *   x  [rows, cols] of dtype (AR_BF16, AR_FP16, AR_FP32);  q  [rows, cols];
+ *   scale  rows floats.  rows = 0 returns AR_OK without a launch. */
+ar_status_t ar_quantize_rows(const void* x, size_t ldx, int8_t* q, size_t ldq, float* scale,
+                             size_t rows, size_t cols, int dtype, void* stream);
+
+/* ar_linear_i8 -- y[m, n] = x_scale[m] * w_scale[n] * sum_k x[m, k] w[n, k].
+ *   x  [tokens, in] int8, w  [out, in] int8 (any value, -128 included),
+ *   x_scale  one float a token, w_scale  one float an output channel,
+ *   y  [tokens, out] of dtype AR_BF16 or AR_FP16, leading dimension ldy.
+ * Products are exact and sums are held in fp32: exact while partial sums stay
+ * within 2^24 (always for in <= 1024), rounded like any fp32 sum beyond.  The
+ * sum is multiplied by x_scale, then by w_scale, and rounded once.
+ * tokens = 0 returns AR_OK without a launch.
+ * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (dtype AR_FP32), AR_ERR_CUDA. */
+ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, const int8_t* w,
+                         size_t ldw, const float* w_scale, void* y, size_t ldy, size_t tokens,
+                         size_t in, size_t out, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

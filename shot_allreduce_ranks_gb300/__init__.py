@@ -4,6 +4,8 @@ Thin Python binding of libar_gb300.so (C ABI in include/ar.h).  PyTorch only
 provides device memory and streams here; every step of the reduction runs in
 the library's CUDA kernels.  Importing this package does not load the
 library; the first ``AllReduce`` does, and fails loudly if it is not built.
+The feed-forward operators that stand around the sum in a tensor-parallel
+layer (``GatedFFN``, ``linear_i8``, ``dropout``) are in ``feed_forward``.
 """
 from __future__ import annotations
 
@@ -13,7 +15,20 @@ from ._lib import (AR_AUTO, AR_BF16, AR_FP16, AR_FP32, AR_FUSED_LL8,  # noqa: F4
                    AR_MAX_PACKET_RANKS, AR_MAX_RANKS, AR_ONESHOT_FANOUT, AR_ONESHOT_PULL,
                    AR_TWOPHASE, VARIANTS, ArError, ArInfo, check, load)
 
-__all__ = ["AllReduce", "ArError", "VARIANTS", "allreduce_fused_noalloc", "load"]
+__all__ = ["AllReduce", "ArError", "GatedFFN", "VARIANTS", "allreduce_fused_noalloc", "dropout",
+           "dropout_backward", "linear_i8", "load", "quantize_rows"]
+
+_FEED_FORWARD = ("GatedFFN", "dropout", "dropout_backward", "linear_i8", "quantize_rows")
+
+
+def __getattr__(name):
+    # The feed-forward operators' binding imports torch, which importing this package does not.
+    if name in _FEED_FORWARD:
+        from . import feed_forward
+        for n in _FEED_FORWARD:
+            globals()[n] = getattr(feed_forward, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 def _variant_id(v) -> int:

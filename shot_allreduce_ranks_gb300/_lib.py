@@ -28,6 +28,8 @@ VARIANTS = {
     "fused_ll8_staged": AR_FUSED_LL8_STAGED,
     "packet_3op": AR_PACKET_3OP,
 }
+AR_ACT_SILU, AR_ACT_GELU_TANH = 0, 1
+ACTIVATIONS = {"silu": AR_ACT_SILU, "gelu": AR_ACT_GELU_TANH}
 AR_MAX_RANKS = 16
 AR_MAX_PACKET_RANKS = 8
 
@@ -50,6 +52,7 @@ _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _ST = ctypes.c_int
+_U64 = ctypes.c_uint64
 
 PROTOTYPES = {
     "ar_create": (_ST, [_I, _SZ, _I, ctypes.POINTER(_H)]),
@@ -75,6 +78,17 @@ PROTOTYPES = {
     "ar_allreduce_fused_noalloc": (_ST, [_I, _VP, _VP, _SZ, _VP]),
     "ar_reduce_scatter": (_ST, [_H, _VP, _VP, _SZ, _VP]),
     "ar_all_gather": (_ST, [_H, _VP, _VP, _SZ, _VP]),
+    "ar_ffn_create": (_ST, [_SZ, _SZ, _SZ, _I, _I, _I, ctypes.POINTER(_H)]),
+    "ar_ffn_destroy": (_ST, [_H]),
+    "ar_ffn_forward": (_ST, [_H, _VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _VP, _SZ, _SZ, _VP]),
+    "ar_ffn_backward": (_ST, [_H, _VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _VP, _SZ, _VP, _SZ,
+                              _VP, _VP, _SZ, _SZ, _VP]),
+    "ar_dropout": (_ST, [_VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, ctypes.c_double,
+                         _U64, _U64, _U64, _VP]),
+    "ar_dropout_backward": (_ST, [_VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, ctypes.c_double,
+                                  _U64, _U64, _U64, _VP]),
+    "ar_quantize_rows": (_ST, [_VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, _I, _VP]),
+    "ar_linear_i8": (_ST, [_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _I, _VP]),
 }
 
 AR_NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -1,0 +1,128 @@
+// Element-wise and row-wise steps of the feed-forward operators: the gradients
+// of the two pre-activations, and the quantisation of rows to 8 bits.
+#include "ops_internal.cuh"
+
+namespace ar {
+namespace {
+
+constexpr int kGateThreads = 256;
+
+// dgate = dout * up * act'(gate), dup = dout * act(gate): 3 reads and 2 writes
+// an element, bound by memory.  A thread takes eight columns of a row at a
+// time; the workspace rows are 16-byte aligned, the caller's need not be.
+template <class E, int ACT, bool VEC>
+__global__ void __launch_bounds__(kGateThreads)
+    k_gate_grad(const char* gate, const char* up, const char* dout, int64_t ldo, char* dgate,
+                char* dup, int64_t ldw, int64_t rows, int64_t cols, int64_t groups_per_row) {
+  const int64_t total = rows * groups_per_row;
+  for (int64_t i = (int64_t)blockIdx.x * kGateThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kGateThreads) {
+    const int64_t row = i / groups_per_row, col = (i - row * groups_per_row) * 8;
+    const int64_t from = (row * ldo + col) * 2, to = (row * ldw + col) * 2;
+    const int n = (int)(cols - col < 8 ? cols - col : 8);
+    uint32_t gw[4] = {}, uw[4] = {}, dw[4] = {};
+    if (VEC && n == 8) {
+      const uint4 a = ld_v4_stream(gate + from), b = ld_v4_stream(up + from),
+                  c = ld_v4_stream(dout + from);
+      gw[0] = a.x, gw[1] = a.y, gw[2] = a.z, gw[3] = a.w;
+      uw[0] = b.x, uw[1] = b.y, uw[2] = b.z, uw[3] = b.w;
+      dw[0] = c.x, dw[1] = c.y, dw[2] = c.z, dw[3] = c.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) {
+          gw[k >> 1] |= ld_elem<2>(gate + from + 2 * k) << (16 * (k & 1));
+          uw[k >> 1] |= ld_elem<2>(up + from + 2 * k) << (16 * (k & 1));
+          dw[k >> 1] |= ld_elem<2>(dout + from + 2 * k) << (16 * (k & 1));
+        }
+    }
+    uint32_t og[4], ou[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f0, s0, f1, s1;
+      act_slope<ACT>(E::lo(gw[k]), f0, s0);
+      act_slope<ACT>(E::hi(gw[k]), f1, s1);
+      const float d0 = E::lo(dw[k]), d1 = E::hi(dw[k]);
+      og[k] = E::pack(d0 * E::lo(uw[k]) * s0, d1 * E::hi(uw[k]) * s1);
+      ou[k] = E::pack(d0 * f0, d1 * f1);
+    }
+    // The workspace row is ldw = cols rounded up to 8, so a whole group fits;
+    // what lies past cols is never read.
+    st_v4_stream(dgate + to, make_uint4(og[0], og[1], og[2], og[3]));
+    st_v4_stream(dup + to, make_uint4(ou[0], ou[1], ou[2], ou[3]));
+  }
+}
+
+template <class E, int ACT>
+cudaError_t gate_grad(const void* gate, const void* up, const void* dout, int64_t ldo, void* dgate,
+                      void* dup, int64_t ldw, int64_t rows, int64_t cols, int num_sms,
+                      cudaStream_t s) {
+  const int64_t gpr = (cols + 7) / 8;
+  const int64_t want = (rows * gpr + kGateThreads - 1) / kGateThreads;
+  const unsigned grid = (unsigned)(want < (int64_t)num_sms * 8 ? want : (int64_t)num_sms * 8);
+  const bool vec = ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up) |
+                     reinterpret_cast<uintptr_t>(dout)) & 15u) == 0 && ldo % 8 == 0;
+  auto* k = vec ? k_gate_grad<E, ACT, true> : k_gate_grad<E, ACT, false>;
+  k<<<grid, kGateThreads, 0, s>>>(
+      static_cast<const char*>(gate), static_cast<const char*>(up), static_cast<const char*>(dout),
+      ldo, static_cast<char*>(dgate), static_cast<char*>(dup), ldw, rows, cols, gpr);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 256;
+
+// The largest |x| of a row, NaN where the row holds one: as unsigned integers
+// the bit patterns of non-negative floats are ordered as the floats are, and
+// every NaN lies above infinity.
+template <class E>
+__global__ void __launch_bounds__(kQuantThreads)
+    k_quantize_rows(const char* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t cols) {
+  __shared__ uint32_t part[kQuantThreads / 32];
+  const int tid = threadIdx.x;
+  const char* row = x + (int64_t)blockIdx.x * ldx * E::kBytes;
+  uint32_t top = 0;
+  for (int64_t c = tid; c < cols; c += kQuantThreads)
+    top = max(top, __float_as_uint(E::to_f32(ld_elem<E::kBytes>(row + c * E::kBytes))) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((tid & 31) == 0) part[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, part[w]);
+  // Divisions are IEEE ones, rounded once, so that the integers are those of
+  // the definition: rint(x / s), s = absmax / 127.
+  const float s = __fdiv_rn(__uint_as_float(top), 127.0f);
+  if (tid == 0) scale[blockIdx.x] = s;
+  const float by = s > 0.0f ? s : 1.0f;
+  const bool finite = top < 0x7F800000u;
+  for (int64_t c = tid; c < cols; c += kQuantThreads) {
+    const float v = __fdiv_rn(E::to_f32(ld_elem<E::kBytes>(row + c * E::kBytes)), by);
+    const int n = finite ? __float2int_rn(v) : 0;
+    q[(int64_t)blockIdx.x * ldq + c] = (int8_t)min(127, max(-127, n));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
+                             int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,
+                             int64_t cols, int num_sms, cudaStream_t s) {
+  if (dtype == AR_BF16)
+    return act == AR_ACT_SILU
+               ? gate_grad<Bf16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s)
+               : gate_grad<Bf16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s);
+  return act == AR_ACT_SILU
+             ? gate_grad<F16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s)
+             : gate_grad<F16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s);
+}
+
+cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
+                                 float* scale, int64_t rows, int64_t cols, cudaStream_t s) {
+  auto* k = dtype == AR_BF16   ? k_quantize_rows<Bf16>
+            : dtype == AR_FP16 ? k_quantize_rows<F16>
+                               : k_quantize_rows<F32>;
+  k<<<(unsigned)rows, kQuantThreads, 0, s>>>(static_cast<const char*>(x), ldx, q, ldq, scale, cols);
+  return cudaGetLastError();
+}
+
+}  // namespace ar

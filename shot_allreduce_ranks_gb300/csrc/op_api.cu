@@ -1,0 +1,234 @@
+// C ABI of the feed-forward operators: argument checks, workspaces and the
+// choice of kernel.  Declarations and contracts are in include/ar.h.
+#include <math.h>
+
+#include <new>
+
+#include "ops_internal.cuh"
+
+struct ar_ffn_ctx {
+  size_t max_tokens = 0, hidden = 0, width = 0;
+  int dtype = AR_BF16, act = AR_ACT_SILU;
+  int device = 0, num_sms = 0;
+  size_t ldw = 0;         // workspace leading dimension: width rounded up to 16 bytes
+  char* work = nullptr;   // dgate, then dup: max_tokens x ldw each
+};
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr size_t kMaxDim = (size_t)1 << 38;   // rows and leading dimensions: more than the memory holds
+constexpr size_t kMaxSize = (size_t)1 << 30;  // the sizes a handle is made for
+
+bool half_type(int dtype) { return dtype == AR_BF16 || dtype == AR_FP16; }
+bool any_type(int dtype) { return half_type(dtype) || dtype == AR_FP32; }
+
+ar_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? AR_OK : AR_ERR_CUDA; }
+
+// SMs of the current device, looked up once for each.
+ar_status_t current_sms(int* sms) {
+  static int known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return AR_ERR_CUDA;
+  if (dev >= 0 && dev < kMaxDevices && known[dev] > 0) {
+    *sms = known[dev];
+    return AR_OK;
+  }
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return AR_ERR_CUDA;
+  if (dev >= 0 && dev < kMaxDevices) known[dev] = *sms;
+  return AR_OK;
+}
+
+bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
+  return !p || ld < cols || rows > kMaxDim || ld > kMaxDim;
+}
+
+bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+
+ar_status_t dropout_call(const void* x, size_t ldx, const void* res, size_t ldr, void* out,
+                         size_t ldo, size_t rows, size_t cols, int dtype, double p, uint64_t seed,
+                         uint64_t sequence, uint64_t offset, void* stream) {
+  if (!any_type(dtype)) return AR_ERR_UNSUPPORTED;
+  if (!(p >= 0.0 && p <= 1.0)) return AR_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return AR_OK;
+  if (bad_matrix(x, rows, cols, ldx) || bad_matrix(out, rows, cols, ldo) ||
+      (res && bad_matrix(res, rows, cols, ldr)) || offset + (uint64_t)rows * cols < offset)
+    return AR_ERR_INVALID_ARG;
+  const size_t e = dtype == AR_FP32 ? 4 : 2;
+  if (misaligned(x, e) || misaligned(out, e) || misaligned(res, e)) return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  ar::DropoutArgs a = {};
+  a.x = x, a.residual = res, a.out = out;
+  a.ldx = (int64_t)ldx, a.ldr = (int64_t)ldr, a.ldo = (int64_t)ldo;
+  a.rows = (int64_t)rows, a.cols = (int64_t)cols;
+  a.seed = seed, a.sequence = sequence, a.offset = offset;
+  const double t = nearbyint(p * 4294967296.0);
+  a.drop_all = t >= 4294967296.0;
+  a.threshold = a.drop_all ? 0xFFFFFFFFu : (uint32_t)t;
+  a.scale = a.drop_all ? 0.0f : (float)(1.0 / (1.0 - p));
+  return cuda_status(ar::launch_dropout(dtype, a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_status_t ar_ffn_create(size_t max_tokens, size_t hidden, size_t width, int dtype,
+                          int activation, int train, ar_ffn_t* out) {
+  if (!out) return AR_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (max_tokens < 1 || max_tokens > kMaxSize || hidden < 1 || hidden > kMaxSize || width < 1 ||
+      width > kMaxSize || (activation != AR_ACT_SILU && activation != AR_ACT_GELU_TANH))
+    return AR_ERR_INVALID_ARG;
+  if (!half_type(dtype)) return AR_ERR_UNSUPPORTED;
+  int dev = 0, major = 0, minor = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return AR_ERR_CUDA;
+  if (major != 10 || minor != 3) return AR_ERR_UNSUPPORTED;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  ar_ffn_ctx* h = new (std::nothrow) ar_ffn_ctx;
+  if (!h) return AR_ERR_OOM;
+  h->max_tokens = max_tokens, h->hidden = hidden, h->width = width;
+  h->dtype = dtype, h->act = activation, h->device = dev, h->num_sms = sms;
+  h->ldw = (width + 7) / 8 * 8;
+  if (train) {
+    const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->work), 4 * max_tokens * h->ldw);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      delete h;
+      return e == cudaErrorMemoryAllocation ? AR_ERR_OOM : AR_ERR_CUDA;
+    }
+  }
+  *out = h;
+  return AR_OK;
+}
+
+ar_status_t ar_ffn_destroy(ar_ffn_t h) {
+  if (!h) return AR_OK;
+  ar_status_t st = AR_OK;
+  if (h->work && (cudaDeviceSynchronize() != cudaSuccess || cudaFree(h->work) != cudaSuccess))
+    st = AR_ERR_CUDA;
+  delete h;
+  return st;
+}
+
+ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
+                           const void* w_up, size_t ldw, void* out, void* gate, void* up,
+                           size_t ldo, size_t tokens, void* stream) {
+  if (!h || (gate == nullptr) != (up == nullptr)) return AR_ERR_INVALID_ARG;
+  if (tokens == 0) return AR_OK;
+  if (bad_matrix(x, tokens, h->hidden, ldx) || bad_matrix(w_gate, h->width, h->hidden, ldw) ||
+      bad_matrix(w_up, h->width, h->hidden, ldw) || bad_matrix(out, tokens, h->width, ldo) ||
+      misaligned(x, 2) || misaligned(w_gate, 2) || misaligned(w_up, 2) || misaligned(out, 2) ||
+      misaligned(gate, 2) || misaligned(up, 2))
+    return AR_ERR_INVALID_ARG;
+  ar::GemmArgs g = {};
+  g.a0 = x, g.lda = (int64_t)ldx;
+  g.b0 = w_gate, g.b1 = w_up, g.ldb = (int64_t)ldw;
+  g.c0 = out, g.c1 = gate, g.c2 = up, g.ldc = (int64_t)ldo;
+  g.M = (int64_t)tokens, g.N = (int64_t)h->width, g.K = (int64_t)h->hidden;
+  g.act = h->act;
+  return cuda_status(
+      ar::launch_gemm_any(ar::kGemmGated, h->dtype, g, static_cast<cudaStream_t>(stream)));
+}
+
+ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
+                            const void* w_up, size_t ldw, const void* gate, const void* up,
+                            const void* dout, size_t ldo, void* dx, size_t lddx, void* dw_gate,
+                            void* dw_up, size_t lddw, size_t tokens, void* stream) {
+  if (!h || (dw_gate == nullptr) != (dw_up == nullptr) || tokens > h->max_tokens)
+    return AR_ERR_INVALID_ARG;
+  if (!h->work) return AR_ERR_UNSUPPORTED;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t K = h->hidden, F = h->width;
+  if (dw_gate && (bad_matrix(dw_gate, F, K, lddw) || bad_matrix(dw_up, F, K, lddw) ||
+                  misaligned(dw_gate, 2) || misaligned(dw_up, 2)))
+    return AR_ERR_INVALID_ARG;
+  if (tokens == 0) {
+    if (dw_gate && (cudaMemset2DAsync(dw_gate, lddw * 2, 0, K * 2, F, s) != cudaSuccess ||
+                    cudaMemset2DAsync(dw_up, lddw * 2, 0, K * 2, F, s) != cudaSuccess))
+      return AR_ERR_CUDA;
+    return AR_OK;
+  }
+  if (bad_matrix(gate, tokens, F, ldo) || bad_matrix(up, tokens, F, ldo) ||
+      bad_matrix(dout, tokens, F, ldo) || misaligned(gate, 2) || misaligned(up, 2) ||
+      misaligned(dout, 2) || (dx && (bad_matrix(dx, tokens, K, lddx) || misaligned(dx, 2) ||
+                                     bad_matrix(w_gate, F, K, ldw) || bad_matrix(w_up, F, K, ldw) ||
+                                     misaligned(w_gate, 2) || misaligned(w_up, 2))) ||
+      (dw_gate && (bad_matrix(x, tokens, K, ldx) || misaligned(x, 2))))
+    return AR_ERR_INVALID_ARG;
+  if (!dx && !dw_gate) return AR_OK;
+
+  char* dgate = h->work;
+  char* dup = h->work + 2 * h->max_tokens * h->ldw;
+  cudaError_t e = ar::launch_gate_grad(h->dtype, h->act, gate, up, dout, (int64_t)ldo, dgate, dup,
+                                       (int64_t)h->ldw, (int64_t)tokens, (int64_t)F, h->num_sms, s);
+  if (e == cudaSuccess && dx) {
+    ar::GemmArgs g = {};
+    g.a0 = dgate, g.a1 = dup, g.lda = (int64_t)h->ldw;
+    g.b0 = w_gate, g.b1 = w_up, g.ldb = (int64_t)ldw;
+    g.c0 = dx, g.ldc = (int64_t)lddx;
+    g.M = (int64_t)tokens, g.N = (int64_t)K, g.K = (int64_t)F;
+    e = ar::launch_gemm_any(ar::kGemmDx, h->dtype, g, s);
+  }
+  if (e == cudaSuccess && dw_gate) {
+    ar::GemmArgs g = {};
+    g.a0 = dgate, g.a1 = dup, g.lda = (int64_t)h->ldw;
+    g.b0 = x, g.ldb = (int64_t)ldx;
+    g.c0 = dw_gate, g.c1 = dw_up, g.ldc = (int64_t)lddw;
+    g.M = (int64_t)F, g.N = (int64_t)K, g.K = (int64_t)tokens;
+    e = ar::launch_gemm_any(ar::kGemmDw, h->dtype, g, s);
+  }
+  return cuda_status(e);
+}
+
+ar_status_t ar_dropout(const void* x, size_t ldx, const void* residual, size_t ldr, void* out,
+                       size_t ldo, size_t rows, size_t cols, int dtype, double p, uint64_t seed,
+                       uint64_t sequence, uint64_t offset, void* stream) {
+  return dropout_call(x, ldx, residual, ldr, out, ldo, rows, cols, dtype, p, seed, sequence, offset,
+                      stream);
+}
+
+ar_status_t ar_dropout_backward(const void* dy, size_t lddy, void* dx, size_t lddx, size_t rows,
+                                size_t cols, int dtype, double p, uint64_t seed,
+                                uint64_t sequence, uint64_t offset, void* stream) {
+  return dropout_call(dy, lddy, nullptr, 0, dx, lddx, rows, cols, dtype, p, seed, sequence, offset,
+                      stream);
+}
+
+ar_status_t ar_quantize_rows(const void* x, size_t ldx, int8_t* q, size_t ldq, float* scale,
+                             size_t rows, size_t cols, int dtype, void* stream) {
+  if (!any_type(dtype)) return AR_ERR_UNSUPPORTED;
+  if (rows == 0) return AR_OK;
+  if (cols == 0 || !scale || misaligned(scale, 4) || bad_matrix(x, rows, cols, ldx) ||
+      rows > 0x7FFFFFFF || misaligned(x, dtype == AR_FP32 ? 4 : 2) || bad_matrix(q, rows, cols, ldq))
+    return AR_ERR_INVALID_ARG;
+  return cuda_status(ar::launch_quantize_rows(dtype, x, (int64_t)ldx, q, (int64_t)ldq, scale,
+                                              (int64_t)rows, (int64_t)cols,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, const int8_t* w,
+                         size_t ldw, const float* w_scale, void* y, size_t ldy, size_t tokens,
+                         size_t in, size_t out, int dtype, void* stream) {
+  if (!half_type(dtype)) return AR_ERR_UNSUPPORTED;
+  if (in == 0 || out == 0) return AR_ERR_INVALID_ARG;
+  if (tokens == 0) return AR_OK;
+  if (bad_matrix(x, tokens, in, ldx) || bad_matrix(w, out, in, ldw) ||
+      bad_matrix(y, tokens, out, ldy) || !x_scale || !w_scale || misaligned(x_scale, 4) ||
+      misaligned(w_scale, 4) || misaligned(y, 2))
+    return AR_ERR_INVALID_ARG;
+  ar::GemmArgs g = {};
+  g.a0 = x, g.lda = (int64_t)ldx;
+  g.b0 = w, g.ldb = (int64_t)ldw;
+  g.c0 = y, g.ldc = (int64_t)ldy;
+  g.sm = x_scale, g.sn = w_scale;
+  g.M = (int64_t)tokens, g.N = (int64_t)out, g.K = (int64_t)in;
+  return cuda_status(ar::launch_gemm_any(ar::kGemmI8, dtype, g, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

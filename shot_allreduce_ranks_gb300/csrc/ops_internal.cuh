@@ -1,0 +1,131 @@
+// Declarations shared by the feed-forward operators' translation units: the
+// gated feed-forward shard and its gradients, the 8-bit product, dropout.
+// Their entry points and contracts are in include/ar.h.
+#pragma once
+
+#include "ar_internal.cuh"
+
+namespace ar {
+
+// ---------------------------------------------------------------------------
+// Matrix products.  All of them are C[m, n] = sum_k A(m, k) B(n, k); what
+// differs is which matrices stand for A and B, which of their two axes is
+// contiguous, and what is done with the sum.
+enum GemmMode : int {
+  // A = x [M, K], B = both projections' weights [N, K]:
+  // h = act(gate) * up, with gate and up stored where c1 is set.
+  kGemmGated = 0,
+  // A = {dgate, dup} [M, K], B = {Wgate, Wup} [K, N]: the sum of both products.
+  kGemmDx = 1,
+  // A = dgate then dup, [K, M] each, B = x [K, N]: two outputs of M rows.
+  kGemmDw = 2,
+  // A = int8 [M, K], B = int8 [N, K]: sm[m] * sn[n] * sum.
+  kGemmI8 = 3
+};
+
+struct GemmArgs {
+  const void* a0;
+  const void* a1;
+  const void* b0;
+  const void* b1;
+  void* c0;
+  void* c1;
+  void* c2;
+  const float* sm;
+  const float* sn;
+  int64_t lda, ldb, ldc;  // elements between rows
+  int64_t M, N, K;
+  int act;                // ar_activation_t (kGemmGated)
+};
+
+cudaError_t launch_gemm_any(int mode, int dtype, const GemmArgs& g, cudaStream_t s);
+
+// dgate = dout * up * act'(gate), dup = dout * act(gate), rounded to the
+// element type (the operands of the tensor cores' products).
+cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
+                             int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,
+                             int64_t cols, int num_sms, cudaStream_t s);
+
+// One int8 row and one scale for each row of x.
+cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
+                                 float* scale, int64_t rows, int64_t cols, cudaStream_t s);
+
+struct DropoutArgs {
+  const void* x;
+  const void* residual;  // or null
+  void* out;
+  int64_t ldx, ldr, ldo;
+  int64_t rows, cols;
+  uint64_t seed, sequence, offset;
+  uint32_t threshold;  // an element is kept where its draw >= threshold
+  int drop_all;
+  float scale;
+};
+cudaError_t launch_dropout(int dtype, const DropoutArgs& a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Activations.  Both are v * sigmoid(s(v)): s(v) = v for SiLU, and for the
+// tanh form of GELU s(v) = 2 sqrt(2/pi) (v + 0.044715 v^3), because
+// (1 + tanh t) / 2 = sigmoid(2 t).  __expf and __fdividef are good to a few
+// units in 2^-23 here, far below the 16-bit results' rounding.
+__device__ __forceinline__ float sigmoid_fast(float s) {
+  return __fdividef(1.0f, 1.0f + __expf(-s));
+}
+
+constexpr float kGeluTwoC = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGeluA = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float v) {
+  if (ACT == AR_ACT_SILU) return v * sigmoid_fast(v);
+  return v * sigmoid_fast(kGeluTwoC * (v + kGeluA * v * v * v));
+}
+
+// act(v) and act'(v).  Past |v| = 88 the sigmoid is 0 or 1 and its slope 0 in
+// fp32, so the slope is taken at the clamped value, where v^3 and v (1 - sig)
+// stay finite; a NaN passes through the comparisons.
+template <int ACT>
+__device__ __forceinline__ void act_slope(float v, float& f, float& df) {
+  float c = v > 88.0f ? 88.0f : v;
+  c = c < -88.0f ? -88.0f : c;
+  if (ACT == AR_ACT_SILU) {
+    const float sig = sigmoid_fast(c);
+    f = v * sig;
+    df = sig * (1.0f + c * (1.0f - sig));
+  } else {
+    const float sig = sigmoid_fast(kGeluTwoC * (c + kGeluA * c * c * c));
+    f = v * sig;
+    df = sig + c * sig * (1.0f - sig) * kGeluTwoC * (1.0f + 3.0f * kGeluA * c * c);
+  }
+}
+
+// A 16-bit type's two-element word and its mma.sync.
+template <class E>
+struct IsBf16 {
+  static constexpr bool value = false;
+};
+template <>
+struct IsBf16<Bf16> {
+  static constexpr bool value = true;
+};
+
+// D (16x8, fp32) += A (16x16) B (16x8); lane l holds rows l/4 and l/4 + 8.
+template <class E>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
+                                          const uint32_t (&b)[2]) {
+  if (IsBf16<E>::value) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  }
+}
+
+}  // namespace ar
