@@ -556,6 +556,15 @@ ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, cons
                          size_t ldw, const float* w_scale, void* y, size_t ldy, size_t tokens,
                          size_t in, size_t out, int dtype, void* stream);
 
+/* ar_ops_get_device_status -- wait for `stream` to drain, then read and clear
+ * the feed-forward operators' error word on the current device: AR_ERR_TIMEOUT
+ * if a wait inside one of their tensor-core kernels gave up (two seconds; such
+ * a call's outputs are undefined), AR_ERR_CUDA if the stream did not drain.
+ * No wait can run out in a working call: each is for a copy or a matrix
+ * instruction that the same CTA, or its pair, has issued.  Not for stream
+ * capture. */
+ar_status_t ar_ops_get_device_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,9 +16,10 @@ from ._lib import (AR_AUTO, AR_BF16, AR_FP16, AR_FP32, AR_FUSED_LL8,  # noqa: F4
                    AR_TWOPHASE, VARIANTS, ArError, ArInfo, check, load)
 
 __all__ = ["AllReduce", "ArError", "GatedFFN", "VARIANTS", "allreduce_fused_noalloc", "dropout",
-           "dropout_backward", "linear_i8", "load", "quantize_rows"]
+           "dropout_backward", "linear_i8", "load", "ops_device_status", "quantize_rows"]
 
-_FEED_FORWARD = ("GatedFFN", "dropout", "dropout_backward", "linear_i8", "quantize_rows")
+_FEED_FORWARD = ("GatedFFN", "dropout", "dropout_backward", "linear_i8", "ops_device_status",
+                 "quantize_rows")
 
 
 def __getattr__(name):

@@ -87,6 +87,7 @@ PROTOTYPES = {
                          _U64, _U64, _U64, _VP]),
     "ar_dropout_backward": (_ST, [_VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, ctypes.c_double,
                                   _U64, _U64, _U64, _VP]),
+    "ar_ops_get_device_status": (_ST, [_VP]),
     "ar_quantize_rows": (_ST, [_VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, _I, _VP]),
     "ar_linear_i8": (_ST, [_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _I, _VP]),
 }

@@ -46,6 +46,11 @@ bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
 
 bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
+cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaStream_t s) {
+  if (ar::gemm_tc_takes(mode, g)) return ar::launch_gemm_tc(mode, dtype, g, num_sms, s);
+  return ar::launch_gemm_any(mode, dtype, g, s);
+}
+
 ar_status_t dropout_call(const void* x, size_t ldx, const void* res, size_t ldr, void* out,
                          size_t ldo, size_t rows, size_t cols, int dtype, double p, uint64_t seed,
                          uint64_t sequence, uint64_t offset, void* stream) {
@@ -132,8 +137,7 @@ ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_
   g.c0 = out, g.c1 = gate, g.c2 = up, g.ldc = (int64_t)ldo;
   g.M = (int64_t)tokens, g.N = (int64_t)h->width, g.K = (int64_t)h->hidden;
   g.act = h->act;
-  return cuda_status(
-      ar::launch_gemm_any(ar::kGemmGated, h->dtype, g, static_cast<cudaStream_t>(stream)));
+  return cuda_status(gemm(ar::kGemmGated, h->dtype, g, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
@@ -173,7 +177,7 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
     g.b0 = w_gate, g.b1 = w_up, g.ldb = (int64_t)ldw;
     g.c0 = dx, g.ldc = (int64_t)lddx;
     g.M = (int64_t)tokens, g.N = (int64_t)K, g.K = (int64_t)F;
-    e = ar::launch_gemm_any(ar::kGemmDx, h->dtype, g, s);
+    e = gemm(ar::kGemmDx, h->dtype, g, h->num_sms, s);
   }
   if (e == cudaSuccess && dw_gate) {
     ar::GemmArgs g = {};
@@ -181,7 +185,7 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
     g.b0 = x, g.ldb = (int64_t)ldx;
     g.c0 = dw_gate, g.c1 = dw_up, g.ldc = (int64_t)lddw;
     g.M = (int64_t)F, g.N = (int64_t)K, g.K = (int64_t)tokens;
-    e = ar::launch_gemm_any(ar::kGemmDw, h->dtype, g, s);
+    e = gemm(ar::kGemmDw, h->dtype, g, h->num_sms, s);
   }
   return cuda_status(e);
 }
@@ -228,7 +232,15 @@ ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, cons
   g.c0 = y, g.ldc = (int64_t)ldy;
   g.sm = x_scale, g.sn = w_scale;
   g.M = (int64_t)tokens, g.N = (int64_t)out, g.K = (int64_t)in;
-  return cuda_status(ar::launch_gemm_any(ar::kGemmI8, dtype, g, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  return cuda_status(gemm(ar::kGemmI8, dtype, g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+ar_status_t ar_ops_get_device_status(void* stream) {
+  uint32_t error = 0;
+  if (ar::gemm_tc_error(static_cast<cudaStream_t>(stream), &error) != cudaSuccess) return AR_ERR_CUDA;
+  return error ? AR_ERR_TIMEOUT : AR_OK;
 }
 
 }  // extern "C"

@@ -38,6 +38,13 @@ struct GemmArgs {
   int act;                // ar_activation_t (kGemmGated)
 };
 
+// On tcgen05, for operands that a tensor map can describe; gemm_tc_error reads
+// and clears the flag that a wait which gave up leaves on the device.
+bool gemm_tc_takes(int mode, const GemmArgs& g);
+cudaError_t launch_gemm_tc(int mode, int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
+cudaError_t gemm_tc_error(cudaStream_t s, uint32_t* error);
+
+// On mma.sync, for any alignment and stride.
 cudaError_t launch_gemm_any(int mode, int dtype, const GemmArgs& g, cudaStream_t s);
 
 // dgate = dout * up * act'(gate), dup = dout * act(gate), rounded to the

@@ -256,3 +256,9 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
         x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), out.data_ptr(), ldo,
         m, k, n, code, s), "ar_linear_i8")
     return out
+
+
+def ops_device_status(stream=None) -> int:
+    """AR_OK, or AR_ERR_TIMEOUT if a wait in one of these operators' kernels gave up (clears it)."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    return load().ar_ops_get_device_status(s.cuda_stream)
