@@ -47,6 +47,7 @@ bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
 bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
 cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaStream_t s) {
+  if (ar::gemm_few_takes(mode, g)) return ar::launch_gemm_few(mode, dtype, g, s);
   if (ar::gemm_tc_takes(mode, g)) return ar::launch_gemm_tc(mode, dtype, g, num_sms, s);
   return ar::launch_gemm_any(mode, dtype, g, s);
 }

@@ -44,6 +44,10 @@ bool gemm_tc_takes(int mode, const GemmArgs& g);
 cudaError_t launch_gemm_tc(int mode, int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
 cudaError_t gemm_tc_error(cudaStream_t s, uint32_t* error);
 
+// For at most 16 tokens of the gated and the 8-bit product.
+bool gemm_few_takes(int mode, const GemmArgs& g);
+cudaError_t launch_gemm_few(int mode, int dtype, const GemmArgs& g, cudaStream_t s);
+
 // On mma.sync, for any alignment and stride.
 cudaError_t launch_gemm_any(int mode, int dtype, const GemmArgs& g, cudaStream_t s);
 

@@ -4,8 +4,9 @@
 ``linear_i8`` (with ``quantize_rows``) the down projection in 8-bit integers,
 ``dropout`` the step after the sum, its mask drawn from the elements' places
 and never stored.  Matrices are 2-D CUDA tensors whose rows are contiguous
-(any row stride).  Calls are asynchronous on the current (or given) stream and
-run on the tensors' device.
+(any row stride).  Calls are asynchronous on the current (or given) stream,
+which also owns the outputs that a call allocates, and run on the tensors'
+device.
 """
 from __future__ import annotations
 
@@ -18,6 +19,20 @@ from ._lib import ACTIVATIONS, AR_BF16, AR_FP16, AR_FP32, check, load
 _CODES = {torch.bfloat16: AR_BF16, torch.float16: AR_FP16, torch.float32: AR_FP32}
 _U64 = (1 << 64) - 1
 
+# A call costs the host a few microseconds, which is what a single token's
+# step costs the GPU, so the checks below are kept short.
+_get_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_functions = None
+
+
+def _lib():
+    global _functions
+    if _functions is None:
+        _functions = load()
+    return _functions
+
 
 def _code(dtype, what: str, half: bool = False) -> int:
     code = _CODES.get(dtype)
@@ -27,16 +42,17 @@ def _code(dtype, what: str, half: bool = False) -> int:
     return code
 
 
-def _matrix(t, what: str, dtype, device, rows=None, cols=None) -> int:
-    """Checks a matrix and gives its leading dimension."""
-    if t.dim() != 2 or t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be a 2-D %s tensor on %s" % (what, dtype, device))
-    m, n = t.shape
+def _matrix(t, what: str, dtype, index: int, rows=None, cols=None) -> int:
+    """Checks a matrix on GPU `index` and gives its leading dimension."""
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != index or len(shape) != 2:
+        raise ValueError("%s must be a 2-D %s tensor on cuda:%d" % (what, dtype, index))
+    m, n = shape
     if (rows is not None and m != rows) or (cols is not None and n != cols):
         raise ValueError("%s must be %s x %s, got %d x %d"
                          % (what, "?" if rows is None else rows, "?" if cols is None else cols, m, n))
     step, inner = t.stride()
-    if n > 1 and inner != 1:
+    if inner != 1 and n > 1:
         raise ValueError("%s must have contiguous rows" % what)
     if m <= 1:
         return n
@@ -45,21 +61,24 @@ def _matrix(t, what: str, dtype, device, rows=None, cols=None) -> int:
     return step
 
 
-def _on_gpu(t, what: str):
-    if not t.is_cuda:
+def _on_gpu(t, what: str) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("%s must be a CUDA tensor" % what)
-    return t.device
+    return index
 
 
-def _launch(device, stream, call, what: str) -> None:
-    """call(stream handle) with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        check(call(s.cuda_stream), what)
-        return
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream() if stream is None else stream
-        check(call(s.cuda_stream), what)
+def _call(name: str, index: int, *args) -> None:
+    """The C call on the current stream, with the tensors' device current."""
+    fn = getattr(_functions or _lib(), name)
+    s = _raw_stream(index)
+    if index == _get_device():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, s)
+    if status:
+        check(status, name)
 
 
 class GatedFFN:
@@ -73,7 +92,7 @@ class GatedFFN:
 
     def __init__(self, max_tokens: int, hidden: int, width: int, dtype=torch.bfloat16,
                  activation: str = "silu", train: bool = False, device=None):
-        self._lib = load()
+        lib = load()
         if activation not in ACTIVATIONS:
             raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
         self.max_tokens, self.hidden, self.width = int(max_tokens), int(hidden), int(width)
@@ -85,15 +104,16 @@ class GatedFFN:
         self.device = torch.device("cuda", torch.cuda.current_device() if index is None else index)
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
-            check(self._lib.ar_ffn_create(self.max_tokens, self.hidden, self.width, code,
+            check(lib.ar_ffn_create(self.max_tokens, self.hidden, self.width, code,
                                           ACTIVATIONS[activation], int(self.train),
                                           ctypes.byref(h)), "ar_ffn_create")
         self._h = h
+        self._index = self.device.index
 
     def close(self) -> None:
         if getattr(self, "_h", None):
             with torch.cuda.device(self.device):
-                check(self._lib.ar_ffn_destroy(self._h), "ar_ffn_destroy")
+                check(load().ar_ffn_destroy(self._h), "ar_ffn_destroy")
             self._h = None
 
     def __del__(self):
@@ -109,76 +129,79 @@ class GatedFFN:
         self.close()
 
     def _weights(self, w_gate, w_up) -> int:
-        ld = _matrix(w_gate, "w_gate", self.dtype, self.device, self.width, self.hidden)
-        if _matrix(w_up, "w_up", self.dtype, self.device, self.width, self.hidden) != ld:
+        ld = _matrix(w_gate, "w_gate", self.dtype, self._index, self.width, self.hidden)
+        if _matrix(w_up, "w_up", self.dtype, self._index, self.width, self.hidden) != ld:
             raise ValueError("w_gate and w_up must have the same row stride")
         return ld
 
     def forward(self, x, w_gate, w_up, out=None, gate=None, up=None, save: bool = False, stream=None):
         """``out``; with ``save`` (or given ``gate`` and ``up``) ``(out, gate, up)``."""
-        ldx = _matrix(x, "x", self.dtype, self.device, None, self.hidden)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, w_gate, w_up, out, gate, up, save)
+        dt, index, width = self.dtype, self._index, self.width
+        ldx = _matrix(x, "x", dt, index, None, self.hidden)
         ldw = self._weights(w_gate, w_up)
         m = x.shape[0]
-        if (gate is None) != (up is None):
-            raise ValueError("gate and up are given together")
-        save = save or gate is not None
         if out is None:
-            out = torch.empty((m, self.width), dtype=self.dtype, device=self.device)
-        ldo = _matrix(out, "out", self.dtype, self.device, m, self.width)
-        if save:
+            out, ldo = x.new_empty((m, width)), width
+        else:
+            ldo = _matrix(out, "out", dt, index, m, width)
+        g = u = None
+        if save or gate is not None or up is not None:
+            if (gate is None) != (up is None):
+                raise ValueError("gate and up are given together")
+            save = True
             if gate is None:
-                gate = torch.empty_strided(out.shape, out.stride(), dtype=self.dtype, device=self.device)
-                up = torch.empty_strided(out.shape, out.stride(), dtype=self.dtype, device=self.device)
-            for t, what in ((gate, "gate"), (up, "up")):
-                if _matrix(t, what, self.dtype, self.device, m, self.width) != ldo:
-                    raise ValueError("%s must have the row stride of out" % what)
-        _launch(self.device, stream, lambda s: self._lib.ar_ffn_forward(
-            self._h, x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw, out.data_ptr(),
-            gate.data_ptr() if save else None, up.data_ptr() if save else None, ldo, m, s),
-            "ar_ffn_forward")
+                gate, up = (torch.empty_strided((m, width), (ldo, 1), dtype=dt, device=self.device) for _ in "gu")
+            elif _matrix(gate, "gate", dt, index, m, width) != ldo or _matrix(up, "up", dt, index, m, width) != ldo:
+                raise ValueError("gate and up must have the row stride of out")
+            g, u = gate.data_ptr(), up.data_ptr()
+        _call("ar_ffn_forward", index, self._h, x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(),
+              ldw, out.data_ptr(), g, u, ldo, m)
         return (out, gate, up) if save else out
 
     def backward(self, x, w_gate, w_up, gate, up, dout, dx=None, dw_gate=None, dw_up=None,
                  need_dx: bool = True, need_dw: bool = True, stream=None):
         """``(dx, dw_gate, dw_up)`` from the saved ``gate`` and ``up``; None for what is not needed."""
-        dev, dt = self.device, self.dtype
-        ldx = _matrix(x, "x", dt, dev, None, self.hidden)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, need_dx, need_dw)
+        dt, index, hidden, width = self.dtype, self._index, self.hidden, self.width
+        ldx = _matrix(x, "x", dt, index, None, hidden)
         ldw = self._weights(w_gate, w_up)
         m = x.shape[0]
         if m > self.max_tokens:
             raise ValueError("x has %d rows, the handle's workspace %d" % (m, self.max_tokens))
-        ldo = _matrix(dout, "dout", dt, dev, m, self.width)
-        if (_matrix(gate, "gate", dt, dev, m, self.width) != ldo
-                or _matrix(up, "up", dt, dev, m, self.width) != ldo):
+        ldo = _matrix(dout, "dout", dt, index, m, width)
+        if _matrix(gate, "gate", dt, index, m, width) != ldo or _matrix(up, "up", dt, index, m, width) != ldo:
             raise ValueError("gate, up and dout must have the same row stride")
-        lddx = lddw = 0
-        if need_dx:
-            dx = torch.empty((m, self.hidden), dtype=dt, device=dev) if dx is None else dx
-            lddx = _matrix(dx, "dx", dt, dev, m, self.hidden)
-        if need_dw:
-            if (dw_gate is None) != (dw_up is None):
+        lddx = lddw = hidden
+        if not need_dx:
+            dx = None
+        elif dx is None:
+            dx = x.new_empty((m, hidden))
+        else:
+            lddx = _matrix(dx, "dx", dt, index, m, hidden)
+        if not need_dw:
+            dw_gate = dw_up = None
+        elif dw_gate is None and dw_up is None:
+            dw_gate, dw_up = x.new_empty((width, hidden)), x.new_empty((width, hidden))
+        else:
+            if dw_gate is None or dw_up is None:
                 raise ValueError("dw_gate and dw_up are given together")
-            if dw_gate is None:
-                dw_gate = torch.empty((self.width, self.hidden), dtype=dt, device=dev)
-                dw_up = torch.empty((self.width, self.hidden), dtype=dt, device=dev)
-            lddw = _matrix(dw_gate, "dw_gate", dt, dev, self.width, self.hidden)
-            if _matrix(dw_up, "dw_up", dt, dev, self.width, self.hidden) != lddw:
+            lddw = _matrix(dw_gate, "dw_gate", dt, index, width, hidden)
+            if _matrix(dw_up, "dw_up", dt, index, width, hidden) != lddw:
                 raise ValueError("dw_gate and dw_up must have the same row stride")
-        _launch(dev, stream, lambda s: self._lib.ar_ffn_backward(
-            self._h, x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw, gate.data_ptr(),
-            up.data_ptr(), dout.data_ptr(), ldo, dx.data_ptr() if need_dx else None, lddx,
-            dw_gate.data_ptr() if need_dw else None, dw_up.data_ptr() if need_dw else None, lddw,
-            m, s), "ar_ffn_backward")
-        return dx if need_dx else None, dw_gate if need_dw else None, dw_up if need_dw else None
+        _call("ar_ffn_backward", index, self._h, x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw,
+              gate.data_ptr(), up.data_ptr(), dout.data_ptr(), ldo, dx.data_ptr() if need_dx else None, lddx,
+              dw_gate.data_ptr() if need_dw else None, dw_up.data_ptr() if need_dw else None, lddw, m)
+        return dx, dw_gate, dw_up
 
 
-def _dropout_args(x, seed, sequence, offset):
-    _on_gpu(x, "x")
-    code = _code(x.dtype, "x")
-    for v, what in ((seed, "seed"), (sequence, "sequence"), (offset, "offset")):
-        if not 0 <= v <= _U64:
-            raise ValueError("%s must be in [0, 2^64)" % what)
-    return code
+def _draw_args(seed, sequence, offset) -> None:
+    if not (0 <= seed <= _U64 and 0 <= sequence <= _U64 and 0 <= offset <= _U64):
+        raise ValueError("seed, sequence and offset must be in [0, 2^64)")
 
 
 def dropout(x, p: float, seed: int, sequence: int = 0, offset: int = 0, residual=None, out=None,
@@ -188,77 +211,94 @@ def dropout(x, p: float, seed: int, sequence: int = 0, offset: int = 0, residual
     Element (i, j) draws at ``offset + i * cols + j`` of the stream that
     ``seed`` and ``sequence`` name; equal arguments draw equal masks.
     """
-    code = _dropout_args(x, seed, sequence, offset)
-    ldx = _matrix(x, "x", x.dtype, x.device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dropout(x, p, seed, sequence, offset, residual, out)
+    index, dt = _on_gpu(x, "x"), x.dtype
+    code = _code(dt, "x")
+    _draw_args(seed, sequence, offset)
+    ldx = _matrix(x, "x", dt, index)
     m, n = x.shape
-    ldr = 0 if residual is None else _matrix(residual, "residual", x.dtype, x.device, m, n)
+    r, ldr = None, 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _matrix(residual, "residual", dt, index, m, n)
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    ldo = _matrix(out, "out", x.dtype, x.device, m, n)
-    lib = load()
-    _launch(x.device, stream, lambda s: lib.ar_dropout(
-        x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldo,
-        m, n, code, p, seed, sequence, offset, s), "ar_dropout")
+        out, ldo = x.new_empty((m, n)), n
+    else:
+        ldo = _matrix(out, "out", dt, index, m, n)
+    _call("ar_dropout", index, x.data_ptr(), ldx, r, ldr, out.data_ptr(), ldo, m, n, code, p, seed,
+          sequence, offset)
     return out
 
 
 def dropout_backward(dy, p: float, seed: int, sequence: int = 0, offset: int = 0, dx=None, stream=None):
     """Gradient of ``dropout`` with respect to x (that of ``residual`` is dy)."""
-    code = _dropout_args(dy, seed, sequence, offset)
-    lddy = _matrix(dy, "dy", dy.dtype, dy.device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dropout_backward(dy, p, seed, sequence, offset, dx)
+    index, dt = _on_gpu(dy, "dy"), dy.dtype
+    code = _code(dt, "dy")
+    _draw_args(seed, sequence, offset)
+    lddy = _matrix(dy, "dy", dt, index)
     m, n = dy.shape
     if dx is None:
-        dx = torch.empty((m, n), dtype=dy.dtype, device=dy.device)
-    lddx = _matrix(dx, "dx", dy.dtype, dy.device, m, n)
-    lib = load()
-    _launch(dy.device, stream, lambda s: lib.ar_dropout_backward(
-        dy.data_ptr(), lddy, dx.data_ptr(), lddx, m, n, code, p, seed, sequence, offset, s),
-        "ar_dropout_backward")
+        dx, lddx = dy.new_empty((m, n)), n
+    else:
+        lddx = _matrix(dx, "dx", dt, index, m, n)
+    _call("ar_dropout_backward", index, dy.data_ptr(), lddy, dx.data_ptr(), lddx, m, n, code, p, seed,
+          sequence, offset)
     return dx
+
+
+def _vector(t, what: str, n: int, index: int) -> None:
+    if t.dtype is not torch.float32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be %d contiguous float32 values on cuda:%d" % (what, n, index))
 
 
 def quantize_rows(x, q=None, scale=None, stream=None):
     """``(q, scale)``: ``scale[i] = max |x[i]| / 127``, ``q = rint(x / scale)`` in int8."""
-    dev = _on_gpu(x, "x")
-    code = _code(x.dtype, "x")
-    ldx = _matrix(x, "x", x.dtype, dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_rows(x, q, scale)
+    index, dt = _on_gpu(x, "x"), x.dtype
+    code = _code(dt, "x")
+    ldx = _matrix(x, "x", dt, index)
     m, n = x.shape
-    q = torch.empty((m, n), dtype=torch.int8, device=dev) if q is None else q
-    scale = torch.empty(m, dtype=torch.float32, device=dev) if scale is None else scale
-    ldq = _matrix(q, "q", torch.int8, dev, m, n)
-    _vector(scale, "scale", m, dev)
-    lib = load()
-    _launch(dev, stream, lambda s: lib.ar_quantize_rows(
-        x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), m, n, code, s), "ar_quantize_rows")
+    if q is None:
+        q, ldq = x.new_empty((m, n), dtype=torch.int8), n
+    else:
+        ldq = _matrix(q, "q", torch.int8, index, m, n)
+    if scale is None:
+        scale = x.new_empty(m, dtype=torch.float32)
+    else:
+        _vector(scale, "scale", m, index)
+    _call("ar_quantize_rows", index, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), m, n, code)
     return q, scale
-
-
-def _vector(t, what: str, n: int, device) -> None:
-    if t.dtype != torch.float32 or t.device != device or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError("%s must be %d contiguous float32 values on %s" % (what, n, device))
 
 
 def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=None):
     """``x_scale[m] * w_scale[n] * sum_k x[m, k] w[n, k]`` of int8 matrices, rounded to ``dtype``."""
-    dev = _on_gpu(x, "x")
-    ldx = _matrix(x, "x", torch.int8, dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_i8(x, x_scale, w, w_scale, out, dtype)
+    index = _on_gpu(x, "x")
+    ldx = _matrix(x, "x", torch.int8, index)
     m, k = x.shape
-    ldw = _matrix(w, "w", torch.int8, dev, None, k)
+    ldw = _matrix(w, "w", torch.int8, index, None, k)
     n = w.shape[0]
-    _vector(x_scale, "x_scale", m, dev)
-    _vector(w_scale, "w_scale", n, dev)
+    _vector(x_scale, "x_scale", m, index)
+    _vector(w_scale, "w_scale", n, index)
+    code = _code(dtype if out is None else out.dtype, "dtype", half=True)
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=dev)
-    code = _code(out.dtype, "dtype", half=True)
-    ldo = _matrix(out, "out", out.dtype, dev, m, n)
-    lib = load()
-    _launch(dev, stream, lambda s: lib.ar_linear_i8(
-        x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), out.data_ptr(), ldo,
-        m, k, n, code, s), "ar_linear_i8")
+        out, ldo = x.new_empty((m, n), dtype=dtype), n
+    else:
+        ldo = _matrix(out, "out", out.dtype, index, m, n)
+    _call("ar_linear_i8", index, x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw,
+          w_scale.data_ptr(), out.data_ptr(), ldo, m, k, n, code)
     return out
 
 
 def ops_device_status(stream=None) -> int:
     """AR_OK, or AR_ERR_TIMEOUT if a wait in one of these operators' kernels gave up (clears it)."""
     s = torch.cuda.current_stream() if stream is None else stream
-    return load().ar_ops_get_device_status(s.cuda_stream)
+    return _lib().ar_ops_get_device_status(s.cuda_stream)
