@@ -373,6 +373,7 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
 
 template <int MODE, class E, int ACT>
 cudaError_t launch_shape(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
+  if (g.M > 128) return launch<MODE, E, ACT, 256, 2>(dtype, g, num_sms, s);
   return launch<MODE, E, ACT, 256, 1>(dtype, g, num_sms, s);
 }
 

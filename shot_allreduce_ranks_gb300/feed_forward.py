@@ -144,7 +144,7 @@ class GatedFFN:
         ldw = self._weights(w_gate, w_up)
         m = x.shape[0]
         if out is None:
-            out, ldo = x.new_empty((m, width)), width
+            out, ldo = torch.empty((m, width), dtype=dt, device=self.device), width
         else:
             ldo = _matrix(out, "out", dt, index, m, width)
         g = u = None
@@ -180,13 +180,13 @@ class GatedFFN:
         if not need_dx:
             dx = None
         elif dx is None:
-            dx = x.new_empty((m, hidden))
+            dx = torch.empty((m, hidden), dtype=dt, device=self.device)
         else:
             lddx = _matrix(dx, "dx", dt, index, m, hidden)
         if not need_dw:
             dw_gate = dw_up = None
         elif dw_gate is None and dw_up is None:
-            dw_gate, dw_up = x.new_empty((width, hidden)), x.new_empty((width, hidden))
+            dw_gate, dw_up = (torch.empty((width, hidden), dtype=dt, device=self.device) for _ in "gu")
         else:
             if dw_gate is None or dw_up is None:
                 raise ValueError("dw_gate and dw_up are given together")
@@ -223,7 +223,7 @@ def dropout(x, p: float, seed: int, sequence: int = 0, offset: int = 0, residual
     if residual is not None:
         r, ldr = residual.data_ptr(), _matrix(residual, "residual", dt, index, m, n)
     if out is None:
-        out, ldo = x.new_empty((m, n)), n
+        out, ldo = torch.empty((m, n), dtype=dt, device=x.device), n
     else:
         ldo = _matrix(out, "out", dt, index, m, n)
     _call("ar_dropout", index, x.data_ptr(), ldx, r, ldr, out.data_ptr(), ldo, m, n, code, p, seed,
@@ -242,7 +242,7 @@ def dropout_backward(dy, p: float, seed: int, sequence: int = 0, offset: int = 0
     lddy = _matrix(dy, "dy", dt, index)
     m, n = dy.shape
     if dx is None:
-        dx, lddx = dy.new_empty((m, n)), n
+        dx, lddx = torch.empty((m, n), dtype=dt, device=dy.device), n
     else:
         lddx = _matrix(dx, "dx", dt, index, m, n)
     _call("ar_dropout_backward", index, dy.data_ptr(), lddy, dx.data_ptr(), lddx, m, n, code, p, seed,
@@ -265,11 +265,11 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     ldx = _matrix(x, "x", dt, index)
     m, n = x.shape
     if q is None:
-        q, ldq = x.new_empty((m, n), dtype=torch.int8), n
+        q, ldq = torch.empty((m, n), dtype=torch.int8, device=x.device), n
     else:
         ldq = _matrix(q, "q", torch.int8, index, m, n)
     if scale is None:
-        scale = x.new_empty(m, dtype=torch.float32)
+        scale = torch.empty(m, dtype=torch.float32, device=x.device)
     else:
         _vector(scale, "scale", m, index)
     _call("ar_quantize_rows", index, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), m, n, code)
@@ -290,7 +290,7 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
     _vector(w_scale, "w_scale", n, index)
     code = _code(dtype if out is None else out.dtype, "dtype", half=True)
     if out is None:
-        out, ldo = x.new_empty((m, n), dtype=dtype), n
+        out, ldo = torch.empty((m, n), dtype=dtype, device=x.device), n
     else:
         ldo = _matrix(out, "out", out.dtype, index, m, n)
     _call("ar_linear_i8", index, x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw,
