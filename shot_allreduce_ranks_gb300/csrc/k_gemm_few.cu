@@ -17,17 +17,6 @@ namespace {
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
 constexpr int kUnroll = 4;  // 64-byte pieces of each row in flight a warp
 
-// Four int8 to four fp16: a byte b + 128 under the exponent of 1024 is the
-// fp16 number 1152 + b, exactly; one subtraction leaves b.
-__device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  uint32_t a, b;
-  asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(a) : "r"(u), "r"(0x64646464u));
-  asm("prmt.b32 %0, %1, %2, 0x4342;" : "=r"(b) : "r"(u), "r"(0x64646464u));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
-}
-
 // 16 bytes at p, of which `left` may be read (the rest zero); VEC: p is 16-byte aligned.
 template <bool VEC, int B>
 __device__ __forceinline__ uint4 load_piece(const char* p, int64_t left) {

@@ -1,0 +1,318 @@
+// The 8-bit product on the fifth-generation tensor cores:
+// y[m, n] = sm[m] sn[n] sum_k x[m, k] w[n, k].
+//
+// This GPU's tensor cores have no fast path for 8-bit integers, but fp16 holds
+// every int8 exactly, a product of two is exact in fp32, and so is their sum
+// while it stays within 2^24 (K <= 1024 whatever the values, far longer for
+// values that vary).  So the operands stay 8-bit in memory, in L2 and on the
+// way into an SM, and eight warps turn each tile into fp16 in shared memory
+// (a byte permutation and a subtraction for every two values), in the swizzled
+// layout that the matrix instruction reads.
+//
+// Roles, persistent over tiles of 128 CG x bn: one thread copies int8 tiles of
+// 64 k into a staging ring by tensor maps, eight warps convert them into the
+// operand ring, one thread issues the matrix instructions, four warps scale and
+// store.  A pair of CTAs (CG = 2) shares one instruction over 256 rows, each
+// converting its own 128 rows of x and half of the rows of w.
+#include "tc_device.cuh"
+
+namespace ar {
+namespace {
+
+using namespace tc;
+
+constexpr int kRowsMax = 256;                        // rows of x and w in a CTA's stage
+constexpr uint32_t kStaged = kRowsMax * 64, kOperand = kRowsMax * 128;
+constexpr int kSS = 5, kOS = 4;                      // stages of the two rings
+constexpr int kConverters = 8;                       // warps
+constexpr int kI8Threads = 32 * (6 + kConverters);
+constexpr uint32_t kI8Smem = kSS * kStaged + kOS * kOperand + 1024;
+constexpr uint32_t kI8TmemCols = 512;
+
+__device__ uint32_t g_i8_error;  // set by a wait that gave up
+
+struct I8Args {
+  GemmArgs g;
+  TileWalk walk;
+  int steps;
+  int bn;         // columns of a tile, a multiple of 32
+  int out_align;
+};
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <class E, int CG>
+__global__ void __launch_bounds__(kI8Threads, 1)
+    k_gemm_i8(const __grid_constant__ I8Args a, const __grid_constant__ CUtensorMap map_x,
+              const __grid_constant__ CUtensorMap map_w) {
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kSS + 2 * kOS + 5];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t dead;
+
+  const uint32_t operands = (smem_u32(raw) + 1023u) & ~1023u, staging = operands + kOS * kOperand;
+  const uint32_t landed = smem_u32(bars), taken = landed + 8 * kSS;      // staging: copied in, converted
+  const uint32_t ready = taken + 8 * kSS, used = ready + 8 * kOS;        // operands: converted, multiplied
+  const uint32_t done = used + 8 * kOS, freed = done + 16, drained = freed + 16;
+  const int warp = threadIdx.x >> 5;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const int rows = 128 + a.bn / CG;  // of a stage: x, then w
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSS; ++i) {
+      bar_init(landed + 8 * i, 1);
+      bar_init(taken + 8 * i, kConverters);
+    }
+    for (int i = 0; i < kOS; ++i) {
+      bar_init(ready + 8 * i, kConverters * CG);
+      bar_init(used + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(done + 8 * i, 1);
+      bar_init(freed + 8 * i, 4 * CG);
+    }
+    bar_init(drained, 1);
+    dead = 0;
+    bar_init_done();
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_u32(&tmem_slot), kI8TmemCols);
+    tmem_no_more_allocs<CG>();
+    fence_before_sync();
+  }
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
+        const Tile tile = tile_at(a.walk, t);
+        const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * a.bn + (int)rank * (a.bn / CG);
+        for (int s = 0; s < a.steps; ++s, ++it) {
+          const uint32_t st = it % kSS;
+          if (!(ok = bar_wait(taken + 8 * st, ((it / kSS) & 1) ^ 1, &dead))) break;
+          const uint32_t dst = staging + st * kStaged, bar = landed + 8 * st;
+          bar_expect_tx(bar, (uint32_t)rows * 64);
+          load_box<1>(dst, &map_x, s * 64, m0, bar);
+          load_box<1>(dst + 128 * 64, &map_w, s * 64, n0, bar);
+        }
+      }
+      if (!ok) atomicExch(&g_i8_error, 1u);
+      for (uint32_t k = it > kSS ? it - kSS : 0; k < it; ++k) bar_wait_copies(landed + 8 * (k % kSS), (k / kSS) & 1);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = instr_desc(false, false, false, 128 * CG, a.bn);
+      uint32_t it = 0, at = 0;
+      bool ok = true;
+      for (int64_t t = first; t < a.walk.tiles && ok; t += stride, ++at) {
+        const uint32_t buf = at & 1;
+        if (!(ok = bar_wait(freed + 8 * buf, ((at >> 1) & 1) ^ 1, &dead))) break;
+        fence_after_sync();
+        for (int s = 0; s < a.steps; ++s, ++it) {
+          const uint32_t st = it % kOS;
+          if (!(ok = bar_wait(ready + 8 * st, (it / kOS) & 1, &dead))) break;
+          fence_after_sync();
+          const uint32_t base = operands + st * kOperand;
+          const uint64_t dx = operand_desc(base, 16, 1024), dw = operand_desc(base + 128 * 128, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f16<CG>(tmem + buf * 256, dx + 2 * k, dw + 2 * k, idesc, s > 0 || k > 0);
+          mma_commit<CG>(used + 8 * st);
+        }
+        if (ok) mma_commit<CG>(done + 8 * buf);
+      }
+      if (!ok) {
+        atomicExch(&g_i8_error, 1u);
+        mma_commit<CG>(drained);  // what was issued ends before tensor memory is freed
+        bar_wait_copies(drained, 0);
+      }
+    }
+  } else if (warp < 6) {
+    const uint32_t lane0 = (uint32_t)(warp & 3) * 32;
+    const int row_in = (int)lane0 + (int)(threadIdx.x & 31);
+    uint32_t at = 0;
+    for (int64_t t = first; t < a.walk.tiles; t += stride, ++at) {
+      const Tile tile = tile_at(a.walk, t);
+      const uint32_t buf = at & 1;
+      const int64_t m = ((int64_t)tile.m * CG + rank) * 128 + row_in;
+      const int n0 = tile.n * a.bn;
+      const float sm = m < a.g.M ? a.g.sm[m] : 0.0f;
+      if (!bar_wait(done + 8 * buf, (at >> 1) & 1, &dead)) {
+        atomicExch(&g_i8_error, 1u);
+        break;
+      }
+      fence_after_sync();
+#pragma unroll 1
+      for (int c = 0; c < a.bn; c += 32) {
+        if (n0 + c >= a.g.N) break;
+        uint32_t r[32];
+        __syncwarp();
+        tmem_load32(r, tmem + (lane0 << 16) + buf * 256 + c);
+        tmem_wait_load32(r);
+        if (m < a.g.M) {
+          const int left = (int)min((int64_t)32, a.g.N - n0 - c);
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * sm * (i < left ? __ldg(a.g.sn + n0 + c + i) : 0.0f);
+          store_row<E>(a.g.c0, m * a.g.ldc + n0 + c, v, left, a.out_align);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (elect_one()) {
+        if (CG == 2)
+          bar_arrive_cluster(map_to_cta(freed + 8 * buf, 0));
+        else
+          bar_arrive(freed + 8 * buf);
+      }
+    }
+  } else {
+    // A row's 64 k: 64 bytes staged, 128 bytes as an operand, of which the 16-byte
+    // piece p lies at p ^ (row % 8).  A warp's lanes take 16 staged bytes each
+    // (two pieces), four lanes a row: neither access has bank conflicts.
+    const int thread = (int)threadIdx.x - 6 * 32;
+    const int pieces = rows * 4;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
+      for (int s = 0; s < a.steps; ++s, ++it) {
+        const uint32_t ss = it % kSS, os = it % kOS;
+        if (!(ok = bar_wait(landed + 8 * ss, (it / kSS) & 1, &dead))) break;
+        uint4 q[kRowsMax * 4 / (32 * kConverters)];
+#pragma unroll
+        for (int i = 0; i < kRowsMax * 4 / (32 * kConverters); ++i) {
+          const int p = thread + i * 32 * kConverters;
+          if (p < pieces)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                         : "r"(staging + ss * kStaged + 16u * p));
+        }
+        if (!(ok = bar_wait(used + 8 * os, ((it / kOS) & 1) ^ 1, &dead))) break;
+#pragma unroll
+        for (int i = 0; i < kRowsMax * 4 / (32 * kConverters); ++i) {
+          const int p = thread + i * 32 * kConverters;
+          if (p < pieces) {
+            const int row = p >> 2, c = (p & 3) * 2;
+            const uint32_t to = operands + os * kOperand + (uint32_t)row * 128;
+            uint32_t h[8];
+            i8_to_f16(q[i].x, h[0], h[1]);
+            i8_to_f16(q[i].y, h[2], h[3]);
+            i8_to_f16(q[i].z, h[4], h[5]);
+            i8_to_f16(q[i].w, h[6], h[7]);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + 16u * (uint32_t)(c ^ (row & 7))), "r"(h[0]),
+                         "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + 16u * (uint32_t)((c + 1) ^ (row & 7))),
+                         "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
+          }
+        }
+        fence_async_smem();  // the matrix unit reads through the asynchronous proxy
+        __syncwarp();
+        if (elect_one()) {
+          bar_arrive(taken + 8 * ss);
+          if (CG == 2)
+            bar_arrive_cluster(map_to_cta(ready + 8 * os, 0));
+          else
+            bar_arrive(ready + 8 * os);
+        }
+      }
+    }
+    if (!ok) atomicExch(&g_i8_error, 1u);
+    // The last operand stages are multiplied before the CTA ends.
+    for (uint32_t k = it > kOS ? it - kOS : 0; k < it && ok; ++k) ok = bar_wait(used + 8 * (k % kOS), (k / kOS) & 1, &dead);
+  }
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  fence_after_sync();
+  if (warp == 1) tmem_free<CG>(tmem, kI8TmemCols);
+}
+
+template <class E, int CG>
+cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
+  CUtensorMap mx, mw;
+  if (!tc_make_map(&mx, kMapU8, g.a0, g.M, g.K, g.lda, 128, 64) ||
+      !tc_make_map(&mw, kMapU8, g.b0, g.N, g.K, g.ldb, bn / CG, 64))
+    return cudaErrorInvalidValue;
+  I8Args a = {};
+  a.g = g;
+  a.walk.tiles_m = (int)((g.M + 128 * CG - 1) / (128 * CG));
+  a.walk.tiles_n = (int)((g.N + bn - 1) / bn);
+  a.walk.tiles = (int64_t)a.walk.tiles_m * a.walk.tiles_n;
+  a.walk.group = 16 / CG;
+  a.steps = (int)((g.K + 63) / 64);
+  a.bn = bn;
+  const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | (uintptr_t)g.ldc * 2;
+  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : 2;
+  auto* kernel = k_gemm_i8<E, CG>;
+  static bool raised[64];  // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !raised[dev & 63])
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kI8Smem);
+  if (e != cudaSuccess) return e;
+  raised[dev & 63] = dev < 64;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t pairs = num_sms / CG;
+  cfg.gridDim = dim3((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = kI8Smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, mx, mw);
+}
+
+// Columns of a tile: the number of rounds of tiles over the SMs times a round's
+// time, which is a step's conversion (about 1.5 clocks a row of the stage on
+// shared memory's bandwidth) or its matrix instruction (2 clocks a column).
+int columns(const GemmArgs& g, int cg, int num_sms) {
+  const int64_t tm = (g.M + 128 * cg - 1) / (128 * cg), slots = num_sms / cg;
+  int best = 32;
+  double least = 1e300;
+  for (int bn = cg == 2 ? 256 : 128; bn >= 32; bn -= 32) {
+    const int64_t tiles = tm * ((g.N + bn - 1) / bn);
+    const double step = 1.5 * (128 + bn / cg) * 2, cost = (double)((tiles + slots - 1) / slots) * (step > 2 * bn ? step : 2 * bn);
+    if (cost < least) least = cost, best = bn;
+  }
+  return best;
+}
+
+template <class E>
+cudaError_t launch_type(const GemmArgs& g, int num_sms, cudaStream_t s) {
+  if (g.M > 128) return launch<E, 2>(g, columns(g, 2, num_sms), num_sms, s);
+  return launch<E, 1>(g, columns(g, 1, num_sms), num_sms, s);
+}
+
+}  // namespace
+
+// A tensor map wants rows that start on 16 bytes.
+bool gemm_i8_takes(int mode, const GemmArgs& g) {
+  const int64_t most = (int64_t)1 << 30;
+  return mode == kGemmI8 && tc_available() && g.M <= most && g.N <= most && g.K <= most && g.lda % 16 == 0 &&
+         g.ldb % 16 == 0 && ((reinterpret_cast<uintptr_t>(g.a0) | reinterpret_cast<uintptr_t>(g.b0)) & 15u) == 0;
+}
+
+cudaError_t launch_gemm_i8(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
+  return dtype == AR_BF16 ? launch_type<Bf16>(g, num_sms, s) : launch_type<F16>(g, num_sms, s);
+}
+
+cudaError_t gemm_i8_error(cudaStream_t s, uint32_t* error) {
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_i8_error);
+  return e == cudaSuccess ? take_error_word(p, s, error) : e;
+}
+
+}  // namespace ar

@@ -20,6 +20,43 @@
 #include "tc_device.cuh"
 
 namespace ar {
+namespace tc {
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+bool tc_available() { return encode_fn() != nullptr; }
+
+// 16-bit operands arrive in the 128-byte swizzle that the matrix instruction
+// reads; 8-bit ones plainly, since threads read and convert them.
+bool tc_make_map(CUtensorMap* map, MapType type, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+                 int box_cols) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * (type == kMapU8 ? 1 : 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  const CUtensorMapDataType t = type == kMapBf16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                : type == kMapF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return encode_fn()(map, t, 2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     type == kMapU8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tc
+
 namespace {
 
 using namespace tc;
@@ -32,8 +69,7 @@ __device__ uint32_t g_tc_error;  // set by a wait that gave up
 
 struct TcArgs {
   GemmArgs g;
-  int tiles_m, tiles_n, group;  // tiles; group: rows of tiles walked together
-  int64_t tiles;
+  TileWalk walk;
   int steps;                    // k steps of one segment
   int out_align;                // bytes that every output row start is a multiple of
 };
@@ -46,51 +82,6 @@ struct Shape {
   // one CTA has an SM's tensor memory to itself.
   static constexpr uint32_t kSmem = kStages * kStage + 1024 < 120 * 1024 ? 120 * 1024 : kStages * kStage + 1024;
 };
-
-struct Tile {
-  int m, n, z;
-};
-
-// Tile t: `group` rows of tiles are walked column by column, so that the tiles
-// in flight at one time form a block whose operands stay in L2.
-__device__ __forceinline__ Tile tile_at(const TcArgs& a, int64_t t) {
-  const int64_t plane = (int64_t)a.tiles_m * a.tiles_n;
-  Tile r;
-  r.z = (int)(t / plane);
-  t -= r.z * plane;
-  const int64_t band = (int64_t)a.group * a.tiles_n;
-  const int first = (int)(t / band) * a.group;
-  const int rows = min(a.group, a.tiles_m - first);
-  t %= band;
-  r.m = first + (int)(t % rows);
-  r.n = (int)(t / rows);
-  return r;
-}
-
-// 32 results of one row, at column n of N.
-template <class E>
-__device__ __forceinline__ void store_row(void* out, int64_t at, const float (&v)[32], int left, int align) {
-  char* p = static_cast<char*>(out) + at * 2;
-  if (left >= 32 && align >= 16) {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = E::pack(v[2 * i], v[2 * i + 1]);
-    if (align >= 32) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        st_wide(p + 32 * i, make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]),
-                make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        st_v4_stream(p + 16 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < left) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)E::from_f32(v[i]);
-  }
-}
 
 template <int MODE, class E, int ACT, int BN, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -145,8 +136,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t t = first; t < a.tiles && ok; t += stride) {
-        const Tile tile = tile_at(a, t);
+      for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
+        const Tile tile = tile_at(a.walk, t);
         const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * kCols;
         for (int s = 0; s < total; ++s, ++it) {
           const uint32_t st = it % kST, round = it / kST;
@@ -195,7 +186,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr uint32_t idesc = instr_desc(IsBf16<E>::value, kAmn, kBmn, 128 * CG, BN);
       uint32_t it = 0, at = 0;
       bool ok = true;
-      for (int64_t t = first; t < a.tiles && ok; t += stride, ++at) {
+      for (int64_t t = first; t < a.walk.tiles && ok; t += stride, ++at) {
         const uint32_t buf = at & 1;
         if (!(ok = bar_wait(freed + 8 * buf, ((at >> 1) & 1) ^ 1, &dead))) break;
         fence_after_sync();
@@ -224,8 +215,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;  // this warp's lanes of tensor memory
     const int row_in = (int)lane0 + (int)(threadIdx.x & 31);
     uint32_t at = 0;
-    for (int64_t t = first; t < a.tiles; t += stride, ++at) {
-      const Tile tile = tile_at(a, t);
+    for (int64_t t = first; t < a.walk.tiles; t += stride, ++at) {
+      const Tile tile = tile_at(a.walk, t);
       const uint32_t buf = at & 1;
       if (!bar_wait(done + 8 * buf, (at >> 1) & 1, &dead)) {
         atomicExch(&g_tc_error, 1u);
@@ -285,32 +276,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) tmem_free<CG>(tmem, kTmemCols);
 }
 
-// ---------------------------------------------------------------------------------
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
-
-// A [rows, cols] matrix of 16-bit elements, copied in boxes of box_rows x 64.
 bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
-  return encode_fn()(map, dtype == AR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                     const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tc_make_map(map, dtype == AR_BF16 ? kMapBf16 : kMapF16, p, rows, cols, ld, box_rows, 64);
 }
 
 template <int MODE, class E, int ACT, int BN, int CG>
@@ -337,10 +304,10 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
 
   TcArgs a = {};
   a.g = g;
-  a.tiles_m = (int)((g.M + 128 * CG - 1) / (128 * CG));
-  a.tiles_n = (int)((g.N + kCols - 1) / kCols);
-  a.tiles = (int64_t)a.tiles_m * a.tiles_n * (MODE == kGemmDw ? 2 : 1);
-  a.group = 16 / CG;
+  a.walk.tiles_m = (int)((g.M + 128 * CG - 1) / (128 * CG));
+  a.walk.tiles_n = (int)((g.N + kCols - 1) / kCols);
+  a.walk.tiles = (int64_t)a.walk.tiles_m * a.walk.tiles_n * (MODE == kGemmDw ? 2 : 1);
+  a.walk.group = 16 / CG;
   a.steps = (int)((g.K + kBK - 1) / kBK);
   const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | reinterpret_cast<uintptr_t>(g.c1) |
                         reinterpret_cast<uintptr_t>(g.c2) | (uintptr_t)g.ldc * 2;
@@ -356,7 +323,7 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
   raised[dev & 63] = dev < 64;
   cudaLaunchConfig_t cfg = {};
   const int64_t pairs = num_sms / CG;
-  cfg.gridDim = dim3((unsigned)((a.tiles < pairs ? a.tiles : pairs) * CG));
+  cfg.gridDim = dim3((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
@@ -398,7 +365,7 @@ bool rows_on_16(const void* p, int64_t ld) {
 // coordinates are 32-bit.
 bool gemm_tc_takes(int mode, const GemmArgs& g) {
   const int64_t most = (int64_t)1 << 30;
-  return mode != kGemmI8 && encode_fn() && g.M <= most && g.N <= most && g.K <= most && rows_on_16(g.a0, g.lda) &&
+  return mode != kGemmI8 && tc_available() && g.M <= most && g.N <= most && g.K <= most && rows_on_16(g.a0, g.lda) &&
          rows_on_16(g.a1, g.lda) && rows_on_16(g.b0, g.ldb) && rows_on_16(g.b1, g.ldb);
 }
 
@@ -406,15 +373,19 @@ cudaError_t launch_gemm_tc(int mode, int dtype, const GemmArgs& g, int num_sms, 
   return dtype == AR_BF16 ? launch_type<Bf16>(mode, dtype, g, num_sms, s) : launch_type<F16>(mode, dtype, g, num_sms, s);
 }
 
-cudaError_t gemm_tc_error(cudaStream_t s, uint32_t* error) {
-  void* p = nullptr;
+cudaError_t take_error_word(void* p, cudaStream_t s, uint32_t* error) {
   const uint32_t zero = 0;
-  cudaError_t e = cudaGetSymbolAddress(&p, g_tc_error);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(error, p, sizeof *error, cudaMemcpyDeviceToHost, s);
+  cudaError_t e = cudaMemcpyAsync(error, p, sizeof *error, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e == cudaSuccess && *error) e = cudaMemcpyAsync(p, &zero, sizeof zero, cudaMemcpyHostToDevice, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return e;
+}
+
+cudaError_t gemm_tc_error(cudaStream_t s, uint32_t* error) {
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_tc_error);
+  return e == cudaSuccess ? take_error_word(p, s, error) : e;
 }
 
 }  // namespace ar

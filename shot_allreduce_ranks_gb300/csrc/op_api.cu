@@ -49,6 +49,7 @@ bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t
 cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaStream_t s) {
   if (ar::gemm_few_takes(mode, g)) return ar::launch_gemm_few(mode, dtype, g, s);
   if (ar::gemm_tc_takes(mode, g)) return ar::launch_gemm_tc(mode, dtype, g, num_sms, s);
+  if (ar::gemm_i8_takes(mode, g)) return ar::launch_gemm_i8(dtype, g, num_sms, s);
   return ar::launch_gemm_any(mode, dtype, g, s);
 }
 
@@ -239,9 +240,10 @@ ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, cons
 }
 
 ar_status_t ar_ops_get_device_status(void* stream) {
-  uint32_t error = 0;
-  if (ar::gemm_tc_error(static_cast<cudaStream_t>(stream), &error) != cudaSuccess) return AR_ERR_CUDA;
-  return error ? AR_ERR_TIMEOUT : AR_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t tc = 0, i8 = 0;
+  if (ar::gemm_tc_error(s, &tc) != cudaSuccess || ar::gemm_i8_error(s, &i8) != cudaSuccess) return AR_ERR_CUDA;
+  return tc || i8 ? AR_ERR_TIMEOUT : AR_OK;
 }
 
 }  // extern "C"

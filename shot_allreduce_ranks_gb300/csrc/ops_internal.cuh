@@ -44,6 +44,13 @@ bool gemm_tc_takes(int mode, const GemmArgs& g);
 cudaError_t launch_gemm_tc(int mode, int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
 cudaError_t gemm_tc_error(cudaStream_t s, uint32_t* error);
 
+cudaError_t take_error_word(void* p, cudaStream_t s, uint32_t* error);  // reads and clears
+
+// The 8-bit product on tcgen05.
+bool gemm_i8_takes(int mode, const GemmArgs& g);
+cudaError_t launch_gemm_i8(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
+cudaError_t gemm_i8_error(cudaStream_t s, uint32_t* error);
+
 // For at most 16 tokens of the gated and the 8-bit product.
 bool gemm_few_takes(int mode, const GemmArgs& g);
 cudaError_t launch_gemm_few(int mode, int dtype, const GemmArgs& g, cudaStream_t s);
@@ -137,6 +144,17 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
   }
+}
+
+// Four int8 to four fp16: a byte b + 128 under the exponent of 1024 is the
+// fp16 number 1152 + b, exactly; one subtraction leaves b.
+__device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(a) : "r"(u), "r"(0x64646464u));
+  asm("prmt.b32 %0, %1, %2, 0x4342;" : "=r"(b) : "r"(u), "r"(0x64646464u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
 }  // namespace ar

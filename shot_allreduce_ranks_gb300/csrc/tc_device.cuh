@@ -212,5 +212,62 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Tiles of the output: `group` rows of tiles are walked column by column, so
+// that the tiles in flight at one time form a block whose operands stay in L2.
+struct TileWalk {
+  int tiles_m, tiles_n, group;
+  int64_t tiles;  // all planes
+};
+
+struct Tile {
+  int m, n, z;
+};
+
+__device__ __forceinline__ Tile tile_at(const TileWalk& w, int64_t t) {
+  const int64_t plane = (int64_t)w.tiles_m * w.tiles_n;
+  Tile r;
+  r.z = (int)(t / plane);
+  t -= r.z * plane;
+  const int64_t band = (int64_t)w.group * w.tiles_n;
+  const int first = (int)(t / band) * w.group;
+  const int rows = min(w.group, w.tiles_m - first);
+  t %= band;
+  r.m = first + (int)(t % rows);
+  r.n = (int)(t / rows);
+  return r;
+}
+
+// 32 results of one row, at column n of N.
+template <class E>
+__device__ __forceinline__ void store_row(void* out, int64_t at, const float (&v)[32], int left, int align) {
+  char* p = static_cast<char*>(out) + at * 2;
+  if (left >= 32 && align >= 16) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = E::pack(v[2 * i], v[2 * i + 1]);
+    if (align >= 32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        st_wide(p + 32 * i, make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]),
+                make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st_v4_stream(p + 16 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < left) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)E::from_f32(v[i]);
+  }
+}
+
+// ---- host: a [rows, cols] matrix copied in boxes of box_rows x box_cols --------------
+
+enum MapType { kMapBf16, kMapF16, kMapU8 };
+bool tc_available();
+bool tc_make_map(CUtensorMap* map, MapType type, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+                 int box_cols);
+
 }  // namespace tc
 }  // namespace ar
