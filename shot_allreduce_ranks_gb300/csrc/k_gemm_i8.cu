@@ -5,14 +5,15 @@
 // every int8 exactly, a product of two is exact in fp32, and so is their sum
 // while it stays within 2^24 (K <= 1024 whatever the values, far longer for
 // values that vary).  So the operands stay 8-bit in memory, in L2 and on the
-// way into an SM, and eight warps turn each tile into fp16 in shared memory
+// way into an SM, and converter warps turn each tile into fp16 in shared memory
 // (a byte permutation and a subtraction for every two values), in the swizzled
 // layout that the matrix instruction reads.
 //
 // Roles, persistent over tiles of 128 CG x bn: one thread copies int8 tiles of
-// 64 k into a staging ring by tensor maps, eight warps convert them into the
-// operand ring, one thread issues the matrix instructions, four warps scale and
-// store.  A pair of CTAs (CG = 2) shares one instruction over 256 rows, each
+// 128 k into a staging ring by tensor maps, groups of warps convert them into
+// the operand ring, one thread issues the matrix instructions, four warps scale
+// and store.  Each group of converters owns one operand stage of 64 k, so that
+// the latencies of four conversions overlap.  A pair of CTAs (CG = 2) shares one instruction over 256 rows, each
 // converting its own 128 rows of x and half of the rows of w.
 #include "tc_device.cuh"
 
@@ -22,10 +23,12 @@ namespace {
 using namespace tc;
 
 constexpr int kRowsMax = 256;                        // rows of x and w in a CTA's stage
-constexpr uint32_t kStaged = kRowsMax * 64, kOperand = kRowsMax * 128;
-constexpr int kSS = 5, kOS = 4;                      // stages of the two rings
-constexpr int kConverters = 8;                       // warps
-constexpr int kI8Threads = 32 * (6 + kConverters);
+constexpr uint32_t kStaged = kRowsMax * 128, kOperand = kRowsMax * 128;
+constexpr int kSS = 3, kOS = 4;                      // stages of the two rings: 128 k and 64 k
+constexpr int kGroups = kOS, kGroupWarps = 2;        // converters
+constexpr int kGroupThreads = 32 * kGroupWarps;
+constexpr int kI8Threads = 32 * 6 + kGroups * kGroupThreads;
+constexpr int kBatch = 4;                            // 16-byte pieces a converter holds at a time
 constexpr uint32_t kI8Smem = kSS * kStaged + kOS * kOperand + 1024;
 constexpr uint32_t kI8TmemCols = 512;
 
@@ -34,7 +37,7 @@ __device__ uint32_t g_i8_error;  // set by a wait that gave up
 struct I8Args {
   GemmArgs g;
   TileWalk walk;
-  int steps;
+  int steps;      // of 64 k, an even number
   int bn;         // columns of a tile, a multiple of 32
   int out_align;
 };
@@ -61,10 +64,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSS; ++i) {
       bar_init(landed + 8 * i, 1);
-      bar_init(taken + 8 * i, kConverters);
+      bar_init(taken + 8 * i, 2 * kGroupWarps);
     }
     for (int i = 0; i < kOS; ++i) {
-      bar_init(ready + 8 * i, kConverters * CG);
+      bar_init(ready + 8 * i, kGroupWarps * CG);
       bar_init(used + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -96,13 +99,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
         const Tile tile = tile_at(a.walk, t);
         const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * a.bn + (int)rank * (a.bn / CG);
-        for (int s = 0; s < a.steps; ++s, ++it) {
+        for (int s = 0; s < a.steps / 2; ++s, ++it) {
           const uint32_t st = it % kSS;
           if (!(ok = bar_wait(taken + 8 * st, ((it / kSS) & 1) ^ 1, &dead))) break;
           const uint32_t dst = staging + st * kStaged, bar = landed + 8 * st;
-          bar_expect_tx(bar, (uint32_t)rows * 64);
-          load_box<1>(dst, &map_x, s * 64, m0, bar);
-          load_box<1>(dst + 128 * 64, &map_w, s * 64, n0, bar);
+          bar_expect_tx(bar, (uint32_t)rows * 128);
+          load_box<1>(dst, &map_x, s * 128, m0, bar);
+          load_box<1>(dst + 128 * 128, &map_w, s * 128, n0, bar);
         }
       }
       if (!ok) atomicExch(&g_i8_error, 1u);
@@ -175,58 +178,73 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
     }
   } else {
-    // A row's 64 k: 64 bytes staged, 128 bytes as an operand, of which the 16-byte
-    // piece p lies at p ^ (row % 8).  A warp's lanes take 16 staged bytes each
-    // (two pieces), four lanes a row: neither access has bank conflicts.
-    const int thread = (int)threadIdx.x - 6 * 32;
-    const int pieces = rows * 4;
-    uint32_t it = 0;
+    // Both rings hold rows of 128 bytes whose 16-byte piece p lies at p ^ (row % 8).
+    // A step converts half of a staged row, pieces 4h .. 4h + 3, into all eight
+    // of an operand row.  Eight lanes take four pieces of rows r and r + 4 (eight
+    // different banks), and the lanes of the second row store their two results
+    // in the other order, which again makes eight.
+    const int group = (warp - 6) / kGroupWarps, thread = (int)(threadIdx.x - 6 * 32) % kGroupThreads;
+    const int lane = thread & 31, j = lane & 3, second = (lane >> 2) & 1;
+    const int row0 = (thread >> 5) * 8 + (lane >> 3) + 4 * second;  // + 8 kGroupWarps each time
+    const int64_t mine = first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0;
+    const int64_t total = mine * a.steps;
     bool ok = true;
-    for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
-      for (int s = 0; s < a.steps; ++s, ++it) {
-        const uint32_t ss = it % kSS, os = it % kOS;
-        if (!(ok = bar_wait(landed + 8 * ss, (it / kSS) & 1, &dead))) break;
-        uint4 q[kRowsMax * 4 / (32 * kConverters)];
+    int64_t it = group;
+    for (; it < total && ok; it += kGroups) {
+      const uint32_t unit = (uint32_t)(it >> 1), ss = unit % kSS, half = (uint32_t)it & 1, round = (uint32_t)(it / kOS);
+      if (!(ok = bar_wait(landed + 8 * ss, (unit / kSS) & 1, &dead))) break;
+      const uint32_t from = staging + ss * kStaged, to = operands + (uint32_t)group * kOperand;
+      bool waited = false;
+#pragma unroll 1
+      for (int r = row0; r < rows; r += 8 * kGroupWarps * kBatch) {
+        uint4 q[kBatch];
 #pragma unroll
-        for (int i = 0; i < kRowsMax * 4 / (32 * kConverters); ++i) {
-          const int p = thread + i * 32 * kConverters;
-          if (p < pieces)
+        for (int i = 0; i < kBatch; ++i) {
+          const int row = r + i * 8 * kGroupWarps;
+          if (row < rows)
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
-                         : "r"(staging + ss * kStaged + 16u * p));
+                         : "r"(from + (uint32_t)row * 128 + 16u * ((half * 4 + j) ^ (row & 7))));
         }
-        if (!(ok = bar_wait(used + 8 * os, ((it / kOS) & 1) ^ 1, &dead))) break;
+        if (!waited) {
+          if (!(ok = bar_wait(used + 8 * group, (round & 1) ^ 1, &dead))) break;
+          waited = true;
+        }
 #pragma unroll
-        for (int i = 0; i < kRowsMax * 4 / (32 * kConverters); ++i) {
-          const int p = thread + i * 32 * kConverters;
-          if (p < pieces) {
-            const int row = p >> 2, c = (p & 3) * 2;
-            const uint32_t to = operands + os * kOperand + (uint32_t)row * 128;
+        for (int i = 0; i < kBatch; ++i) {
+          const int row = r + i * 8 * kGroupWarps;
+          if (row < rows) {
+            const uint32_t line = to + (uint32_t)row * 128;
             uint32_t h[8];
             i8_to_f16(q[i].x, h[0], h[1]);
             i8_to_f16(q[i].y, h[2], h[3]);
             i8_to_f16(q[i].z, h[4], h[5]);
             i8_to_f16(q[i].w, h[6], h[7]);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + 16u * (uint32_t)(c ^ (row & 7))), "r"(h[0]),
-                         "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + 16u * (uint32_t)((c + 1) ^ (row & 7))),
-                         "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const int c = o ^ second;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line + 16u * ((2 * j + c) ^ (row & 7))),
+                           "r"(c ? h[4] : h[0]), "r"(c ? h[5] : h[1]), "r"(c ? h[6] : h[2]), "r"(c ? h[7] : h[3])
+                           : "memory");
+            }
           }
         }
-        fence_async_smem();  // the matrix unit reads through the asynchronous proxy
-        __syncwarp();
-        if (elect_one()) {
-          bar_arrive(taken + 8 * ss);
-          if (CG == 2)
-            bar_arrive_cluster(map_to_cta(ready + 8 * os, 0));
-          else
-            bar_arrive(ready + 8 * os);
-        }
+      }
+      if (!ok) break;
+      fence_async_smem();  // the matrix unit reads through the asynchronous proxy
+      __syncwarp();
+      if (elect_one()) {
+        bar_arrive(taken + 8 * ss);
+        if (CG == 2)
+          bar_arrive_cluster(map_to_cta(ready + 8 * group, 0));
+        else
+          bar_arrive(ready + 8 * group);
       }
     }
     if (!ok) atomicExch(&g_i8_error, 1u);
-    // The last operand stages are multiplied before the CTA ends.
-    for (uint32_t k = it > kOS ? it - kOS : 0; k < it && ok; ++k) ok = bar_wait(used + 8 * (k % kOS), (k / kOS) & 1, &dead);
+    // The group's last operand stage is multiplied before the CTA ends.
+    if (ok && it >= kGroups && it - kGroups < total)
+      bar_wait(used + 8 * group, (uint32_t)((it - kGroups) / kOS) & 1, &dead);
   }
   __syncwarp();
   fence_before_sync();
@@ -239,8 +257,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 template <class E, int CG>
 cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
   CUtensorMap mx, mw;
-  if (!tc_make_map(&mx, kMapU8, g.a0, g.M, g.K, g.lda, 128, 64) ||
-      !tc_make_map(&mw, kMapU8, g.b0, g.N, g.K, g.ldb, bn / CG, 64))
+  if (!tc_make_map(&mx, kMapU8, g.a0, g.M, g.K, g.lda, 128, 128) ||
+      !tc_make_map(&mw, kMapU8, g.b0, g.N, g.K, g.ldb, bn / CG, 128))
     return cudaErrorInvalidValue;
   I8Args a = {};
   a.g = g;
@@ -248,7 +266,7 @@ cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
   a.walk.tiles_n = (int)((g.N + bn - 1) / bn);
   a.walk.tiles = (int64_t)a.walk.tiles_m * a.walk.tiles_n;
   a.walk.group = 16 / CG;
-  a.steps = (int)((g.K + 63) / 64);
+  a.steps = (int)((g.K + 127) / 128) * 2;
   a.bn = bn;
   const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | (uintptr_t)g.ldc * 2;
   a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : 2;

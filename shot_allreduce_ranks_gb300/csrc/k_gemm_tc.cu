@@ -40,8 +40,7 @@ static EncodeFn encode_fn() {
 
 bool tc_available() { return encode_fn() != nullptr; }
 
-// 16-bit operands arrive in the 128-byte swizzle that the matrix instruction
-// reads; 8-bit ones plainly, since threads read and convert them.
+// Boxes arrive in the 128-byte swizzle, which the matrix instruction reads.
 bool tc_make_map(CUtensorMap* map, MapType type, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
                  int box_cols) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -51,8 +50,7 @@ bool tc_make_map(CUtensorMap* map, MapType type, const void* p, int64_t rows, in
                                 : type == kMapF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return encode_fn()(map, t, 2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     type == kMapU8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace tc
