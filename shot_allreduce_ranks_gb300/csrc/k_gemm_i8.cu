@@ -25,10 +25,10 @@ using namespace tc;
 constexpr int kRowsMax = 256;                        // rows of x and w in a CTA's stage
 constexpr uint32_t kStaged = kRowsMax * 128, kOperand = kRowsMax * 128;
 constexpr int kSS = 3, kOS = 4;                      // stages of the two rings: 128 k and 64 k
-constexpr int kGroups = kOS, kGroupWarps = 2;        // converters
+constexpr int kGroups = kOS, kGroupWarps = 4;        // converters
 constexpr int kGroupThreads = 32 * kGroupWarps;
 constexpr int kI8Threads = 32 * 6 + kGroups * kGroupThreads;
-constexpr int kBatch = 4;                            // 16-byte pieces a converter holds at a time
+constexpr int kPieces = kRowsMax / (8 * kGroupWarps);  // 16-byte pieces that a converter takes of a step
 constexpr uint32_t kI8Smem = kSS * kStaged + kOS * kOperand + 1024;
 constexpr uint32_t kI8TmemCols = 512;
 
@@ -147,26 +147,33 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       const uint32_t buf = at & 1;
       const int64_t m = ((int64_t)tile.m * CG + rank) * 128 + row_in;
       const int n0 = tile.n * a.bn;
+      // The scales are on their way while the tile is multiplied: a lane holds
+      // its row's, and column 32 j + lane's for every 32 columns.
       const float sm = m < a.g.M ? a.g.sm[m] : 0.0f;
+      float sn[kRowsMax / 32];
+#pragma unroll
+      for (int j = 0; j < kRowsMax / 32; ++j) {
+        const int n = n0 + 32 * j + (int)(threadIdx.x & 31);
+        sn[j] = 32 * j < a.bn && n < a.g.N ? a.g.sn[n] : 0.0f;
+      }
       if (!bar_wait(done + 8 * buf, (at >> 1) & 1, &dead)) {
         atomicExch(&g_i8_error, 1u);
         break;
       }
       fence_after_sync();
-#pragma unroll 1
-      for (int c = 0; c < a.bn; c += 32) {
-        if (n0 + c >= a.g.N) break;
+#pragma unroll
+      for (int j = 0; j < kRowsMax / 32; ++j) {
+        const int c = 32 * j;
+        if (c >= a.bn || n0 + c >= a.g.N) break;
         uint32_t r[32];
         __syncwarp();
         tmem_load32(r, tmem + (lane0 << 16) + buf * 256 + c);
         tmem_wait_load32(r);
-        if (m < a.g.M) {
-          const int left = (int)min((int64_t)32, a.g.N - n0 - c);
-          float v[32];
+        float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * sm * (i < left ? __ldg(a.g.sn + n0 + c + i) : 0.0f);
-          store_row<E>(a.g.c0, m * a.g.ldc + n0 + c, v, left, a.out_align);
-        }
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * sm * __shfl_sync(0xFFFFFFFFu, sn[j], i);
+        if (m < a.g.M)
+          store_row<E>(a.g.c0, m * a.g.ldc + n0 + c, v, (int)min((int64_t)32, a.g.N - n0 - c), a.out_align);
       }
       fence_before_sync();
       __syncwarp();
@@ -194,47 +201,41 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       const uint32_t unit = (uint32_t)(it >> 1), ss = unit % kSS, half = (uint32_t)it & 1, round = (uint32_t)(it / kOS);
       if (!(ok = bar_wait(landed + 8 * ss, (unit / kSS) & 1, &dead))) break;
       const uint32_t from = staging + ss * kStaged, to = operands + (uint32_t)group * kOperand;
-      bool waited = false;
-#pragma unroll 1
-      for (int r = row0; r < rows; r += 8 * kGroupWarps * kBatch) {
-        uint4 q[kBatch];
+      uint4 q[kPieces];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int row = r + i * 8 * kGroupWarps;
-          if (row < rows)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
-                         : "r"(from + (uint32_t)row * 128 + 16u * ((half * 4 + j) ^ (row & 7))));
-        }
-        if (!waited) {
-          if (!(ok = bar_wait(used + 8 * group, (round & 1) ^ 1, &dead))) break;
-          waited = true;
-        }
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = row0 + i * 8 * kGroupWarps;
+        if (row < rows)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                       : "r"(from + (uint32_t)row * 128 + 16u * ((half * 4 + j) ^ (row & 7))));
+      }
+      // The staged rows are in registers: the next copy need not wait for the operand stage.
+      __syncwarp();
+      if (elect_one()) bar_arrive(taken + 8 * ss);
+      if (!(ok = bar_wait(used + 8 * group, (round & 1) ^ 1, &dead))) break;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int row = r + i * 8 * kGroupWarps;
-          if (row < rows) {
-            const uint32_t line = to + (uint32_t)row * 128;
-            uint32_t h[8];
-            i8_to_f16(q[i].x, h[0], h[1]);
-            i8_to_f16(q[i].y, h[2], h[3]);
-            i8_to_f16(q[i].z, h[4], h[5]);
-            i8_to_f16(q[i].w, h[6], h[7]);
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = row0 + i * 8 * kGroupWarps;
+        if (row < rows) {
+          const uint32_t line = to + (uint32_t)row * 128;
+          uint32_t h[8];
+          i8_to_f16(q[i].x, h[0], h[1]);
+          i8_to_f16(q[i].y, h[2], h[3]);
+          i8_to_f16(q[i].z, h[4], h[5]);
+          i8_to_f16(q[i].w, h[6], h[7]);
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const int c = o ^ second;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line + 16u * ((2 * j + c) ^ (row & 7))),
-                           "r"(c ? h[4] : h[0]), "r"(c ? h[5] : h[1]), "r"(c ? h[6] : h[2]), "r"(c ? h[7] : h[3])
-                           : "memory");
-            }
+          for (int o = 0; o < 2; ++o) {
+            const int c = o ^ second;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line + 16u * ((2 * j + c) ^ (row & 7))),
+                         "r"(c ? h[4] : h[0]), "r"(c ? h[5] : h[1]), "r"(c ? h[6] : h[2]), "r"(c ? h[7] : h[3])
+                         : "memory");
           }
         }
       }
-      if (!ok) break;
       fence_async_smem();  // the matrix unit reads through the asynchronous proxy
       __syncwarp();
       if (elect_one()) {
-        bar_arrive(taken + 8 * ss);
         if (CG == 2)
           bar_arrive_cluster(map_to_cta(ready + 8 * group, 0));
         else
