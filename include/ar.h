@@ -441,8 +441,13 @@ ar_status_t ar_allreduce_fused_noalloc(int R, const void* const* d_in_tbl,
  *
  * Matrices are row-major device arrays: element (i, j) of a matrix with
  * leading dimension ld is at [i * ld + j], ld >= its columns, in elements.
- * Any ld and any element-aligned base address is accepted; rows that start
- * on 16 bytes (base and ld) take the tensor cores' fast path.  All calls are
+ * Any ld and any element-aligned base address is accepted.  The products read
+ * rows that start on 16 bytes (base and ld) as they are.  Other rows they copy
+ * into `scratch` first: device memory, 16-byte aligned, of at least the bytes
+ * that the call's _scratch_bytes function gives for the same operands (0 where
+ * all rows start on 16 bytes; scratch may then be NULL), owned by the caller
+ * and free again when the call has completed.  With scratch NULL such operands
+ * take a slower kernel.  All calls are
  * asynchronous on `stream`, allocate nothing, synchronise nothing, and can be
  * captured into a CUDA graph.  Outputs must not overlap inputs or one another
  * unless a call says so.
@@ -486,10 +491,18 @@ ar_status_t ar_ffn_destroy(ar_ffn_t h);
  *                 ar_ffn_backward takes.  Both or neither.
  * Sums are held in fp32; the activation and the product are taken in fp32
  * from the unrounded sums; each output is rounded once, to nearest even.
- * tokens = 0 returns AR_OK without a launch. */
+ * tokens = 0 returns AR_OK without a launch.  Errors: AR_ERR_INVALID_ARG
+ * (NULL, ld too small, an odd address, scratch too small), AR_ERR_CUDA. */
 ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
                            const void* w_up, size_t ldw, void* out, void* gate, void* up,
-                           size_t ldo, size_t tokens, void* stream);
+                           size_t ldo, size_t tokens, void* scratch, size_t scratch_bytes,
+                           void* stream);
+
+/* ar_ffn_scratch_bytes -- bytes of scratch with which ar_ffn_forward and
+ * ar_ffn_backward can lay these operands out (see above); 0 for a NULL handle.
+ * Host-only. */
+size_t ar_ffn_scratch_bytes(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
+                            const void* w_up, size_t ldw, size_t tokens);
 
 /* ar_ffn_backward -- the gradients of ar_ffn_forward:
  *   dgate = dout * up * act'(gate),  dup = dout * act(gate)
@@ -507,7 +520,8 @@ ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_
 ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
                             const void* w_up, size_t ldw, const void* gate, const void* up,
                             const void* dout, size_t ldo, void* dx, size_t lddx, void* dw_gate,
-                            void* dw_up, size_t lddw, size_t tokens, void* stream);
+                            void* dw_up, size_t lddw, size_t tokens, void* scratch,
+                            size_t scratch_bytes, void* stream);
 
 /* ar_dropout -- out = residual + (keep ? x / (1 - p) : 0).
  *   x, residual, out  [rows, cols] of dtype (AR_BF16, AR_FP16, AR_FP32);
@@ -554,7 +568,12 @@ ar_status_t ar_quantize_rows(const void* x, size_t ldx, int8_t* q, size_t ldq, f
  * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (dtype AR_FP32), AR_ERR_CUDA. */
 ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, const int8_t* w,
                          size_t ldw, const float* w_scale, void* y, size_t ldy, size_t tokens,
-                         size_t in, size_t out, int dtype, void* stream);
+                         size_t in, size_t out, int dtype, void* scratch, size_t scratch_bytes,
+                         void* stream);
+
+/* ar_linear_i8_scratch_bytes -- as ar_ffn_scratch_bytes.  Host-only. */
+size_t ar_linear_i8_scratch_bytes(const int8_t* x, size_t ldx, const int8_t* w, size_t ldw,
+                                  size_t tokens, size_t in, size_t out);
 
 /* ar_ops_get_device_status -- wait for `stream` to drain, then read and clear
  * the feed-forward operators' error word on the current device: AR_ERR_TIMEOUT

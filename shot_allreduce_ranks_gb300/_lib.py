@@ -80,16 +80,18 @@ PROTOTYPES = {
     "ar_all_gather": (_ST, [_H, _VP, _VP, _SZ, _VP]),
     "ar_ffn_create": (_ST, [_SZ, _SZ, _SZ, _I, _I, _I, ctypes.POINTER(_H)]),
     "ar_ffn_destroy": (_ST, [_H]),
-    "ar_ffn_forward": (_ST, [_H, _VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _VP, _SZ, _SZ, _VP]),
+    "ar_ffn_forward": (_ST, [_H, _VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _VP, _SZ, _SZ, _VP, _SZ, _VP]),
+    "ar_ffn_scratch_bytes": (_SZ, [_H, _VP, _SZ, _VP, _VP, _SZ, _SZ]),
     "ar_ffn_backward": (_ST, [_H, _VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _VP, _SZ, _VP, _SZ,
-                              _VP, _VP, _SZ, _SZ, _VP]),
+                              _VP, _VP, _SZ, _SZ, _VP, _SZ, _VP]),
     "ar_dropout": (_ST, [_VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, ctypes.c_double,
                          _U64, _U64, _U64, _VP]),
     "ar_dropout_backward": (_ST, [_VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, ctypes.c_double,
                                   _U64, _U64, _U64, _VP]),
     "ar_ops_get_device_status": (_ST, [_VP]),
     "ar_quantize_rows": (_ST, [_VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, _I, _VP]),
-    "ar_linear_i8": (_ST, [_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _I, _VP]),
+    "ar_linear_i8": (_ST, [_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _I, _VP, _SZ, _VP]),
+    "ar_linear_i8_scratch_bytes": (_SZ, [_VP, _SZ, _VP, _SZ, _SZ, _SZ, _SZ]),
 }
 
 AR_NOALLOC_SCRATCH_BYTES = 32 << 20

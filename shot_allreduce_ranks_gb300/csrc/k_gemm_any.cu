@@ -73,11 +73,11 @@ __global__ void __launch_bounds__(kThreadsAny) k_gemm_any(GemmArgs g, int64_t ti
         const int e = tid + i * kThreadsAny, row = e / kDepth;
         const int64_t n = n0 + (row & 31), k = k0 + e % kDepth;
         const S* p = static_cast<const S*>(row < 32 ? g.b0 : g.b1);
-        rb[i] = n < g.N && k < g.K ? load_bits(p + n * g.ldb + k) : 0u;
+        rb[i] = n < g.N && k < g.K ? load_bits(p + n * (row < 32 ? g.ldb : g.ldb1) + k) : 0u;
       }
     } else {
-      load_tile<kBK>(rb, static_cast<const S*>(MODE == kGemmDx && up ? g.b1 : g.b0), g.ldb, n0, g.N,
-                     k0, g.K, tid);
+      const bool b1 = MODE == kGemmDx && up;
+      load_tile<kBK>(rb, static_cast<const S*>(b1 ? g.b1 : g.b0), b1 ? g.ldb1 : g.ldb, n0, g.N, k0, g.K, tid);
     }
   };
   fetch(0);

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kFewThreads) k_gemm_few(GemmArgs g) {
   const int64_t ra = min(n0 + g8, g.N - 1), rb = MODE == kGemmI8 ? min(n0 + g8 + 8, g.N - 1) : ra;
   const int64_t bytes = g.K * B;
   const char* wa = static_cast<const char*>(g.b0) + ra * g.ldb * B;
-  const char* wb = static_cast<const char*>(MODE == kGemmI8 ? g.b0 : g.b1) + rb * g.ldb * B;
+  const char* wb = static_cast<const char*>(MODE == kGemmI8 ? g.b0 : g.b1) + rb * (MODE == kGemmI8 ? g.ldb : g.ldb1) * B;
   const char* xs[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) xs[j] = static_cast<const char*>(g.a0) + min((int64_t)(8 * j + g8), g.M - 1) * g.lda * B;
@@ -142,7 +142,8 @@ template <int MODE, class E, int ACT>
 cudaError_t launch_align(const GemmArgs& g, cudaStream_t s) {
   const int64_t unit = MODE == kGemmI8 ? 16 : 8;
   const bool vec = ((reinterpret_cast<uintptr_t>(g.a0) | reinterpret_cast<uintptr_t>(g.b0) |
-                     reinterpret_cast<uintptr_t>(g.b1)) & 15u) == 0 && g.lda % unit == 0 && g.ldb % unit == 0;
+                     reinterpret_cast<uintptr_t>(g.b1)) & 15u) == 0 && g.lda % unit == 0 && g.ldb % unit == 0 &&
+                   g.ldb1 % unit == 0;
   return vec ? launch<MODE, E, ACT, true>(g, s) : launch<MODE, E, ACT, false>(g, s);
 }
 

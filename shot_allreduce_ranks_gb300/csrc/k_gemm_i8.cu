@@ -140,12 +140,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
   } else if (warp < 6) {
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;
-    const int row_in = (int)lane0 + (int)(threadIdx.x & 31);
     uint32_t at = 0;
     for (int64_t t = first; t < a.walk.tiles; t += stride, ++at) {
       const Tile tile = tile_at(a.walk, t);
       const uint32_t buf = at & 1;
-      const int64_t m = ((int64_t)tile.m * CG + rank) * 128 + row_in;
+      const int64_t m0 = ((int64_t)tile.m * CG + rank) * 128 + lane0, m = m0 + (threadIdx.x & 31);
       const int n0 = tile.n * a.bn;
       // The scales are on their way while the tile is multiplied: a lane holds
       // its row's, and column 32 j + lane's for every 32 columns.
@@ -172,8 +171,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * sm * __shfl_sync(0xFFFFFFFFu, sn[j], i);
-        if (m < a.g.M)
-          store_row<E>(a.g.c0, m * a.g.ldc + n0 + c, v, (int)min((int64_t)32, a.g.N - n0 - c), a.out_align);
+        store_chunk<E>(a.g.c0, a.g.ldc, m0, n0 + c, a.g.M, a.g.N, v, a.out_align);
       }
       fence_before_sync();
       __syncwarp();
@@ -270,7 +268,7 @@ cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
   a.steps = (int)((g.K + 127) / 128) * 2;
   a.bn = bn;
   const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | (uintptr_t)g.ldc * 2;
-  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : 2;
+  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : out % 4 == 0 ? 4 : 2;
   auto* kernel = k_gemm_i8<E, CG>;
   static bool raised[64];  // by device
   int dev = 0;

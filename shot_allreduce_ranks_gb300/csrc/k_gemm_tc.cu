@@ -211,7 +211,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;  // this warp's lanes of tensor memory
-    const int row_in = (int)lane0 + (int)(threadIdx.x & 31);
     uint32_t at = 0;
     for (int64_t t = first; t < a.walk.tiles; t += stride, ++at) {
       const Tile tile = tile_at(a.walk, t);
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         break;
       }
       fence_after_sync();
-      const int64_t m = ((int64_t)tile.m * CG + rank) * 128 + row_in;
+      const int64_t m0 = ((int64_t)tile.m * CG + rank) * 128 + lane0;
       const int n0 = tile.n * kCols;
       const uint32_t acc = tmem + (lane0 << 16) + buf * 256;
 #pragma unroll 1
@@ -233,27 +232,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (MODE == kGemmGated) tmem_load32(u, acc + kCols + c);
         tmem_wait_load32(r);
         if (MODE == kGemmGated) tmem_wait_load32(u);
-        if (m < a.g.M) {
-          const int left = (int)min((int64_t)32, a.g.N - n0 - c);
-          const int64_t pos = m * a.g.ldc + n0 + c;
-          float v[32];
-          if (MODE == kGemmGated) {
-            if (a.g.c1) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-              store_row<E>(a.g.c1, pos, v, left, a.out_align);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-              store_row<E>(a.g.c2, pos, v, left, a.out_align);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(__uint_as_float(r[i])) * __uint_as_float(u[i]);
-            store_row<E>(a.g.c0, pos, v, left, a.out_align);
-          } else {
+        const auto store = [&](void* out, const float(&v)[32]) {
+          store_chunk<E>(out, a.g.ldc, m0, n0 + c, a.g.M, a.g.N, v, a.out_align);
+        };
+        float v[32];
+        if (MODE == kGemmGated) {
+          if (a.g.c1) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            store_row<E>(MODE == kGemmDw && tile.z ? a.g.c1 : a.g.c0, pos, v, left, a.out_align);
+            store(a.g.c1, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+            store(a.g.c2, v);
           }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(__uint_as_float(r[i])) * __uint_as_float(u[i]);
+          store(a.g.c0, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          store(MODE == kGemmDw && tile.z ? a.g.c1 : a.g.c0, v);
         }
       }
       fence_before_sync();
@@ -292,11 +290,11 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
     if (MODE == kGemmDx) ok = ok && make_map(&ma1, dtype, g.a1, g.M, g.K, g.lda, 128);
   }
   if (MODE == kGemmGated) {
-    ok = ok && make_map(&mb0, dtype, g.b0, g.N, g.K, g.ldb, BN / 2) && make_map(&mb1, dtype, g.b1, g.N, g.K, g.ldb, BN / 2);
+    ok = ok && make_map(&mb0, dtype, g.b0, g.N, g.K, g.ldb, BN / 2) && make_map(&mb1, dtype, g.b1, g.N, g.K, g.ldb1, BN / 2);
   } else {
     ok = ok && make_map(&mb0, dtype, g.b0, g.K, g.N, g.ldb, 64);
     mb1 = mb0;
-    if (MODE == kGemmDx) ok = ok && make_map(&mb1, dtype, g.b1, g.K, g.N, g.ldb, 64);
+    if (MODE == kGemmDx) ok = ok && make_map(&mb1, dtype, g.b1, g.K, g.N, g.ldb1, 64);
   }
   if (!ok) return cudaErrorInvalidValue;
 
@@ -309,7 +307,7 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
   a.steps = (int)((g.K + kBK - 1) / kBK);
   const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | reinterpret_cast<uintptr_t>(g.c1) |
                         reinterpret_cast<uintptr_t>(g.c2) | (uintptr_t)g.ldc * 2;
-  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : 2;
+  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : out % 4 == 0 ? 4 : 2;
 
   auto* kernel = k_gemm_tc<MODE, E, ACT, BN, CG>;
   static bool raised[64];  // by device
@@ -364,7 +362,7 @@ bool rows_on_16(const void* p, int64_t ld) {
 bool gemm_tc_takes(int mode, const GemmArgs& g) {
   const int64_t most = (int64_t)1 << 30;
   return mode != kGemmI8 && tc_available() && g.M <= most && g.N <= most && g.K <= most && rows_on_16(g.a0, g.lda) &&
-         rows_on_16(g.a1, g.lda) && rows_on_16(g.b0, g.ldb) && rows_on_16(g.b1, g.ldb);
+         rows_on_16(g.a1, g.lda) && rows_on_16(g.b0, g.ldb) && rows_on_16(g.b1, g.ldb1);
 }
 
 cudaError_t launch_gemm_tc(int mode, int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {

@@ -1,5 +1,6 @@
 // Element-wise and row-wise steps of the feed-forward operators: the gradients
-// of the two pre-activations, and the quantisation of rows to 8 bits.
+// of the two pre-activations, the quantisation of rows to 8 bits, and the copy
+// of unaligned rows to where a tensor map can read them.
 #include "ops_internal.cuh"
 
 namespace ar {
@@ -102,7 +103,54 @@ __global__ void __launch_bounds__(kQuantThreads)
   }
 }
 
+// ---------------------------------------------------------------------------
+constexpr int kPackThreads = 256;
+
+struct PackJobs {
+  PackJob job[3];
+};
+
+// A thread makes 16 bytes of a row from its elements, one load each: the
+// source rows begin anywhere, and neighbouring lanes' loads share cache lines.
+template <int B>
+__global__ void __launch_bounds__(kPackThreads) k_pack(const __grid_constant__ PackJobs jobs) {
+  constexpr int G = 16 / B;
+  const PackJob j = jobs.job[blockIdx.y];
+  const int64_t per_row = (j.cols + G - 1) / G, total = j.rows * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kPackThreads) {
+    const int64_t row = total >> 32 ? i / per_row : (int64_t)((uint32_t)i / (uint32_t)per_row);
+    const int64_t col = (i - row * per_row) * G;
+    const char* p = static_cast<const char*>(j.from) + (row * j.ld_from + col) * B;
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int k = 0; k < G; ++k)
+      if (col + k < j.cols) {
+        const uint32_t v = B == 2 ? *reinterpret_cast<const uint16_t*>(p + 2 * k) : *reinterpret_cast<const uint8_t*>(p + k);
+        w[k * B / 4] |= v << (8 * (k * B % 4));
+      }
+    *reinterpret_cast<uint4*>(static_cast<char*>(j.to) + (row * j.ld_to + col) * B) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_sms, cudaStream_t s) {
+  PackJobs all = {};
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    all.job[i] = jobs[i];
+    const int64_t g = 16 / elem_bytes, n = jobs[i].rows * ((jobs[i].cols + g - 1) / g);
+    most = n > most ? n : most;
+  }
+  const int64_t want = (most + kPackThreads - 1) / kPackThreads, cap = (int64_t)num_sms * 8;
+  const dim3 grid((unsigned)(want < cap ? want : cap), (unsigned)count);
+  if (elem_bytes == 2)
+    k_pack<2><<<grid, kPackThreads, 0, s>>>(all);
+  else
+    k_pack<1><<<grid, kPackThreads, 0, s>>>(all);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
                              int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,

@@ -46,11 +46,55 @@ bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
 
 bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
+// A matrix with its row stride; packed rows take the place of ones that do not
+// start on 16 bytes where the caller gave scratch memory for them.
+struct Rows {
+  const void* p;
+  size_t rows, cols, ld;
+};
+
+bool on_16(const Rows& r, size_t elem) { return !misaligned(r.p, 16) && r.ld * elem % 16 == 0; }
+size_t packed_ld(const Rows& r, size_t elem) { return (r.cols * elem + 15) / 16 * 16 / elem; }
+
+// Bytes that packing takes: 0 where every matrix can be read as it is.
+size_t pack_bytes(const Rows* m, int count, size_t elem) {
+  size_t bytes = 0;
+  for (int i = 0; i < count; ++i)
+    if (!on_16(m[i], elem)) bytes += m[i].rows * packed_ld(m[i], elem) * elem;
+  return bytes;
+}
+
+ar_status_t pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_bytes, int num_sms, cudaStream_t s) {
+  const size_t need = pack_bytes(m, count, elem);
+  if (need == 0 || !scratch) return AR_OK;
+  if (misaligned(scratch, 16) || scratch_bytes < need) return AR_ERR_INVALID_ARG;
+  ar::PackJob jobs[3];
+  int n = 0;
+  char* to = static_cast<char*>(scratch);
+  for (int i = 0; i < count; ++i) {
+    if (on_16(m[i], elem)) continue;
+    const size_t ld = packed_ld(m[i], elem);
+    jobs[n++] = {m[i].p, to, (int64_t)m[i].rows, (int64_t)m[i].cols, (int64_t)m[i].ld, (int64_t)ld};
+    m[i].p = to;
+    m[i].ld = ld;
+    to += m[i].rows * ld * elem;
+  }
+  return cuda_status(ar::launch_pack(jobs, n, (int)elem, num_sms, s));
+}
+
 cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaStream_t s) {
   if (ar::gemm_few_takes(mode, g)) return ar::launch_gemm_few(mode, dtype, g, s);
   if (ar::gemm_tc_takes(mode, g)) return ar::launch_gemm_tc(mode, dtype, g, num_sms, s);
   if (ar::gemm_i8_takes(mode, g)) return ar::launch_gemm_i8(dtype, g, num_sms, s);
   return ar::launch_gemm_any(mode, dtype, g, s);
+}
+
+// x, w_gate, w_up of a call.
+void operands(const ar_ffn_ctx* h, const void* x, size_t ldx, const void* w_gate, const void* w_up, size_t ldw,
+              size_t tokens, Rows (&m)[3]) {
+  m[0] = {x, tokens, h->hidden, ldx};
+  m[1] = {w_gate, h->width, h->hidden, ldw};
+  m[2] = {w_up, h->width, h->hidden, ldw};
 }
 
 ar_status_t dropout_call(const void* x, size_t ldx, const void* res, size_t ldr, void* out,
@@ -123,9 +167,18 @@ ar_status_t ar_ffn_destroy(ar_ffn_t h) {
   return st;
 }
 
+size_t ar_ffn_scratch_bytes(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate, const void* w_up,
+                            size_t ldw, size_t tokens) {
+  if (!h) return 0;
+  Rows m[3];
+  operands(h, x, ldx, w_gate, w_up, ldw, tokens, m);
+  return pack_bytes(m, 3, 2);
+}
+
 ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
                            const void* w_up, size_t ldw, void* out, void* gate, void* up,
-                           size_t ldo, size_t tokens, void* stream) {
+                           size_t ldo, size_t tokens, void* scratch, size_t scratch_bytes,
+                           void* stream) {
   if (!h || (gate == nullptr) != (up == nullptr)) return AR_ERR_INVALID_ARG;
   if (tokens == 0) return AR_OK;
   if (bad_matrix(x, tokens, h->hidden, ldx) || bad_matrix(w_gate, h->width, h->hidden, ldw) ||
@@ -133,19 +186,24 @@ ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_
       misaligned(x, 2) || misaligned(w_gate, 2) || misaligned(w_up, 2) || misaligned(out, 2) ||
       misaligned(gate, 2) || misaligned(up, 2))
     return AR_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Rows m[3];
+  operands(h, x, ldx, w_gate, w_up, ldw, tokens, m);
+  if (ar_status_t st = pack(m, 3, 2, scratch, scratch_bytes, h->num_sms, s)) return st;
   ar::GemmArgs g = {};
-  g.a0 = x, g.lda = (int64_t)ldx;
-  g.b0 = w_gate, g.b1 = w_up, g.ldb = (int64_t)ldw;
+  g.a0 = m[0].p, g.lda = (int64_t)m[0].ld;
+  g.b0 = m[1].p, g.b1 = m[2].p, g.ldb = (int64_t)m[1].ld, g.ldb1 = (int64_t)m[2].ld;
   g.c0 = out, g.c1 = gate, g.c2 = up, g.ldc = (int64_t)ldo;
   g.M = (int64_t)tokens, g.N = (int64_t)h->width, g.K = (int64_t)h->hidden;
   g.act = h->act;
-  return cuda_status(gemm(ar::kGemmGated, h->dtype, g, h->num_sms, static_cast<cudaStream_t>(stream)));
+  return cuda_status(gemm(ar::kGemmGated, h->dtype, g, h->num_sms, s));
 }
 
 ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w_gate,
                             const void* w_up, size_t ldw, const void* gate, const void* up,
                             const void* dout, size_t ldo, void* dx, size_t lddx, void* dw_gate,
-                            void* dw_up, size_t lddw, size_t tokens, void* stream) {
+                            void* dw_up, size_t lddw, size_t tokens, void* scratch,
+                            size_t scratch_bytes, void* stream) {
   if (!h || (dw_gate == nullptr) != (dw_up == nullptr) || tokens > h->max_tokens)
     return AR_ERR_INVALID_ARG;
   if (!h->work) return AR_ERR_UNSUPPORTED;
@@ -169,6 +227,12 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
     return AR_ERR_INVALID_ARG;
   if (!dx && !dw_gate) return AR_OK;
 
+  // dx wants the weights, the weights' gradients want x.
+  Rows m[3];
+  operands(h, x, ldx, w_gate, w_up, ldw, tokens, m);
+  if (ar_status_t st = dx ? pack(dw_gate ? m : m + 1, dw_gate ? 3 : 2, 2, scratch, scratch_bytes, h->num_sms, s)
+                          : pack(m, 1, 2, scratch, scratch_bytes, h->num_sms, s))
+    return st;
   char* dgate = h->work;
   char* dup = h->work + 2 * h->max_tokens * h->ldw;
   cudaError_t e = ar::launch_gate_grad(h->dtype, h->act, gate, up, dout, (int64_t)ldo, dgate, dup,
@@ -176,7 +240,7 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
   if (e == cudaSuccess && dx) {
     ar::GemmArgs g = {};
     g.a0 = dgate, g.a1 = dup, g.lda = (int64_t)h->ldw;
-    g.b0 = w_gate, g.b1 = w_up, g.ldb = (int64_t)ldw;
+    g.b0 = m[1].p, g.b1 = m[2].p, g.ldb = (int64_t)m[1].ld, g.ldb1 = (int64_t)m[2].ld;
     g.c0 = dx, g.ldc = (int64_t)lddx;
     g.M = (int64_t)tokens, g.N = (int64_t)K, g.K = (int64_t)F;
     e = gemm(ar::kGemmDx, h->dtype, g, h->num_sms, s);
@@ -184,7 +248,7 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
   if (e == cudaSuccess && dw_gate) {
     ar::GemmArgs g = {};
     g.a0 = dgate, g.a1 = dup, g.lda = (int64_t)h->ldw;
-    g.b0 = x, g.ldb = (int64_t)ldx;
+    g.b0 = m[0].p, g.ldb = (int64_t)m[0].ld;
     g.c0 = dw_gate, g.c1 = dw_up, g.ldc = (int64_t)lddw;
     g.M = (int64_t)F, g.N = (int64_t)K, g.K = (int64_t)tokens;
     e = gemm(ar::kGemmDw, h->dtype, g, h->num_sms, s);
@@ -220,7 +284,8 @@ ar_status_t ar_quantize_rows(const void* x, size_t ldx, int8_t* q, size_t ldq, f
 
 ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, const int8_t* w,
                          size_t ldw, const float* w_scale, void* y, size_t ldy, size_t tokens,
-                         size_t in, size_t out, int dtype, void* stream) {
+                         size_t in, size_t out, int dtype, void* scratch, size_t scratch_bytes,
+                         void* stream) {
   if (!half_type(dtype)) return AR_ERR_UNSUPPORTED;
   if (in == 0 || out == 0) return AR_ERR_INVALID_ARG;
   if (tokens == 0) return AR_OK;
@@ -228,15 +293,24 @@ ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, cons
       bad_matrix(y, tokens, out, ldy) || !x_scale || !w_scale || misaligned(x_scale, 4) ||
       misaligned(w_scale, 4) || misaligned(y, 2))
     return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Rows m[2] = {{x, tokens, in, ldx}, {w, out, in, ldw}};
+  if (ar_status_t st = pack(m, 2, 1, scratch, scratch_bytes, sms, s)) return st;
   ar::GemmArgs g = {};
-  g.a0 = x, g.lda = (int64_t)ldx;
-  g.b0 = w, g.ldb = (int64_t)ldw;
+  g.a0 = m[0].p, g.lda = (int64_t)m[0].ld;
+  g.b0 = m[1].p, g.ldb = (int64_t)m[1].ld;
   g.c0 = y, g.ldc = (int64_t)ldy;
   g.sm = x_scale, g.sn = w_scale;
   g.M = (int64_t)tokens, g.N = (int64_t)out, g.K = (int64_t)in;
-  int sms = 0;
-  if (ar_status_t st = current_sms(&sms)) return st;
-  return cuda_status(gemm(ar::kGemmI8, dtype, g, sms, static_cast<cudaStream_t>(stream)));
+  return cuda_status(gemm(ar::kGemmI8, dtype, g, sms, s));
+}
+
+size_t ar_linear_i8_scratch_bytes(const int8_t* x, size_t ldx, const int8_t* w, size_t ldw, size_t tokens, size_t in,
+                                  size_t out) {
+  const Rows m[2] = {{x, tokens, in, ldx}, {w, out, in, ldw}};
+  return pack_bytes(m, 2, 1);
 }
 
 ar_status_t ar_ops_get_device_status(void* stream) {

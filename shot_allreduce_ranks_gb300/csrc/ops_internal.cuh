@@ -33,7 +33,7 @@ struct GemmArgs {
   void* c2;
   const float* sm;
   const float* sn;
-  int64_t lda, ldb, ldc;  // elements between rows
+  int64_t lda, ldb, ldb1, ldc;  // elements between rows (ldb1: b1's)
   int64_t M, N, K;
   int act;                // ar_activation_t (kGemmGated)
 };
@@ -67,6 +67,14 @@ cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* u
 // One int8 row and one scale for each row of x.
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
                                  float* scale, int64_t rows, int64_t cols, cudaStream_t s);
+
+// Copies up to three matrices to rows that start on 16 bytes.
+struct PackJob {
+  const void* from;
+  void* to;
+  int64_t rows, cols, ld_from, ld_to;  // elements
+};
+cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_sms, cudaStream_t s);
 
 struct DropoutArgs {
   const void* x;

@@ -237,14 +237,23 @@ __device__ __forceinline__ Tile tile_at(const TileWalk& w, int64_t t) {
   return r;
 }
 
-// 32 results of one row, at column n of N.
+// A warp's 32 x 32 results, lane l holding row m0 + l, to columns n0 .. of an
+// M x N matrix.  Rows that start on 16 bytes: each lane stores its row's 64
+// bytes.  Others: the lanes exchange their words (four butterfly steps swap the
+// low four bits of lane and word), so that 16 lanes store 64 contiguous bytes
+// of a row; a lane on its own would touch a sector for every element.  All
+// lanes of the warp call this.
 template <class E>
-__device__ __forceinline__ void store_row(void* out, int64_t at, const float (&v)[32], int left, int align) {
-  char* p = static_cast<char*>(out) + at * 2;
-  if (left >= 32 && align >= 16) {
-    uint32_t w[16];
+__device__ __forceinline__ void store_chunk(void* out, int64_t ldc, int64_t m0, int64_t n0, int64_t M, int64_t N,
+                                            const float (&v)[32], int align) {
+  const int lane = (int)(threadIdx.x & 31);
+  const int left = (int)min((int64_t)32, N - n0);
+  uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = E::pack(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 16; ++i) w[i] = E::pack(v[2 * i], v[2 * i + 1]);
+  if (left == 32 && align >= 16) {
+    if (m0 + lane >= M) return;
+    char* p = static_cast<char*>(out) + ((m0 + lane) * ldc + n0) * 2;
     if (align >= 32) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -255,10 +264,31 @@ __device__ __forceinline__ void store_row(void* out, int64_t at, const float (&v
       for (int i = 0; i < 4; ++i)
         st_v4_stream(p + 16 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
     }
-  } else {
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < left) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)E::from_f32(v[i]);
+  for (int bit = 1; bit < 16; bit <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(i & bit)) {
+        const bool up = (lane & bit) != 0;
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[i] : w[i | bit], bit);
+        (up ? w[i] : w[i | bit]) = got;
+      }
+  }
+  const int c = 2 * (lane & 15);
+  char* p = static_cast<char*>(out) + ((m0 + (lane & 16)) * ldc + n0 + c) * 2;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (m0 + (lane & 16) + j < M && c < left) {
+      uint16_t* q = reinterpret_cast<uint16_t*>(p + j * ldc * 2);
+      if (align >= 4 && c + 1 < left) {
+        *reinterpret_cast<uint32_t*>(q) = w[j];
+      } else {
+        q[0] = (uint16_t)w[j];
+        if (c + 1 < left) q[1] = (uint16_t)(w[j] >> 16);
+      }
+    }
   }
 }
 

@@ -81,6 +81,13 @@ def _call(name: str, index: int, *args) -> None:
         check(status, name)
 
 
+def _scratch(name: str, device, *args):
+    """(address, bytes, tensor) of the memory in which unaligned rows are laid out."""
+    n = getattr(_functions or _lib(), name)(*args)
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    return t.data_ptr(), n, t
+
+
 class GatedFFN:
     """One rank's gated feed-forward shard: ``act(x Wgate^T) * (x Wup^T)``.
 
@@ -157,8 +164,12 @@ class GatedFFN:
             elif _matrix(gate, "gate", dt, index, m, width) != ldo or _matrix(up, "up", dt, index, m, width) != ldo:
                 raise ValueError("gate and up must have the row stride of out")
             g, u = gate.data_ptr(), up.data_ptr()
-        _call("ar_ffn_forward", index, self._h, x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(),
-              ldw, out.data_ptr(), g, u, ldo, m)
+        xp, wg, wu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+        scratch = None, 0
+        if (xp | wg | wu | ldx * 2 | ldw * 2) & 15:
+            scratch = _scratch("ar_ffn_scratch_bytes", x.device, self._h, xp, ldx, wg, wu, ldw, m)
+        _call("ar_ffn_forward", index, self._h, xp, ldx, wg, wu, ldw, out.data_ptr(), g, u, ldo, m, scratch[0],
+              scratch[1])
         return (out, gate, up) if save else out
 
     def backward(self, x, w_gate, w_up, gate, up, dout, dx=None, dw_gate=None, dw_up=None,
@@ -193,9 +204,14 @@ class GatedFFN:
             lddw = _matrix(dw_gate, "dw_gate", dt, index, width, hidden)
             if _matrix(dw_up, "dw_up", dt, index, width, hidden) != lddw:
                 raise ValueError("dw_gate and dw_up must have the same row stride")
-        _call("ar_ffn_backward", index, self._h, x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw,
+        xp, wg, wu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+        scratch = None, 0
+        if (xp | wg | wu | ldx * 2 | ldw * 2) & 15:
+            scratch = _scratch("ar_ffn_scratch_bytes", x.device, self._h, xp, ldx, wg, wu, ldw, m)
+        _call("ar_ffn_backward", index, self._h, xp, ldx, wg, wu, ldw,
               gate.data_ptr(), up.data_ptr(), dout.data_ptr(), ldo, dx.data_ptr() if need_dx else None, lddx,
-              dw_gate.data_ptr() if need_dw else None, dw_up.data_ptr() if need_dw else None, lddw, m)
+              dw_gate.data_ptr() if need_dw else None, dw_up.data_ptr() if need_dw else None, lddw, m, scratch[0],
+              scratch[1])
         return dx, dw_gate, dw_up
 
 
@@ -293,8 +309,11 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
         out, ldo = torch.empty((m, n), dtype=dtype, device=x.device), n
     else:
         ldo = _matrix(out, "out", out.dtype, index, m, n)
-    _call("ar_linear_i8", index, x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw,
-          w_scale.data_ptr(), out.data_ptr(), ldo, m, k, n, code)
+    xp, wp, scratch = x.data_ptr(), w.data_ptr(), (None, 0)
+    if (xp | wp | ldx | ldw) & 15:
+        scratch = _scratch("ar_linear_i8_scratch_bytes", x.device, xp, ldx, wp, ldw, m, k, n)
+    _call("ar_linear_i8", index, xp, ldx, x_scale.data_ptr(), wp, ldw, w_scale.data_ptr(), out.data_ptr(), ldo, m, k,
+          n, code, scratch[0], scratch[1])
     return out
 
 

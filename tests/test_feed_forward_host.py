@@ -32,8 +32,9 @@ def test_ffn_create_refuses(lib, args, want):
 
 
 def test_ffn_calls_without_a_handle(lib):
-    assert lib.ar_ffn_forward(None, 16, 8, 16, 16, 8, 16, None, None, 8, 1, None) == INVALID
-    assert lib.ar_ffn_backward(None, 16, 8, 16, 16, 8, 16, 16, 16, 8, 16, 8, 16, 16, 8, 1, None) == INVALID
+    assert lib.ar_ffn_forward(None, 16, 8, 16, 16, 8, 16, None, None, 8, 1, None, 0, None) == INVALID
+    assert lib.ar_ffn_backward(None, 16, 8, 16, 16, 8, 16, 16, 16, 8, 16, 8, 16, 16, 8, 1, None, 0, None) == INVALID
+    assert lib.ar_ffn_scratch_bytes(None, 16, 8, 16, 16, 8, 1) == 0
     assert lib.ar_ffn_destroy(None) == OK
 
 
@@ -76,7 +77,16 @@ def test_quantize_rows_refuses(lib, args, want):
 def test_linear_i8_refuses(lib, change, want):
     a = dict(x=16, ldx=8, sx=16, w=16, ldw=8, sw=16, y=16, ldy=4, m=2, k=8, n=4, dtype=0)
     a.update(change)
-    assert lib.ar_linear_i8(*a.values(), None) == want
+    assert lib.ar_linear_i8(*a.values(), None, 0, None) == want
+
+
+def test_linear_i8_scratch_bytes(lib):
+    """Only rows that do not start on 16 bytes are counted, each rounded up to 16."""
+    f = lib.ar_linear_i8_scratch_bytes
+    assert f(16, 32, 32, 32, 5, 32, 7) == 0
+    assert f(17, 32, 32, 32, 5, 32, 7) == 5 * 32
+    assert f(16, 33, 32, 33, 5, 33, 7) == (5 + 7) * 48
+    assert f(16, 32, 33, 32, 5, 20, 7) == 7 * 32
 
 
 def test_python_refuses_what_is_not_on_a_gpu():

@@ -428,6 +428,40 @@ def test_streams_graphs_and_repetition(ar, M):
         assert all(torch.equal(a, b) for a, b in zip(given, want[0]))
 
 
+def test_scratch_is_optional_at_the_c_entry(ar):
+    """Unaligned operands without scratch take another kernel, with too little they are refused."""
+    from shot_allreduce_ranks_gb300 import _lib
+    lib, (M, K, N) = ar.load(), (150, 131, 72)
+    g = gen(8)
+    x = torch.randint(-128, 128, (M, K), generator=g, device=DEV, dtype=torch.int8)
+    w = torch.randint(-128, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    sx, sw = torch.rand(M, device=DEV), torch.rand(N, device=DEV)
+    outs = [torch.empty(M, N, dtype=FP16, device=DEV) for _ in range(2)]
+    need = lib.ar_linear_i8_scratch_bytes(x.data_ptr(), K, w.data_ptr(), K, M, K, N)
+    scratch = torch.empty(need, dtype=torch.uint8, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+    for out, p, n, want in ((outs[0], None, 0, _lib.AR_OK), (outs[1], scratch.data_ptr(), need, _lib.AR_OK),
+                            (outs[1], scratch.data_ptr(), need - 1, _lib.AR_ERR_INVALID_ARG)):
+        assert lib.ar_linear_i8(x.data_ptr(), K, sx.data_ptr(), w.data_ptr(), K, sw.data_ptr(), out.data_ptr(), N, M, K, N,
+                                _lib.AR_FP16, p, n, s) == want
+    assert torch.equal(*outs)  # sums of integers below 2^24 are exact in either
+    x, wg, wu = normal(g, (M, K), BF16), normal(g, (N, K), BF16, 0.1), normal(g, (N, K), BF16, 0.1)
+    gate, up, dout = normal(g, (M, N), BF16), normal(g, (M, N), BF16), normal(g, (M, N), BF16)
+    with ar.GatedFFN(M, K, N, train=True) as ffn:
+        out = torch.empty(M, N, dtype=BF16, device=DEV)
+        assert lib.ar_ffn_forward(ffn._h, x.data_ptr(), K, wg.data_ptr(), wu.data_ptr(), K, out.data_ptr(), None, None, N,
+                                  M, None, 0, s) == _lib.AR_OK
+        want, bounds = ref.forward(x, wg, wu, "silu")
+        ref.assert_close(out, want[0], bounds[0], "forward")
+        grads = [torch.empty(a, K, dtype=BF16, device=DEV) for a in (M, N, N)]
+        ptrs = [t.data_ptr() for t in grads]
+        assert lib.ar_ffn_backward(ffn._h, x.data_ptr(), K, wg.data_ptr(), wu.data_ptr(), K, gate.data_ptr(), up.data_ptr(),
+                                   dout.data_ptr(), N, ptrs[0], K, ptrs[1], ptrs[2], K, M, None, 0, s) == _lib.AR_OK
+        want, bounds = ref.backward(x, wg, wu, gate, up, dout, "silu")
+        for a, b, e in zip(grads, want, bounds):
+            ref.assert_close(a, b, e, "backward")
+
+
 def test_python_refusals(ar):
     x, w = torch.zeros(4, 16, dtype=BF16, device=DEV), torch.zeros(8, 16, dtype=BF16, device=DEV)
     h = torch.zeros(4, 8, dtype=BF16, device=DEV)
