@@ -17,6 +17,8 @@
 // both projections in one accumulation, with B read along its other axis
 // (MN-major), and the two weight gradients read both operands so: nothing is
 // transposed in memory.
+#include <math.h>
+
 #include "tc_device.cuh"
 
 namespace ar {
@@ -69,26 +71,26 @@ struct TcArgs {
   GemmArgs g;
   TileWalk walk;
   int steps;                    // k steps of one segment
+  int bn;                       // columns of the matrix instruction, a multiple of 32
   int out_align;                // bytes that every output row start is a multiple of
 };
 
-template <int BN, int CG>
+// A stage holds 128 rows of A and up to 256 / CG of B.  1 KiB aligns the ring.
+template <int CG>
 struct Shape {
-  static constexpr uint32_t kA = 128 * kBK * 2, kB = BN / CG * kBK * 2, kStage = kA + kB;
-  static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
-  // 1 KiB to align the ring; more than half of an SM's shared memory, so that
-  // one CTA has an SM's tensor memory to itself.
-  static constexpr uint32_t kSmem = kStages * kStage + 1024 < 120 * 1024 ? 120 * 1024 : kStages * kStage + 1024;
+  static constexpr uint32_t kA = 128 * kBK * 2, kB = 256 / CG * kBK * 2, kStage = kA + kB;
+  static constexpr int kStages = 196608 / kStage;
+  static constexpr uint32_t kSmem = kStages * kStage + 1024;
 };
 
-template <int MODE, class E, int ACT, int BN, int CG>
+template <int MODE, class E, int ACT, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_gemm_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a0,
               const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b0,
               const __grid_constant__ CUtensorMap map_b1) {
-  using S = Shape<BN, CG>;
+  using S = Shape<CG>;
   constexpr bool kAmn = MODE == kGemmDw, kBmn = MODE != kGemmGated;
-  constexpr int kCols = MODE == kGemmGated ? BN / 2 : BN;  // output columns of a tile
+  const int cols = MODE == kGemmGated ? a.bn / 2 : a.bn;  // output columns of a tile
   constexpr int kST = S::kStages;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[2 * kST + 5];
@@ -132,17 +134,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 0) {
     if (elect_one()) {
+      const int chunks = (a.bn / CG + 63) / 64;  // of an MN-major B
+      const uint32_t stage_bytes = S::kA + (MODE == kGemmGated ? a.bn / CG * 128 : chunks * 8192);
       uint32_t it = 0;
       bool ok = true;
       for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
         const Tile tile = tile_at(a.walk, t);
-        const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * kCols;
+        const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * cols;
         for (int s = 0; s < total; ++s, ++it) {
           const uint32_t st = it % kST, round = it / kST;
           if (!(ok = bar_wait(empty + 8 * st, (round & 1) ^ 1, &dead))) break;
           const uint32_t sa = ring + st * S::kStage, sb = sa + S::kA;
           uint32_t bar = full + 8 * st;
-          if (rank == 0) bar_expect_tx(bar, CG * S::kStage);
+          if (rank == 0) bar_expect_tx(bar, CG * stage_bytes);
           if (CG == 2) bar = map_to_cta(bar, 0);
           const bool up = MODE == kGemmDx ? s >= a.steps : MODE == kGemmDw && tile.z != 0;
           const int k0 = (MODE == kGemmDx && up ? s - a.steps : s) * kBK;
@@ -159,13 +163,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               load_box<CG>(sb, rank ? &map_b1 : &map_b0, k0, n0, bar);
             } else {
               load_box<CG>(sb, &map_b0, k0, n0, bar);
-              load_box<CG>(sb + S::kB / 2, &map_b1, k0, n0, bar);
+              load_box<CG>(sb + (uint32_t)a.bn * 64, &map_b1, k0, n0, bar);
             }
           } else {
             const CUtensorMap* mb = MODE == kGemmDx && up ? &map_b1 : &map_b0;
-#pragma unroll
-            for (int c = 0; c < BN / CG / 64; ++c)
-              load_box<CG>(sb + 8192 * c, mb, n0 + (int)rank * (BN / CG) + 64 * c, k0, bar);
+            for (int c = 0; c < chunks; ++c)
+              load_box<CG>(sb + 8192 * c, mb, n0 + (int)rank * (a.bn / CG) + 64 * c, k0, bar);
           }
         }
       }
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      constexpr uint32_t idesc = instr_desc(IsBf16<E>::value, kAmn, kBmn, 128 * CG, BN);
+      const uint32_t idesc = instr_desc(IsBf16<E>::value, kAmn, kBmn, 128 * CG, a.bn);
       uint32_t it = 0, at = 0;
       bool ok = true;
       for (int64_t t = first; t < a.walk.tiles && ok; t += stride, ++at) {
@@ -221,19 +224,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       fence_after_sync();
       const int64_t m0 = ((int64_t)tile.m * CG + rank) * 128 + lane0;
-      const int n0 = tile.n * kCols;
+      const int n0 = tile.n * cols;
       const uint32_t acc = tmem + (lane0 << 16) + buf * 256;
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
+      for (int c = 0; c < cols; c += 32) {
         if (n0 + c >= a.g.N) break;
         uint32_t r[32], u[32];
         __syncwarp();
         tmem_load32(r, acc + c);
-        if (MODE == kGemmGated) tmem_load32(u, acc + kCols + c);
+        if (MODE == kGemmGated) tmem_load32(u, acc + cols + c);
         tmem_wait_load32(r);
         if (MODE == kGemmGated) tmem_wait_load32(u);
         const auto store = [&](void* out, const float(&v)[32]) {
-          store_chunk<E>(out, a.g.ldc, m0, n0 + c, a.g.M, a.g.N, v, a.out_align);
+          store_chunk<E>(out, a.g.ldc, m0, n0 + c, a.g.M, min(a.g.N, (int64_t)(n0 + cols)), v, a.out_align);
         };
         float v[32];
         if (MODE == kGemmGated) {
@@ -276,10 +279,10 @@ bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t 
   return tc_make_map(map, dtype == AR_BF16 ? kMapBf16 : kMapF16, p, rows, cols, ld, box_rows, 64);
 }
 
-template <int MODE, class E, int ACT, int BN, int CG>
-cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
-  using S = Shape<BN, CG>;
-  constexpr int kCols = MODE == kGemmGated ? BN / 2 : BN;
+template <int MODE, class E, int ACT, int CG>
+cudaError_t launch(int dtype, const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
+  using S = Shape<CG>;
+  const int cols = MODE == kGemmGated ? bn / 2 : bn;
   CUtensorMap ma0, ma1, mb0, mb1;
   bool ok;
   if (MODE == kGemmDw) {
@@ -290,7 +293,7 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
     if (MODE == kGemmDx) ok = ok && make_map(&ma1, dtype, g.a1, g.M, g.K, g.lda, 128);
   }
   if (MODE == kGemmGated) {
-    ok = ok && make_map(&mb0, dtype, g.b0, g.N, g.K, g.ldb, BN / 2) && make_map(&mb1, dtype, g.b1, g.N, g.K, g.ldb1, BN / 2);
+    ok = ok && make_map(&mb0, dtype, g.b0, g.N, g.K, g.ldb, bn / 2) && make_map(&mb1, dtype, g.b1, g.N, g.K, g.ldb1, bn / 2);
   } else {
     ok = ok && make_map(&mb0, dtype, g.b0, g.K, g.N, g.ldb, 64);
     mb1 = mb0;
@@ -301,15 +304,16 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
   TcArgs a = {};
   a.g = g;
   a.walk.tiles_m = (int)((g.M + 128 * CG - 1) / (128 * CG));
-  a.walk.tiles_n = (int)((g.N + kCols - 1) / kCols);
+  a.walk.tiles_n = (int)((g.N + cols - 1) / cols);
   a.walk.tiles = (int64_t)a.walk.tiles_m * a.walk.tiles_n * (MODE == kGemmDw ? 2 : 1);
   a.walk.group = 16 / CG;
+  a.bn = bn;
   a.steps = (int)((g.K + kBK - 1) / kBK);
   const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | reinterpret_cast<uintptr_t>(g.c1) |
                         reinterpret_cast<uintptr_t>(g.c2) | (uintptr_t)g.ldc * 2;
   a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : out % 4 == 0 ? 4 : 2;
 
-  auto* kernel = k_gemm_tc<MODE, E, ACT, BN, CG>;
+  auto* kernel = k_gemm_tc<MODE, E, ACT, CG>;
   static bool raised[64];  // by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -334,10 +338,30 @@ cudaError_t launch(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, a, ma0, ma1, mb0, mb1);
 }
 
+// Columns of the matrix instruction.  A step of 64 k takes the longer of its
+// instruction (bn clocks x 2) and its copies (an SM takes in 64 bytes a clock);
+// a tile ends with its stores, about ten clocks a column, which the next tile
+// hides; the tiles go round the SMs in whole rounds.
+int columns(int mode, const GemmArgs& g, int cg, int num_sms) {
+  const int64_t slots = num_sms / cg, steps = (g.K + kBK - 1) / kBK * (mode == kGemmDx ? 2 : 1);
+  int best = 256;
+  double least = 1e300;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    const int64_t cols = mode == kGemmGated ? bn / 2 : bn, planes = mode == kGemmDw ? 2 : 1;
+    const int64_t tiles = (g.M + 128 * cg - 1) / (128 * cg) * ((g.N + cols - 1) / cols) * planes;
+    const int64_t b_rows = mode == kGemmGated ? bn / cg : (bn / cg + 63) / 64 * 64;
+    const double step = fmax(2.0 * bn, 2.0 * (128 + b_rows)), stores = 10.0 * bn;
+    const double rounds = (double)((tiles + slots - 1) / slots);
+    const double cost = rounds * fmax(steps * step, stores) + fmin(steps * step, stores);
+    if (cost < 0.98 * least) least = cost, best = bn;
+  }
+  return best;
+}
+
 template <int MODE, class E, int ACT>
 cudaError_t launch_shape(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
-  if (g.M > 128) return launch<MODE, E, ACT, 256, 2>(dtype, g, num_sms, s);
-  return launch<MODE, E, ACT, 256, 1>(dtype, g, num_sms, s);
+  if (g.M > 128) return launch<MODE, E, ACT, 2>(dtype, g, columns(MODE, g, 2, num_sms), num_sms, s);
+  return launch<MODE, E, ACT, 1>(dtype, g, columns(MODE, g, 1, num_sms), num_sms, s);
 }
 
 template <class E>
