@@ -66,6 +66,7 @@ __device__ __forceinline__ void pack_group(uint32_t (&o)[4], const float (&y)[G]
 template <class E, bool RES, bool VEC, bool WHOLE>
 __global__ void __launch_bounds__(kDropThreads)
     k_dropout(const __grid_constant__ DropoutArgs a, const __grid_constant__ RoundKeys key, int64_t groups_per_row) {
+  pdl_enter();
   constexpr int G = E::kGroup, B = E::kBytes, W = 4;
   const int64_t total = a.rows * groups_per_row;
   const uint64_t scale = f32x2_make(__float_as_uint(a.scale), __float_as_uint(a.scale));
@@ -174,8 +175,8 @@ cudaError_t dropout(DropoutArgs a, int num_sms, cudaStream_t s) {
       k_dropout<E, false, false, false>, k_dropout<E, false, false, true>, k_dropout<E, false, true, false>,
       k_dropout<E, false, true, true>,   k_dropout<E, true, false, false>, k_dropout<E, true, false, true>,
       k_dropout<E, true, true, false>,   k_dropout<E, true, true, true>};
-  kernels[(a.residual ? 4 : 0) + (vec ? 2 : 0) + (whole ? 1 : 0)]<<<grid, kDropThreads, 0, s>>>(a, key, gpr);
-  return cudaGetLastError();
+  const Kernel k = kernels[(a.residual ? 4 : 0) + (vec ? 2 : 0) + (whole ? 1 : 0)];
+  return launch_op(k, dim3(grid), kDropThreads, 0, 1, s, a, key, gpr);
 }
 
 }  // namespace

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kThreadsAny) k_gemm_any(GemmArgs g, int64_t ti
   constexpr bool kAK = MODE != kGemmDw, kBK = MODE == kGemmGated || MODE == kGemmI8;
   constexpr int kCols = MODE == kGemmGated ? kTile / 2 : kTile;  // output columns of a tile
   __shared__ uint16_t sa[kTile][kPitch], sb[kTile][kPitch];
+  pdl_enter();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wm = warp >> 1, wn = warp & 1, g4 = lane >> 2, t4 = lane & 3;
   const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * kTile;
@@ -144,8 +145,7 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t s) {
   const int64_t tn = (g.N + cols - 1) / cols, tm = (g.M + kTile - 1) / kTile;
   if (tn * tm > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(tn * tm), MODE == kGemmDw ? 2 : 1);
-  k_gemm_any<MODE, E, ACT><<<grid, kThreadsAny, 0, s>>>(g, tn);
-  return cudaGetLastError();
+  return launch_op(k_gemm_any<MODE, E, ACT>, grid, kThreadsAny, 0, 1, s, g, tn);
 }
 
 template <class E>

@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kFewThreads) k_gemm_few(GemmArgs g) {
   constexpr int kRows = MODE == kGemmI8 ? 16 : 8;
   using F = typename std::conditional<MODE == kGemmI8, F16, E>::type;
   __shared__ float4 part[kFewWarps][NT][32];
+  pdl_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   const int64_t n0 = (int64_t)blockIdx.x * kRows;
   // Rows past the last are read as the last one; their results are dropped.
@@ -131,11 +132,8 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t s) {
   constexpr int kRows = MODE == kGemmI8 ? 16 : 8;
   const int64_t grid = (g.N + kRows - 1) / kRows;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  if (g.M <= 8)
-    k_gemm_few<MODE, E, ACT, 1, VEC><<<(unsigned)grid, kFewThreads, 0, s>>>(g);
-  else
-    k_gemm_few<MODE, E, ACT, 2, VEC><<<(unsigned)grid, kFewThreads, 0, s>>>(g);
-  return cudaGetLastError();
+  auto* k = g.M <= 8 ? k_gemm_few<MODE, E, ACT, 1, VEC> : k_gemm_few<MODE, E, ACT, 2, VEC>;
+  return launch_op(k, dim3((unsigned)grid), kFewThreads, 0, 1, s, g);
 }
 
 template <int MODE, class E, int ACT>

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   if (CG == 2) cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  pdl_enter();  // nothing before this has touched global memory
   const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (warp == 0) {
@@ -277,19 +278,9 @@ cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kI8Smem);
   if (e != cudaSuccess) return e;
   raised[dev & 63] = dev < 64;
-  cudaLaunchConfig_t cfg = {};
   const int64_t pairs = num_sms / CG;
-  cfg.gridDim = dim3((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
-  cfg.blockDim = dim3(kI8Threads);
-  cfg.dynamicSmemBytes = kI8Smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, mx, mw);
+  const dim3 grid((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
+  return launch_op(kernel, grid, kI8Threads, kI8Smem, CG, s, a, mx, mw);
 }
 
 // Columns of a tile: the number of rounds of tiles over the SMs times a round's

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (CG == 2) cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  pdl_enter();  // nothing before this has touched global memory
 
   const int total = MODE == kGemmDx ? 2 * a.steps : a.steps;
   const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
@@ -321,21 +322,9 @@ cudaError_t launch(int dtype, const GemmArgs& g, int bn, int num_sms, cudaStream
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
   raised[dev & 63] = dev < 64;
-  cudaLaunchConfig_t cfg = {};
   const int64_t pairs = num_sms / CG;
-  cfg.gridDim = dim3((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
-  cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (CG == 2) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kernel, a, ma0, ma1, mb0, mb1);
+  const dim3 grid((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
+  return launch_op(kernel, grid, kTcThreads, S::kSmem, CG, s, a, ma0, ma1, mb0, mb1);
 }
 
 // Columns of the matrix instruction.  A step of 64 k takes the longer of its
@@ -346,7 +335,7 @@ int columns(int mode, const GemmArgs& g, int cg, int num_sms) {
   const int64_t slots = num_sms / cg, steps = (g.K + kBK - 1) / kBK * (mode == kGemmDx ? 2 : 1);
   int best = 256;
   double least = 1e300;
-  for (int bn = 256; bn >= 64; bn -= 32) {
+  for (int bn = 256; bn >= 64; bn -= mode == kGemmGated ? 64 : 32) {
     const int64_t cols = mode == kGemmGated ? bn / 2 : bn, planes = mode == kGemmDw ? 2 : 1;
     const int64_t tiles = (g.M + 128 * cg - 1) / (128 * cg) * ((g.N + cols - 1) / cols) * planes;
     const int64_t b_rows = mode == kGemmGated ? bn / cg : (bn / cg + 63) / 64 * 64;

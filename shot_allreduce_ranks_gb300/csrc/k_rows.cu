@@ -15,6 +15,7 @@ template <class E, int ACT, bool VEC>
 __global__ void __launch_bounds__(kGateThreads)
     k_gate_grad(const char* gate, const char* up, const char* dout, int64_t ldo, char* dgate,
                 char* dup, int64_t ldw, int64_t rows, int64_t cols, int64_t groups_per_row) {
+  pdl_enter();
   const int64_t total = rows * groups_per_row;
   for (int64_t i = (int64_t)blockIdx.x * kGateThreads + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * kGateThreads) {
@@ -64,10 +65,9 @@ cudaError_t gate_grad(const void* gate, const void* up, const void* dout, int64_
   const bool vec = ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up) |
                      reinterpret_cast<uintptr_t>(dout)) & 15u) == 0 && ldo % 8 == 0;
   auto* k = vec ? k_gate_grad<E, ACT, true> : k_gate_grad<E, ACT, false>;
-  k<<<grid, kGateThreads, 0, s>>>(
-      static_cast<const char*>(gate), static_cast<const char*>(up), static_cast<const char*>(dout),
-      ldo, static_cast<char*>(dgate), static_cast<char*>(dup), ldw, rows, cols, gpr);
-  return cudaGetLastError();
+  return launch_op(k, dim3(grid), kGateThreads, 0, 1, s, static_cast<const char*>(gate),
+                   static_cast<const char*>(up), static_cast<const char*>(dout), ldo,
+                   static_cast<char*>(dgate), static_cast<char*>(dup), ldw, rows, cols, gpr);
 }
 
 // ---------------------------------------------------------------------------
@@ -80,6 +80,7 @@ template <class E>
 __global__ void __launch_bounds__(kQuantThreads)
     k_quantize_rows(const char* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t cols) {
   __shared__ uint32_t part[kQuantThreads / 32];
+  pdl_enter();
   const int tid = threadIdx.x;
   const char* row = x + (int64_t)blockIdx.x * ldx * E::kBytes;
   uint32_t top = 0;
@@ -114,6 +115,7 @@ struct PackJobs {
 // source rows begin anywhere, and neighbouring lanes' loads share cache lines.
 template <int B>
 __global__ void __launch_bounds__(kPackThreads) k_pack(const __grid_constant__ PackJobs jobs) {
+  pdl_enter();
   constexpr int G = 16 / B;
   const PackJob j = jobs.job[blockIdx.y];
   const int64_t per_row = (j.cols + G - 1) / G, total = j.rows * per_row;
@@ -145,11 +147,7 @@ cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_
   }
   const int64_t want = (most + kPackThreads - 1) / kPackThreads, cap = (int64_t)num_sms * 8;
   const dim3 grid((unsigned)(want < cap ? want : cap), (unsigned)count);
-  if (elem_bytes == 2)
-    k_pack<2><<<grid, kPackThreads, 0, s>>>(all);
-  else
-    k_pack<1><<<grid, kPackThreads, 0, s>>>(all);
-  return cudaGetLastError();
+  return launch_op(elem_bytes == 2 ? k_pack<2> : k_pack<1>, grid, kPackThreads, 0, 1, s, all);
 }
 
 cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
@@ -169,8 +167,8 @@ cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* 
   auto* k = dtype == AR_BF16   ? k_quantize_rows<Bf16>
             : dtype == AR_FP16 ? k_quantize_rows<F16>
                                : k_quantize_rows<F32>;
-  k<<<(unsigned)rows, kQuantThreads, 0, s>>>(static_cast<const char*>(x), ldx, q, ldq, scale, cols);
-  return cudaGetLastError();
+  return launch_op(k, dim3((unsigned)rows), kQuantThreads, 0, 1, s, static_cast<const char*>(x), ldx, q, ldq,
+                   scale, cols);
 }
 
 }  // namespace ar

@@ -1,6 +1,8 @@
 // C ABI of the feed-forward operators: argument checks, workspaces and the
 // choice of kernel.  Declarations and contracts are in include/ar.h.
 #include <math.h>
+#include <stdlib.h>
+#include <string.h>
 
 #include <new>
 
@@ -123,6 +125,14 @@ ar_status_t dropout_call(const void* x, size_t ldx, const void* res, size_t ldr,
 }
 
 }  // namespace
+
+bool ar::ops_pdl() {
+  static const bool on = [] {
+    const char* v = getenv("AR_PDL");
+    return !(v && strcmp(v, "0") == 0);
+  }();
+  return on;
+}
 
 extern "C" {
 

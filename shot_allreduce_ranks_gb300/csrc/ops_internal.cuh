@@ -8,6 +8,26 @@
 namespace ar {
 
 // ---------------------------------------------------------------------------
+// Launch of one of these operators' kernels, each of which calls pdl_enter()
+// before it touches global memory: with programmatic dependent launch its
+// launch and set-up overlap the end of the kernel before (AR_PDL=0 turns it
+// off, as for the collectives).
+bool ops_pdl();
+
+template <class... P, class... A>
+cudaError_t launch_op(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = plain_config({0, threads, ops_pdl()}, grid, smem, s, attr);
+  if (cluster > 1) {
+    cudaLaunchAttribute& a = attr[cfg.numAttrs++];
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = (unsigned)cluster;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// ---------------------------------------------------------------------------
 // Matrix products.  All of them are C[m, n] = sum_k A(m, k) B(n, k); what
 // differs is which matrices stand for A and B, which of their two axes is
 // contiguous, and what is done with the sum.

@@ -273,7 +273,8 @@ __device__ __forceinline__ void store_chunk(void* out, int64_t ldc, int64_t m0, 
       if (!(i & bit)) {
         const bool up = (lane & bit) != 0;
         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[i] : w[i | bit], bit);
-        (up ? w[i] : w[i | bit]) = got;
+        w[i] = up ? got : w[i];
+        w[i | bit] = up ? w[i | bit] : got;
       }
   }
   const int c = 2 * (lane & 15);
