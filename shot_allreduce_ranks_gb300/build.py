@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libar_gb300.so")
 
 SOURCES = ["ar_api.cu", "k_oneshot.cu", "k_oneshot_bulk.cu", "k_twophase.cu", "k_fused_ll8.cu",
            "k_rs_ag.cu", "op_api.cu", "k_gemm_any.cu", "k_gemm_tc.cu",
-           "k_gemm_i8.cu", "k_gemm_few.cu", "k_rows.cu", "k_dropout.cu"]
+           "k_gemm_mid.cu", "k_gemm_i8.cu", "k_gemm_few.cu", "k_rows.cu", "k_dropout.cu"]
 HEADERS = [os.path.join(CSRC, "ar_internal.cuh"), os.path.join(CSRC, "ops_internal.cuh"),
            os.path.join(CSRC, "tc_device.cuh"),
            os.path.join(INCLUDE, "ar.h")]

@@ -15,7 +15,6 @@ namespace ar {
 namespace {
 
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
-constexpr int kUnroll = 4;  // 64-byte pieces of each row in flight a warp
 
 // 16 bytes at p, of which `left` may be read (the rest zero); VEC: p is 16-byte aligned.
 template <bool VEC, int B>
@@ -34,6 +33,7 @@ __device__ __forceinline__ uint4 load_piece(const char* p, int64_t left) {
 template <int MODE, class E, int ACT, int NT, bool VEC>
 __global__ void __launch_bounds__(kFewThreads) k_gemm_few(GemmArgs g) {
   constexpr int B = MODE == kGemmI8 ? 1 : 2;  // bytes of an element
+  constexpr int kUnroll = NT > 2 ? 2 : 4;     // 64-byte pieces of each row in flight a warp
   constexpr int kRows = MODE == kGemmI8 ? 16 : 8;
   using F = typename std::conditional<MODE == kGemmI8, F16, E>::type;
   __shared__ float4 part[kFewWarps][NT][32];
@@ -132,7 +132,9 @@ cudaError_t launch(const GemmArgs& g, cudaStream_t s) {
   constexpr int kRows = MODE == kGemmI8 ? 16 : 8;
   const int64_t grid = (g.N + kRows - 1) / kRows;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  auto* k = g.M <= 8 ? k_gemm_few<MODE, E, ACT, 1, VEC> : k_gemm_few<MODE, E, ACT, 2, VEC>;
+  auto* k = g.M <= 8    ? k_gemm_few<MODE, E, ACT, 1, VEC>
+            : g.M <= 16 ? k_gemm_few<MODE, E, ACT, 2, VEC>
+                        : k_gemm_few<MODE, E, ACT, 4, VEC>;
   return launch_op(k, dim3((unsigned)grid), kFewThreads, 0, 1, s, g);
 }
 
@@ -155,7 +157,7 @@ cudaError_t launch_type(int mode, const GemmArgs& g, cudaStream_t s) {
 }  // namespace
 
 bool gemm_few_takes(int mode, const GemmArgs& g) {
-  return (mode == kGemmGated || mode == kGemmI8) && g.M <= 16;
+  return (mode == kGemmGated || mode == kGemmI8) && g.M <= 32;
 }
 
 cudaError_t launch_gemm_few(int mode, int dtype, const GemmArgs& g, cudaStream_t s) {

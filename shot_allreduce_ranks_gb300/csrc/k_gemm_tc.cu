@@ -6,9 +6,9 @@
 // 256 rows) makes tiles of 128 CG x BN.  One thread copies operand tiles of 64
 // k into a ring of shared-memory stages by tensor maps with 128-byte swizzle
 // (out-of-range elements arrive as zeros, so ragged sizes need no other code),
-// one thread issues the matrix instructions, and four warps read a finished
-// accumulator while the next tile is multiplied into the other half of tensor
-// memory.
+// one thread issues the matrix instructions, and eight warps (two for each
+// quarter of the rows, taking turns by 32 columns) read a finished accumulator
+// while the next tile is multiplied into the other half of tensor memory.
 //
 // In the gated product the BN rows of B are BN/2 rows of the gate's weights and
 // the same BN/2 of the up projection's, so both pre-activations of an element
@@ -62,7 +62,7 @@ namespace {
 using namespace tc;
 
 constexpr int kBK = 64;                // k of one stage: 128 bytes
-constexpr int kTcThreads = 192;        // copy, matrix, four epilogue warps
+constexpr int kTcThreads = 320;        // copy, matrix, eight epilogue warps
 constexpr uint32_t kTmemCols = 512;
 
 __device__ uint32_t g_tc_error;  // set by a wait that gave up
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(done + 8 * i, 1);
-      bar_init(freed + 8 * i, 4 * CG);
+      bar_init(freed + 8 * i, 8 * CG);
     }
     bar_init(drained, 1);
     dead = 0;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int n0 = tile.n * cols;
       const uint32_t acc = tmem + (lane0 << 16) + buf * 256;
 #pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
+      for (int c = warp < 6 ? 0 : 32; c < cols; c += 64) {
         if (n0 + c >= a.g.N) break;
         uint32_t r[32], u[32];
         __syncwarp();

@@ -86,6 +86,7 @@ ar_status_t pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_
 
 cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaStream_t s) {
   if (ar::gemm_few_takes(mode, g)) return ar::launch_gemm_few(mode, dtype, g, s);
+  if (ar::gemm_mid_takes(mode, g)) return ar::launch_gemm_mid(dtype, g, num_sms, s);
   if (ar::gemm_tc_takes(mode, g)) return ar::launch_gemm_tc(mode, dtype, g, num_sms, s);
   if (ar::gemm_i8_takes(mode, g)) return ar::launch_gemm_i8(dtype, g, num_sms, s);
   return ar::launch_gemm_any(mode, dtype, g, s);
@@ -325,9 +326,11 @@ size_t ar_linear_i8_scratch_bytes(const int8_t* x, size_t ldx, const int8_t* w, 
 
 ar_status_t ar_ops_get_device_status(void* stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t tc = 0, i8 = 0;
-  if (ar::gemm_tc_error(s, &tc) != cudaSuccess || ar::gemm_i8_error(s, &i8) != cudaSuccess) return AR_ERR_CUDA;
-  return tc || i8 ? AR_ERR_TIMEOUT : AR_OK;
+  uint32_t tc = 0, mid = 0, i8 = 0;
+  if (ar::gemm_tc_error(s, &tc) != cudaSuccess || ar::gemm_mid_error(s, &mid) != cudaSuccess ||
+      ar::gemm_i8_error(s, &i8) != cudaSuccess)
+    return AR_ERR_CUDA;
+  return tc || mid || i8 ? AR_ERR_TIMEOUT : AR_OK;
 }
 
 }  // extern "C"

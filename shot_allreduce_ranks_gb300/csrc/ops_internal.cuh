@@ -66,12 +66,17 @@ cudaError_t gemm_tc_error(cudaStream_t s, uint32_t* error);
 
 cudaError_t take_error_word(void* p, cudaStream_t s, uint32_t* error);  // reads and clears
 
+// The gated product on tcgen05 for at most 128 tokens.
+bool gemm_mid_takes(int mode, const GemmArgs& g);
+cudaError_t launch_gemm_mid(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
+cudaError_t gemm_mid_error(cudaStream_t s, uint32_t* error);
+
 // The 8-bit product on tcgen05.
 bool gemm_i8_takes(int mode, const GemmArgs& g);
 cudaError_t launch_gemm_i8(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
 cudaError_t gemm_i8_error(cudaStream_t s, uint32_t* error);
 
-// For at most 16 tokens of the gated and the 8-bit product.
+// For at most 32 tokens of the gated and the 8-bit product.
 bool gemm_few_takes(int mode, const GemmArgs& g);
 cudaError_t launch_gemm_few(int mode, int dtype, const GemmArgs& g, cudaStream_t s);
 
