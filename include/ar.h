@@ -536,7 +536,7 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
  * The mask depends on (seed, sequence, n) alone and is never stored: ranks
  * with equal arguments draw equal masks, and ar_dropout_backward (dx = keep ?
  * dy / (1 - p) : 0; the residual's gradient is dy) draws it again.
- * x * (1 / (1 - p)) and the sum are fp32 steps, rounded once to dtype.  A
+ * Multiplied by 1 / (1 - p) and added in fp32 (one fused step), rounded once to dtype.  A
  * dropped element counts as 0 whatever it holds, infinities and NaN included.
  * Errors: AR_ERR_INVALID_ARG (NULL x or out, ld < cols, p outside [0, 1] or
  * NaN, offset + rows * cols past 2^64), AR_ERR_UNSUPPORTED (dtype). */

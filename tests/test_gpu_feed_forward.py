@@ -246,7 +246,7 @@ def test_rows_past_2_31_elements(ar):
 @pytest.mark.parametrize("rows,cols,pad,shift", [
     (1, 1, 0, 0), (1, 8, 0, 0), (3, 5, 0, 0), (7, 64, 8, 0), (5, 129, 7, 0), (4, 100, 3, 1), (65, 257, 0, 0),
     (33, 96, 0, 1), (300, 40, 16, 0)])
-@pytest.mark.parametrize("p,offset", [(0.1, 0), (0.5, (1 << 33) + 3), (0.25, 6)])
+@pytest.mark.parametrize("p,offset", [(0.1, 0), (0.5, (1 << 33) + 3), (0.25, 6), (0.3, (1 << 34) - 40)])
 def test_dropout(ar, dtype, rows, cols, pad, shift, p, offset):
     g = gen(rows * 1000 + cols)
     x, r = normal(g, (rows, cols), dtype), normal(g, (rows, cols), dtype)
