@@ -84,9 +84,19 @@ ar_status_t pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_
   return cuda_status(ar::launch_pack(jobs, n, (int)elem, num_sms, s));
 }
 
+// Which kernel makes a product.  Up to 32 tokens the weights can be streamed
+// past them by mma.sync, whose time grows with every eight tokens; the tensor
+// cores' form for some tens of tokens costs about 2 us more to set up but
+// stays flat: it takes over where tokens x width x hidden passes 2^26 (16 tokens
+// of 2048 x 1024: 3.6 against 5.1 us, of 2048 x 2048: 5.4 against 5.2; 32 tokens
+// of 2048 x 1024: 4.8 against 5.5, of 2048 x 2048: 7.1 against 5.5), but not
+// for the eight tokens of one instruction (8192 x 3584: 21.3 against 22.3 us).
 cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaStream_t s) {
-  if (ar::gemm_few_takes(mode, g)) return ar::launch_gemm_few(mode, dtype, g, s);
-  if (ar::gemm_mid_takes(mode, g)) return ar::launch_gemm_mid(dtype, g, num_sms, s);
+  const bool mid = ar::gemm_mid_takes(mode, g);
+  if (ar::gemm_few_takes(mode, g) &&
+      (!mid || g.M <= 8 || (double)g.M * (double)g.N * (double)g.K <= (double)(1 << 26)))
+    return ar::launch_gemm_few(mode, dtype, g, s);
+  if (mid) return ar::launch_gemm_mid(dtype, g, num_sms, s);
   if (ar::gemm_tc_takes(mode, g)) return ar::launch_gemm_tc(mode, dtype, g, num_sms, s);
   if (ar::gemm_i8_takes(mode, g)) return ar::launch_gemm_i8(dtype, g, num_sms, s);
   return ar::launch_gemm_any(mode, dtype, g, s);
