@@ -42,8 +42,6 @@ struct I8Args {
   int out_align;
 };
 
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 template <class E, int CG>
 __global__ void __launch_bounds__(kI8Threads, 1)
     k_gemm_i8(const __grid_constant__ I8Args a, const __grid_constant__ CUtensorMap map_x,

@@ -42,7 +42,6 @@ static EncodeFn encode_fn() {
 
 bool tc_available() { return encode_fn() != nullptr; }
 
-// Boxes arrive in the 128-byte swizzle, which the matrix instruction reads.
 bool tc_make_map(CUtensorMap* map, MapType type, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
                  int box_cols) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -52,7 +51,8 @@ bool tc_make_map(CUtensorMap* map, MapType type, const void* p, int64_t rows, in
                                 : type == kMapF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return encode_fn()(map, t, 2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     box_cols * (type == kMapU8 ? 1 : 2) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace tc
@@ -80,14 +80,19 @@ template <int CG>
 struct Shape {
   static constexpr uint32_t kA = 128 * kBK * 2, kB = 256 / CG * kBK * 2, kStage = kA + kB;
   static constexpr int kStages = 196608 / kStage;
-  static constexpr uint32_t kSmem = kStages * kStage + 1024;
+  static constexpr uint32_t kStores = 8 * 2 * 2048;  // two 32 x 32 boxes an epilogue warp
+  static constexpr uint32_t kSmem = kStages * kStage + kStores + 1024;
+};
+
+struct OutMaps {
+  CUtensorMap c[3];
 };
 
 template <int MODE, class E, int ACT, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_gemm_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a0,
               const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b0,
-              const __grid_constant__ CUtensorMap map_b1) {
+              const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ OutMaps out) {
   using S = Shape<CG>;
   constexpr bool kAmn = MODE == kGemmDw, kBmn = MODE != kGemmGated;
   const int cols = MODE == kGemmGated ? a.bn / 2 : a.bn;  // output columns of a tile
@@ -215,7 +220,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;  // this warp's lanes of tensor memory
-    uint32_t at = 0;
+    const int lane = (int)(threadIdx.x & 31);
+    const uint32_t boxes = ring + kST * S::kStage + (uint32_t)(warp - 2) * 4096;
+    uint32_t stored = 0, at = 0;
     for (int64_t t = first; t < a.walk.tiles; t += stride, ++at) {
       const Tile tile = tile_at(a.walk, t);
       const uint32_t buf = at & 1;
@@ -236,26 +243,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (MODE == kGemmGated) tmem_load32(u, acc + cols + c);
         tmem_wait_load32(r);
         if (MODE == kGemmGated) tmem_wait_load32(u);
-        const auto store = [&](void* out, const float(&v)[32]) {
-          store_chunk<E>(out, a.g.ldc, m0, n0 + c, a.g.M, min(a.g.N, (int64_t)(n0 + cols)), v, a.out_align);
+        // Rows that start on 16 bytes leave through shared memory as boxes of 64-byte
+        // rows; a lane storing its own row would touch 32 lines at a time.
+        const auto store = [&](int which, void* c_out, const float(&v)[32]) {
+          if (a.out_align < 16) {
+            store_chunk<E>(c_out, a.g.ldc, m0, n0 + c, a.g.M, min(a.g.N, (int64_t)(n0 + cols)), v, a.out_align);
+            return;
+          }
+          const uint32_t box = boxes + (stored & 1) * 2048, row = box + (uint32_t)lane * 64;
+          if (lane == 0) store_box_wait_read<1>();  // the box's last copy but one has been read
+          __syncwarp();
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + 16u * (uint32_t)(p ^ ((lane >> 1) & 3))),
+                         "r"(E::pack(v[8 * p], v[8 * p + 1])), "r"(E::pack(v[8 * p + 2], v[8 * p + 3])),
+                         "r"(E::pack(v[8 * p + 4], v[8 * p + 5])), "r"(E::pack(v[8 * p + 6], v[8 * p + 7])) : "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0 && m0 < a.g.M) store_box(&out.c[which], n0 + c, (int)m0, box);
+          ++stored;
         };
         float v[32];
         if (MODE == kGemmGated) {
           if (a.g.c1) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            store(a.g.c1, v);
+            store(1, a.g.c1, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-            store(a.g.c2, v);
+            store(2, a.g.c2, v);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(__uint_as_float(r[i])) * __uint_as_float(u[i]);
-          store(a.g.c0, v);
+          store(0, a.g.c0, v);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          store(MODE == kGemmDw && tile.z ? a.g.c1 : a.g.c0, v);
+          store(MODE == kGemmDw ? tile.z : 0, MODE == kGemmDw && tile.z ? a.g.c1 : a.g.c0, v);
         }
       }
       fence_before_sync();
@@ -267,6 +291,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           bar_arrive(freed + 8 * buf);
       }
     }
+    if (lane == 0) store_box_wait_all();
   }
   __syncwarp();
   fence_before_sync();
@@ -314,6 +339,13 @@ cudaError_t launch(int dtype, const GemmArgs& g, int bn, int num_sms, cudaStream
                         reinterpret_cast<uintptr_t>(g.c2) | (uintptr_t)g.ldc * 2;
   a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : out % 4 == 0 ? 4 : 2;
 
+  OutMaps out_maps;
+  if (a.out_align >= 16) {
+    void* const c[3] = {g.c0, g.c1 ? g.c1 : g.c0, g.c2 ? g.c2 : g.c0};
+    for (int i = 0; i < 3; ++i)
+      if (!tc_make_map(&out_maps.c[i], dtype == AR_BF16 ? kMapBf16 : kMapF16, c[i], g.M, g.N, g.ldc, 32, 32))
+        return cudaErrorInvalidValue;
+  }
   auto* kernel = k_gemm_tc<MODE, E, ACT, CG>;
   static bool raised[64];  // by device
   int dev = 0;
@@ -324,7 +356,7 @@ cudaError_t launch(int dtype, const GemmArgs& g, int bn, int num_sms, cudaStream
   raised[dev & 63] = dev < 64;
   const int64_t pairs = num_sms / CG;
   const dim3 grid((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
-  return launch_op(kernel, grid, kTcThreads, S::kSmem, CG, s, a, ma0, ma1, mb0, mb1);
+  return launch_op(kernel, grid, kTcThreads, S::kSmem, CG, s, a, ma0, ma1, mb0, mb1, out_maps);
 }
 
 // Columns of the matrix instruction.  A step of 64 k takes the longer of its

@@ -105,6 +105,19 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
+// The other way, for what the thread's earlier fence has made visible; done
+// (shared memory free again, all written) by the thread's waits below.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int32_t x, int32_t y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
+               "cp.async.bulk.commit_group;" ::"l"(map), "r"(src), "r"(x), "r"(y) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void store_box_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_box_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -297,6 +310,8 @@ __device__ __forceinline__ void store_chunk(void* out, int64_t ldc, int64_t m0, 
 
 enum MapType { kMapBf16, kMapF16, kMapU8 };
 bool tc_available();
+// Boxes of 128-byte rows in the 128-byte swizzle (the 16-byte piece p of row r at
+// p ^ (r % 8)), of 64-byte rows in the 64-byte one (p ^ (r / 2 % 4)).
 bool tc_make_map(CUtensorMap* map, MapType type, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
                  int box_cols);
 
