@@ -73,35 +73,97 @@ cudaError_t gate_grad(const void* gate, const void* up, const void* dout, int64_
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
 
-// The largest |x| of a row, NaN where the row holds one: as unsigned integers
-// the bit patterns of non-negative floats are ordered as the floats are, and
-// every NaN lies above infinity.
+// Absolute values as unsigned integers are ordered as the floats are, with every
+// NaN above infinity, so that a NaN in a row becomes its scale.
 template <class E>
-__global__ void __launch_bounds__(kQuantThreads)
-    k_quantize_rows(const char* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t cols) {
-  __shared__ uint32_t part[kQuantThreads / 32];
-  pdl_enter();
-  const int tid = threadIdx.x;
-  const char* row = x + (int64_t)blockIdx.x * ldx * E::kBytes;
-  uint32_t top = 0;
-  for (int64_t c = tid; c < cols; c += kQuantThreads)
-    top = max(top, __float_as_uint(E::to_f32(ld_elem<E::kBytes>(row + c * E::kBytes))) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if ((tid & 31) == 0) part[tid >> 5] = top;
+__device__ __forceinline__ uint32_t magnitude(uint32_t bits) {
+  return __float_as_uint(E::to_f32(bits)) & 0x7FFFFFFFu;
+}
+
+// The largest of the CTA's values.
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* part) {
+  v = __reduce_max_sync(0xFFFFFFFFu, v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, part[w]);
-  // Divisions are IEEE ones, rounded once, so that the integers are those of
-  // the definition: rint(x / s), s = absmax / 127.
+  for (int w = 0; w < kQuantThreads / 32; ++w) v = max(v, part[w]);
+  return v;
+}
+
+// Divisions are IEEE ones, rounded once, so that the integers are those of the
+// definition: rint(x / s), s = absmax / 127.
+__device__ __forceinline__ uint32_t quantized(float x, float by, bool finite) {
+  const int n = finite ? __float2int_rn(__fdiv_rn(x, by)) : 0;
+  return (uint32_t)min(127, max(-127, n)) & 0xFFu;
+}
+
+// A CTA a row, read once: each thread keeps up to kHeld groups of 16 bytes
+// (8192 16-bit columns in all) in registers between the maximum and the
+// division.  Longer rows, and rows that do not start on 16 bytes, are read
+// twice, an element at a time (HELD false).
+constexpr int kHeld = 4;
+
+template <class E, bool HELD>
+__global__ void __launch_bounds__(kQuantThreads)
+    k_quantize_rows(const char* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t cols) {
+  pdl_enter();
+  __shared__ uint32_t part[kQuantThreads / 32];
+  constexpr int G = E::kGroup, B = E::kBytes;
+  const int tid = threadIdx.x;
+  const char* row = x + (int64_t)blockIdx.x * ldx * B;
+  int8_t* to = q + (int64_t)blockIdx.x * ldq;
+  uint4 held[kHeld];
+  uint32_t top = 0;
+  const auto bits = [](const uint4& v, int k) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    return B == 2 ? (w[k / 2] >> (16 * (k & 1))) & 0xFFFFu : w[k & 3];
+  };
+  if (HELD) {
+    const int groups = (int)(cols / G);  // whole ones: the columns left are read below
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int g = tid + i * kQuantThreads;
+      held[i] = g < groups ? ld_v4_stream(row + (int64_t)g * 16) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+      for (int k = 0; k < G; ++k) top = max(top, magnitude<E>(bits(held[i], k)));
+  }
+  const int64_t rest = HELD ? cols / G * G : 0;
+  for (int64_t c = rest + tid; c < cols; c += kQuantThreads) top = max(top, magnitude<E>(ld_elem<B>(row + c * B)));
+  top = cta_max(top, part);
   const float s = __fdiv_rn(__uint_as_float(top), 127.0f);
   if (tid == 0) scale[blockIdx.x] = s;
   const float by = s > 0.0f ? s : 1.0f;
   const bool finite = top < 0x7F800000u;
-  for (int64_t c = tid; c < cols; c += kQuantThreads) {
-    const float v = __fdiv_rn(E::to_f32(ld_elem<E::kBytes>(row + c * E::kBytes)), by);
-    const int n = finite ? __float2int_rn(v) : 0;
-    q[(int64_t)blockIdx.x * ldq + c] = (int8_t)min(127, max(-127, n));
+  if (HELD) {
+    const int groups = (int)(cols / G);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int g = tid + i * kQuantThreads;
+      if (g >= groups) break;
+      uint32_t w[2] = {};
+#pragma unroll
+      for (int k = 0; k < G; ++k) w[k / 4] |= quantized(E::to_f32(bits(held[i], k)), by, finite) << (8 * (k & 3));
+      if (G == 8)
+        *reinterpret_cast<uint2*>(to + (int64_t)g * G) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t*>(to + (int64_t)g * G) = w[0];
+    }
   }
+  for (int64_t c = rest + tid; c < cols; c += kQuantThreads)
+    to[c] = (int8_t)quantized(E::to_f32(ld_elem<B>(row + c * B)), by, finite);
+}
+
+template <class E>
+cudaError_t quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t rows, int64_t cols,
+                     cudaStream_t s) {
+  constexpr int G = E::kGroup;
+  const bool held = cols <= (int64_t)kHeld * kQuantThreads * G && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(q) % G == 0 && (rows == 1 || (ldx % G == 0 && ldq % G == 0));
+  return launch_op(held ? k_quantize_rows<E, true> : k_quantize_rows<E, false>, dim3((unsigned)rows), kQuantThreads, 0, 1,
+                   s, static_cast<const char*>(x), ldx, q, ldq, scale, cols);
 }
 
 // ---------------------------------------------------------------------------
@@ -164,11 +226,9 @@ cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* u
 
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
                                  float* scale, int64_t rows, int64_t cols, cudaStream_t s) {
-  auto* k = dtype == AR_BF16   ? k_quantize_rows<Bf16>
-            : dtype == AR_FP16 ? k_quantize_rows<F16>
-                               : k_quantize_rows<F32>;
-  return launch_op(k, dim3((unsigned)rows), kQuantThreads, 0, 1, s, static_cast<const char*>(x), ldx, q, ldq,
-                   scale, cols);
+  if (dtype == AR_BF16) return quantize<Bf16>(x, ldx, q, ldq, scale, rows, cols, s);
+  if (dtype == AR_FP16) return quantize<F16>(x, ldx, q, ldq, scale, rows, cols, s);
+  return quantize<F32>(x, ldx, q, ldq, scale, rows, cols, s);
 }
 
 }  // namespace ar

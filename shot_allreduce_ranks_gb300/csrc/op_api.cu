@@ -19,7 +19,7 @@ struct ar_ffn_ctx {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr size_t kMaxDim = (size_t)1 << 38;   // rows and leading dimensions: more than the memory holds
+constexpr size_t kMaxElems = (size_t)1 << 40;  // of a matrix: more than the memory holds
 constexpr size_t kMaxSize = (size_t)1 << 30;  // the sizes a handle is made for
 
 bool half_type(int dtype) { return dtype == AR_BF16 || dtype == AR_FP16; }
@@ -43,7 +43,7 @@ ar_status_t current_sms(int* sms) {
 }
 
 bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
-  return !p || ld < cols || rows > kMaxDim || ld > kMaxDim;
+  return !p || ld < cols || ld > kMaxElems || (ld && rows > kMaxElems / ld);
 }
 
 bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }

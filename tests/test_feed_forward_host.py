@@ -51,6 +51,7 @@ def dropout_args(**kw):
     (dict(ldx=7), INVALID), (dict(ldo=7), INVALID), (dict(res=64, ldr=7), INVALID),
     (dict(x=17), INVALID), (dict(out=33), INVALID), (dict(dtype=2, x=18), INVALID),
     (dict(offset=2 ** 64 - 8), INVALID), (dict(rows=BIG), INVALID),
+    (dict(rows=1 << 38, cols=1 << 38, ldx=1 << 38, ldo=1 << 38), INVALID),
     (dict(rows=0, x=None, out=None), OK), (dict(cols=0), OK)])
 def test_dropout_refuses(lib, kw, want):
     a = dropout_args(**kw)

@@ -94,7 +94,10 @@ def test_forward_layouts(ar, size, layout, dtype, act):
     run_forward(ar, *size, dtype, act, *layout, seed=1)
 
 
-@pytest.mark.parametrize("size", [(1030, 520, 3000), (2100, 128, 1400), (130, 8192, 256), (1, 8192, 512)])
+@pytest.mark.parametrize("size", [(1030, 520, 3000), (2100, 128, 1400), (130, 8192, 256), (1, 8192, 512),
+                                  # the split of k over a cluster: whole, in two, in four, and fewer tokens than it is made for
+                                  (20, 2048, 2100), (9, 8192, 1032), (100, 4096, 4000), (128, 2056, 10000), (33, 520, 2048),
+                                  (65, 72, 2048), (128, 4160, 1288)])
 def test_forward_many_tiles_and_deep_sums(ar, size):
     run_forward(ar, *size, BF16, "silu", 0, 0, seed=2)
 
@@ -183,7 +186,7 @@ def test_gradients_against_differences(ar, act, dtype):
         assert abs(float((got * d).sum()) - slope) <= float(limit)
 
 
-@pytest.mark.parametrize("size", [(5, 64, 40), (140, 136, 72)])
+@pytest.mark.parametrize("size", [(5, 64, 40), (50, 264, 200), (40, 2048, 1032), (140, 136, 72)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_not_finite_values_stay_in_their_rows(ar, size, bad):
     M, K, F = size
@@ -316,7 +319,8 @@ def test_dropout_past_2_31_elements(ar):
 # ---------------------------------------------------------------------------------------------------------- 8-bit product
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
-@pytest.mark.parametrize("rows,cols,pad,shift", [(1, 1, 0, 0), (1, 3584, 0, 0), (5, 77, 3, 1), (40, 2048, 0, 0), (300, 264, 8, 0), (2, 40000, 0, 0)])
+@pytest.mark.parametrize("rows,cols,pad,shift", [(1, 1, 0, 0), (1, 3584, 0, 0), (5, 77, 3, 1), (40, 2048, 0, 0), (300, 264, 8, 0), (2, 40000, 0, 0), (3, 8192, 0, 0), (3, 8200, 0, 0),
+                                                    (4, 4097, 7, 0), (1, 2051, 0, 0)])
 def test_quantize_rows(ar, dtype, rows, cols, pad, shift):
     x = normal(gen(rows + cols), (rows, cols), dtype)
     if rows > 1:
