@@ -89,13 +89,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
   pdl_enter();  // nothing before this has touched global memory
-  const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (warp == 0) {
     if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
+      for (uint32_t t = first; t < a.walk.tiles && ok; t += stride) {
         const Tile tile = tile_at(a.walk, t);
         const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * a.bn + (int)rank * (a.bn / CG);
         for (int s = 0; s < a.steps / 2; ++s, ++it) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       const uint32_t idesc = instr_desc(false, false, false, 128 * CG, a.bn);
       uint32_t it = 0, at = 0;
       bool ok = true;
-      for (int64_t t = first; t < a.walk.tiles && ok; t += stride, ++at) {
+      for (uint32_t t = first; t < a.walk.tiles && ok; t += stride, ++at) {
         const uint32_t buf = at & 1;
         if (!(ok = bar_wait(freed + 8 * buf, ((at >> 1) & 1) ^ 1, &dead))) break;
         fence_after_sync();
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   } else if (warp < 6) {
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;
     uint32_t at = 0;
-    for (int64_t t = first; t < a.walk.tiles; t += stride, ++at) {
+    for (uint32_t t = first; t < a.walk.tiles; t += stride, ++at) {
       const Tile tile = tile_at(a.walk, t);
       const uint32_t buf = at & 1;
       const int64_t m0 = ((int64_t)tile.m * CG + rank) * 128 + lane0, m = m0 + (threadIdx.x & 31);
@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int group = (warp - 6) / kGroupWarps, thread = (int)(threadIdx.x - 6 * 32) % kGroupThreads;
     const int lane = thread & 31, j = lane & 3, second = (lane >> 2) & 1;
     const int row0 = (thread >> 5) * 8 + (lane >> 3) + 4 * second;  // + 8 kGroupWarps each time
-    const int64_t mine = first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0;
-    const int64_t total = mine * a.steps;
+    const int64_t total = (int64_t)(first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0) * a.steps;
     bool ok = true;
     int64_t it = group;
     for (; it < total && ok; it += kGroups) {
@@ -260,10 +259,8 @@ cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
     return cudaErrorInvalidValue;
   I8Args a = {};
   a.g = g;
-  a.walk.tiles_m = (int)((g.M + 128 * CG - 1) / (128 * CG));
-  a.walk.tiles_n = (int)((g.N + bn - 1) / bn);
-  a.walk.tiles = (int64_t)a.walk.tiles_m * a.walk.tiles_n;
-  a.walk.group = 16 / CG;
+  if (!make_walk(&a.walk, (g.M + 128 * CG - 1) / (128 * CG), (g.N + bn - 1) / bn, 1, 16 / CG))
+    return cudaErrorInvalidConfiguration;
   a.steps = (int)((g.K + 127) / 128) * 2;
   a.bn = bn;
   const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | (uintptr_t)g.ldc * 2;
@@ -276,8 +273,8 @@ cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kI8Smem);
   if (e != cudaSuccess) return e;
   raised[dev & 63] = dev < 64;
-  const int64_t pairs = num_sms / CG;
-  const dim3 grid((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
+  const uint32_t pairs = (uint32_t)(num_sms / CG);
+  const dim3 grid((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG);
   return launch_op(kernel, grid, kI8Threads, kI8Smem, CG, s, a, mx, mw);
 }
 

@@ -16,7 +16,8 @@
 // without a trip through memory.  Of the backward products, dx contracts over
 // both projections in one accumulation, with B read along its other axis
 // (MN-major), and the two weight gradients read both operands so: nothing is
-// transposed in memory.
+// transposed in memory.  All three are one launch: one kind's last round of tiles
+// would leave SMs idle, which the other's tiles fill.
 #include <math.h>
 
 #include "tc_device.cuh"
@@ -67,13 +68,55 @@ constexpr uint32_t kTmemCols = 512;
 
 __device__ uint32_t g_tc_error;  // set by a wait that gave up
 
-struct TcArgs {
-  GemmArgs g;
+enum { kTcGated = 0, kTcGrad = 1 };
+
+// One product's tiles and outputs.
+struct Part {
   TileWalk walk;
-  int steps;                    // k steps of one segment
-  int bn;                       // columns of the matrix instruction, a multiple of 32
-  int out_align;                // bytes that every output row start is a multiple of
+  int64_t M, N, ldc;
+  int steps;      // k steps of one segment
+  int out_align;  // bytes that every output row start is a multiple of
 };
+
+struct TcArgs {
+  Part part[2];      // kTcGrad: dx, then the two weight gradients; kTcGated: part[1] alone
+  void* c[3];        // h, gate, up; or dx, dWgate, dWup
+  int bn;            // columns of the matrix instruction, a multiple of 32
+  // See job_at: dx's whole rounds and the tiles left over, the slots that those
+  // leave free, and the tiles of the weights' gradients that a free slot takes first.
+  uint32_t rounds, left, free, ahead;
+};
+
+// kTcGated: a[0] = x, b = the two weights.  kTcGrad: a[0], a[1] = dgate, dup along
+// their columns and b[0], b[1] = the weights, for dx; a[2], a[3] = dgate, dup
+// along their rows and b[2] = x, for the weights' gradients.
+struct TcMaps {
+  CUtensorMap a[4], b[3], c[3];
+};
+
+// The j-th tile of slot p (a CTA or a pair) of P: its part and number.  dx's tiles
+// come first, round by round; where its last round leaves slots free, those
+// take `ahead` tiles of the weight gradients each (about as many as fit beside one
+// of dx), and the rest goes round all slots.  Every tile has one slot, fixed by
+// its number.
+template <int WHAT>
+__device__ __forceinline__ bool job_at(const TcArgs& a, uint32_t p, uint32_t P, uint32_t j, int& part, uint32_t& t) {
+  t = p + j * P;
+  part = 1;
+  if (WHAT == kTcGrad) {
+    const uint32_t mine = a.rounds + (p < a.left ? 1 : 0);
+    if (j < mine) {
+      part = 0;
+    } else {
+      const uint32_t k = j - mine;
+      if (p < a.left || a.left == 0)
+        t = a.ahead * a.free + k * P + p;
+      else
+        t = k < a.ahead ? k * a.free + (p - a.left) : a.ahead * a.free + (k - a.ahead) * P + p;
+    }
+  }
+  return t < a.part[part].walk.tiles;
+}
 
 // A stage holds 128 rows of A and up to 256 / CG of B.  1 KiB aligns the ring.
 template <int CG>
@@ -84,18 +127,12 @@ struct Shape {
   static constexpr uint32_t kSmem = kStages * kStage + kStores + 1024;
 };
 
-struct OutMaps {
-  CUtensorMap c[3];
-};
-
-template <int MODE, class E, int ACT, int CG>
+template <int WHAT, class E, int ACT, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    k_gemm_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a0,
-              const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b0,
-              const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ OutMaps out) {
+    k_gemm_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
   using S = Shape<CG>;
-  constexpr bool kAmn = MODE == kGemmDw, kBmn = MODE != kGemmGated;
-  const int cols = MODE == kGemmGated ? a.bn / 2 : a.bn;  // output columns of a tile
+  constexpr bool kBmn = WHAT == kTcGrad;
+  const int cols = WHAT == kTcGated ? a.bn / 2 : a.bn;  // output columns of a tile
   constexpr int kST = S::kStages;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[2 * kST + 5];
@@ -120,8 +157,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bar_init(drained, 1);
     dead = 0;
     bar_init_done();
-    prefetch_map(&map_a0);
-    prefetch_map(&map_b0);
+    prefetch_map(&maps.a[0]);
+    prefetch_map(&maps.b[0]);
   }
   __syncwarp();
   if (warp == 1) {
@@ -135,18 +172,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = tmem_slot;
   pdl_enter();  // nothing before this has touched global memory
 
-  const int total = MODE == kGemmDx ? 2 * a.steps : a.steps;
-  const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const uint32_t slot = blockIdx.x / CG, slots = gridDim.x / CG;
+  int which;       // part and number of the tile at hand
+  uint32_t number;
 
   if (warp == 0) {
     if (elect_one()) {
       const int chunks = (a.bn / CG + 63) / 64;  // of an MN-major B
-      const uint32_t stage_bytes = S::kA + (MODE == kGemmGated ? a.bn / CG * 128 : chunks * 8192);
+      const uint32_t stage_bytes = S::kA + (WHAT == kTcGated ? a.bn / CG * 128 : chunks * 8192);
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t t = first; t < a.walk.tiles && ok; t += stride) {
-        const Tile tile = tile_at(a.walk, t);
+      for (uint32_t j = 0; ok && job_at<WHAT>(a, slot, slots, j, which, number); ++j) {
+        const Tile tile = tile_at(a.part[which].walk, number);
         const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * cols;
+        const bool dx = WHAT == kTcGrad && which == 0, dw = WHAT == kTcGrad && which == 1;
+        const int steps = a.part[which].steps, total = dx ? 2 * steps : steps;
         for (int s = 0; s < total; ++s, ++it) {
           const uint32_t st = it % kST, round = it / kST;
           if (!(ok = bar_wait(empty + 8 * st, (round & 1) ^ 1, &dead))) break;
@@ -154,25 +194,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint32_t bar = full + 8 * st;
           if (rank == 0) bar_expect_tx(bar, CG * stage_bytes);
           if (CG == 2) bar = map_to_cta(bar, 0);
-          const bool up = MODE == kGemmDx ? s >= a.steps : MODE == kGemmDw && tile.z != 0;
-          const int k0 = (MODE == kGemmDx && up ? s - a.steps : s) * kBK;
-          const CUtensorMap* ma = up ? &map_a1 : &map_a0;
-          if (kAmn) {
-            load_box<CG>(sa, ma, m0, k0, bar);
-            load_box<CG>(sa + 8192, ma, m0 + 64, k0, bar);
+          const int up = dx ? s >= steps : tile.z;  // which projection
+          const int k0 = (dx && up ? s - steps : s) * kBK;
+          if (dw) {
+            load_box<CG>(sa, &maps.a[2 + up], m0, k0, bar);
+            load_box<CG>(sa + 8192, &maps.a[2 + up], m0 + 64, k0, bar);
           } else {
-            load_box<CG>(sa, ma, k0, m0, bar);
+            load_box<CG>(sa, &maps.a[up], k0, m0, bar);
           }
-          if (MODE == kGemmGated) {
+          if (WHAT == kTcGated) {
             // The pair's first CTA holds the gate's rows, its second the up projection's.
             if (CG == 2) {
-              load_box<CG>(sb, rank ? &map_b1 : &map_b0, k0, n0, bar);
+              load_box<CG>(sb, &maps.b[rank], k0, n0, bar);
             } else {
-              load_box<CG>(sb, &map_b0, k0, n0, bar);
-              load_box<CG>(sb + (uint32_t)a.bn * 64, &map_b1, k0, n0, bar);
+              load_box<CG>(sb, &maps.b[0], k0, n0, bar);
+              load_box<CG>(sb + (uint32_t)a.bn * 64, &maps.b[1], k0, n0, bar);
             }
           } else {
-            const CUtensorMap* mb = MODE == kGemmDx && up ? &map_b1 : &map_b0;
+            const CUtensorMap* mb = &maps.b[dw ? 2 : up];
             for (int c = 0; c < chunks; ++c)
               load_box<CG>(sb + 8192 * c, mb, n0 + (int)rank * (a.bn / CG) + 64 * c, k0, bar);
           }
@@ -190,10 +229,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      const uint32_t idesc = instr_desc(IsBf16<E>::value, kAmn, kBmn, 128 * CG, a.bn);
       uint32_t it = 0, at = 0;
       bool ok = true;
-      for (int64_t t = first; t < a.walk.tiles && ok; t += stride, ++at) {
+      for (; ok && job_at<WHAT>(a, slot, slots, at, which, number); ++at) {
+        const bool a_mn = WHAT == kTcGrad && which == 1;
+        const uint32_t idesc = instr_desc(IsBf16<E>::value, a_mn, kBmn, 128 * CG, a.bn);
+        const int total = a.part[which].steps * (WHAT == kTcGrad && which == 0 ? 2 : 1);
         const uint32_t buf = at & 1;
         if (!(ok = bar_wait(freed + 8 * buf, ((at >> 1) & 1) ^ 1, &dead))) break;
         fence_after_sync();
@@ -203,11 +244,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!(ok = bar_wait(full + 8 * st, round & 1, &dead))) break;
           fence_after_sync();
           const uint32_t sa = ring + st * S::kStage, sb = sa + S::kA;
-          const uint64_t da = kAmn ? operand_desc(sa, 8192, 1024) : operand_desc(sa, 16, 1024);
+          const uint64_t da = operand_desc(sa, a_mn ? 8192 : 16, 1024);
           const uint64_t db = kBmn ? operand_desc(sb, 8192, 1024) : operand_desc(sb, 16, 1024);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 16 k: 32 bytes of a K-major row, 16 rows of an MN-major tile
-            mma_f16<CG>(acc, da + (kAmn ? 128 : 2) * k, db + (kBmn ? 128 : 2) * k, idesc, s > 0 || k > 0);
+            mma_f16<CG>(acc, da + (a_mn ? 128 : 2) * k, db + (kBmn ? 128 : 2) * k, idesc, s > 0 || k > 0);
           mma_commit<CG>(empty + 8 * st);
         }
         if (ok) mma_commit<CG>(done + 8 * buf);
@@ -223,8 +264,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int lane = (int)(threadIdx.x & 31);
     const uint32_t boxes = ring + kST * S::kStage + (uint32_t)(warp - 2) * 4096;
     uint32_t stored = 0, at = 0;
-    for (int64_t t = first; t < a.walk.tiles; t += stride, ++at) {
-      const Tile tile = tile_at(a.walk, t);
+    for (; job_at<WHAT>(a, slot, slots, at, which, number); ++at) {
+      const Part& part = a.part[which];
+      const Tile tile = tile_at(part.walk, number);
       const uint32_t buf = at & 1;
       if (!bar_wait(done + 8 * buf, (at >> 1) & 1, &dead)) {
         atomicExch(&g_tc_error, 1u);
@@ -236,18 +278,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t acc = tmem + (lane0 << 16) + buf * 256;
 #pragma unroll 1
       for (int c = warp < 6 ? 0 : 32; c < cols; c += 64) {
-        if (n0 + c >= a.g.N) break;
+        if (n0 + c >= part.N) break;
         uint32_t r[32], u[32];
         __syncwarp();
         tmem_load32(r, acc + c);
-        if (MODE == kGemmGated) tmem_load32(u, acc + cols + c);
+        if (WHAT == kTcGated) tmem_load32(u, acc + cols + c);
         tmem_wait_load32(r);
-        if (MODE == kGemmGated) tmem_wait_load32(u);
+        if (WHAT == kTcGated) tmem_wait_load32(u);
         // Rows that start on 16 bytes leave through shared memory as boxes of 64-byte
         // rows; a lane storing its own row would touch 32 lines at a time.
-        const auto store = [&](int which, void* c_out, const float(&v)[32]) {
-          if (a.out_align < 16) {
-            store_chunk<E>(c_out, a.g.ldc, m0, n0 + c, a.g.M, min(a.g.N, (int64_t)(n0 + cols)), v, a.out_align);
+        const auto store = [&](int to, const float(&v)[32]) {
+          if (part.out_align < 16) {
+            store_chunk<E>(a.c[to], part.ldc, m0, n0 + c, part.M, min(part.N, (int64_t)(n0 + cols)), v, part.out_align);
             return;
           }
           const uint32_t box = boxes + (stored & 1) * 2048, row = box + (uint32_t)lane * 64;
@@ -260,26 +302,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          "r"(E::pack(v[8 * p + 4], v[8 * p + 5])), "r"(E::pack(v[8 * p + 6], v[8 * p + 7])) : "memory");
           fence_async_smem();
           __syncwarp();
-          if (lane == 0 && m0 < a.g.M) store_box(&out.c[which], n0 + c, (int)m0, box);
+          if (lane == 0 && m0 < part.M) store_box(&maps.c[to], n0 + c, (int)m0, box);
           ++stored;
         };
         float v[32];
-        if (MODE == kGemmGated) {
-          if (a.g.c1) {
+        if (WHAT == kTcGated) {
+          if (a.c[1]) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            store(1, a.g.c1, v);
+            store(1, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-            store(2, a.g.c2, v);
+            store(2, v);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(__uint_as_float(r[i])) * __uint_as_float(u[i]);
-          store(0, a.g.c0, v);
+          store(0, v);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          store(MODE == kGemmDw ? tile.z : 0, MODE == kGemmDw && tile.z ? a.g.c1 : a.g.c0, v);
+          store(which == 0 ? 0 : 1 + tile.z, v);
         }
       }
       fence_before_sync();
@@ -301,52 +343,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) tmem_free<CG>(tmem, kTmemCols);
 }
 
-bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-  return tc_make_map(map, dtype == AR_BF16 ? kMapBf16 : kMapF16, p, rows, cols, ld, box_rows, 64);
+bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+              int box_cols = 64) {
+  return tc_make_map(map, dtype == AR_BF16 ? kMapBf16 : kMapF16, p, rows, cols, ld, box_rows, box_cols);
 }
 
-template <int MODE, class E, int ACT, int CG>
-cudaError_t launch(int dtype, const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// One product's tiles; false if there are too many or an output map could not be made.
+bool make_part(TcArgs& a, TcMaps& maps, int which, int dtype, const GemmArgs& g, int cols, int planes, int cg,
+               void* const* c, int outs) {
+  Part& p = a.part[which];
+  p.M = g.M, p.N = g.N, p.ldc = g.ldc;
+  if (!make_walk(&p.walk, ceil_div(g.M, 128 * cg), ceil_div(g.N, cols), planes, 16 / cg)) return false;
+  p.steps = (int)ceil_div(g.K, kBK);
+  uintptr_t bits = (uintptr_t)g.ldc * 2;
+  for (int i = 0; i < outs; ++i) bits |= reinterpret_cast<uintptr_t>(c[i]);
+  p.out_align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  for (int i = 0; i < outs && p.out_align == 16; ++i)
+    if (c[i] && !make_map(&maps.c[c - a.c + i], dtype, c[i], g.M, g.N, g.ldc, 32, 32)) return false;
+  return true;
+}
+
+template <int WHAT, class E, int ACT, int CG>
+cudaError_t launch(const TcArgs& a, const TcMaps& maps, int num_sms, cudaStream_t s) {
   using S = Shape<CG>;
-  const int cols = MODE == kGemmGated ? bn / 2 : bn;
-  CUtensorMap ma0, ma1, mb0, mb1;
-  bool ok;
-  if (MODE == kGemmDw) {
-    ok = make_map(&ma0, dtype, g.a0, g.K, g.M, g.lda, 64) && make_map(&ma1, dtype, g.a1, g.K, g.M, g.lda, 64);
-  } else {
-    ok = make_map(&ma0, dtype, g.a0, g.M, g.K, g.lda, 128);
-    ma1 = ma0;
-    if (MODE == kGemmDx) ok = ok && make_map(&ma1, dtype, g.a1, g.M, g.K, g.lda, 128);
-  }
-  if (MODE == kGemmGated) {
-    ok = ok && make_map(&mb0, dtype, g.b0, g.N, g.K, g.ldb, bn / 2) && make_map(&mb1, dtype, g.b1, g.N, g.K, g.ldb1, bn / 2);
-  } else {
-    ok = ok && make_map(&mb0, dtype, g.b0, g.K, g.N, g.ldb, 64);
-    mb1 = mb0;
-    if (MODE == kGemmDx) ok = ok && make_map(&mb1, dtype, g.b1, g.K, g.N, g.ldb1, 64);
-  }
-  if (!ok) return cudaErrorInvalidValue;
-
-  TcArgs a = {};
-  a.g = g;
-  a.walk.tiles_m = (int)((g.M + 128 * CG - 1) / (128 * CG));
-  a.walk.tiles_n = (int)((g.N + cols - 1) / cols);
-  a.walk.tiles = (int64_t)a.walk.tiles_m * a.walk.tiles_n * (MODE == kGemmDw ? 2 : 1);
-  a.walk.group = 16 / CG;
-  a.bn = bn;
-  a.steps = (int)((g.K + kBK - 1) / kBK);
-  const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | reinterpret_cast<uintptr_t>(g.c1) |
-                        reinterpret_cast<uintptr_t>(g.c2) | (uintptr_t)g.ldc * 2;
-  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : out % 4 == 0 ? 4 : 2;
-
-  OutMaps out_maps;
-  if (a.out_align >= 16) {
-    void* const c[3] = {g.c0, g.c1 ? g.c1 : g.c0, g.c2 ? g.c2 : g.c0};
-    for (int i = 0; i < 3; ++i)
-      if (!tc_make_map(&out_maps.c[i], dtype == AR_BF16 ? kMapBf16 : kMapF16, c[i], g.M, g.N, g.ldc, 32, 32))
-        return cudaErrorInvalidValue;
-  }
-  auto* kernel = k_gemm_tc<MODE, E, ACT, CG>;
+  auto* kernel = k_gemm_tc<WHAT, E, ACT, CG>;
   static bool raised[64];  // by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -354,46 +376,110 @@ cudaError_t launch(int dtype, const GemmArgs& g, int bn, int num_sms, cudaStream
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
   raised[dev & 63] = dev < 64;
-  const int64_t pairs = num_sms / CG;
-  const dim3 grid((unsigned)((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG));
-  return launch_op(kernel, grid, kTcThreads, S::kSmem, CG, s, a, ma0, ma1, mb0, mb1, out_maps);
+  const int64_t slots = num_sms / CG, tiles = (int64_t)a.part[0].walk.tiles + a.part[1].walk.tiles;
+  const dim3 grid((unsigned)((tiles < slots ? tiles : slots) * CG));
+  return launch_op(kernel, grid, kTcThreads, S::kSmem, CG, s, a, maps);
 }
 
-// Columns of the matrix instruction.  A step of 64 k takes the longer of its
-// instruction (bn clocks x 2) and its copies (an SM takes in 64 bytes a clock);
-// a tile ends with its stores, about ten clocks a column, which the next tile
-// hides; the tiles go round the SMs in whole rounds.
-int columns(int mode, const GemmArgs& g, int cg, int num_sms) {
-  const int64_t slots = num_sms / cg, steps = (g.K + kBK - 1) / kBK * (mode == kGemmDx ? 2 : 1);
-  int best = 256;
+// What a tile takes, in clocks: a step of 64 k the longer of its instruction (2
+// a column) and its copies (an SM takes in 64 bytes a clock); its stores about
+// ten a column, which the next tile hides.
+struct TileCost {
+  double steps, stores;
+  double whole() const { return fmax(steps, stores); }
+};
+TileCost tile_cost(int64_t steps, int bn, int64_t b_rows) {
+  return {(double)steps * fmax(2.0 * bn, 2.0 * (double)(128 + b_rows)), 10.0 * bn};
+}
+
+template <class E, int ACT, int CG>
+cudaError_t launch_gated(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
+  const int64_t slots = num_sms / CG;
+  int bn = 256;
   double least = 1e300;
-  for (int bn = 256; bn >= 64; bn -= mode == kGemmGated ? 64 : 32) {
-    const int64_t cols = mode == kGemmGated ? bn / 2 : bn, planes = mode == kGemmDw ? 2 : 1;
-    const int64_t tiles = (g.M + 128 * cg - 1) / (128 * cg) * ((g.N + cols - 1) / cols) * planes;
-    const int64_t b_rows = mode == kGemmGated ? bn / cg : (bn / cg + 63) / 64 * 64;
-    const double step = fmax(2.0 * bn, 2.0 * (128 + b_rows)), stores = 10.0 * bn;
-    const double rounds = (double)((tiles + slots - 1) / slots);
-    const double cost = rounds * fmax(steps * step, stores) + fmin(steps * step, stores);
-    if (cost < 0.98 * least) least = cost, best = bn;
+  for (int b = 256; b >= 64; b -= 64) {
+    const TileCost c = tile_cost(ceil_div(g.K, kBK), b, b / CG);
+    const int64_t rounds = ceil_div(ceil_div(g.M, 128 * CG) * ceil_div(g.N, b / 2), slots);
+    const double cost = (double)rounds * c.whole() + fmin(c.steps, c.stores);
+    if (cost < 0.98 * least) least = cost, bn = b;
   }
-  return best;
+  TcArgs a = {};
+  TcMaps maps = {};
+  a.c[0] = g.c0, a.c[1] = g.c1, a.c[2] = g.c2;
+  a.bn = bn;
+  if (!make_part(a, maps, 1, dtype, g, bn / 2, 1, CG, a.c, 3) ||
+      !make_map(&maps.a[0], dtype, g.a0, g.M, g.K, g.lda, 128) ||
+      !make_map(&maps.b[0], dtype, g.b0, g.N, g.K, g.ldb, bn / 2) ||
+      !make_map(&maps.b[1], dtype, g.b1, g.N, g.K, g.ldb1, bn / 2))
+    return cudaErrorInvalidValue;
+  return launch<kTcGated, E, ACT, CG>(a, maps, num_sms, s);
 }
 
-template <int MODE, class E, int ACT>
-cudaError_t launch_shape(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
-  if (g.M > 128) return launch<MODE, E, ACT, 2>(dtype, g, columns(MODE, g, 2, num_sms), num_sms, s);
-  return launch<MODE, E, ACT, 1>(dtype, g, columns(MODE, g, 1, num_sms), num_sms, s);
+// dx and the weights' gradients, either of which may be absent.
+template <class E, int CG>
+cudaError_t launch_grad(int dtype, const GemmArgs* dx, const GemmArgs* dw, int num_sms, cudaStream_t s) {
+  const int64_t N = (dx ? dx : dw)->N, P = num_sms / CG;
+  int bn = 256;
+  int64_t ahead = 0;
+  double least = 1e300;
+  for (int b = 256; b >= 64; b -= 32) {
+    const int64_t tiles_n = ceil_div(N, b), b_rows = ceil_div(b / CG, 64) * 64;
+    const TileCost cx = tile_cost(dx ? 2 * ceil_div(dx->K, kBK) : 0, b, b_rows);
+    const TileCost cw = tile_cost(dw ? ceil_div(dw->K, kBK) : 0, b, b_rows);
+    const int64_t D = dx ? ceil_div(dx->M, 128 * CG) * tiles_n : 0, left = D % P;
+    int64_t W = dw ? 2 * ceil_div(dw->M, 128 * CG) * tiles_n : 0, first = 0;
+    double cost = (double)(D / P) * cx.whole();
+    if (left) {
+      first = W ? (int64_t)(cx.whole() / cw.whole()) : 0;
+      if (first > ceil_div(W, P - left)) first = ceil_div(W, P - left);
+      W -= first * (P - left);
+      cost += fmax(cx.whole(), (double)first * cw.whole());
+    }
+    if (W > 0) cost += (double)ceil_div(W, P) * cw.whole();
+    cost += dw ? fmin(cw.steps, cw.stores) : fmin(cx.steps, cx.stores);
+    if (cost < 0.98 * least) least = cost, bn = b, ahead = first;
+  }
+  TcArgs a = {};
+  TcMaps maps = {};
+  a.bn = bn;
+  bool ok = true;
+  if (dx) {
+    a.c[0] = dx->c0;
+    ok = make_part(a, maps, 0, dtype, *dx, bn, 1, CG, a.c, 1) &&
+         make_map(&maps.a[0], dtype, dx->a0, dx->M, dx->K, dx->lda, 128) &&
+         make_map(&maps.a[1], dtype, dx->a1, dx->M, dx->K, dx->lda, 128) &&
+         make_map(&maps.b[0], dtype, dx->b0, dx->K, dx->N, dx->ldb, 64) &&
+         make_map(&maps.b[1], dtype, dx->b1, dx->K, dx->N, dx->ldb1, 64);
+  }
+  if (dw && ok) {
+    a.c[1] = dw->c0, a.c[2] = dw->c1;
+    ok = make_part(a, maps, 1, dtype, *dw, bn, 2, CG, a.c + 1, 2) &&
+         make_map(&maps.a[2], dtype, dw->a0, dw->K, dw->M, dw->lda, 64) &&
+         make_map(&maps.a[3], dtype, dw->a1, dw->K, dw->M, dw->lda, 64) &&
+         make_map(&maps.b[2], dtype, dw->b0, dw->K, dw->N, dw->ldb, 64);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  // The grid is smaller than P where there are fewer tiles.
+  const int64_t D = a.part[0].walk.tiles, all = D + a.part[1].walk.tiles, slots = all < P ? all : P;
+  a.rounds = (uint32_t)(D / slots), a.left = (uint32_t)(D % slots), a.free = (uint32_t)(slots - D % slots);
+  a.ahead = a.left && all >= P ? (uint32_t)ahead : 0;
+  return launch<kTcGrad, E, 0, CG>(a, maps, num_sms, s);
 }
 
 template <class E>
-cudaError_t launch_type(int mode, int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
-  switch (mode) {
-    case kGemmGated:
-      return g.act == AR_ACT_SILU ? launch_shape<kGemmGated, E, AR_ACT_SILU>(dtype, g, num_sms, s)
-                                  : launch_shape<kGemmGated, E, AR_ACT_GELU_TANH>(dtype, g, num_sms, s);
-    case kGemmDx: return launch_shape<kGemmDx, E, 0>(dtype, g, num_sms, s);
-    default: return launch_shape<kGemmDw, E, 0>(dtype, g, num_sms, s);
-  }
+cudaError_t gated_type(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
+  // One CTA for what its 128 rows hold, pairs above.
+  if (g.M <= 128)
+    return g.act == AR_ACT_SILU ? launch_gated<E, AR_ACT_SILU, 1>(dtype, g, num_sms, s)
+                                : launch_gated<E, AR_ACT_GELU_TANH, 1>(dtype, g, num_sms, s);
+  return g.act == AR_ACT_SILU ? launch_gated<E, AR_ACT_SILU, 2>(dtype, g, num_sms, s)
+                              : launch_gated<E, AR_ACT_GELU_TANH, 2>(dtype, g, num_sms, s);
+}
+
+template <class E>
+cudaError_t grad_type(int dtype, const GemmArgs* dx, const GemmArgs* dw, int num_sms, cudaStream_t s) {
+  if ((!dx || dx->M <= 128) && (!dw || dw->M <= 128)) return launch_grad<E, 1>(dtype, dx, dw, num_sms, s);
+  return launch_grad<E, 2>(dtype, dx, dw, num_sms, s);
 }
 
 bool rows_on_16(const void* p, int64_t ld) {
@@ -410,8 +496,12 @@ bool gemm_tc_takes(int mode, const GemmArgs& g) {
          rows_on_16(g.a1, g.lda) && rows_on_16(g.b0, g.ldb) && rows_on_16(g.b1, g.ldb1);
 }
 
-cudaError_t launch_gemm_tc(int mode, int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
-  return dtype == AR_BF16 ? launch_type<Bf16>(mode, dtype, g, num_sms, s) : launch_type<F16>(mode, dtype, g, num_sms, s);
+cudaError_t launch_gated_tc(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
+  return dtype == AR_BF16 ? gated_type<Bf16>(dtype, g, num_sms, s) : gated_type<F16>(dtype, g, num_sms, s);
+}
+
+cudaError_t launch_grad_tc(int dtype, const GemmArgs* dx, const GemmArgs* dw, int num_sms, cudaStream_t s) {
+  return dtype == AR_BF16 ? grad_type<Bf16>(dtype, dx, dw, num_sms, s) : grad_type<F16>(dtype, dx, dw, num_sms, s);
 }
 
 cudaError_t take_error_word(void* p, cudaStream_t s, uint32_t* error) {

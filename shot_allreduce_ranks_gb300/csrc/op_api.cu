@@ -84,7 +84,7 @@ ar_status_t pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_
   return cuda_status(ar::launch_pack(jobs, n, (int)elem, num_sms, s));
 }
 
-// Which kernel makes a product.  Up to 32 tokens the weights can be streamed
+// Which kernel makes a forward product.  Up to 32 tokens the weights can be streamed
 // past them by mma.sync, whose time grows with every eight tokens; the tensor
 // cores' form for some tens of tokens costs about 2 us more to set up but
 // stays flat: it takes over where tokens x width x hidden passes 2^26 (16 tokens
@@ -97,7 +97,7 @@ cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaSt
       (!mid || g.M <= 8 || (double)g.M * (double)g.N * (double)g.K <= (double)(1 << 26)))
     return ar::launch_gemm_few(mode, dtype, g, s);
   if (mid) return ar::launch_gemm_mid(dtype, g, num_sms, s);
-  if (ar::gemm_tc_takes(mode, g)) return ar::launch_gemm_tc(mode, dtype, g, num_sms, s);
+  if (ar::gemm_tc_takes(mode, g)) return ar::launch_gated_tc(dtype, g, num_sms, s);
   if (ar::gemm_i8_takes(mode, g)) return ar::launch_gemm_i8(dtype, g, num_sms, s);
   return ar::launch_gemm_any(mode, dtype, g, s);
 }
@@ -258,22 +258,19 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
   char* dup = h->work + 2 * h->max_tokens * h->ldw;
   cudaError_t e = ar::launch_gate_grad(h->dtype, h->act, gate, up, dout, (int64_t)ldo, dgate, dup,
                                        (int64_t)h->ldw, (int64_t)tokens, (int64_t)F, h->num_sms, s);
-  if (e == cudaSuccess && dx) {
-    ar::GemmArgs g = {};
-    g.a0 = dgate, g.a1 = dup, g.lda = (int64_t)h->ldw;
-    g.b0 = m[1].p, g.b1 = m[2].p, g.ldb = (int64_t)m[1].ld, g.ldb1 = (int64_t)m[2].ld;
-    g.c0 = dx, g.ldc = (int64_t)lddx;
-    g.M = (int64_t)tokens, g.N = (int64_t)K, g.K = (int64_t)F;
-    e = gemm(ar::kGemmDx, h->dtype, g, h->num_sms, s);
-  }
-  if (e == cudaSuccess && dw_gate) {
-    ar::GemmArgs g = {};
-    g.a0 = dgate, g.a1 = dup, g.lda = (int64_t)h->ldw;
-    g.b0 = m[0].p, g.ldb = (int64_t)m[0].ld;
-    g.c0 = dw_gate, g.c1 = dw_up, g.ldc = (int64_t)lddw;
-    g.M = (int64_t)F, g.N = (int64_t)K, g.K = (int64_t)tokens;
-    e = gemm(ar::kGemmDw, h->dtype, g, h->num_sms, s);
-  }
+  ar::GemmArgs gx = {}, gw = {};
+  gx.a0 = gw.a0 = dgate, gx.a1 = gw.a1 = dup, gx.lda = gw.lda = (int64_t)h->ldw;
+  gx.b0 = m[1].p, gx.b1 = m[2].p, gx.ldb = (int64_t)m[1].ld, gx.ldb1 = (int64_t)m[2].ld;
+  gx.c0 = dx, gx.ldc = (int64_t)lddx;
+  gx.M = (int64_t)tokens, gx.N = (int64_t)K, gx.K = (int64_t)F;
+  gw.b0 = m[0].p, gw.ldb = (int64_t)m[0].ld;
+  gw.c0 = dw_gate, gw.c1 = dw_up, gw.ldc = (int64_t)lddw;
+  gw.M = (int64_t)F, gw.N = (int64_t)K, gw.K = (int64_t)tokens;
+  const bool tc_x = dx && ar::gemm_tc_takes(ar::kGemmDx, gx), tc_w = dw_gate && ar::gemm_tc_takes(ar::kGemmDw, gw);
+  if (e == cudaSuccess && (tc_x || tc_w))
+    e = ar::launch_grad_tc(h->dtype, tc_x ? &gx : nullptr, tc_w ? &gw : nullptr, h->num_sms, s);
+  if (e == cudaSuccess && dx && !tc_x) e = ar::launch_gemm_any(ar::kGemmDx, h->dtype, gx, s);
+  if (e == cudaSuccess && dw_gate && !tc_w) e = ar::launch_gemm_any(ar::kGemmDw, h->dtype, gw, s);
   return cuda_status(e);
 }
 

@@ -61,7 +61,8 @@ struct GemmArgs {
 // On tcgen05, for operands that a tensor map can describe; gemm_tc_error reads
 // and clears the flag that a wait which gave up leaves on the device.
 bool gemm_tc_takes(int mode, const GemmArgs& g);
-cudaError_t launch_gemm_tc(int mode, int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
+cudaError_t launch_gated_tc(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s);
+cudaError_t launch_grad_tc(int dtype, const GemmArgs* dx, const GemmArgs* dw, int num_sms, cudaStream_t s);  // null: absent
 cudaError_t gemm_tc_error(cudaStream_t s, uint32_t* error);
 
 cudaError_t take_error_word(void* p, cudaStream_t s, uint32_t* error);  // reads and clears

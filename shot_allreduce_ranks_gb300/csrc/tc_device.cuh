@@ -227,27 +227,35 @@ __device__ __forceinline__ bool elect_one() {
 
 // Tiles of the output: `group` rows of tiles are walked column by column, so
 // that the tiles in flight at one time form a block whose operands stay in L2.
+// 32-bit numbers: a thread that copies or stores finds its next tile by four
+// divisions, which 64-bit ones would make a good part of a short tile's time.
 struct TileWalk {
-  int tiles_m, tiles_n, group;
-  int64_t tiles;  // all planes
+  uint32_t tiles_m, tiles_n, group;
+  uint32_t tiles;  // all planes
 };
 
 struct Tile {
   int m, n, z;
 };
 
-__device__ __forceinline__ Tile tile_at(const TileWalk& w, int64_t t) {
-  const int64_t plane = (int64_t)w.tiles_m * w.tiles_n;
+__device__ __forceinline__ Tile tile_at(const TileWalk& w, uint32_t t) {
+  const uint32_t plane = w.tiles_m * w.tiles_n;
   Tile r;
   r.z = (int)(t / plane);
-  t -= r.z * plane;
-  const int64_t band = (int64_t)w.group * w.tiles_n;
-  const int first = (int)(t / band) * w.group;
-  const int rows = min(w.group, w.tiles_m - first);
-  t %= band;
-  r.m = first + (int)(t % rows);
+  t -= (uint32_t)r.z * plane;
+  const uint32_t band = w.group * w.tiles_n, b = t / band;
+  const uint32_t first = b * w.group, rows = min(w.group, w.tiles_m - first);
+  t -= b * band;
   r.n = (int)(t / rows);
+  r.m = (int)(first + t - (uint32_t)r.n * rows);
   return r;
+}
+
+// Host: false where there are more tiles than the numbers hold.
+inline bool make_walk(TileWalk* w, int64_t tiles_m, int64_t tiles_n, int64_t planes, int group) {
+  if (tiles_m > (1 << 30) || tiles_n > (1 << 30) || tiles_m * tiles_n > (1 << 30)) return false;
+  *w = {(uint32_t)tiles_m, (uint32_t)tiles_n, (uint32_t)group, (uint32_t)(tiles_m * tiles_n * planes)};
+  return true;
 }
 
 // A warp's 32 x 32 results, lane l holding row m0 + l, to columns n0 .. of an
