@@ -5,16 +5,20 @@
 // every int8 exactly, a product of two is exact in fp32, and so is their sum
 // while it stays within 2^24 (K <= 1024 whatever the values, far longer for
 // values that vary).  So the operands stay 8-bit in memory, in L2 and on the
-// way into an SM, and converter warps turn each tile into fp16 in shared memory
-// (a byte permutation and a subtraction for every two values), in the swizzled
-// layout that the matrix instruction reads.
+// way into an SM, and converter warps turn each tile into fp16 (a byte
+// permutation and a subtraction for every two values): x into tensor memory,
+// which the matrix instruction can take its A operand from, w into shared memory in
+// the swizzled layout that it reads B in.  Shared memory's bandwidth is what
+// bounds this (copy in, read, write, and read by the instruction), and x takes
+// only the first two of those four there.
 //
 // Roles, persistent over tiles of 128 CG x bn: one thread copies int8 tiles of
-// 128 k into a staging ring by tensor maps, groups of warps convert them into
-// the operand ring, one thread issues the matrix instructions, four warps scale
-// and store.  Each group of converters owns one operand stage of 64 k, so that
-// the latencies of four conversions overlap.  A pair of CTAs (CG = 2) shares one instruction over 256 rows, each
-// converting its own 128 rows of x and half of the rows of w.
+// 128 k into a staging ring by tensor maps, groups of warps convert them, one
+// thread issues the matrix instructions, four warps scale and store.  Four
+// groups of converters take steps of 64 k in turn, so that their latencies
+// overlap, and eight operand stages cover the way from a conversion through the
+// pair's barriers and the instruction back to a free stage.  A pair of CTAs (CG = 2) shares one instruction over
+// 256 rows, each converting its own 128 rows of x and half of the rows of w.
 #include "tc_device.cuh"
 
 namespace ar {
@@ -23,14 +27,17 @@ namespace {
 using namespace tc;
 
 constexpr int kRowsMax = 256;                        // rows of x and w in a CTA's stage
-constexpr uint32_t kStaged = kRowsMax * 128, kOperand = kRowsMax * 128;
-constexpr int kSS = 3, kOS = 4;                      // stages of the two rings: 128 k and 64 k
-constexpr int kGroups = kOS, kGroupWarps = 4;        // converters
+constexpr uint32_t kStaged = kRowsMax * 128;         // bytes of a staging stage, 128 k
+constexpr uint32_t kOperand = (kRowsMax - 128) * 128;  // of an operand stage of w, 64 k
+constexpr int kSS = 3, kOS = 8;                      // stages of the two rings
+constexpr int kGroups = 4, kGroupWarps = 4;          // converters: a warp for each quarter of tensor memory's lanes
 constexpr int kGroupThreads = 32 * kGroupWarps;
 constexpr int kI8Threads = 32 * 6 + kGroups * kGroupThreads;
-constexpr int kPieces = kRowsMax / (8 * kGroupWarps);  // 16-byte pieces that a converter takes of a step
+constexpr int kPieces = (kRowsMax - 128) / (8 * kGroupWarps);  // 16-byte pieces of w that a converter takes of a step
 constexpr uint32_t kI8Smem = kSS * kStaged + kOS * kOperand + 1024;
-constexpr uint32_t kI8TmemCols = 512;
+// Tensor memory: accumulators from column 0, two of up to 128 columns or one of
+// 256, and eight stages of x, 32 columns each.
+constexpr uint32_t kI8TmemCols = 512, kAccStride = 128, kXCols = 256;
 
 __device__ uint32_t g_i8_error;  // set by a wait that gave up
 
@@ -58,6 +65,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int rows = 128 + a.bn / CG;  // of a stage: x, then w
+  const uint32_t accs = a.bn <= (int)kAccStride ? 2 : 1;  // accumulators
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSS; ++i) {
@@ -116,17 +124,18 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       uint32_t it = 0, at = 0;
       bool ok = true;
       for (uint32_t t = first; t < a.walk.tiles && ok; t += stride, ++at) {
-        const uint32_t buf = at & 1;
-        if (!(ok = bar_wait(freed + 8 * buf, ((at >> 1) & 1) ^ 1, &dead))) break;
+        const uint32_t buf = at % accs;
+        if (!(ok = bar_wait(freed + 8 * buf, (at / accs & 1) ^ 1, &dead))) break;
         fence_after_sync();
         for (int s = 0; s < a.steps; ++s, ++it) {
           const uint32_t st = it % kOS;
           if (!(ok = bar_wait(ready + 8 * st, (it / kOS) & 1, &dead))) break;
           fence_after_sync();
-          const uint32_t base = operands + st * kOperand;
-          const uint64_t dx = operand_desc(base, 16, 1024), dw = operand_desc(base + 128 * 128, 16, 1024);
+          const uint32_t x = tmem + kXCols + st * 32;
+          const uint64_t w = operand_desc(operands + st * kOperand, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16<CG>(tmem + buf * 256, dx + 2 * k, dw + 2 * k, idesc, s > 0 || k > 0);
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ts<CG>(tmem + buf * kAccStride, x + 8 * k, w + 2 * k, idesc, s > 0 || k > 0);
           mma_commit<CG>(used + 8 * st);
         }
         if (ok) mma_commit<CG>(done + 8 * buf);
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     uint32_t at = 0;
     for (uint32_t t = first; t < a.walk.tiles; t += stride, ++at) {
       const Tile tile = tile_at(a.walk, t);
-      const uint32_t buf = at & 1;
+      const uint32_t buf = at % accs;
       const int64_t m0 = ((int64_t)tile.m * CG + rank) * 128 + lane0, m = m0 + (threadIdx.x & 31);
       const int n0 = tile.n * a.bn;
       // The scales are on their way while the tile is multiplied: a lane holds
@@ -154,7 +163,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const int n = n0 + 32 * j + (int)(threadIdx.x & 31);
         sn[j] = 32 * j < a.bn && n < a.g.N ? a.g.sn[n] : 0.0f;
       }
-      if (!bar_wait(done + 8 * buf, (at >> 1) & 1, &dead)) {
+      if (!bar_wait(done + 8 * buf, at / accs & 1, &dead)) {
         atomicExch(&g_i8_error, 1u);
         break;
       }
@@ -165,7 +174,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         if (c >= a.bn || n0 + c >= a.g.N) break;
         uint32_t r[32];
         __syncwarp();
-        tmem_load32(r, tmem + (lane0 << 16) + buf * 256 + c);
+        tmem_load32(r, tmem + (lane0 << 16) + buf * kAccStride + c);
         tmem_wait_load32(r);
         float v[32];
 #pragma unroll
@@ -182,66 +191,86 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
     }
   } else {
-    // Both rings hold rows of 128 bytes whose 16-byte piece p lies at p ^ (row % 8).
-    // A step converts half of a staged row, pieces 4h .. 4h + 3, into all eight
-    // of an operand row.  Eight lanes take four pieces of rows r and r + 4 (eight
-    // different banks), and the lanes of the second row store their two results
-    // in the other order, which again makes eight.
+    // Staged rows are 128 bytes whose 16-byte piece p lies at p ^ (row % 8), and
+    // so are w's operand rows.  A step converts half of a staged row, pieces 4h ..
+    // 4h + 3.  A thread takes a whole such row of x (eight lanes read eight
+    // different banks) into its lane of tensor memory.  Of w, eight lanes take four
+    // pieces of rows r and r + 4 (eight banks again) into all eight of an
+    // operand row, and the lanes of the second row store their two results in
+    // the other order, which again makes eight.
     const int group = (warp - 6) / kGroupWarps, thread = (int)(threadIdx.x - 6 * 32) % kGroupThreads;
     const int lane = thread & 31, j = lane & 3, second = (lane >> 2) & 1;
-    const int row0 = (thread >> 5) * 8 + (lane >> 3) + 4 * second;  // + 8 kGroupWarps each time
+    const int row0 = (thread >> 5) * 8 + (lane >> 3) + 4 * second;  // of w, + 8 kGroupWarps each time
+    const int x_row = (warp & 3) * 32 + lane;
     const int64_t total = (int64_t)(first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0) * a.steps;
     bool ok = true;
     int64_t it = group;
     for (; it < total && ok; it += kGroups) {
-      const uint32_t unit = (uint32_t)(it >> 1), ss = unit % kSS, half = (uint32_t)it & 1, round = (uint32_t)(it / kOS);
+      const uint32_t unit = (uint32_t)(it >> 1), ss = unit % kSS, half = (uint32_t)it & 1;
+      const uint32_t os = (uint32_t)(it % kOS), round = (uint32_t)(it / kOS);
       if (!(ok = bar_wait(landed + 8 * ss, (unit / kSS) & 1, &dead))) break;
-      const uint32_t from = staging + ss * kStaged, to = operands + (uint32_t)group * kOperand;
-      uint4 q[kPieces];
+      const uint32_t from = staging + ss * kStaged, to = operands + os * kOperand;
+      uint4 q[kPieces], xq[4];
+      const auto load = [&](uint4& v, int row, int piece) {
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(from + (uint32_t)row * 128 + 16u * ((half * 4 + piece) ^ (row & 7))));
+      };
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int row = row0 + i * 8 * kGroupWarps;
-        if (row < rows)
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
-                       : "r"(from + (uint32_t)row * 128 + 16u * ((half * 4 + j) ^ (row & 7))));
-      }
+      for (int p = 0; p < 4; ++p) load(xq[p], x_row, p);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (row0 + i * 8 * kGroupWarps < rows - 128) load(q[i], 128 + row0 + i * 8 * kGroupWarps, j);
       // The staged rows are in registers: the next copy need not wait for the operand stage.
       __syncwarp();
       if (elect_one()) bar_arrive(taken + 8 * ss);
-      if (!(ok = bar_wait(used + 8 * group, (round & 1) ^ 1, &dead))) break;
+      if (!(ok = bar_wait(used + 8 * os, (round & 1) ^ 1, &dead))) break;
+      fence_after_sync();
+      {
+        uint32_t h[32];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          i8_to_f16(xq[p].x, h[8 * p], h[8 * p + 1]);
+          i8_to_f16(xq[p].y, h[8 * p + 2], h[8 * p + 3]);
+          i8_to_f16(xq[p].z, h[8 * p + 4], h[8 * p + 5]);
+          i8_to_f16(xq[p].w, h[8 * p + 6], h[8 * p + 7]);
+        }
+        __syncwarp();
+        tmem_store32(tmem + ((uint32_t)(warp & 3) << 21) + kXCols + os * 32, h);
+      }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int row = row0 + i * 8 * kGroupWarps;
-        if (row < rows) {
+        if (row < rows - 128) {
           const uint32_t line = to + (uint32_t)row * 128;
-          uint32_t h[8];
-          i8_to_f16(q[i].x, h[0], h[1]);
-          i8_to_f16(q[i].y, h[2], h[3]);
-          i8_to_f16(q[i].z, h[4], h[5]);
-          i8_to_f16(q[i].w, h[6], h[7]);
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             const int c = o ^ second;
+            uint32_t h[4];
+            i8_to_f16(c ? q[i].z : q[i].x, h[0], h[1]);
+            i8_to_f16(c ? q[i].w : q[i].y, h[2], h[3]);
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(line + 16u * ((2 * j + c) ^ (row & 7))),
-                         "r"(c ? h[4] : h[0]), "r"(c ? h[5] : h[1]), "r"(c ? h[6] : h[2]), "r"(c ? h[7] : h[3])
-                         : "memory");
+                         "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
           }
         }
       }
+      fence_before_sync();
       fence_async_smem();  // the matrix unit reads through the asynchronous proxy
       __syncwarp();
       if (elect_one()) {
         if (CG == 2)
-          bar_arrive_cluster(map_to_cta(ready + 8 * group, 0));
+          bar_arrive_cluster(map_to_cta(ready + 8 * os, 0));
         else
-          bar_arrive(ready + 8 * group);
+          bar_arrive(ready + 8 * os);
       }
     }
     if (!ok) atomicExch(&g_i8_error, 1u);
-    // The group's last operand stage is multiplied before the CTA ends.
-    if (ok && it >= kGroups && it - kGroups < total)
-      bar_wait(used + 8 * group, (uint32_t)((it - kGroups) / kOS) & 1, &dead);
+    // What the group made last is multiplied before the CTA ends, and so is all
+    // that it made before.
+    if (ok && it >= kGroups && it - kGroups < total) {
+      const uint32_t last = (uint32_t)(it - kGroups);
+      bar_wait(used + 8 * (last % kOS), last / kOS & 1, &dead);
+    }
   }
   __syncwarp();
   fence_before_sync();
@@ -279,15 +308,17 @@ cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
 }
 
 // Columns of a tile: the number of rounds of tiles over the SMs times a round's
-// time, which is a step's conversion (about 1.5 clocks a row of the stage on
-// shared memory's bandwidth) or its matrix instruction (2 clocks a column).
+// time, which is a step's traffic in shared memory at 128 bytes a clock (a row of
+// x 128 bytes, one of w 384) or its matrix instruction (2 clocks a column).
 int columns(const GemmArgs& g, int cg, int num_sms) {
-  const int64_t tm = (g.M + 128 * cg - 1) / (128 * cg), slots = num_sms / cg;
+  const int64_t tm = (g.M + 128 * cg - 1) / (128 * cg), slots = num_sms / cg, steps = (g.K + 63) / 64;
   int best = 32;
   double least = 1e300;
   for (int bn = cg == 2 ? 256 : 128; bn >= 32; bn -= 32) {
-    const int64_t tiles = tm * ((g.N + bn - 1) / bn);
-    const double step = 1.5 * (128 + bn / cg) * 2, cost = (double)((tiles + slots - 1) / slots) * (step > 2 * bn ? step : 2 * bn);
+    const int64_t rounds = (tm * ((g.N + bn - 1) / bn) + slots - 1) / slots;
+    const double smem = 128.0 + 3.0 * bn / cg, step = smem > 2 * bn ? smem : 2 * bn, stores = 15.0 * bn;
+    // One accumulator: each tile's stores are waited for; two: the last tile's.
+    const double cost = (double)rounds * (steps * step + (bn > (int)kAccStride ? stores : 0)) + (bn > (int)kAccStride ? 0 : stores);
     if (cost < least) least = cost, best = bn;
   }
   return best;
