@@ -348,6 +348,10 @@ bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t 
   return tc_make_map(map, dtype == AR_BF16 ? kMapBf16 : kMapF16, p, rows, cols, ld, box_rows, box_cols);
 }
 
+bool rows_on_16(const void* p, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+}
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // One product's tiles; false if there are too many or an output map could not be made.
@@ -383,13 +387,14 @@ cudaError_t launch(const TcArgs& a, const TcMaps& maps, int num_sms, cudaStream_
 
 // What a tile takes, in clocks: a step of 64 k the longer of its instruction (2
 // a column) and its copies (an SM takes in 64 bytes a clock); its stores about
-// ten a column, which the next tile hides.
+// ten a column, or forty where rows do not start on 16 bytes, which the next
+// tile hides.
 struct TileCost {
   double steps, stores;
   double whole() const { return fmax(steps, stores); }
 };
-TileCost tile_cost(int64_t steps, int bn, int64_t b_rows) {
-  return {(double)steps * fmax(2.0 * bn, 2.0 * (double)(128 + b_rows)), 10.0 * bn};
+TileCost tile_cost(int64_t steps, int bn, int64_t b_rows, bool aligned) {
+  return {(double)steps * fmax(2.0 * bn, 2.0 * (double)(128 + b_rows)), (aligned ? 10.0 : 40.0) * bn};
 }
 
 template <class E, int ACT, int CG>
@@ -398,7 +403,7 @@ cudaError_t launch_gated(int dtype, const GemmArgs& g, int num_sms, cudaStream_t
   int bn = 256;
   double least = 1e300;
   for (int b = 256; b >= 64; b -= 64) {
-    const TileCost c = tile_cost(ceil_div(g.K, kBK), b, b / CG);
+    const TileCost c = tile_cost(ceil_div(g.K, kBK), b, b / CG, rows_on_16(g.c0, g.ldc));
     const int64_t rounds = ceil_div(ceil_div(g.M, 128 * CG) * ceil_div(g.N, b / 2), slots);
     const double cost = (double)rounds * c.whole() + fmin(c.steps, c.stores);
     if (cost < 0.98 * least) least = cost, bn = b;
@@ -424,8 +429,8 @@ cudaError_t launch_grad(int dtype, const GemmArgs* dx, const GemmArgs* dw, int n
   double least = 1e300;
   for (int b = 256; b >= 64; b -= 32) {
     const int64_t tiles_n = ceil_div(N, b), b_rows = ceil_div(b / CG, 64) * 64;
-    const TileCost cx = tile_cost(dx ? 2 * ceil_div(dx->K, kBK) : 0, b, b_rows);
-    const TileCost cw = tile_cost(dw ? ceil_div(dw->K, kBK) : 0, b, b_rows);
+    const TileCost cx = tile_cost(dx ? 2 * ceil_div(dx->K, kBK) : 0, b, b_rows, !dx || rows_on_16(dx->c0, dx->ldc));
+    const TileCost cw = tile_cost(dw ? ceil_div(dw->K, kBK) : 0, b, b_rows, !dw || rows_on_16(dw->c0, dw->ldc));
     const int64_t D = dx ? ceil_div(dx->M, 128 * CG) * tiles_n : 0, left = D % P;
     int64_t W = dw ? 2 * ceil_div(dw->M, 128 * CG) * tiles_n : 0, first = 0;
     double cost = (double)(D / P) * cx.whole();
@@ -480,10 +485,6 @@ template <class E>
 cudaError_t grad_type(int dtype, const GemmArgs* dx, const GemmArgs* dw, int num_sms, cudaStream_t s) {
   if ((!dx || dx->M <= 128) && (!dw || dw->M <= 128)) return launch_grad<E, 1>(dtype, dx, dw, num_sms, s);
   return launch_grad<E, 2>(dtype, dx, dw, num_sms, s);
-}
-
-bool rows_on_16(const void* p, int64_t ld) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
 }
 
 }  // namespace

@@ -330,17 +330,19 @@ __device__ __forceinline__ void store_chunk(void* out, int64_t ldc, int64_t m0, 
       }
   }
   const int c = 2 * (lane & 15);
-  char* p = static_cast<char*>(out) + ((m0 + (lane & 16)) * ldc + n0 + c) * 2;
+  const int64_t first = m0 + (lane & 16);
+  const int rows = first < M ? (int)min((int64_t)16, M - first) : 0;
+  char* p = static_cast<char*>(out) + (first * ldc + n0 + c) * 2;
+  const bool two = c + 1 < left;
+  if (c >= left) return;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (m0 + (lane & 16) + j < M && c < left) {
-      uint16_t* q = reinterpret_cast<uint16_t*>(p + j * ldc * 2);
-      if (align >= 4 && c + 1 < left) {
-        *reinterpret_cast<uint32_t*>(q) = w[j];
-      } else {
-        q[0] = (uint16_t)w[j];
-        if (c + 1 < left) q[1] = (uint16_t)(w[j] >> 16);
-      }
+  for (int j = 0; j < 16; ++j, p += ldc * 2) {
+    if (j >= rows) break;
+    if (align >= 4 && two) {
+      *reinterpret_cast<uint32_t*>(p) = w[j];
+    } else {
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[j];
+      if (two) *reinterpret_cast<uint16_t*>(p + 2) = (uint16_t)(w[j] >> 16);
     }
   }
 }
