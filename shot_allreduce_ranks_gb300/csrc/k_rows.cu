@@ -6,16 +6,67 @@
 namespace ar {
 namespace {
 
-constexpr int kGateThreads = 256;
+constexpr int kPackThreads = 256, kGateThreads = 256;
+
+struct PackJobs {
+  PackJob job[3];
+};
+
+// One matrix's rows.  A thread makes 16 bytes of a row from its elements, one
+// load each: the source rows begin anywhere, and neighbouring lanes' loads share
+// cache lines.
+template <int B>
+__device__ __forceinline__ void pack_rows(const PackJob& j) {
+  constexpr int G = 16 / B;
+  const int64_t per_row = (j.cols + G - 1) / G, total = j.rows * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kPackThreads) {
+    const int64_t row = total >> 32 ? i / per_row : (int64_t)((uint32_t)i / (uint32_t)per_row);
+    const int64_t col = (i - row * per_row) * G;
+    const char* p = static_cast<const char*>(j.from) + (row * j.ld_from + col) * B;
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int k = 0; k < G; ++k)
+      if (col + k < j.cols) {
+        const uint32_t v = B == 2 ? *reinterpret_cast<const uint16_t*>(p + 2 * k) : *reinterpret_cast<const uint8_t*>(p + k);
+        w[k * B / 4] |= v << (8 * (k * B % 4));
+      }
+    *reinterpret_cast<uint4*>(static_cast<char*>(j.to) + (row * j.ld_to + col) * B) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <int B>
+__global__ void __launch_bounds__(kPackThreads) k_pack(const __grid_constant__ PackJobs jobs) {
+  pdl_enter();
+  pack_rows<B>(jobs.job[blockIdx.y]);
+}
+
+// CTAs in x for the largest of the jobs, and the jobs side by side.
+int64_t pack_ctas(const PackJob* jobs, int count, int elem_bytes, PackJobs* all) {
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    all->job[i] = jobs[i];
+    const int64_t g = 16 / elem_bytes, n = jobs[i].rows * ((jobs[i].cols + g - 1) / g);
+    most = n > most ? n : most;
+  }
+  return (most + kPackThreads - 1) / kPackThreads;
+}
 
 // dgate = dout * up * act'(gate), dup = dout * act(gate): 3 reads and 2 writes
 // an element, bound by memory.  A thread takes eight columns of a row at a
-// time; the workspace rows are 16-byte aligned, the caller's need not be.
+// time; the workspace rows are 16-byte aligned, the caller's need not be.  The
+// rows of CTAs past the first copy the operands that the products want laid out:
+// neither waits for the other, and a launch costs about 2 us.
 template <class E, int ACT, bool VEC>
 __global__ void __launch_bounds__(kGateThreads)
     k_gate_grad(const char* gate, const char* up, const char* dout, int64_t ldo, char* dgate,
-                char* dup, int64_t ldw, int64_t rows, int64_t cols, int64_t groups_per_row) {
+                char* dup, int64_t ldw, int64_t rows, int64_t cols, int64_t groups_per_row,
+                const __grid_constant__ PackJobs jobs) {
   pdl_enter();
+  if (blockIdx.y > 0) {
+    pack_rows<2>(jobs.job[blockIdx.y - 1]);
+    return;
+  }
   const int64_t total = rows * groups_per_row;
   for (int64_t i = (int64_t)blockIdx.x * kGateThreads + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * kGateThreads) {
@@ -57,17 +108,19 @@ __global__ void __launch_bounds__(kGateThreads)
 
 template <class E, int ACT>
 cudaError_t gate_grad(const void* gate, const void* up, const void* dout, int64_t ldo, void* dgate,
-                      void* dup, int64_t ldw, int64_t rows, int64_t cols, int num_sms,
-                      cudaStream_t s) {
+                      void* dup, int64_t ldw, int64_t rows, int64_t cols, const PackJob* jobs, int count,
+                      int num_sms, cudaStream_t s) {
   const int64_t gpr = (cols + 7) / 8;
-  const int64_t want = (rows * gpr + kGateThreads - 1) / kGateThreads;
-  const unsigned grid = (unsigned)(want < (int64_t)num_sms * 8 ? want : (int64_t)num_sms * 8);
+  PackJobs all = {};
+  const int64_t pack = pack_ctas(jobs, count, 2, &all), gate_ctas = (rows * gpr + kGateThreads - 1) / kGateThreads;
+  const int64_t want = pack > gate_ctas ? pack : gate_ctas, cap = (int64_t)num_sms * 8;
+  const dim3 grid((unsigned)(want < cap ? want : cap), (unsigned)(1 + count));
   const bool vec = ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up) |
                      reinterpret_cast<uintptr_t>(dout)) & 15u) == 0 && ldo % 8 == 0;
   auto* k = vec ? k_gate_grad<E, ACT, true> : k_gate_grad<E, ACT, false>;
-  return launch_op(k, dim3(grid), kGateThreads, 0, 1, s, static_cast<const char*>(gate),
+  return launch_op(k, grid, kGateThreads, 0, 1, s, static_cast<const char*>(gate),
                    static_cast<const char*>(up), static_cast<const char*>(dout), ldo,
-                   static_cast<char*>(dgate), static_cast<char*>(dup), ldw, rows, cols, gpr);
+                   static_cast<char*>(dgate), static_cast<char*>(dup), ldw, rows, cols, gpr, all);
 }
 
 // ---------------------------------------------------------------------------
@@ -166,62 +219,25 @@ cudaError_t quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* 
                    s, static_cast<const char*>(x), ldx, q, ldq, scale, cols);
 }
 
-// ---------------------------------------------------------------------------
-constexpr int kPackThreads = 256;
-
-struct PackJobs {
-  PackJob job[3];
-};
-
-// A thread makes 16 bytes of a row from its elements, one load each: the
-// source rows begin anywhere, and neighbouring lanes' loads share cache lines.
-template <int B>
-__global__ void __launch_bounds__(kPackThreads) k_pack(const __grid_constant__ PackJobs jobs) {
-  pdl_enter();
-  constexpr int G = 16 / B;
-  const PackJob j = jobs.job[blockIdx.y];
-  const int64_t per_row = (j.cols + G - 1) / G, total = j.rows * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kPackThreads) {
-    const int64_t row = total >> 32 ? i / per_row : (int64_t)((uint32_t)i / (uint32_t)per_row);
-    const int64_t col = (i - row * per_row) * G;
-    const char* p = static_cast<const char*>(j.from) + (row * j.ld_from + col) * B;
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int k = 0; k < G; ++k)
-      if (col + k < j.cols) {
-        const uint32_t v = B == 2 ? *reinterpret_cast<const uint16_t*>(p + 2 * k) : *reinterpret_cast<const uint8_t*>(p + k);
-        w[k * B / 4] |= v << (8 * (k * B % 4));
-      }
-    *reinterpret_cast<uint4*>(static_cast<char*>(j.to) + (row * j.ld_to + col) * B) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_sms, cudaStream_t s) {
   PackJobs all = {};
-  int64_t most = 0;
-  for (int i = 0; i < count; ++i) {
-    all.job[i] = jobs[i];
-    const int64_t g = 16 / elem_bytes, n = jobs[i].rows * ((jobs[i].cols + g - 1) / g);
-    most = n > most ? n : most;
-  }
-  const int64_t want = (most + kPackThreads - 1) / kPackThreads, cap = (int64_t)num_sms * 8;
+  const int64_t want = pack_ctas(jobs, count, elem_bytes, &all), cap = (int64_t)num_sms * 8;
   const dim3 grid((unsigned)(want < cap ? want : cap), (unsigned)count);
   return launch_op(elem_bytes == 2 ? k_pack<2> : k_pack<1>, grid, kPackThreads, 0, 1, s, all);
 }
 
 cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
                              int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,
-                             int64_t cols, int num_sms, cudaStream_t s) {
+                             int64_t cols, const PackJob* jobs, int count, int num_sms, cudaStream_t s) {
   if (dtype == AR_BF16)
     return act == AR_ACT_SILU
-               ? gate_grad<Bf16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s)
-               : gate_grad<Bf16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s);
+               ? gate_grad<Bf16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s)
+               : gate_grad<Bf16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s);
   return act == AR_ACT_SILU
-             ? gate_grad<F16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s)
-             : gate_grad<F16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, num_sms, s);
+             ? gate_grad<F16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s)
+             : gate_grad<F16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s);
 }
 
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,

@@ -66,22 +66,29 @@ size_t pack_bytes(const Rows* m, int count, size_t elem) {
   return bytes;
 }
 
-ar_status_t pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_bytes, int num_sms, cudaStream_t s) {
+// Points such matrices at their place in scratch and lists the copies.
+ar_status_t plan_pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_bytes, ar::PackJob* jobs, int* n) {
   const size_t need = pack_bytes(m, count, elem);
+  *n = 0;
   if (need == 0 || !scratch) return AR_OK;
   if (misaligned(scratch, 16) || scratch_bytes < need) return AR_ERR_INVALID_ARG;
-  ar::PackJob jobs[3];
-  int n = 0;
   char* to = static_cast<char*>(scratch);
   for (int i = 0; i < count; ++i) {
     if (on_16(m[i], elem)) continue;
     const size_t ld = packed_ld(m[i], elem);
-    jobs[n++] = {m[i].p, to, (int64_t)m[i].rows, (int64_t)m[i].cols, (int64_t)m[i].ld, (int64_t)ld};
+    jobs[(*n)++] = {m[i].p, to, (int64_t)m[i].rows, (int64_t)m[i].cols, (int64_t)m[i].ld, (int64_t)ld};
     m[i].p = to;
     m[i].ld = ld;
     to += m[i].rows * ld * elem;
   }
-  return cuda_status(ar::launch_pack(jobs, n, (int)elem, num_sms, s));
+  return AR_OK;
+}
+
+ar_status_t pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_bytes, int num_sms, cudaStream_t s) {
+  ar::PackJob jobs[3];
+  int n = 0;
+  if (ar_status_t st = plan_pack(m, count, elem, scratch, scratch_bytes, jobs, &n)) return st;
+  return n ? cuda_status(ar::launch_pack(jobs, n, (int)elem, num_sms, s)) : AR_OK;
 }
 
 // Which kernel makes a forward product.  Up to 32 tokens the weights can be streamed
@@ -251,13 +258,14 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
   // dx wants the weights, the weights' gradients want x.
   Rows m[3];
   operands(h, x, ldx, w_gate, w_up, ldw, tokens, m);
-  if (ar_status_t st = dx ? pack(dw_gate ? m : m + 1, dw_gate ? 3 : 2, 2, scratch, scratch_bytes, h->num_sms, s)
-                          : pack(m, 1, 2, scratch, scratch_bytes, h->num_sms, s))
-    return st;
+  ar::PackJob jobs[3];
+  int copies = 0;
+  Rows* const from = dw_gate ? m : m + 1;
+  if (ar_status_t st = plan_pack(from, dx ? (dw_gate ? 3 : 2) : 1, 2, scratch, scratch_bytes, jobs, &copies)) return st;
   char* dgate = h->work;
   char* dup = h->work + 2 * h->max_tokens * h->ldw;
   cudaError_t e = ar::launch_gate_grad(h->dtype, h->act, gate, up, dout, (int64_t)ldo, dgate, dup,
-                                       (int64_t)h->ldw, (int64_t)tokens, (int64_t)F, h->num_sms, s);
+                                       (int64_t)h->ldw, (int64_t)tokens, (int64_t)F, jobs, copies, h->num_sms, s);
   ar::GemmArgs gx = {}, gw = {};
   gx.a0 = gw.a0 = dgate, gx.a1 = gw.a1 = dup, gx.lda = gw.lda = (int64_t)h->ldw;
   gx.b0 = m[1].p, gx.b1 = m[2].p, gx.ldb = (int64_t)m[1].ld, gx.ldb1 = (int64_t)m[2].ld;

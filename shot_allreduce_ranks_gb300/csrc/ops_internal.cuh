@@ -84,12 +84,6 @@ cudaError_t launch_gemm_few(int mode, int dtype, const GemmArgs& g, cudaStream_t
 // On mma.sync, for any alignment and stride.
 cudaError_t launch_gemm_any(int mode, int dtype, const GemmArgs& g, cudaStream_t s);
 
-// dgate = dout * up * act'(gate), dup = dout * act(gate), rounded to the
-// element type (the operands of the tensor cores' products).
-cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
-                             int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,
-                             int64_t cols, int num_sms, cudaStream_t s);
-
 // One int8 row and one scale for each row of x.
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
                                  float* scale, int64_t rows, int64_t cols, cudaStream_t s);
@@ -101,6 +95,13 @@ struct PackJob {
   int64_t rows, cols, ld_from, ld_to;  // elements
 };
 cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_sms, cudaStream_t s);
+
+// dgate = dout * up * act'(gate), dup = dout * act(gate), rounded to the
+// element type (the operands of the tensor cores' products); and the copies of
+// `jobs`, 16-bit matrices, in the same launch.
+cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
+                             int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,
+                             int64_t cols, const PackJob* jobs, int count, int num_sms, cudaStream_t s);
 
 struct DropoutArgs {
   const void* x;
