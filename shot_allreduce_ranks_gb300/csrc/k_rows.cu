@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kGateThreads)
   const int64_t total = rows * groups_per_row;
   for (int64_t i = (int64_t)blockIdx.x * kGateThreads + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * kGateThreads) {
-    const int64_t row = i / groups_per_row, col = (i - row * groups_per_row) * 8;
+    const int64_t row = total >> 32 ? i / groups_per_row : (int64_t)((uint32_t)i / (uint32_t)groups_per_row);
+    const int64_t col = (i - row * groups_per_row) * 8;
     const int64_t from = (row * ldo + col) * 2, to = (row * ldw + col) * 2;
     const int n = (int)(cols - col < 8 ? cols - col : 8);
     uint32_t gw[4] = {}, uw[4] = {}, dw[4] = {};

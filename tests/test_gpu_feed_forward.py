@@ -432,6 +432,21 @@ def test_streams_graphs_and_repetition(ar, M):
         assert all(torch.equal(a, b) for a, b in zip(given, want[0]))
 
 
+@pytest.mark.parametrize("M,K,F", [(24, 2048, 1032), (100, 4096, 1032), (700, 1032, 2600), (300, 777, 501)])
+def test_many_calls_give_the_same_bits(ar, M, K, F):
+    """Hundreds of calls back to back, several tiles to a CTA: a stage reused too
+    early or a sum read too soon would show as a difference."""
+    t = inputs(M, K, F, 3)
+    with ar.GatedFFN(M, K, F, train=True) as ffn:
+        want = everything(ar, ffn, t)
+        off = torch.zeros((), dtype=torch.int64, device=DEV)
+        for _ in range(150):
+            for a, b in zip(everything(ar, ffn, t), want):
+                off += (a != b).sum()
+    assert int(off) == 0
+    assert ar.ops_device_status() == 0
+
+
 def test_scratch_is_optional_at_the_c_entry(ar):
     """Unaligned operands without scratch take another kernel, with too little they are refused."""
     from shot_allreduce_ranks_gb300 import _lib
