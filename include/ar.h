@@ -470,7 +470,7 @@ typedef struct ar_ffn_ctx* ar_ffn_t;
  *               products run on 16-bit tensor-core operands).
  *   activation  ar_activation_t.
  *   train       non-zero: allocate the workspace of ar_ffn_backward (two
- *               max_tokens x width matrices of dtype); zero: allocate nothing,
+ *               max_tokens x width matrices of dtype, and at most 128 rows more); zero: allocate nothing,
  *               and ar_ffn_backward returns AR_ERR_UNSUPPORTED.
  * ar_ffn_backward calls on one handle share the workspace: order them on one
  * stream.  ar_ffn_forward calls share nothing.
@@ -513,7 +513,8 @@ size_t ar_ffn_scratch_bytes(ar_ffn_t h, const void* x, size_t ldx, const void* w
  *   dw_gate, dw_up   both NULL: not computed
  * Sums in fp32, outputs rounded once.  dgate and dup are rounded to dtype
  * between the two steps, since they are operands of 16-bit tensor-core
- * products.  The gradients are written, not added to what the outputs held.
+ * products; for at most 64 tokens they are kept as the sum of two numbers of
+ * dtype (where rows start on 16 bytes, or scratch is given).  The gradients are written, not added to what the outputs held.
  * tokens = 0 writes zeros to dw_gate and dw_up.
  * Errors: AR_ERR_INVALID_ARG (also tokens > max_tokens), AR_ERR_UNSUPPORTED
  * (handle made with train = 0), AR_ERR_CUDA. */

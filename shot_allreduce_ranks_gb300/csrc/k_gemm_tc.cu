@@ -76,6 +76,7 @@ struct Part {
   int64_t M, N, ldc;
   int steps;      // k steps of one segment
   int out_align;  // bytes that every output row start is a multiple of
+  int fold;       // rows come in blocks of 16 first and 16 second parts: added, M counts the sums
 };
 
 struct TcArgs {
@@ -273,7 +274,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         break;
       }
       fence_after_sync();
-      const int64_t m0 = ((int64_t)tile.m * CG + rank) * 128 + lane0;
+      const int fold = WHAT == kTcGrad ? part.fold : 0;
+      const int64_t m0 = (((int64_t)tile.m * CG + rank) * 128 + lane0) >> fold;
       const int n0 = tile.n * cols;
       const uint32_t acc = tmem + (lane0 << 16) + buf * 256;
 #pragma unroll 1
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // rows; a lane storing its own row would touch 32 lines at a time.
         const auto store = [&](int to, const float(&v)[32]) {
           if (part.out_align < 16) {
-            store_chunk<E>(a.c[to], part.ldc, m0, n0 + c, part.M, min(part.N, (int64_t)(n0 + cols)), v, part.out_align);
+            store_chunk<E>(a.c[to], part.ldc, m0, n0 + c, fold ? min(part.M, m0 + 16) : part.M, min(part.N, (int64_t)(n0 + cols)), v, part.out_align);
             return;
           }
           const uint32_t box = boxes + (stored & 1) * 2048, row = box + (uint32_t)lane * 64;
@@ -321,6 +323,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (fold) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += __shfl_down_sync(0xFFFFFFFFu, v[i], 16);
+          }
           store(which == 0 ? 0 : 1 + tile.z, v);
         }
       }
@@ -358,14 +364,15 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool make_part(TcArgs& a, TcMaps& maps, int which, int dtype, const GemmArgs& g, int cols, int planes, int cg,
                void* const* c, int outs) {
   Part& p = a.part[which];
-  p.M = g.M, p.N = g.N, p.ldc = g.ldc;
+  p.fold = g.tokens > 0;
+  p.M = p.fold ? g.tokens : g.M, p.N = g.N, p.ldc = g.ldc;
   if (!make_walk(&p.walk, ceil_div(g.M, 128 * cg), ceil_div(g.N, cols), planes, 16 / cg)) return false;
   p.steps = (int)ceil_div(g.K, kBK);
   uintptr_t bits = (uintptr_t)g.ldc * 2;
   for (int i = 0; i < outs; ++i) bits |= reinterpret_cast<uintptr_t>(c[i]);
   p.out_align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
   for (int i = 0; i < outs && p.out_align == 16; ++i)
-    if (c[i] && !make_map(&maps.c[c - a.c + i], dtype, c[i], g.M, g.N, g.ldc, 32, 32)) return false;
+    if (c[i] && !make_map(&maps.c[c - a.c + i], dtype, c[i], p.M, g.N, g.ldc, p.fold ? 16 : 32, 32)) return false;
   return true;
 }
 

@@ -23,11 +23,13 @@ __device__ __forceinline__ void pack_rows(const PackJob& j) {
        i += (int64_t)gridDim.x * kPackThreads) {
     const int64_t row = total >> 32 ? i / per_row : (int64_t)((uint32_t)i / (uint32_t)per_row);
     const int64_t col = (i - row * per_row) * G;
-    const char* p = static_cast<const char*>(j.from) + (row * j.ld_from + col) * B;
+    const int64_t source = j.twice ? row / 32 * 16 + row % 16 : row;
+    const char* p = static_cast<const char*>(j.from) + (source * j.ld_from + col) * B;
+    const int64_t cols = j.twice && source >= j.twice ? 0 : j.cols;
     uint32_t w[4] = {};
 #pragma unroll
     for (int k = 0; k < G; ++k)
-      if (col + k < j.cols) {
+      if (col + k < cols) {
         const uint32_t v = B == 2 ? *reinterpret_cast<const uint16_t*>(p + 2 * k) : *reinterpret_cast<const uint8_t*>(p + k);
         w[k * B / 4] |= v << (8 * (k * B % 4));
       }
@@ -61,19 +63,20 @@ template <class E, int ACT, bool VEC>
 __global__ void __launch_bounds__(kGateThreads)
     k_gate_grad(const char* gate, const char* up, const char* dout, int64_t ldo, char* dgate,
                 char* dup, int64_t ldw, int64_t rows, int64_t cols, int64_t groups_per_row,
-                const __grid_constant__ PackJobs jobs) {
+                int two_parts, const __grid_constant__ PackJobs jobs) {
   pdl_enter();
   if (blockIdx.y > 0) {
     pack_rows<2>(jobs.job[blockIdx.y - 1]);
     return;
   }
-  const int64_t total = rows * groups_per_row;
+  const int64_t total = (two_parts ? (rows + 15) / 16 * 16 : rows) * groups_per_row;
   for (int64_t i = (int64_t)blockIdx.x * kGateThreads + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * kGateThreads) {
     const int64_t row = total >> 32 ? i / groups_per_row : (int64_t)((uint32_t)i / (uint32_t)groups_per_row);
     const int64_t col = (i - row * groups_per_row) * 8;
-    const int64_t from = (row * ldo + col) * 2, to = (row * ldw + col) * 2;
-    const int n = (int)(cols - col < 8 ? cols - col : 8);
+    const int64_t from = (row * ldo + col) * 2;
+    const int64_t to = ((two_parts ? two_part_row(row) : row) * ldw + col) * 2;
+    const int n = row >= rows ? 0 : (int)(cols - col < 8 ? cols - col : 8);
     uint32_t gw[4] = {}, uw[4] = {}, dw[4] = {};
     if (VEC && n == 8) {
       const uint4 a = ld_v4_stream(gate + from), b = ld_v4_stream(up + from),
@@ -90,30 +93,38 @@ __global__ void __launch_bounds__(kGateThreads)
           dw[k >> 1] |= ld_elem<2>(dout + from + 2 * k) << (16 * (k & 1));
         }
     }
-    uint32_t og[4], ou[4];
+    uint32_t og[4], ou[4], rg[4], ru[4];  // rounded, and what that left
+    const auto rest = [](float v, float rounded) { return fabsf(rounded) < INFINITY ? v - rounded : 0.0f; };
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float f0, s0, f1, s1;
       act_slope<ACT>(E::lo(gw[k]), f0, s0);
       act_slope<ACT>(E::hi(gw[k]), f1, s1);
       const float d0 = E::lo(dw[k]), d1 = E::hi(dw[k]);
-      og[k] = E::pack(d0 * E::lo(uw[k]) * s0, d1 * E::hi(uw[k]) * s1);
-      ou[k] = E::pack(d0 * f0, d1 * f1);
+      const float g0 = d0 * E::lo(uw[k]) * s0, g1 = d1 * E::hi(uw[k]) * s1, u0 = d0 * f0, u1 = d1 * f1;
+      og[k] = E::pack(g0, g1);
+      ou[k] = E::pack(u0, u1);
+      rg[k] = E::pack(rest(g0, E::lo(og[k])), rest(g1, E::hi(og[k])));
+      ru[k] = E::pack(rest(u0, E::lo(ou[k])), rest(u1, E::hi(ou[k])));
     }
     // The workspace row is ldw = cols rounded up to 8, so a whole group fits;
     // what lies past cols is never read.
     st_v4_stream(dgate + to, make_uint4(og[0], og[1], og[2], og[3]));
     st_v4_stream(dup + to, make_uint4(ou[0], ou[1], ou[2], ou[3]));
+    if (two_parts) {
+      st_v4_stream(dgate + to + 32 * ldw, make_uint4(rg[0], rg[1], rg[2], rg[3]));
+      st_v4_stream(dup + to + 32 * ldw, make_uint4(ru[0], ru[1], ru[2], ru[3]));
+    }
   }
 }
 
 template <class E, int ACT>
 cudaError_t gate_grad(const void* gate, const void* up, const void* dout, int64_t ldo, void* dgate,
-                      void* dup, int64_t ldw, int64_t rows, int64_t cols, const PackJob* jobs, int count,
-                      int num_sms, cudaStream_t s) {
+                      void* dup, int64_t ldw, int64_t rows, int64_t cols, bool two_parts, const PackJob* jobs,
+                      int count, int num_sms, cudaStream_t s) {
   const int64_t gpr = (cols + 7) / 8;
   PackJobs all = {};
-  const int64_t pack = pack_ctas(jobs, count, 2, &all), gate_ctas = (rows * gpr + kGateThreads - 1) / kGateThreads;
+  const int64_t pack = pack_ctas(jobs, count, 2, &all), gate_ctas = ((rows + 15) * gpr + kGateThreads - 1) / kGateThreads;
   const int64_t want = pack > gate_ctas ? pack : gate_ctas, cap = (int64_t)num_sms * 8;
   const dim3 grid((unsigned)(want < cap ? want : cap), (unsigned)(1 + count));
   const bool vec = ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up) |
@@ -121,7 +132,7 @@ cudaError_t gate_grad(const void* gate, const void* up, const void* dout, int64_
   auto* k = vec ? k_gate_grad<E, ACT, true> : k_gate_grad<E, ACT, false>;
   return launch_op(k, grid, kGateThreads, 0, 1, s, static_cast<const char*>(gate),
                    static_cast<const char*>(up), static_cast<const char*>(dout), ldo,
-                   static_cast<char*>(dgate), static_cast<char*>(dup), ldw, rows, cols, gpr, all);
+                   static_cast<char*>(dgate), static_cast<char*>(dup), ldw, rows, cols, gpr, two_parts ? 1 : 0, all);
 }
 
 // ---------------------------------------------------------------------------
@@ -231,14 +242,15 @@ cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_
 
 cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
                              int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,
-                             int64_t cols, const PackJob* jobs, int count, int num_sms, cudaStream_t s) {
+                             int64_t cols, bool two_parts, const PackJob* jobs, int count, int num_sms,
+                             cudaStream_t s) {
   if (dtype == AR_BF16)
     return act == AR_ACT_SILU
-               ? gate_grad<Bf16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s)
-               : gate_grad<Bf16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s);
+               ? gate_grad<Bf16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, two_parts, jobs, count, num_sms, s)
+               : gate_grad<Bf16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, two_parts, jobs, count, num_sms, s);
   return act == AR_ACT_SILU
-             ? gate_grad<F16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s)
-             : gate_grad<F16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, jobs, count, num_sms, s);
+             ? gate_grad<F16, AR_ACT_SILU>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, two_parts, jobs, count, num_sms, s)
+             : gate_grad<F16, AR_ACT_GELU_TANH>(gate, up, dout, ldo, dgate, dup, ldw, rows, cols, two_parts, jobs, count, num_sms, s);
 }
 
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,

@@ -13,7 +13,9 @@ struct ar_ffn_ctx {
   int dtype = AR_BF16, act = AR_ACT_SILU;
   int device = 0, num_sms = 0;
   size_t ldw = 0;         // workspace leading dimension: width rounded up to 16 bytes
-  char* work = nullptr;   // dgate, then dup: max_tokens x ldw each
+  size_t ldx = 0;         // hidden rounded up likewise
+  size_t rows = 0;        // of dgate and of dup
+  char* work = nullptr;   // dgate, dup: rows x ldw each; x for two-part rows: up to 128 x ldx
 };
 
 namespace {
@@ -21,6 +23,10 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr size_t kMaxElems = (size_t)1 << 40;  // of a matrix: more than the memory holds
 constexpr size_t kMaxSize = (size_t)1 << 30;  // the sizes a handle is made for
+// Up to this many tokens the gradients of the pre-activations reach the products
+// in two parts: there the rows of a tile are not filled otherwise, so it costs
+// no instruction, and with few values the rounding of each shows most.
+constexpr size_t kTwoPartTokens = 64;
 
 bool half_type(int dtype) { return dtype == AR_BF16 || dtype == AR_FP16; }
 bool any_type(int dtype) { return half_type(dtype) || dtype == AR_FP32; }
@@ -76,7 +82,7 @@ ar_status_t plan_pack(Rows* m, int count, size_t elem, void* scratch, size_t scr
   for (int i = 0; i < count; ++i) {
     if (on_16(m[i], elem)) continue;
     const size_t ld = packed_ld(m[i], elem);
-    jobs[(*n)++] = {m[i].p, to, (int64_t)m[i].rows, (int64_t)m[i].cols, (int64_t)m[i].ld, (int64_t)ld};
+    jobs[(*n)++] = {m[i].p, to, (int64_t)m[i].rows, (int64_t)m[i].cols, (int64_t)m[i].ld, (int64_t)ld, 0};
     m[i].p = to;
     m[i].ld = ld;
     to += m[i].rows * ld * elem;
@@ -174,8 +180,11 @@ ar_status_t ar_ffn_create(size_t max_tokens, size_t hidden, size_t width, int dt
   h->max_tokens = max_tokens, h->hidden = hidden, h->width = width;
   h->dtype = dtype, h->act = activation, h->device = dev, h->num_sms = sms;
   h->ldw = (width + 7) / 8 * 8;
+  h->ldx = (hidden + 7) / 8 * 8;
   if (train) {
-    const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->work), 4 * max_tokens * h->ldw);
+    const size_t two = (size_t)ar::two_part_rows((int64_t)(max_tokens < kTwoPartTokens ? max_tokens : kTwoPartTokens));
+    h->rows = max_tokens > two ? max_tokens : two;
+    const cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->work), 4 * h->rows * h->ldw + 2 * two * h->ldx);
     if (e != cudaSuccess) {
       cudaGetLastError();
       delete h;
@@ -255,6 +264,9 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
     return AR_ERR_INVALID_ARG;
   if (!dx && !dw_gate) return AR_OK;
 
+  char* dgate = h->work;
+  char* dup = h->work + 2 * h->rows * h->ldw;
+  char* x_twice = h->work + 4 * h->rows * h->ldw;
   // dx wants the weights, the weights' gradients want x.
   Rows m[3];
   operands(h, x, ldx, w_gate, w_up, ldw, tokens, m);
@@ -262,10 +274,6 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
   int copies = 0;
   Rows* const from = dw_gate ? m : m + 1;
   if (ar_status_t st = plan_pack(from, dx ? (dw_gate ? 3 : 2) : 1, 2, scratch, scratch_bytes, jobs, &copies)) return st;
-  char* dgate = h->work;
-  char* dup = h->work + 2 * h->max_tokens * h->ldw;
-  cudaError_t e = ar::launch_gate_grad(h->dtype, h->act, gate, up, dout, (int64_t)ldo, dgate, dup,
-                                       (int64_t)h->ldw, (int64_t)tokens, (int64_t)F, jobs, copies, h->num_sms, s);
   ar::GemmArgs gx = {}, gw = {};
   gx.a0 = gw.a0 = dgate, gx.a1 = gw.a1 = dup, gx.lda = gw.lda = (int64_t)h->ldw;
   gx.b0 = m[1].p, gx.b1 = m[2].p, gx.ldb = (int64_t)m[1].ld, gx.ldb1 = (int64_t)m[2].ld;
@@ -275,6 +283,20 @@ ar_status_t ar_ffn_backward(ar_ffn_t h, const void* x, size_t ldx, const void* w
   gw.c0 = dw_gate, gw.c1 = dw_up, gw.ldc = (int64_t)lddw;
   gw.M = (int64_t)F, gw.N = (int64_t)K, gw.K = (int64_t)tokens;
   const bool tc_x = dx && ar::gemm_tc_takes(ar::kGemmDx, gx), tc_w = dw_gate && ar::gemm_tc_takes(ar::kGemmDw, gw);
+  const bool two_parts = tokens <= kTwoPartTokens && tc_x == (dx != nullptr) && tc_w == (dw_gate != nullptr);
+  if (two_parts) {
+    gx.tokens = (int64_t)tokens;
+    gx.M = gw.K = ar::two_part_rows((int64_t)tokens);
+    if (dw_gate) {  // x beside both parts, from where the caller has it
+      int at = 0;
+      while (at < copies && jobs[at].to != m[0].p) ++at;
+      copies += at == copies;
+      jobs[at] = {x, x_twice, gw.K, (int64_t)K, (int64_t)ldx, (int64_t)h->ldx, (int64_t)tokens};
+      gw.b0 = x_twice, gw.ldb = (int64_t)h->ldx;
+    }
+  }
+  cudaError_t e = ar::launch_gate_grad(h->dtype, h->act, gate, up, dout, (int64_t)ldo, dgate, dup, (int64_t)h->ldw,
+                                       (int64_t)tokens, (int64_t)F, two_parts, jobs, copies, h->num_sms, s);
   if (e == cudaSuccess && (tc_x || tc_w))
     e = ar::launch_grad_tc(h->dtype, tc_x ? &gx : nullptr, tc_w ? &gw : nullptr, h->num_sms, s);
   if (e == cudaSuccess && dx && !tc_x) e = ar::launch_gemm_any(ar::kGemmDx, h->dtype, gx, s);

@@ -56,6 +56,9 @@ struct GemmArgs {
   int64_t lda, ldb, ldb1, ldc;  // elements between rows (ldb1: b1's)
   int64_t M, N, K;
   int act;                // ar_activation_t (kGemmGated)
+  // kGemmDx on two-part rows (see launch_gate_grad): the tokens, whose results are
+  // the sums of both parts' rows; 0: rows are tokens.
+  int64_t tokens;
 };
 
 // On tcgen05, for operands that a tensor map can describe; gemm_tc_error reads
@@ -93,15 +96,23 @@ struct PackJob {
   const void* from;
   void* to;
   int64_t rows, cols, ld_from, ld_to;  // elements
+  int64_t twice;  // 0, or the source's rows, each copied to both rows of its token in two-part rows
 };
 cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_sms, cudaStream_t s);
 
-// dgate = dout * up * act'(gate), dup = dout * act(gate), rounded to the
-// element type (the operands of the tensor cores' products); and the copies of
-// `jobs`, 16-bit matrices, in the same launch.
+// dgate = dout * up * act'(gate), dup = dout * act(gate), the operands of the
+// tensor cores' products, rounded to the element type; and the copies of `jobs`,
+// 16-bit matrices, in the same launch.
+// two_parts: each value as the sum of two numbers of the element type, the
+// second what the first's rounding left, so that about 16 (bfloat16) or 22
+// (float16) bits reach the products.  Token t's first parts are row 32 (t / 16) + t % 16, its
+// second parts 16 rows on; rows without a token are zeros.
+constexpr int64_t two_part_rows(int64_t tokens) { return (tokens + 15) / 16 * 32; }
+__host__ __device__ constexpr int64_t two_part_row(int64_t t) { return (t / 16) * 32 + t % 16; }
 cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* up, const void* dout,
                              int64_t ldo, void* dgate, void* dup, int64_t ldw, int64_t rows,
-                             int64_t cols, const PackJob* jobs, int count, int num_sms, cudaStream_t s);
+                             int64_t cols, bool two_parts, const PackJob* jobs, int count, int num_sms,
+                             cudaStream_t s);
 
 struct DropoutArgs {
   const void* x;

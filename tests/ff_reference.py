@@ -47,9 +47,14 @@ def forward(x, wg, wu, act):
     return (h, g, u), (ef * u.abs() + f.abs() * eu + ef * eu + E32 * h.abs(), eg, eu)
 
 
-def backward(x, wg, wu, gate, up, dout, act):
-    """((dx, dwg, dwu), their bounds without the final rounding)."""
+def backward(x, wg, wu, gate, up, dout, act, two_parts=False):
+    """((dx, dwg, dwu), their bounds without the final rounding).
+
+    two_parts: the pre-activations' gradients are held as the sum of two 16-bit
+    numbers, so that what remains of their rounding is its square.
+    """
     r, tiny = U[x.dtype], TINY[x.dtype]
+    r = r * r if two_parts else r
     x, wg, wu, gate, up, dout = (t.double() for t in (x, wg, wu, gate, up, dout))
     f, df, ef, edf = activation(gate, act)
     a, b = dout * up * df, dout * f

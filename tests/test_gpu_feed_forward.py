@@ -138,6 +138,26 @@ def test_backward_many_tiles_and_deep_sums(ar, size):
     run_backward(ar, *size, FP16, "silu", 0, 0, seed=2)
 
 
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 33, 64])
+@pytest.mark.parametrize("K,F,dtype,act", [(136, 72, BF16, "silu"), (131, 77, FP16, "gelu"), (520, 1032, FP16, "silu")])
+def test_gradients_of_a_few_tokens_in_two_parts(ar, M, K, F, dtype, act):
+    """Up to 64 tokens dgate and dup reach the products in two 16-bit parts: what is
+    left is the outputs' own rounding and the sums'."""
+    g = gen(M + K)
+    x, wg, wu = normal(g, (M, K), dtype), normal(g, (F, K), dtype, K ** -0.5), normal(g, (F, K), dtype, K ** -0.5)
+    gate, up, dout = normal(g, (M, F), dtype), normal(g, (M, F), dtype), normal(g, (M, F), dtype)
+    outs = [Framed(*s, dtype, 3, 1) for s in ((M, K), (F, K), (F, K))]
+    with ar.GatedFFN(200, K, F, dtype=dtype, activation=act, train=True) as ffn:
+        # the workspace holds another call's values first
+        big = normal(g, (200, F), dtype, float("inf"))
+        ffn.backward(normal(g, (200, K), dtype), wg, wu, big, big, big)
+        got = ffn.backward(x, wg, wu, gate, up, dout, *(f.t for f in outs))
+    want, bounds = ref.backward(x, wg, wu, gate, up, dout, act, two_parts=True)
+    for a, b, e, what in zip(got, want, bounds, ("dx", "dw_gate", "dw_up")):
+        ref.assert_close(a, b, e, what)
+    assert all(f.intact() for f in outs)
+
+
 def test_backward_parts(ar):
     run_backward(ar, 70, 72, 136, BF16, "silu", 0, 0, need_dx=False)
     run_backward(ar, 70, 72, 136, BF16, "silu", 0, 0, need_dw=False)
