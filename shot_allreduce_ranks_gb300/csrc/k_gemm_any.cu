@@ -9,6 +9,11 @@
 // 8-bit integers become fp16 on the way into shared memory: fp16 holds them
 // exactly, their products are exact in fp32, and so are the sums while they
 // stay below 2^24 (always so for K <= 1024).
+//
+// It makes what the tensor-map kernels cannot read and the caller gave no scratch
+// to lay out for them.  Measured on one GB300: 46 TFLOP/s on large sizes, a
+// thirtieth of theirs (gradients at 1001 x 1031 -> 777: 153 us, 24 with scratch);
+// bound by its element loads.
 #include "ops_internal.cuh"
 
 namespace ar {

@@ -9,6 +9,11 @@
 // and of its token and uses them as they come: no shared memory, no shuffles.
 // The gate's and the up projection's sums of one output land in one lane.  The
 // warps' sums are joined in shared memory in a fixed order.
+//
+// Measured on one GB300: one token 8192 -> 3584 (117 MB of weights) 18.8-20 us,
+// 5.9-6.2 TB/s, 87-92% of a copy's rate; 8 tokens 21.6 us; 8-bit, one token 3584
+// -> 8192 (29 MB) 8.6 us.  Four-warp CTAs, and register limits for four CTAs an
+// SM, were slower at most sizes (24.5 and 24.6 against 20.4 us for the first).
 #include "ops_internal.cuh"
 
 namespace ar {

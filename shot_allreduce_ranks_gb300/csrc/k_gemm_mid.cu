@@ -9,6 +9,12 @@
 // SMs, so a cluster of KS CTAs splits a tile's k: each takes every KS-th part,
 // and at the end sends its sums to the CTAs' shared memory, quarter of the rows
 // by quarter, where they are added in the order of the parts.
+//
+// Bound by the weights' way into the SMs (about 64 bytes a clock each), and below
+// that by launch, set-up and two trips through the cluster, about 7 us.  Measured
+// on one GB300 (bf16, replayed graph): 13 tokens 5120 -> 2048 10.3 us (42 MB of
+// weights, 4.1 TB/s), 64 tokens 11.5 us (25 us by tiles of 128 padded tokens), 64
+// tokens 8192 -> 3584 24 us (117 MB, 4.9 TB/s; was 40), 128 tokens 26 us.
 #include "tc_device.cuh"
 
 namespace ar {

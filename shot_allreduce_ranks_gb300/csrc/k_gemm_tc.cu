@@ -18,6 +18,22 @@
 // (MN-major), and the two weight gradients read both operands so: nothing is
 // transposed in memory.  All three are one launch: one kind's last round of tiles
 // would leave SMs idle, which the other's tiles fill.
+//
+// What bounds it.  A 256x256 tile's step of 64 k keeps a pair's tensor pipes busy
+// for 512 clocks, and each SM's shared memory for as long: 32 KB copied in and 32
+// KB read by the instruction, at 128 bytes a clock.  (A CTA by itself, 128x256,
+// copies in 48 KB a step and measured 613 us where the pairs take 501.)  Stores
+// come on top, 64 KB written and read again a tile, which shows where the
+// contraction is short.  Measured on one GB300 (bf16, replayed graph):
+//   forward with saved pre-activations, 8192 tokens x 8192 -> 3584: 490-510 us,
+//   1,900-1,960 TFLOP/s, tensor pipe active 94% of the time (a library product
+//   of 8192^3 reached 1,924); in a loop under the power limit 560 us;
+//   forward 440 x 5120 -> 1736: 21 us, of which about 8 are launch, set-up, the
+//   first copies and the last tile's stores;
+//   gradients 4096 x 8192 -> 3584: 545 us (1,770 TFLOP/s); 512 x 8192 -> 3584: 89
+//   us (tensor pipe active 60%: the weights' tiles have eight steps each).
+// Measured and left out: clusters of four that share A by multicast (the same
+// time: an SM's own intake binds, and only 36 of 38 such clusters fit).
 #include <math.h>
 
 #include "tc_device.cuh"
@@ -131,6 +147,7 @@ struct Shape {
 template <int WHAT, class E, int ACT, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_gemm_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
+  static_assert(WHAT == kTcGrad || CG == 2, "the gated product is made by pairs");
   using S = Shape<CG>;
   constexpr bool kBmn = WHAT == kTcGrad;
   const int cols = WHAT == kTcGated ? a.bn / 2 : a.bn;  // output columns of a tile
@@ -205,12 +222,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (WHAT == kTcGated) {
             // The pair's first CTA holds the gate's rows, its second the up projection's.
-            if (CG == 2) {
-              load_box<CG>(sb, &maps.b[rank], k0, n0, bar);
-            } else {
-              load_box<CG>(sb, &maps.b[0], k0, n0, bar);
-              load_box<CG>(sb + (uint32_t)a.bn * 64, &maps.b[1], k0, n0, bar);
-            }
+            load_box<CG>(sb, &maps.b[rank], k0, n0, bar);
           } else {
             const CUtensorMap* mb = &maps.b[dw ? 2 : up];
             for (int c = 0; c < chunks; ++c)
@@ -404,8 +416,9 @@ TileCost tile_cost(int64_t steps, int bn, int64_t b_rows, bool aligned) {
   return {(double)steps * fmax(2.0 * bn, 2.0 * (double)(128 + b_rows)), (aligned ? 10.0 : 40.0) * bn};
 }
 
-template <class E, int ACT, int CG>
+template <class E, int ACT>
 cudaError_t launch_gated(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
+  constexpr int CG = 2;
   const int64_t slots = num_sms / CG;
   int bn = 256;
   double least = 1e300;
@@ -480,14 +493,11 @@ cudaError_t launch_grad(int dtype, const GemmArgs* dx, const GemmArgs* dw, int n
 
 template <class E>
 cudaError_t gated_type(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
-  // One CTA for what its 128 rows hold, pairs above.
-  if (g.M <= 128)
-    return g.act == AR_ACT_SILU ? launch_gated<E, AR_ACT_SILU, 1>(dtype, g, num_sms, s)
-                                : launch_gated<E, AR_ACT_GELU_TANH, 1>(dtype, g, num_sms, s);
-  return g.act == AR_ACT_SILU ? launch_gated<E, AR_ACT_SILU, 2>(dtype, g, num_sms, s)
-                              : launch_gated<E, AR_ACT_GELU_TANH, 2>(dtype, g, num_sms, s);
+  return g.act == AR_ACT_SILU ? launch_gated<E, AR_ACT_SILU>(dtype, g, num_sms, s)
+                              : launch_gated<E, AR_ACT_GELU_TANH>(dtype, g, num_sms, s);
 }
 
+// Pairs, unless every matrix has no more rows than one CTA's tile.
 template <class E>
 cudaError_t grad_type(int dtype, const GemmArgs* dx, const GemmArgs* dw, int num_sms, cudaStream_t s) {
   if ((!dx || dx->M <= 128) && (!dw || dw->M <= 128)) return launch_grad<E, 1>(dtype, dx, dw, num_sms, s);

@@ -58,7 +58,8 @@ int64_t pack_ctas(const PackJob* jobs, int count, int elem_bytes, PackJobs* all)
 // an element, bound by memory.  A thread takes eight columns of a row at a
 // time; the workspace rows are 16-byte aligned, the caller's need not be.  The
 // rows of CTAs past the first copy the operands that the products want laid out:
-// neither waits for the other, and a launch costs about 2 us.
+// neither waits for the other, and a launch costs about 2 us.  512 x 3584: 6 us
+// under a profiler from cold caches, of a call's 89.
 template <class E, int ACT, bool VEC>
 __global__ void __launch_bounds__(kGateThreads)
     k_gate_grad(const char* gate, const char* up, const char* dout, int64_t ldo, char* dgate,
@@ -165,7 +166,8 @@ __device__ __forceinline__ uint32_t quantized(float x, float by, bool finite) {
 // A CTA a row, read once: each thread keeps up to kHeld groups of 16 bytes
 // (8192 16-bit columns in all) in registers between the maximum and the
 // division.  Longer rows, and rows that do not start on 16 bytes, are read
-// twice, an element at a time (HELD false).
+// twice, an element at a time (HELD false).  One row of 3584: 3.6 us from cold
+// caches; 440 rows of 2048: 4 us; latency of two dependent steps and the launch.
 constexpr int kHeld = 4;
 
 template <class E, bool HELD>

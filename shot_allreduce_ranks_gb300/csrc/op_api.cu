@@ -11,7 +11,7 @@
 struct ar_ffn_ctx {
   size_t max_tokens = 0, hidden = 0, width = 0;
   int dtype = AR_BF16, act = AR_ACT_SILU;
-  int device = 0, num_sms = 0;
+  int num_sms = 0;
   size_t ldw = 0;         // workspace leading dimension: width rounded up to 16 bytes
   size_t ldx = 0;         // hidden rounded up likewise
   size_t rows = 0;        // of dgate and of dup
@@ -178,7 +178,7 @@ ar_status_t ar_ffn_create(size_t max_tokens, size_t hidden, size_t width, int dt
   ar_ffn_ctx* h = new (std::nothrow) ar_ffn_ctx;
   if (!h) return AR_ERR_OOM;
   h->max_tokens = max_tokens, h->hidden = hidden, h->width = width;
-  h->dtype = dtype, h->act = activation, h->device = dev, h->num_sms = sms;
+  h->dtype = dtype, h->act = activation, h->num_sms = sms;
   h->ldw = (width + 7) / 8 * 8;
   h->ldx = (hidden + 7) / 8 * 8;
   if (train) {
