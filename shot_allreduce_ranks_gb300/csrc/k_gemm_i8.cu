@@ -21,11 +21,12 @@
 // 256 rows, each converting its own 128 rows of x and half of the rows of w.
 //
 // Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 284-287 us, 1,920
-// TFLOP/s counted as products, what a 16-bit library product reaches here (with x
-// in shared memory too: 365; with converters that own one operand stage each:
-// 395; before arrivals on the pair's barriers were ordered at the CTA's scope:
-// 365); 440 x 2048 -> 5120 14 us, of which about 7 are launch, set-up and the
-// last tile.
+// TFLOP/s counted as products, what a 16-bit library product reaches here (315
+// us in a loop under the power limit).  It was 395 us with x in shared memory,
+// 387 with x in tensor memory, 365 with eight operand stages instead of four, and
+// 287 with the arrivals on the pair's barriers ordered at the CTA's scope.
+// 440 x 2048 -> 5120: 14 us, of which about 7 are launch, set-up and the last
+// tile.
 #include "tc_device.cuh"
 
 namespace ar {

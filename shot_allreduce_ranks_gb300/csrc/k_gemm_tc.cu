@@ -27,7 +27,8 @@
 // contraction is short.  Measured on one GB300 (bf16, replayed graph):
 //   forward with saved pre-activations, 8192 tokens x 8192 -> 3584: 490-510 us,
 //   1,900-1,960 TFLOP/s, tensor pipe active 94% of the time (a library product
-//   of 8192^3 reached 1,924); in a loop under the power limit 560 us;
+//   of 8192^3 reached 1,924); in a loop the power limit takes the clock from
+//   2,070 to about 1,470 MHz and the time to 560 us;
 //   forward 440 x 5120 -> 1736: 21 us, of which about 8 are launch, set-up, the
 //   first copies and the last tile's stores;
 //   gradients 4096 x 8192 -> 3584: 545 us (1,770 TFLOP/s); 512 x 8192 -> 3584: 89
