@@ -20,13 +20,18 @@
 // pair's barriers and the instruction back to a free stage.  A pair of CTAs (CG = 2) shares one instruction over
 // 256 rows, each converting its own 128 rows of x and half of the rows of w.
 //
+// Up to 128 tokens (SWAP, CG = 1) would leave rows of x empty: there w's rows
+// are the instruction's A and the tokens its columns, one tile of 128 channels to
+// a cluster whose KS CTAs split k, and the sums are sent to the CTAs' shared
+// memory, quarter of the channels by quarter, and added in the order of the parts.
+//
 // Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 284-287 us, 1,920
 // TFLOP/s counted as products, what a 16-bit library product reaches here (315
 // us in a loop under the power limit).  It was 395 us with x in shared memory,
 // 387 with x in tensor memory, 365 with eight operand stages instead of four, and
 // 287 with the arrivals on the pair's barriers ordered at the CTA's scope.
 // 440 x 2048 -> 5120: 14 us, of which about 7 are launch, set-up and the last
-// tile.
+// tile.  64 tokens 3584 -> 8192: 13.4 us (16.9 by padded tiles of tokens).
 #include "tc_device.cuh"
 
 namespace ar {
@@ -52,15 +57,73 @@ __device__ uint32_t g_i8_error;  // set by a wait that gave up
 struct I8Args {
   GemmArgs g;
   TileWalk walk;
-  int steps;      // of 64 k, an even number
+  int units;      // of 128 k
   int bn;         // columns of a tile, a multiple of 32
   int out_align;
 };
 
-template <class E, int CG>
+// The end of a tile of 128 channels and up to 128 tokens, by all of the CTA's
+// threads: sums go to [part][quarter here][token][channel] in the CTA that
+// finishes that quarter of the channels, in the rings' memory, which is idle by
+// then, and from there, scaled, to y.
+template <class E, int KS>
+__device__ __forceinline__ void join_parts(const I8Args& a, uint32_t room, uint32_t tmem, uint32_t done, uint32_t tile,
+                                           uint32_t part, bool any, volatile uint32_t* dead) {
+  constexpr int kHere = 4 / KS;  // quarters that a CTA finishes
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, M = (int)a.g.M;
+  if (!bar_wait(done, 0, dead) && lane == 0) atomicExch(&g_i8_error, 1u);
+  fence_after_sync();
+  __syncthreads();
+  if (KS > 1) cluster_sync();  // every CTA's rings are idle
+  const uint32_t own = room + (uint32_t)((int)part * kHere + quarter % kHere) * (128 * 128);
+  const uint32_t to = KS > 1 ? map_to_cta(own, (uint32_t)(quarter / kHere)) : own;
+  // Columns of 32 by turns: warps 4 i + quarter.
+  for (int c = (warp >> 2) * 32; c < M; c += (kI8Threads / 128) * 32) {
+    if (warp >= kI8Threads / 128 * 4) break;  // the last, incomplete set of four warps
+    uint32_t r[32];
+    __syncwarp();
+    tmem_load32(r, tmem + ((uint32_t)quarter << 21) + c);
+    tmem_wait_load32(r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < M) {
+        const uint32_t at = to + (uint32_t)((c + i) * 32 + lane) * 4;
+        // A part of no steps adds nothing (its tensor memory was never written).
+        const float v = any ? __uint_as_float(r[i]) : 0.0f;
+        if (KS > 1)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+        else
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+      }
+  }
+  fence_before_sync();
+  if (KS > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  for (int e = warp; e < kHere * M; e += kI8Threads / 32) {
+    const int q = e / M, m = e % M;
+    const int64_t n = (int64_t)tile * 128 + ((int)part * kHere + q) * 32 + lane;
+    float sum = 0.0f;
+#pragma unroll
+    for (int p = 0; p < KS; ++p) {
+      float v;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(v) : "r"(room + (uint32_t)(p * kHere + q) * (128 * 128) + (uint32_t)(m * 32 + lane) * 4));
+      sum = p ? sum + v : v;
+    }
+    if (n < a.g.N)
+      static_cast<uint16_t*>(a.g.c0)[(int64_t)m * a.g.ldc + n] = (uint16_t)E::from_f32(sum * a.g.sm[m] * a.g.sn[n]);
+  }
+}
+
+// map_x and map_w: the matrices whose rows are the instruction's rows and its
+// columns (SWAP: w and x).
+template <class E, int CG, bool SWAP, int KS>
 __global__ void __launch_bounds__(kI8Threads, 1)
     k_gemm_i8(const __grid_constant__ I8Args a, const __grid_constant__ CUtensorMap map_x,
               const __grid_constant__ CUtensorMap map_w) {
+  static_assert(SWAP == (CG == 1) && (SWAP || KS == 1), "");
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[2 * kSS + 2 * kOS + 5];
   __shared__ uint32_t tmem_slot;
@@ -74,6 +137,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int rows = 128 + a.bn / CG;  // of a stage: x, then w
   const uint32_t accs = a.bn <= (int)kAccStride ? 2 : 1;  // accumulators
+  const uint32_t part = KS > 1 ? cluster_rank() : 0;       // of k
+  const int u0 = (int)((int64_t)a.units * part / KS), u1 = (int)((int64_t)a.units * (part + 1) / KS);
+  const int steps = 2 * (u1 - u0);  // of 64 k
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSS; ++i) {
@@ -105,7 +171,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
   pdl_enter();  // nothing before this has touched global memory
-  const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+  // SWAP: a cluster makes one tile.
+  const uint32_t first = blockIdx.x / (CG * KS), stride = SWAP ? 1u << 30 : gridDim.x / CG;
 
   if (warp == 0) {
     if (elect_one()) {
@@ -114,7 +181,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       for (uint32_t t = first; t < a.walk.tiles && ok; t += stride) {
         const Tile tile = tile_at(a.walk, t);
         const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * a.bn + (int)rank * (a.bn / CG);
-        for (int s = 0; s < a.steps / 2; ++s, ++it) {
+        for (int s = u0; s < u1; ++s, ++it) {
           const uint32_t st = it % kSS;
           if (!(ok = bar_wait(taken + 8 * st, ((it / kSS) & 1) ^ 1, &dead))) break;
           const uint32_t dst = staging + st * kStaged, bar = landed + 8 * st;
@@ -135,7 +202,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const uint32_t buf = at % accs;
         if (!(ok = bar_wait(freed + 8 * buf, (at / accs & 1) ^ 1, &dead))) break;
         fence_after_sync();
-        for (int s = 0; s < a.steps; ++s, ++it) {
+        for (int s = 0; s < steps; ++s, ++it) {
           const uint32_t st = it % kOS;
           if (!(ok = bar_wait(ready + 8 * st, (it / kOS) & 1, &dead))) break;
           fence_after_sync();
@@ -154,7 +221,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         bar_wait_copies(drained, 0);
       }
     }
-  } else if (warp < 6) {
+  } else if (warp < 6 && !SWAP) {
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;
     uint32_t at = 0;
     for (uint32_t t = first; t < a.walk.tiles; t += stride, ++at) {
@@ -191,14 +258,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
       fence_before_sync();
       __syncwarp();
-      if (elect_one()) {
-        if (CG == 2)
-          bar_arrive_cluster(map_to_cta(freed + 8 * buf, 0));
-        else
-          bar_arrive(freed + 8 * buf);
-      }
+      if (elect_one()) bar_arrive_cluster(map_to_cta(freed + 8 * buf, 0));
     }
-  } else {
+  } else if (warp >= 6) {
     // Staged rows are 128 bytes whose 16-byte piece p lies at p ^ (row % 8), and
     // so are w's operand rows.  A step converts half of a staged row, pieces 4h ..
     // 4h + 3.  A thread takes a whole such row of x (eight lanes read eight
@@ -210,7 +272,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int lane = thread & 31, j = lane & 3, second = (lane >> 2) & 1;
     const int row0 = (thread >> 5) * 8 + (lane >> 3) + 4 * second;  // of w, + 8 kGroupWarps each time
     const int x_row = (warp & 3) * 32 + lane;
-    const int64_t total = (int64_t)(first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0) * a.steps;
+    const int64_t total = (int64_t)(first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0) * steps;
     bool ok = true;
     int64_t it = group;
     for (; it < total && ok; it += kGroups) {
@@ -281,28 +343,20 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
   }
   __syncwarp();
-  fence_before_sync();
-  __syncthreads();
-  if (CG == 2) cluster_sync();
+  if (SWAP) {
+    join_parts<E, KS>(a, operands, tmem, done, first, part, steps > 0, &dead);
+  } else {
+    fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+  }
   fence_after_sync();
   if (warp == 1) tmem_free<CG>(tmem, kI8TmemCols);
 }
 
-template <class E, int CG>
-cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
-  CUtensorMap mx, mw;
-  if (!tc_make_map(&mx, kMapU8, g.a0, g.M, g.K, g.lda, 128, 128) ||
-      !tc_make_map(&mw, kMapU8, g.b0, g.N, g.K, g.ldb, bn / CG, 128))
-    return cudaErrorInvalidValue;
-  I8Args a = {};
-  a.g = g;
-  if (!make_walk(&a.walk, (g.M + 128 * CG - 1) / (128 * CG), (g.N + bn - 1) / bn, 1, 16 / CG))
-    return cudaErrorInvalidConfiguration;
-  a.steps = (int)((g.K + 127) / 128) * 2;
-  a.bn = bn;
-  const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | (uintptr_t)g.ldc * 2;
-  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : out % 4 == 0 ? 4 : 2;
-  auto* kernel = k_gemm_i8<E, CG>;
+template <class E, int CG, bool SWAP, int KS>
+cudaError_t launch(const I8Args& a, const CUtensorMap& mx, const CUtensorMap& mw, unsigned ctas, cudaStream_t s) {
+  auto* kernel = k_gemm_i8<E, CG, SWAP, KS>;
   static bool raised[64];  // by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -310,32 +364,59 @@ cudaError_t launch(const GemmArgs& g, int bn, int num_sms, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kI8Smem);
   if (e != cudaSuccess) return e;
   raised[dev & 63] = dev < 64;
-  const uint32_t pairs = (uint32_t)(num_sms / CG);
-  const dim3 grid((a.walk.tiles < pairs ? a.walk.tiles : pairs) * CG);
-  return launch_op(kernel, grid, kI8Threads, kI8Smem, CG, s, a, mx, mw);
+  return launch_op(kernel, dim3(ctas), kI8Threads, kI8Smem, CG * KS, s, a, mx, mw);
 }
 
-// Columns of a tile: the number of rounds of tiles over the SMs times a round's
-// time, which is a step's traffic in shared memory at 128 bytes a clock (a row of
-// x 128 bytes, one of w 384) or its matrix instruction (2 clocks a column).
-int columns(const GemmArgs& g, int cg, int num_sms) {
-  const int64_t tm = (g.M + 128 * cg - 1) / (128 * cg), slots = num_sms / cg, steps = (g.K + 63) / 64;
-  int best = 32;
+// Pairs.  Columns of a tile: the number of rounds of tiles over the pairs times a
+// round's time, which is a step's traffic in shared memory at 128 bytes a clock
+// (a row of x 128 bytes, one of w 384) or its matrix instruction (2 clocks a column).
+template <class E>
+cudaError_t launch_pairs(const GemmArgs& g, int num_sms, cudaStream_t s) {
+  const int64_t tiles_m = (g.M + 255) / 256, pairs = num_sms / 2;
+  I8Args a = {};
+  a.g = g;
+  a.units = (int)((g.K + 127) / 128);
   double least = 1e300;
-  for (int bn = cg == 2 ? 256 : 128; bn >= 32; bn -= 32) {
-    const int64_t rounds = (tm * ((g.N + bn - 1) / bn) + slots - 1) / slots;
-    const double smem = 128.0 + 3.0 * bn / cg, step = smem > 2 * bn ? smem : 2 * bn, stores = 15.0 * bn;
+  for (int bn = 256; bn >= 32; bn -= 32) {
+    const int64_t rounds = (tiles_m * ((g.N + bn - 1) / bn) + pairs - 1) / pairs;
+    const double smem = 128.0 + 1.5 * bn, step = smem > 2 * bn ? smem : 2 * bn, stores = 15.0 * bn;
     // One accumulator: each tile's stores are waited for; two: the last tile's.
-    const double cost = (double)rounds * (steps * step + (bn > (int)kAccStride ? stores : 0)) + (bn > (int)kAccStride ? 0 : stores);
-    if (cost < least) least = cost, best = bn;
+    const bool one = bn > (int)kAccStride;
+    const double cost = (double)rounds * (2 * a.units * step + (one ? stores : 0)) + (one ? 0 : stores);
+    if (cost < least) least = cost, a.bn = bn;
   }
-  return best;
+  if (!make_walk(&a.walk, tiles_m, (g.N + a.bn - 1) / a.bn, 1, 8)) return cudaErrorInvalidConfiguration;
+  const uintptr_t out = reinterpret_cast<uintptr_t>(g.c0) | (uintptr_t)g.ldc * 2;
+  a.out_align = out % 32 == 0 ? 32 : out % 16 == 0 ? 16 : out % 4 == 0 ? 4 : 2;
+  CUtensorMap mx, mw;
+  if (!tc_make_map(&mx, kMapU8, g.a0, g.M, g.K, g.lda, 128, 128) ||
+      !tc_make_map(&mw, kMapU8, g.b0, g.N, g.K, g.ldb, a.bn / 2, 128))
+    return cudaErrorInvalidValue;
+  const unsigned slots = a.walk.tiles < (uint32_t)pairs ? a.walk.tiles : (unsigned)pairs;
+  return launch<E, 2, false, 1>(a, mx, mw, slots * 2, s);
+}
+
+// Up to 128 tokens: as many parts of k as fill the SMs.
+template <class E>
+cudaError_t launch_swapped(const GemmArgs& g, int num_sms, cudaStream_t s) {
+  const int64_t tiles = (g.N + 127) / 128;
+  I8Args a = {};
+  a.g = g;
+  a.units = (int)((g.K + 127) / 128);
+  a.bn = (int)((g.M + 31) / 32 * 32);
+  CUtensorMap mw, mx;
+  if (!make_walk(&a.walk, tiles, 1, 1, 1)) return cudaErrorInvalidConfiguration;
+  if (!tc_make_map(&mw, kMapU8, g.b0, g.N, g.K, g.ldb, 128, 128) ||
+      !tc_make_map(&mx, kMapU8, g.a0, g.M, g.K, g.lda, a.bn, 128))
+    return cudaErrorInvalidValue;
+  if (tiles * 4 <= num_sms && a.units >= 4) return launch<E, 1, true, 4>(a, mw, mx, (unsigned)tiles * 4, s);
+  if (tiles * 2 <= num_sms && a.units >= 2) return launch<E, 1, true, 2>(a, mw, mx, (unsigned)tiles * 2, s);
+  return launch<E, 1, true, 1>(a, mw, mx, (unsigned)tiles, s);
 }
 
 template <class E>
 cudaError_t launch_type(const GemmArgs& g, int num_sms, cudaStream_t s) {
-  if (g.M > 128) return launch<E, 2>(g, columns(g, 2, num_sms), num_sms, s);
-  return launch<E, 1>(g, columns(g, 1, num_sms), num_sms, s);
+  return g.M > 128 ? launch_pairs<E>(g, num_sms, s) : launch_swapped<E>(g, num_sms, s);
 }
 
 }  // namespace

@@ -104,14 +104,18 @@ ar_status_t pack(Rows* m, int count, size_t elem, void* scratch, size_t scratch_
 // of 2048 x 1024: 3.6 against 5.1 us, of 2048 x 2048: 5.4 against 5.2; 32 tokens
 // of 2048 x 1024: 4.8 against 5.5, of 2048 x 2048: 7.1 against 5.5), but not
 // for the eight tokens of one instruction (8192 x 3584: 21.3 against 22.3 us).
+// The 8-bit product likewise, at 2^28 and past 16 tokens (24 tokens of 5120 x
+// 2048: 8.3 against 8.4 us, of 8192 x 3584: 16.4 against 12.2; 16 tokens of that:
+// 11.9 against 11.5, of 2048 x 8192: 8.1 against 11.3).
 cudaError_t gemm(int mode, int dtype, const ar::GemmArgs& g, int num_sms, cudaStream_t s) {
-  const bool mid = ar::gemm_mid_takes(mode, g);
-  if (ar::gemm_few_takes(mode, g) &&
-      (!mid || g.M <= 8 || (double)g.M * (double)g.N * (double)g.K <= (double)(1 << 26)))
+  const bool mid = ar::gemm_mid_takes(mode, g), i8 = ar::gemm_i8_takes(mode, g);
+  const double work = (double)g.M * (double)g.N * (double)g.K;
+  if (ar::gemm_few_takes(mode, g) && ((!mid && !i8) || (mid ? g.M <= 8 || work <= (double)(1 << 26)
+                                                           : g.M <= 16 || work <= (double)(1 << 28))))
     return ar::launch_gemm_few(mode, dtype, g, s);
   if (mid) return ar::launch_gemm_mid(dtype, g, num_sms, s);
   if (ar::gemm_tc_takes(mode, g)) return ar::launch_gated_tc(dtype, g, num_sms, s);
-  if (ar::gemm_i8_takes(mode, g)) return ar::launch_gemm_i8(dtype, g, num_sms, s);
+  if (i8) return ar::launch_gemm_i8(dtype, g, num_sms, s);
   return ar::launch_gemm_any(mode, dtype, g, s);
 }
 

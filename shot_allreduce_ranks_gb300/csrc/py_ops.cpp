@@ -333,8 +333,12 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& x = tensor(a[0], "x");
     const int index = gpu_of(x, "x"), code = type_code(x.scalar_type(), "x", false);
     const int64_t ldx = matrix(x, "x", x.scalar_type(), index), rows = x.size(0), cols = x.size(1);
-    int64_t ldq;
-    const at::Tensor q = output(a[1], "q", at::kChar, index, rows, cols, x, &ldq);
+    int64_t ldq = (cols + 15) / 16 * 16;
+    // A new q's rows start on 16 bytes, as the product wants them.
+    const at::Tensor q = a[1] != Py_None ? output(a[1], "q", at::kChar, index, rows, cols, x, &ldq)
+                         : ldq == cols   ? fresh(rows, cols, at::kChar, x)
+                                         : fresh(rows, ldq, at::kChar, x).narrow(1, 0, cols);
+    if (rows <= 1 && a[1] == Py_None) ldq = cols;
     at::Tensor scale;
     if (a[2] == Py_None) {
       scale = at::empty({rows}, x.options().dtype(at::kFloat));

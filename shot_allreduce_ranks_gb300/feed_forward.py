@@ -123,7 +123,10 @@ def dropout_backward(dy, p: float, seed: int, sequence: int = 0, offset: int = 0
 
 
 def quantize_rows(x, q=None, scale=None, stream=None):
-    """``(q, scale)``: ``scale[i] = max |x[i]| / 127``, ``q = rint(x / scale)`` in int8."""
+    """``(q, scale)``: ``scale[i] = max |x[i]| / 127``, ``q = rint(x / scale)`` in int8.
+
+    The rows of a new ``q`` start on 16 bytes, so that ``linear_i8`` reads them as they are.
+    """
     if stream is not None:
         with torch.cuda.stream(stream):
             return _ops.quantize_rows(x, q, scale)
