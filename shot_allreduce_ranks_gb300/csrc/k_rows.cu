@@ -146,91 +146,137 @@ __device__ __forceinline__ uint32_t magnitude(uint32_t bits) {
   return __float_as_uint(E::to_f32(bits)) & 0x7FFFFFFFu;
 }
 
-// The largest of the CTA's values.
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* part) {
-  v = __reduce_max_sync(0xFFFFFFFFu, v);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
+// A row's divisor, 1 for a scale of 0, and its reciprocal.
+struct Divisor {
+  float by, inverse;
+  bool finite;  // no infinity or NaN in the row, which gives zeros
+  bool exact;   // below 2^-100, where the reciprocal could overflow: always divide
+};
+
+// rint(x / s), s = absmax / 127, with the division an IEEE one, rounded once.
+__device__ __forceinline__ uint32_t divided(float x, const Divisor& d) {
+  return (uint32_t)min(127, max(-127, __float2int_rn(__fdiv_rn(x, d.by)))) & 0xFFu;
+}
+
+// The same integers for a group of G values, mostly without dividing.  x times
+// the reciprocal is within 127 x 1.5 x 2^-23 < 3e-5 of the quotient, so only next
+// to a half can the two round differently, and a group with such a value is
+// divided.  Adding 1.5 x 2^23 rounds to an integer, ties to even, and leaves it in
+// the low bits.  Divisions alone took 27 us for 4096 x 8192, whose bytes take 15.
+template <int G>
+__device__ __forceinline__ void quantized(const float (&x)[G], const Divisor& d, uint32_t (&out)[2]) {
+  constexpr float kRound = 12582912.0f;
+  uint32_t n[G];
+  bool near = d.exact;
 #pragma unroll
-  for (int w = 0; w < kQuantThreads / 32; ++w) v = max(v, part[w]);
-  return v;
+  for (int k = 0; k < G; ++k) {
+    const float t = __fmul_rn(x[k], d.inverse), r = __fadd_rn(t, kRound);
+    n[k] = __float_as_uint(r) & 0xFFu;
+    near = near || fabsf(__fadd_rn(t, -__fadd_rn(r, -kRound))) > 0.5f - 1e-4f;
+  }
+  if (near) {
+#pragma unroll
+    for (int k = 0; k < G; ++k) n[k] = divided(x[k], d);
+  }
+  out[0] = out[1] = 0;
+#pragma unroll
+  for (int k = 0; k < G; ++k) out[k / 4] |= d.finite ? n[k] << (8 * (k & 3)) : 0u;
 }
 
-// Divisions are IEEE ones, rounded once, so that the integers are those of the
-// definition: rint(x / s), s = absmax / 127.
-__device__ __forceinline__ uint32_t quantized(float x, float by, bool finite) {
-  const int n = finite ? __float2int_rn(__fdiv_rn(x, by)) : 0;
-  return (uint32_t)min(127, max(-127, n)) & 0xFFu;
-}
-
-// A CTA a row, read once: each thread keeps up to kHeld groups of 16 bytes
-// (8192 16-bit columns in all) in registers between the maximum and the
-// division.  Longer rows, and rows that do not start on 16 bytes, are read
-// twice, an element at a time (HELD false).  One row of 3584: 3.6 us from cold
-// caches; 440 rows of 2048: 4 us; latency of two dependent steps and the launch.
-constexpr int kHeld = 4;
-
-template <class E, bool HELD>
+// LANES threads a row: a warp for short rows, of which a CTA then makes eight,
+// else the CTA.  Rows are read once: each thread keeps up to HELD groups of 16
+// bytes in registers between the maximum and the division (2048 16-bit columns
+// a warp, 8192 a CTA).  HELD = 0, for longer rows and rows that do not start on
+// 16 bytes: read twice, an element at a time.  (A CTA for each row of 512
+// columns took 16 us for 8192 of them, whose bytes take 2.)
+template <class E, int LANES, int HELD>
 __global__ void __launch_bounds__(kQuantThreads)
-    k_quantize_rows(const char* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t cols) {
+    k_quantize_rows(const char* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t rows, int64_t cols) {
   pdl_enter();
   __shared__ uint32_t part[kQuantThreads / 32];
-  constexpr int G = E::kGroup, B = E::kBytes;
-  const int tid = threadIdx.x;
-  const char* row = x + (int64_t)blockIdx.x * ldx * B;
-  int8_t* to = q + (int64_t)blockIdx.x * ldq;
-  uint4 held[kHeld];
+  constexpr int G = E::kGroup, B = E::kBytes, kRows = kQuantThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  const int64_t at = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+  if (at >= rows) return;  // whole warps: LANES is 32 there
+  const char* row = x + at * ldx * B;
+  int8_t* to = q + at * ldq;
+  uint4 held[HELD ? HELD : 1];
   uint32_t top = 0;
   const auto bits = [](const uint4& v, int k) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     return B == 2 ? (w[k / 2] >> (16 * (k & 1))) & 0xFFFFu : w[k & 3];
   };
-  if (HELD) {
-    const int groups = (int)(cols / G);  // whole ones: the columns left are read below
+  const int groups = HELD ? (int)(cols / G) : 0;  // whole ones: the columns left are read below
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int g = tid + i * kQuantThreads;
-      held[i] = g < groups ? ld_v4_stream(row + (int64_t)g * 16) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-#pragma unroll
-      for (int k = 0; k < G; ++k) top = max(top, magnitude<E>(bits(held[i], k)));
+  for (int i = 0; i < HELD; ++i) {
+    const int g = lane + i * LANES;
+    held[i] = g < groups ? ld_v4_stream(row + (int64_t)g * 16) : make_uint4(0, 0, 0, 0);
   }
-  const int64_t rest = HELD ? cols / G * G : 0;
-  for (int64_t c = rest + tid; c < cols; c += kQuantThreads) top = max(top, magnitude<E>(ld_elem<B>(row + c * B)));
-  top = cta_max(top, part);
-  const float s = __fdiv_rn(__uint_as_float(top), 127.0f);
-  if (tid == 0) scale[blockIdx.x] = s;
-  const float by = s > 0.0f ? s : 1.0f;
-  const bool finite = top < 0x7F800000u;
-  if (HELD) {
-    const int groups = (int)(cols / G);
+  // 16-bit types' magnitudes are ordered as integers too: two at a time.
+  uint32_t pair = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int g = tid + i * kQuantThreads;
-      if (g >= groups) break;
-      uint32_t w[2] = {};
+  for (int i = 0; i < HELD; ++i) {
+    const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
 #pragma unroll
-      for (int k = 0; k < G; ++k) w[k / 4] |= quantized(E::to_f32(bits(held[i], k)), by, finite) << (8 * (k & 3));
-      if (G == 8)
-        *reinterpret_cast<uint2*>(to + (int64_t)g * G) = make_uint2(w[0], w[1]);
+    for (int k = 0; k < 4; ++k) {
+      if (B == 2)
+        pair = __vmaxu2(pair, w[k] & 0x7FFF7FFFu);
       else
-        *reinterpret_cast<uint32_t*>(to + (int64_t)g * G) = w[0];
+        top = max(top, magnitude<E>(w[k]));
     }
   }
-  for (int64_t c = rest + tid; c < cols; c += kQuantThreads)
-    to[c] = (int8_t)quantized(E::to_f32(ld_elem<B>(row + c * B)), by, finite);
+  if (B == 2) top = magnitude<E>(max(pair & 0xFFFFu, pair >> 16));
+  const int64_t rest = (int64_t)groups * G;
+  for (int64_t c = rest + lane; c < cols; c += LANES) top = max(top, magnitude<E>(ld_elem<B>(row + c * B)));
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (LANES > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, part[w]);
+  }
+  const float s = __fdiv_rn(__uint_as_float(top), 127.0f);
+  if (lane == 0) scale[at] = s;
+  Divisor by;
+  by.by = s > 0.0f ? s : 1.0f;
+  by.inverse = __frcp_rn(by.by);
+  by.finite = top < 0x7F800000u;
+  by.exact = by.by < 7.9e-31f;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int g = lane + i * LANES;
+    if (g >= groups) break;
+    float v[G];
+#pragma unroll
+    for (int k = 0; k < G; ++k) v[k] = E::to_f32(bits(held[i], k));
+    uint32_t w[2];
+    quantized<G>(v, by, w);
+    if (G == 8)
+      *reinterpret_cast<uint2*>(to + (int64_t)g * G) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(to + (int64_t)g * G) = w[0];
+  }
+  for (int64_t c = rest + lane; c < cols; c += LANES) {
+    const uint32_t n = divided(E::to_f32(ld_elem<B>(row + c * B)), by);
+    to[c] = (int8_t)(by.finite ? n : 0u);
+  }
 }
 
 template <class E>
 cudaError_t quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t rows, int64_t cols,
-                     cudaStream_t s) {
-  constexpr int G = E::kGroup;
-  const bool held = cols <= (int64_t)kHeld * kQuantThreads * G && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
-                    reinterpret_cast<uintptr_t>(q) % G == 0 && (rows == 1 || (ldx % G == 0 && ldq % G == 0));
-  return launch_op(held ? k_quantize_rows<E, true> : k_quantize_rows<E, false>, dim3((unsigned)rows), kQuantThreads, 0, 1,
-                   s, static_cast<const char*>(x), ldx, q, ldq, scale, cols);
+                     int num_sms, cudaStream_t s) {
+  constexpr int64_t G = E::kGroup;
+  const bool aligned = reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % G == 0 &&
+                       (rows == 1 || (ldx % G == 0 && ldq % G == 0));
+  // A warp a row where that fills the SMs (440 rows of 2048: 5.4 us by warps, 3.0
+  // by CTAs; 3104: 8.6 and 9.8).
+  const bool warp = aligned && cols <= 8 * 32 * G && rows > 8 * num_sms;
+  const bool held = aligned && cols <= 4 * kQuantThreads * G;
+  const dim3 grid((unsigned)(warp ? (rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32) : rows));
+  return launch_op(warp   ? k_quantize_rows<E, 32, 8>
+                   : held ? k_quantize_rows<E, kQuantThreads, 4>
+                          : k_quantize_rows<E, kQuantThreads, 0>,
+                   grid, kQuantThreads, 0, 1, s, static_cast<const char*>(x), ldx, q, ldq, scale, rows, cols);
 }
 
 }  // namespace
@@ -256,10 +302,10 @@ cudaError_t launch_gate_grad(int dtype, int act, const void* gate, const void* u
 }
 
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
-                                 float* scale, int64_t rows, int64_t cols, cudaStream_t s) {
-  if (dtype == AR_BF16) return quantize<Bf16>(x, ldx, q, ldq, scale, rows, cols, s);
-  if (dtype == AR_FP16) return quantize<F16>(x, ldx, q, ldq, scale, rows, cols, s);
-  return quantize<F32>(x, ldx, q, ldq, scale, rows, cols, s);
+                                 float* scale, int64_t rows, int64_t cols, int num_sms, cudaStream_t s) {
+  if (dtype == AR_BF16) return quantize<Bf16>(x, ldx, q, ldq, scale, rows, cols, num_sms, s);
+  if (dtype == AR_FP16) return quantize<F16>(x, ldx, q, ldq, scale, rows, cols, num_sms, s);
+  return quantize<F32>(x, ldx, q, ldq, scale, rows, cols, num_sms, s);
 }
 
 }  // namespace ar

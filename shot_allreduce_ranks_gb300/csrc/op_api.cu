@@ -329,8 +329,10 @@ ar_status_t ar_quantize_rows(const void* x, size_t ldx, int8_t* q, size_t ldq, f
   if (cols == 0 || !scale || misaligned(scale, 4) || bad_matrix(x, rows, cols, ldx) ||
       rows > 0x7FFFFFFF || misaligned(x, dtype == AR_FP32 ? 4 : 2) || bad_matrix(q, rows, cols, ldq))
     return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
   return cuda_status(ar::launch_quantize_rows(dtype, x, (int64_t)ldx, q, (int64_t)ldq, scale,
-                                              (int64_t)rows, (int64_t)cols,
+                                              (int64_t)rows, (int64_t)cols, sms,
                                               static_cast<cudaStream_t>(stream)));
 }
 

@@ -89,7 +89,7 @@ cudaError_t launch_gemm_any(int mode, int dtype, const GemmArgs& g, cudaStream_t
 
 // One int8 row and one scale for each row of x.
 cudaError_t launch_quantize_rows(int dtype, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
-                                 float* scale, int64_t rows, int64_t cols, cudaStream_t s);
+                                 float* scale, int64_t rows, int64_t cols, int num_sms, cudaStream_t s);
 
 // Copies up to three matrices to rows that start on 16 bytes.
 struct PackJob {

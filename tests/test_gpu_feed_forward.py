@@ -340,7 +340,8 @@ def test_dropout_past_2_31_elements(ar):
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("rows,cols,pad,shift", [(1, 1, 0, 0), (1, 3584, 0, 0), (5, 77, 3, 1), (40, 2048, 0, 0), (300, 264, 8, 0), (2, 40000, 0, 0), (3, 8192, 0, 0), (3, 8200, 0, 0),
-                                                    (4, 4097, 7, 0), (1, 2051, 0, 0)])
+                                                    (4, 4097, 7, 0), (1, 2051, 0, 0), (1700, 512, 0, 0), (1333, 2048, 16, 0),
+                                                    (1301, 2057, 7, 0), (1310, 96, 0, 0), (1305, 13, 3, 0), (1900, 1000, 5, 1)])
 def test_quantize_rows(ar, dtype, rows, cols, pad, shift):
     x = normal(gen(rows + cols), (rows, cols), dtype)
     if rows > 1:
@@ -351,6 +352,23 @@ def test_quantize_rows(ar, dtype, rows, cols, pad, shift):
     assert np.array_equal(s.cpu().numpy(), want_s)
     assert np.array_equal(q.t.cpu().numpy(), want_q)
     assert q.intact()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_quantize_rows_near_halves_and_far_scales(ar, dtype):
+    """Quotients that fall on and next to halves, and scales from the smallest
+    normal numbers up: the integers are those of an IEEE division."""
+    k = torch.arange(-127, 128, device=DEV).float()
+    rows = [torch.cat([k, k + 0.5, k - 0.5 + 2.0 ** -12, k + 0.5 - 2.0 ** -12, k / 127]).clamp(-127, 127) * f
+            for f in (1.0, 3.0, 0.1, 1 / 3, 2.0 ** -10, 7e4 / 127)]
+    x = torch.stack(rows + [normal(gen(s), (5 * 255,), FP32) * 2.0 ** e for s, e in ((1, 0), (2, -12), (3, 9))])
+    if dtype is not FP16:
+        x = torch.cat([x, x * 2.0 ** -99, x * 2.0 ** -110, x * 2.0 ** 100])
+    x = x.to(dtype)
+    x = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+    q, s = ar.quantize_rows(x)
+    want_q, want_s = ref.quantize(x)
+    assert np.array_equal(s.cpu().numpy(), want_s) and np.array_equal(q.cpu().numpy(), want_q)
 
 
 def test_quantize_rows_that_are_not_finite(ar):
