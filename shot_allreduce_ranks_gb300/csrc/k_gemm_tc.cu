@@ -136,36 +136,45 @@ __device__ __forceinline__ bool job_at(const TcArgs& a, uint32_t p, uint32_t P, 
   return t < a.part[part].walk.tiles;
 }
 
-// A stage holds 128 rows of A and up to 256 / CG of B.  1 KiB aligns the ring.
-template <int CG>
-struct Shape {
-  static constexpr uint32_t kA = 128 * kBK * 2, kB = 256 / CG * kBK * 2, kStage = kA + kB;
-  static constexpr int kStages = 196608 / kStage;
-  static constexpr uint32_t kStores = 8 * 2 * 2048;  // two 32 x 32 boxes an epilogue warp
-  static constexpr uint32_t kSmem = kStages * kStage + kStores + 1024;
+// The ring has as many stages as fit: 128 rows of A and what a tile's columns
+// need of B each.  More stages matter where tiles are narrow: copies take about
+// 1,800 clocks to arrive, 3,000 under load, and a step of 128 columns 256.
+constexpr uint32_t kRing = 196608;
+constexpr int kMostStages = 10;
+constexpr uint32_t kABytes = 128 * kBK * 2;
+constexpr uint32_t kStores = 8 * 2 * 2048;  // two 32 x 32 boxes an epilogue warp
+constexpr uint32_t kTcSmem = kRing + kStores + 1024;  // 1 KiB aligns the ring
+
+// A stage of the ring and the parity of its use, step by step.
+struct Stage {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++at == stages) at = 0, parity ^= 1;
+  }
 };
 
 template <int WHAT, class E, int ACT, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_gemm_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
   static_assert(WHAT == kTcGrad || CG == 2, "the gated product is made by pairs");
-  using S = Shape<CG>;
   constexpr bool kBmn = WHAT == kTcGrad;
   const int cols = WHAT == kTcGated ? a.bn / 2 : a.bn;  // output columns of a tile
-  constexpr int kST = S::kStages;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kST + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kMostStages + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t dead;
 
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * kST, done = empty + 8 * kST, freed = done + 16,
-                 drained = freed + 16;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMostStages, done = empty + 8 * kMostStages,
+                 freed = done + 16, drained = freed + 16;
+  const int chunks = (a.bn / CG + 63) / 64;  // of an MN-major B
+  const uint32_t stage_bytes = kABytes + (WHAT == kTcGated ? a.bn / CG * 128 : chunks * 8192);
+  const uint32_t stages = min((uint32_t)kMostStages, kRing / stage_bytes);
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kST; ++i) {
+    for (int i = 0; i < kMostStages; ++i) {
       bar_init(full + 8 * i, 1);
       bar_init(empty + 8 * i, 1);
     }
@@ -197,20 +206,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 0) {
     if (elect_one()) {
-      const int chunks = (a.bn / CG + 63) / 64;  // of an MN-major B
-      const uint32_t stage_bytes = S::kA + (WHAT == kTcGated ? a.bn / CG * 128 : chunks * 8192);
-      uint32_t it = 0;
+      Stage stage;
+      uint32_t filled = 0;  // stages in use, up to all
       bool ok = true;
       for (uint32_t j = 0; ok && job_at<WHAT>(a, slot, slots, j, which, number); ++j) {
         const Tile tile = tile_at(a.part[which].walk, number);
         const int m0 = (tile.m * CG + (int)rank) * 128, n0 = tile.n * cols;
         const bool dx = WHAT == kTcGrad && which == 0, dw = WHAT == kTcGrad && which == 1;
         const int steps = a.part[which].steps, total = dx ? 2 * steps : steps;
-        for (int s = 0; s < total; ++s, ++it) {
-          const uint32_t st = it % kST, round = it / kST;
-          if (!(ok = bar_wait(empty + 8 * st, (round & 1) ^ 1, &dead))) break;
-          const uint32_t sa = ring + st * S::kStage, sb = sa + S::kA;
-          uint32_t bar = full + 8 * st;
+        for (int s = 0; s < total; ++s, stage.next(stages)) {
+          if (!(ok = bar_wait(empty + 8 * stage.at, stage.parity ^ 1, &dead))) break;
+          const uint32_t sa = ring + stage.at * stage_bytes, sb = sa + kABytes;
+          uint32_t bar = full + 8 * stage.at;
+          filled += filled < stages;
           if (rank == 0) bar_expect_tx(bar, CG * stage_bytes);
           if (CG == 2) bar = map_to_cta(bar, 0);
           const int up = dx ? s >= steps : tile.z;  // which projection
@@ -231,19 +239,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
-      // Nothing of the ring is left behind: the last stages are consumed, or, after
-      // a wait that gave up, at least their copies are done.
-      const uint32_t oldest = it > kST ? it - kST : 0;
-      for (uint32_t k = oldest; k < it && ok; ++k) ok = bar_wait(empty + 8 * (k % kST), (k / kST) & 1, &dead);
+      // Nothing of the ring is left behind: every stage in use is consumed, or, after
+      // a wait that gave up, at least its copies are done.  The stages before the
+      // next one have been filled last; from there on, a round earlier.
+      const auto parity_of = [&](uint32_t i) { return i < stage.at ? stage.parity : stage.parity ^ 1; };
+      for (uint32_t i = 0; i < filled && ok; ++i) ok = bar_wait(empty + 8 * i, parity_of(i), &dead);
       if (!ok) {
         atomicExch(&g_tc_error, 1u);
         if (rank == 0)
-          for (uint32_t k = oldest; k < it; ++k) bar_wait_copies(full + 8 * (k % kST), (k / kST) & 1);
+          for (uint32_t i = 0; i < filled; ++i) bar_wait_copies(full + 8 * i, parity_of(i));
       }
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      uint32_t it = 0, at = 0;
+      Stage stage;
+      uint32_t at = 0;
       bool ok = true;
       for (; ok && job_at<WHAT>(a, slot, slots, at, which, number); ++at) {
         const bool a_mn = WHAT == kTcGrad && which == 1;
@@ -253,17 +263,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!(ok = bar_wait(freed + 8 * buf, ((at >> 1) & 1) ^ 1, &dead))) break;
         fence_after_sync();
         const uint32_t acc = tmem + buf * 256;
-        for (int s = 0; s < total; ++s, ++it) {
-          const uint32_t st = it % kST, round = it / kST;
-          if (!(ok = bar_wait(full + 8 * st, round & 1, &dead))) break;
+        for (int s = 0; s < total; ++s, stage.next(stages)) {
+          if (!(ok = bar_wait(full + 8 * stage.at, stage.parity, &dead))) break;
           fence_after_sync();
-          const uint32_t sa = ring + st * S::kStage, sb = sa + S::kA;
+          const uint32_t sa = ring + stage.at * stage_bytes, sb = sa + kABytes;
           const uint64_t da = operand_desc(sa, a_mn ? 8192 : 16, 1024);
           const uint64_t db = kBmn ? operand_desc(sb, 8192, 1024) : operand_desc(sb, 16, 1024);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 16 k: 32 bytes of a K-major row, 16 rows of an MN-major tile
             mma_f16<CG>(acc, da + (a_mn ? 128 : 2) * k, db + (kBmn ? 128 : 2) * k, idesc, s > 0 || k > 0);
-          mma_commit<CG>(empty + 8 * st);
+          mma_commit<CG>(empty + 8 * stage.at);
         }
         if (ok) mma_commit<CG>(done + 8 * buf);
       }
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else {
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;  // this warp's lanes of tensor memory
     const int lane = (int)(threadIdx.x & 31);
-    const uint32_t boxes = ring + kST * S::kStage + (uint32_t)(warp - 2) * 4096;
+    const uint32_t boxes = ring + kRing + (uint32_t)(warp - 2) * 4096;
     uint32_t stored = 0, at = 0;
     for (; job_at<WHAT>(a, slot, slots, at, which, number); ++at) {
       const Part& part = a.part[which];
@@ -391,18 +400,17 @@ bool make_part(TcArgs& a, TcMaps& maps, int which, int dtype, const GemmArgs& g,
 
 template <int WHAT, class E, int ACT, int CG>
 cudaError_t launch(const TcArgs& a, const TcMaps& maps, int num_sms, cudaStream_t s) {
-  using S = Shape<CG>;
   auto* kernel = k_gemm_tc<WHAT, E, ACT, CG>;
   static bool raised[64];  // by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && !raised[dev & 63])
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
   if (e != cudaSuccess) return e;
   raised[dev & 63] = dev < 64;
   const int64_t slots = num_sms / CG, tiles = (int64_t)a.part[0].walk.tiles + a.part[1].walk.tiles;
   const dim3 grid((unsigned)((tiles < slots ? tiles : slots) * CG));
-  return launch_op(kernel, grid, kTcThreads, S::kSmem, CG, s, a, maps);
+  return launch_op(kernel, grid, kTcThreads, kTcSmem, CG, s, a, maps);
 }
 
 // What a tile takes, in clocks: a step of 64 k the longer of its instruction (2
