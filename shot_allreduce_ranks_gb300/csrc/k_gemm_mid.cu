@@ -24,9 +24,11 @@ using namespace tc;
 
 constexpr int kMidBK = 64, kMidMost = 128;  // k of a stage; tokens
 constexpr int kMidThreads = 256;
-constexpr int kMidStages = 6;
-constexpr uint32_t kMidA = 128 * 128, kMidStage = kMidA + kMidMost * 128;
-constexpr uint32_t kMidSmem = kMidStages * kMidStage + 1024;
+// The ring: 128 rows of weights and the tokens' a stage, as many as fit (11 for
+// 16 tokens, six for 128): what is on its way hides the copies' latency.
+constexpr uint32_t kMidA = 128 * 128, kMidRing = 208896;
+constexpr int kMidStages = 11;
+constexpr uint32_t kMidSmem = kMidRing + 1024;
 constexpr int kMidBlock = 16;               // rows of a block of either projection
 
 __device__ uint32_t g_mid_error;  // set by a wait that gave up
@@ -57,6 +59,8 @@ __global__ void __launch_bounds__(kMidThreads, 1)
 
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMidStages, done = empty + 8 * kMidStages;
+  const uint32_t stage_bytes = kMidA + (uint32_t)a.tokens * 128;
+  const uint32_t stages = min((uint32_t)kMidStages, kMidRing / stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t part = KS > 1 ? cluster_rank() : 0;
   const int f0 = (int)(blockIdx.x / KS) * 64;  // outputs of this tile
@@ -88,12 +92,13 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   if (warp == 0) {
     if (elect_one()) {
       bool ok = true;
-      int it = 0;
-      for (int s = s0; s < s1; ++s, ++it) {
-        const uint32_t st = (uint32_t)it % kMidStages;
-        if (!(ok = bar_wait(empty + 8 * st, ((it / kMidStages) & 1) ^ 1, &dead))) break;
-        const uint32_t sa = ring + st * kMidStage, bar = full + 8 * st;
-        bar_expect_tx(bar, kMidA + (uint32_t)a.tokens * 128);
+      Stage stage;
+      uint32_t filled = 0;  // stages in use, up to all
+      for (int s = s0; s < s1; ++s, stage.next(stages)) {
+        if (!(ok = bar_wait(empty + 8 * stage.at, stage.parity ^ 1, &dead))) break;
+        filled += filled < stages;
+        const uint32_t sa = ring + stage.at * stage_bytes, bar = full + 8 * stage.at;
+        bar_expect_tx(bar, stage_bytes);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           load_box<1>(sa + (2 * b) * kMidBlock * 128, &map_g, s * kMidBK, f0 + b * kMidBlock, bar);
@@ -102,24 +107,23 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         load_box<1>(sa + kMidA, &map_x, s * kMidBK, 0, bar);
       }
       // The ring is used again below: every copy has landed by then, consumed or not.
-      for (int k = it > kMidStages ? it - kMidStages : 0; k < it; ++k)
-        bar_wait_copies(full + 8 * (k % kMidStages), (k / kMidStages) & 1);
+      for (uint32_t i = 0; i < filled; ++i)
+        bar_wait_copies(full + 8 * i, i < stage.at ? stage.parity : stage.parity ^ 1);
       if (!ok) atomicExch(&g_mid_error, 1u);
     }
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = instr_desc(IsBf16<E>::value, false, false, 128, a.tokens);
       bool ok = true;
-      int it = 0;
-      for (int s = s0; s < s1; ++s, ++it) {
-        const uint32_t st = (uint32_t)it % kMidStages;
-        if (!(ok = bar_wait(full + 8 * st, (it / kMidStages) & 1, &dead))) break;
+      Stage stage;
+      for (int s = s0; s < s1; ++s, stage.next(stages)) {
+        if (!(ok = bar_wait(full + 8 * stage.at, stage.parity, &dead))) break;
         fence_after_sync();
-        const uint64_t dw = operand_desc(ring + st * kMidStage, 16, 1024);
-        const uint64_t dx = operand_desc(ring + st * kMidStage + kMidA, 16, 1024);
+        const uint64_t dw = operand_desc(ring + stage.at * stage_bytes, 16, 1024);
+        const uint64_t dx = operand_desc(ring + stage.at * stage_bytes + kMidA, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f16<1>(tmem, dw + 2 * k, dx + 2 * k, idesc, it > 0 || k > 0);
-        mma_commit<1>(empty + 8 * st);
+        for (int k = 0; k < 4; ++k) mma_f16<1>(tmem, dw + 2 * k, dx + 2 * k, idesc, s > s0 || k > 0);
+        mma_commit<1>(empty + 8 * stage.at);
       }
       mma_commit<1>(done);  // of whatever was issued
       if (!ok) atomicExch(&g_mid_error, 1u);

@@ -145,14 +145,6 @@ constexpr uint32_t kABytes = 128 * kBK * 2;
 constexpr uint32_t kStores = 8 * 2 * 2048;  // two 32 x 32 boxes an epilogue warp
 constexpr uint32_t kTcSmem = kRing + kStores + 1024;  // 1 KiB aligns the ring
 
-// A stage of the ring and the parity of its use, step by step.
-struct Stage {
-  uint32_t at = 0, parity = 0;
-  __device__ __forceinline__ void next(uint32_t stages) {
-    if (++at == stages) at = 0, parity ^= 1;
-  }
-};
-
 template <int WHAT, class E, int ACT, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_gemm_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {

@@ -93,6 +93,14 @@ static __device__ __noinline__ void bar_wait_copies(uint32_t bar, uint32_t parit
     if ((k & 31u) == 31u && now_ns() - t0 > kWaitNs) break;
 }
 
+// A stage of a ring and the parity of its use, step by step.
+struct Stage {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++at == stages) at = 0, parity ^= 1;
+  }
+};
+
 // A box of a 2-D tensor map into shared memory; CG = 2: the barrier may be the
 // pair's other CTA's.
 template <int CG>
