@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kGateThreads)
       rg[k] = E::pack(rest(g0, E::lo(og[k])), rest(g1, E::hi(og[k])));
       ru[k] = E::pack(rest(u0, E::lo(ou[k])), rest(u1, E::hi(ou[k])));
     }
-    // The workspace row is ldw = cols rounded up to 8, so a whole group fits;
-    // what lies past cols is never read.
+    // The workspace row is longer than cols, up to a whole group at least; what
+    // lies past cols is never read.
     st_v4_stream(dgate + to, make_uint4(og[0], og[1], og[2], og[3]));
     st_v4_stream(dup + to, make_uint4(ou[0], ou[1], ou[2], ou[3]));
     if (two_parts) {

@@ -12,7 +12,7 @@ struct ar_ffn_ctx {
   size_t max_tokens = 0, hidden = 0, width = 0;
   int dtype = AR_BF16, act = AR_ACT_SILU;
   int num_sms = 0;
-  size_t ldw = 0;         // workspace leading dimension: width rounded up to 16 bytes
+  size_t ldw = 0;         // workspace leading dimension: width rounded up to 128 bytes
   size_t ldx = 0;         // hidden rounded up likewise
   size_t rows = 0;        // of dgate and of dup
   char* work = nullptr;   // dgate, dup: rows x ldw each; x for two-part rows: up to 128 x ldx
@@ -62,7 +62,9 @@ struct Rows {
 };
 
 bool on_16(const Rows& r, size_t elem) { return !misaligned(r.p, 16) && r.ld * elem % 16 == 0; }
-size_t packed_ld(const Rows& r, size_t elem) { return (r.cols * elem + 15) / 16 * 16 / elem; }
+// Packed rows start on 128 bytes, so that a box's rows of 128 bytes are whole
+// cache lines.
+size_t packed_ld(const Rows& r, size_t elem) { return (r.cols * elem + 127) / 128 * 128 / elem; }
 
 // Bytes that packing takes: 0 where every matrix can be read as it is.
 size_t pack_bytes(const Rows* m, int count, size_t elem) {
@@ -183,8 +185,8 @@ ar_status_t ar_ffn_create(size_t max_tokens, size_t hidden, size_t width, int dt
   if (!h) return AR_ERR_OOM;
   h->max_tokens = max_tokens, h->hidden = hidden, h->width = width;
   h->dtype = dtype, h->act = activation, h->num_sms = sms;
-  h->ldw = (width + 7) / 8 * 8;
-  h->ldx = (hidden + 7) / 8 * 8;
+  h->ldw = (width + 63) / 64 * 64;
+  h->ldx = (hidden + 63) / 64 * 64;
   if (train) {
     const size_t two = (size_t)ar::two_part_rows((int64_t)(max_tokens < kTwoPartTokens ? max_tokens : kTwoPartTokens));
     h->rows = max_tokens > two ? max_tokens : two;
