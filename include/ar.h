@@ -447,7 +447,8 @@ ar_status_t ar_allreduce_fused_noalloc(int R, const void* const* d_in_tbl,
  * that the call's _scratch_bytes function gives for the same operands (0 where
  * all rows start on 16 bytes; scratch may then be NULL), owned by the caller
  * and free again when the call has completed.  With scratch NULL such operands
- * take a slower kernel.  All calls are
+ * take a slower kernel.  (Forward products of up to 32 tokens read any rows as
+ * they are and use no scratch.)  All calls are
  * asynchronous on `stream`, allocate nothing, synchronise nothing, and can be
  * captured into a CUDA graph.  Outputs must not overlap inputs or one another
  * unless a call says so.

@@ -12,7 +12,7 @@
 //
 // It makes what the tensor-map kernels cannot read and the caller gave no scratch
 // to lay out for them.  Measured on one GB300: 46 TFLOP/s on large sizes, a
-// thirtieth of theirs (gradients at 1001 x 1031 -> 777: 153 us, 24 with scratch);
+// thirtieth of theirs (gradients at 1001 x 1031 -> 777: 153 us, 23 with scratch);
 // bound by its element loads.
 #include "ops_internal.cuh"
 

@@ -12,7 +12,8 @@
 //
 // Measured on one GB300: one token 8192 -> 3584 (117 MB of weights) 18.8-20 us,
 // 5.9-6.2 TB/s, 87-92% of a copy's rate; 8 tokens 21.6 us; 8-bit, one token 3584
-// -> 8192 (29 MB) 8.6 us.  Four-warp CTAs, and register limits for four CTAs an
+// -> 8192 (29 MB) 8.6 us; rows that begin anywhere, read by pairs of aligned
+// pieces and shifted: 8001 -> 3500 40 us (62 by laying them out first).  Four-warp CTAs, and register limits for four CTAs an
 // SM, were slower at most sizes (24.5 and 24.6 against 20.4 us for the first).
 #include "ops_internal.cuh"
 
@@ -21,24 +22,36 @@ namespace {
 
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
 
-// 16 bytes at p, of which `left` may be read (the rest zero); VEC: p is 16-byte aligned.
+// 16 bytes of a row at p, of which `left` may be read (the rest zero); VEC: rows
+// start on 16 bytes.
 template <bool VEC, int B>
-__device__ __forceinline__ uint4 load_piece(const char* p, int64_t left) {
+__device__ __forceinline__ uint4 load_piece(const char* p, int64_t left, const char* begin, const char* end) {
   if (VEC && left >= 16) return ld_v4_stream(p);
-  uint32_t w[4] = {};
-#pragma unroll
-  for (int i = 0; i < 16 / B; ++i)
-    if (i * B < left) {
-      const uint32_t v = B == 2 ? ld_elem<2>(p + 2 * i) : *reinterpret_cast<const uint8_t*>(p + i);
-      w[i * B / 4] |= v << (8 * (i * B % 4));
-    }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return load_anywhere<B>(p, left, begin, end);
+}
+
+__device__ __forceinline__ uint32_t offset_of(const char* row) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);  // of its pieces too: they lie 16 bytes apart
+}
+
+// Whether the aligned windows of a row's pieces k0 .. k1 lie within the matrix.
+__device__ __forceinline__ bool within(const char* row, int64_t k0, int64_t k1, const char* begin, const char* end) {
+  const char* base = row - offset_of(row);
+  return base + k0 >= begin && base + k1 + 32 <= end;
+}
+
+__device__ __forceinline__ void load_window(const char* p, uint4& u, uint4& v) {
+  const uint4* base = reinterpret_cast<const uint4*>(p - offset_of(p));
+  u = __ldg(base);
+  v = __ldg(base + 1);
 }
 
 template <int MODE, class E, int ACT, int NT, bool VEC>
 __global__ void __launch_bounds__(kFewThreads) k_gemm_few(GemmArgs g) {
   constexpr int B = MODE == kGemmI8 ? 1 : 2;  // bytes of an element
-  constexpr int kUnroll = NT > 2 ? 2 : 4;     // 64-byte pieces of each row in flight a warp
+  // 64-byte pieces of each row in flight a warp; rows that begin anywhere take two
+  // loads a piece.
+  constexpr int kUnroll = VEC ? (NT > 2 ? 2 : 4) : (NT > 2 ? 1 : 2);
   constexpr int kRows = MODE == kGemmI8 ? 16 : 8;
   using F = typename std::conditional<MODE == kGemmI8, F16, E>::type;
   __shared__ float4 part[kFewWarps][NT][32];
@@ -50,6 +63,12 @@ __global__ void __launch_bounds__(kFewThreads) k_gemm_few(GemmArgs g) {
   const int64_t bytes = g.K * B;
   const char* wa = static_cast<const char*>(g.b0) + ra * g.ldb * B;
   const char* wb = static_cast<const char*>(MODE == kGemmI8 ? g.b0 : g.b1) + rb * (MODE == kGemmI8 ? g.ldb : g.ldb1) * B;
+  // Where the matrices begin and end.
+  const char *begin_a = static_cast<const char*>(g.b0), *begin_b = static_cast<const char*>(MODE == kGemmI8 ? g.b0 : g.b1),
+             *begin_x = static_cast<const char*>(g.a0);
+  const char* end_a = begin_a + ((g.N - 1) * g.ldb + g.K) * B;
+  const char* end_b = MODE == kGemmI8 ? end_a : begin_b + ((g.N - 1) * g.ldb1 + g.K) * B;
+  const char* end_x = begin_x + ((g.M - 1) * g.lda + g.K) * B;
   const char* xs[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) xs[j] = static_cast<const char*>(g.a0) + min((int64_t)(8 * j + g8), g.M - 1) * g.lda * B;
@@ -58,14 +77,39 @@ __global__ void __launch_bounds__(kFewThreads) k_gemm_few(GemmArgs g) {
   constexpr int kUnit = 64 * kUnroll;  // bytes of a row that a warp takes at a time
   for (int64_t at = (int64_t)warp * kUnit; at < bytes; at += kFewWarps * kUnit) {
     uint4 a[kUnroll], b[kUnroll], x[NT][kUnroll];
+    // Inside the matrices, the windows around all pieces are loaded before the
+    // first is shifted.
+    const int64_t k0 = at + 16 * t4, k1 = k0 + 64 * (kUnroll - 1);
+    bool inside = !VEC && k1 + 16 <= bytes && within(wa, k0, k1, begin_a, end_a) && within(wb, k0, k1, begin_b, end_b);
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int64_t k = at + 64 * i + 16 * t4;
-      a[i] = load_piece<VEC, B>(wa + k, bytes - k);
-      b[i] = load_piece<VEC, B>(wb + k, bytes - k);
+    for (int j = 0; j < NT; ++j) inside = inside && within(xs[j], k0, k1, begin_x, end_x);
+    if (inside) {
+      uint4 av[kUnroll], bv[kUnroll], xv[NT][kUnroll];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        x[j][i] = 8 * j + g8 < g.M ? load_piece<VEC, B>(xs[j] + k, bytes - k) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kUnroll; ++i) {
+        load_window(wa + k0 + 64 * i, a[i], av[i]);
+        load_window(wb + k0 + 64 * i, b[i], bv[i]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) load_window(xs[j] + k0 + 64 * i, x[j][i], xv[j][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        a[i] = shift_window(a[i], av[i], offset_of(wa));
+        b[i] = shift_window(b[i], bv[i], offset_of(wb));
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          x[j][i] = 8 * j + g8 < g.M ? shift_window(x[j][i], xv[j][i], offset_of(xs[j])) : make_uint4(0, 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int64_t k = k0 + 64 * i;
+        a[i] = load_piece<VEC, B>(wa + k, bytes - k, begin_a, end_a);
+        b[i] = load_piece<VEC, B>(wb + k, bytes - k, begin_b, end_b);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          x[j][i] = 8 * j + g8 < g.M ? load_piece<VEC, B>(xs[j] + k, bytes - k, begin_x, end_x) : make_uint4(0, 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {

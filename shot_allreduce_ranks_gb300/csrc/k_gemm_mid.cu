@@ -12,9 +12,9 @@
 //
 // Bound by the weights' way into the SMs (about 64 bytes a clock each), and below
 // that by launch, set-up and two trips through the cluster, about 7 us.  Measured
-// on one GB300 (bf16, replayed graph): 13 tokens 5120 -> 2048 10.3 us (42 MB of
-// weights, 4.1 TB/s), 64 tokens 11.5 us (25 us by tiles of 128 padded tokens), 64
-// tokens 8192 -> 3584 24 us (117 MB, 4.9 TB/s; was 40), 128 tokens 26 us.
+// on one GB300 (bf16, replayed graph): 13 tokens 5120 -> 2048 10.2 us (42 MB of
+// weights, 4.1 TB/s), 64 tokens 11.4 us (25 us by tiles of 128 padded tokens), 64
+// tokens 8192 -> 3584 22.8 us (117 MB, 5.1 TB/s; was 40), 128 tokens 25.4 us.
 #include "tc_device.cuh"
 
 namespace ar {

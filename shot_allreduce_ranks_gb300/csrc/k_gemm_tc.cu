@@ -29,8 +29,9 @@
 //   1,900-1,960 TFLOP/s, tensor pipe active 94% of the time (a library product
 //   of 8192^3 reached 1,924); in a loop the power limit takes the clock from
 //   2,070 to about 1,470 MHz and the time to 560 us;
-//   forward 440 x 5120 -> 1736: 21 us, of which about 8 are launch, set-up, the
-//   first copies and the last tile's stores;
+//   forward 440 x 5120 -> 1736: 18.3 us, of which about 8 are launch, set-up, the
+//   first copies and the last tile's stores (21.0 with six stages for narrow
+//   tiles too, instead of eight);
 //   gradients 4096 x 8192 -> 3584: 545 us (1,770 TFLOP/s); 512 x 8192 -> 3584: 89
 //   us (tensor pipe active 60%: the weights' tiles have eight steps each).
 // Measured and left out: clusters of four that share A by multicast (the same

@@ -12,28 +12,21 @@ struct PackJobs {
   PackJob job[3];
 };
 
-// One matrix's rows.  A thread makes 16 bytes of a row from its elements, one
-// load each: the source rows begin anywhere, and neighbouring lanes' loads share
-// cache lines.
+// One matrix's rows, 16 bytes a thread.
 template <int B>
 __device__ __forceinline__ void pack_rows(const PackJob& j) {
   constexpr int G = 16 / B;
-  const int64_t per_row = (j.cols + G - 1) / G, total = j.rows * per_row;
+  const int64_t per_row = (j.cols + G - 1) / G, total = j.rows * per_row, sources = j.twice ? j.twice : j.rows;
+  const char* begin = static_cast<const char*>(j.from);
+  const char* end = begin + ((sources - 1) * j.ld_from + j.cols) * B;
   for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * kPackThreads) {
     const int64_t row = total >> 32 ? i / per_row : (int64_t)((uint32_t)i / (uint32_t)per_row);
     const int64_t col = (i - row * per_row) * G;
     const int64_t source = j.twice ? row / 32 * 16 + row % 16 : row;
-    const char* p = static_cast<const char*>(j.from) + (source * j.ld_from + col) * B;
-    const int64_t cols = j.twice && source >= j.twice ? 0 : j.cols;
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int k = 0; k < G; ++k)
-      if (col + k < cols) {
-        const uint32_t v = B == 2 ? *reinterpret_cast<const uint16_t*>(p + 2 * k) : *reinterpret_cast<const uint8_t*>(p + k);
-        w[k * B / 4] |= v << (8 * (k * B % 4));
-      }
-    *reinterpret_cast<uint4*>(static_cast<char*>(j.to) + (row * j.ld_to + col) * B) = make_uint4(w[0], w[1], w[2], w[3]);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (source < sources) v = load_anywhere<B>(begin + (source * j.ld_from + col) * B, (j.cols - col) * B, begin, end);
+    *reinterpret_cast<uint4*>(static_cast<char*>(j.to) + (row * j.ld_to + col) * B) = v;
   }
 }
 

@@ -27,6 +27,9 @@ constexpr size_t kMaxSize = (size_t)1 << 30;  // the sizes a handle is made for
 // in two parts: there the rows of a tile are not filled otherwise, so it costs
 // no instruction, and with few values the rounding of each shows most.
 constexpr size_t kTwoPartTokens = 64;
+// Up to this many tokens a forward product reads the weights once, where they
+// are: laying them out first costs two passes more.
+constexpr size_t kFewTokens = 32;
 
 bool half_type(int dtype) { return dtype == AR_BF16 || dtype == AR_FP16; }
 bool any_type(int dtype) { return half_type(dtype) || dtype == AR_FP32; }
@@ -232,7 +235,8 @@ ar_status_t ar_ffn_forward(ar_ffn_t h, const void* x, size_t ldx, const void* w_
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   Rows m[3];
   operands(h, x, ldx, w_gate, w_up, ldw, tokens, m);
-  if (ar_status_t st = pack(m, 3, 2, scratch, scratch_bytes, h->num_sms, s)) return st;
+  if (tokens > kFewTokens)
+    if (ar_status_t st = pack(m, 3, 2, scratch, scratch_bytes, h->num_sms, s)) return st;
   ar::GemmArgs g = {};
   g.a0 = m[0].p, g.lda = (int64_t)m[0].ld;
   g.b0 = m[1].p, g.b1 = m[2].p, g.ldb = (int64_t)m[1].ld, g.ldb1 = (int64_t)m[2].ld;
@@ -353,7 +357,8 @@ ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, cons
   if (ar_status_t st = current_sms(&sms)) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   Rows m[2] = {{x, tokens, in, ldx}, {w, out, in, ldw}};
-  if (ar_status_t st = pack(m, 2, 1, scratch, scratch_bytes, sms, s)) return st;
+  if (tokens > kFewTokens)
+    if (ar_status_t st = pack(m, 2, 1, scratch, scratch_bytes, sms, s)) return st;
   ar::GemmArgs g = {};
   g.a0 = m[0].p, g.lda = (int64_t)m[0].ld;
   g.b0 = m[1].p, g.ldb = (int64_t)m[1].ld;
@@ -366,7 +371,7 @@ ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, cons
 size_t ar_linear_i8_scratch_bytes(const int8_t* x, size_t ldx, const int8_t* w, size_t ldw, size_t tokens, size_t in,
                                   size_t out) {
   const Rows m[2] = {{x, tokens, in, ldx}, {w, out, in, ldw}};
-  return pack_bytes(m, 2, 1);
+  return tokens > kFewTokens ? pack_bytes(m, 2, 1) : 0;
 }
 
 ar_status_t ar_ops_get_device_status(void* stream) {

@@ -163,6 +163,38 @@ __device__ __forceinline__ void act_slope(float v, float& f, float& df) {
   }
 }
 
+// 16 bytes that begin o bytes into the aligned 32 of u and v.
+__device__ __forceinline__ uint4 shift_window(const uint4& u, const uint4& v, uint32_t o) {
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  uint32_t by8[6], by4[5], r[4];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) by8[i] = o & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) by4[i] = o & 4 ? by8[i + 1] : by8[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(by4[i], by4[i + 1], 8 * (o & 3));
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// 16 bytes at p, which may lie anywhere: the two aligned 16-byte pieces around
+// them, shifted into place.  `left` of them may be read, the rest is zero; what
+// would touch memory before `begin` or from `end` on (a matrix's first and last
+// elements) is read an element of B bytes at a time.
+template <int B>
+__device__ __forceinline__ uint4 load_anywhere(const char* p, int64_t left, const char* begin, const char* end) {
+  const uint32_t o = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* base = reinterpret_cast<const uint4*>(p - o);
+  if (left >= 16 && p - o >= begin && p - o + 32 <= end) return shift_window(__ldg(base), __ldg(base + 1), o);
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int i = 0; i < 16 / B; ++i)
+    if (i * B < left) {
+      const uint32_t v = B == 2 ? ld_elem<2>(p + 2 * i) : *reinterpret_cast<const uint8_t*>(p + i);
+      w[i * B / 4] |= v << (8 * (i * B % 4));
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A 16-bit type's two-element word and its mma.sync.
 template <class E>
 struct IsBf16 {

@@ -220,13 +220,14 @@ struct FfnInputs {
   const at::Tensor &x, &wg, &wu;
   int64_t ldx, ldw, m;
   at::Tensor room;
-  FfnInputs(const Ffn& f, PyObject* xo, PyObject* wgo, PyObject* wuo)
+  FfnInputs(const Ffn& f, PyObject* xo, PyObject* wgo, PyObject* wuo, bool backward)
       : x(tensor(xo, "x")), wg(tensor(wgo, "w_gate")), wu(tensor(wuo, "w_up")) {
     ldx = matrix(x, "x", f.type, f.index, kAny, f.hidden);
     ldw = matrix(wg, "w_gate", f.type, f.index, f.width, f.hidden);
     if (matrix(wu, "w_up", f.type, f.index, f.width, f.hidden) != ldw)
       refuse("w_gate and w_up must have the same row stride");
     m = x.size(0);
+    if (m <= 32 && !backward) return;  // read as they are
     if (unaligned(x, ldx, 2) || unaligned(wg, ldw, 2) || unaligned(wu, ldw, 2))
       room = scratch(ar_ffn_scratch_bytes(f.h, x.data_ptr(), ldx, wg.data_ptr(), wu.data_ptr(), ldw, m), x);
   }
@@ -236,7 +237,7 @@ struct FfnInputs {
 PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject* {
     const Ffn f(a[0]);
-    FfnInputs in(f, a[1], a[2], a[3]);
+    FfnInputs in(f, a[1], a[2], a[3], false);
     int64_t ldo;
     const at::Tensor out = output(a[4], "out", f.type, f.index, in.m, f.width, in.x, &ldo);
     at::Tensor gate, up;
@@ -262,7 +263,7 @@ PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> PyObject* {
     const Ffn f(a[0]);
-    FfnInputs in(f, a[1], a[2], a[3]);
+    FfnInputs in(f, a[1], a[2], a[3], true);
     if (in.m > f.max_tokens)
       refuse("x has " + std::to_string(in.m) + " rows, the handle's workspace " + std::to_string(f.max_tokens));
     const at::Tensor &gate = tensor(a[4], "gate"), &up = tensor(a[5], "up"), &dout = tensor(a[6], "dout");

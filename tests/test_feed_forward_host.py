@@ -84,10 +84,11 @@ def test_linear_i8_refuses(lib, change, want):
 def test_linear_i8_scratch_bytes(lib):
     """Only rows that do not start on 16 bytes are counted, each rounded up to 128."""
     f = lib.ar_linear_i8_scratch_bytes
-    assert f(16, 32, 32, 32, 5, 32, 7) == 0
-    assert f(17, 32, 32, 32, 5, 32, 7) == 5 * 128
-    assert f(16, 133, 32, 133, 5, 133, 7) == (5 + 7) * 256
-    assert f(16, 32, 33, 32, 5, 20, 7) == 7 * 128
+    assert f(16, 32, 32, 32, 50, 32, 7) == 0
+    assert f(17, 32, 32, 32, 50, 32, 7) == 50 * 128
+    assert f(16, 133, 32, 133, 50, 133, 7) == (50 + 7) * 256
+    assert f(16, 32, 33, 32, 50, 20, 7) == 7 * 128
+    assert f(17, 33, 33, 33, 32, 20, 7) == 0  # few tokens are read where they are
 
 
 def test_python_refuses_what_is_not_on_a_gpu():

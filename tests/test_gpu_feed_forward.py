@@ -88,7 +88,7 @@ def test_forward_sizes(ar, size, dtype, act):
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
-@pytest.mark.parametrize("size", [(1, 264, 72), (13, 136, 264), (150, 264, 200)])
+@pytest.mark.parametrize("size", [(1, 264, 72), (13, 136, 264), (30, 2056, 72), (6, 1040, 40), (150, 264, 200)])
 @pytest.mark.parametrize("dtype,act", [(BF16, "gelu"), (FP16, "silu")])
 def test_forward_layouts(ar, size, layout, dtype, act):
     run_forward(ar, *size, dtype, act, *layout, seed=1)
@@ -410,8 +410,8 @@ def test_linear_i8_sizes(ar, size, dtype):
     run_i8(ar, *size, dtype)
 
 
-@pytest.mark.parametrize("layout", [(0, 0), (16, 0), (8, 0), (5, 0), (0, 1), (3, 3), (0, 8)])
-@pytest.mark.parametrize("size", [(1, 272, 72), (9, 272, 72), (150, 272, 200)])
+@pytest.mark.parametrize("layout", [(0, 0), (16, 0), (8, 0), (5, 0), (0, 1), (3, 3), (0, 8), (1, 15)])
+@pytest.mark.parametrize("size", [(1, 272, 72), (9, 272, 72), (30, 2064, 72), (6, 4112, 40), (70, 272, 200), (150, 272, 200)])
 def test_linear_i8_layouts(ar, size, layout):
     run_i8(ar, *size, BF16, *layout)
 
