@@ -14,7 +14,7 @@
 //
 // Roles, persistent over tiles of 128 CG x bn: one thread copies int8 tiles of
 // 128 k into a staging ring by tensor maps, groups of warps convert them, one
-// thread issues the matrix instructions, four warps scale and store.  Four
+// thread issues the matrix instructions, eight warps scale and store.  Four
 // groups of converters take steps of 64 k in turn, so that their latencies
 // overlap, and eight operand stages cover the way from a conversion through the
 // pair's barriers and the instruction back to a free stage.  A pair of CTAs (CG = 2) shares one instruction over
@@ -25,13 +25,14 @@
 // a cluster whose KS CTAs split k, and the sums are sent to the CTAs' shared
 // memory, quarter of the channels by quarter, and added in the order of the parts.
 //
-// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 284-287 us, 1,920
-// TFLOP/s counted as products, what a 16-bit library product reaches here (315
-// us in a loop under the power limit).  It was 395 us with x in shared memory,
-// 387 with x in tensor memory, 365 with eight operand stages instead of four, and
-// 287 with the arrivals on the pair's barriers ordered at the CTA's scope.
-// 440 x 2048 -> 5120: 14 us, of which about 7 are launch, set-up and the last
-// tile.  64 tokens 3584 -> 8192: 13.4 us (16.9 by padded tiles of tokens).
+// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 273 us, 2,010
+// TFLOP/s counted as products (a 16-bit library product of 8192^3 reached 1,924);
+// 306 us in a loop under the power limit.  It was 395 us with x in shared memory,
+// 387 with x in tensor memory, 365 with eight operand stages instead of four, 285
+// with the arrivals on the pair's barriers ordered at the CTA's scope, 273 with
+// eight instead of four warps storing.  440 x 2048 -> 5120: 13.5 us, of which
+// about 7 are launch, set-up and the last tile.  64 tokens 3584 -> 8192: 13.4 us
+// (16.9 by padded tiles of tokens).
 #include "tc_device.cuh"
 
 namespace ar {
@@ -45,7 +46,9 @@ constexpr uint32_t kOperand = (kRowsMax - 128) * 128;  // of an operand stage of
 constexpr int kSS = 3, kOS = 8;                      // stages of the two rings
 constexpr int kGroups = 4, kGroupWarps = 4;          // converters: a warp for each quarter of tensor memory's lanes
 constexpr int kGroupThreads = 32 * kGroupWarps;
-constexpr int kI8Threads = 32 * 6 + kGroups * kGroupThreads;
+constexpr int kStoreWarps = 8;                       // two for each quarter, taking turns by 32 columns
+constexpr int kFirstConverter = 2 + kStoreWarps;     // warp
+constexpr int kI8Threads = 32 * kFirstConverter + kGroups * kGroupThreads;
 constexpr int kPieces = (kRowsMax - 128) / (8 * kGroupWarps);  // 16-byte pieces of w that a converter takes of a step
 constexpr uint32_t kI8Smem = kSS * kStaged + kOS * kOperand + 1024;
 // Tensor memory: accumulators from column 0, two of up to 128 columns or one of
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(done + 8 * i, 1);
-      bar_init(freed + 8 * i, 4 * CG);
+      bar_init(freed + 8 * i, kStoreWarps * CG);
     }
     bar_init(drained, 1);
     dead = 0;
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         bar_wait_copies(drained, 0);
       }
     }
-  } else if (warp < 6 && !SWAP) {
+  } else if (warp < kFirstConverter && !SWAP) {
     const uint32_t lane0 = (uint32_t)(warp & 3) * 32;
     uint32_t at = 0;
     for (uint32_t t = first; t < a.walk.tiles; t += stride, ++at) {
@@ -230,13 +233,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       const int64_t m0 = ((int64_t)tile.m * CG + rank) * 128 + lane0, m = m0 + (threadIdx.x & 31);
       const int n0 = tile.n * a.bn;
       // The scales are on their way while the tile is multiplied: a lane holds
-      // its row's, and column 32 j + lane's for every 32 columns.
+      // its row's, and one column's for every 32 columns that the warp stores.
       const float sm = m < a.g.M ? a.g.sm[m] : 0.0f;
-      float sn[kRowsMax / 32];
+      const int c0 = warp < 6 ? 0 : 32;
+      float sn[kRowsMax / 64];
 #pragma unroll
-      for (int j = 0; j < kRowsMax / 32; ++j) {
-        const int n = n0 + 32 * j + (int)(threadIdx.x & 31);
-        sn[j] = 32 * j < a.bn && n < a.g.N ? a.g.sn[n] : 0.0f;
+      for (int j = 0; j < kRowsMax / 64; ++j) {
+        const int n = n0 + c0 + 64 * j + (int)(threadIdx.x & 31);
+        sn[j] = c0 + 64 * j < a.bn && n < a.g.N ? a.g.sn[n] : 0.0f;
       }
       if (!bar_wait(done + 8 * buf, at / accs & 1, &dead)) {
         atomicExch(&g_i8_error, 1u);
@@ -244,8 +248,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
       fence_after_sync();
 #pragma unroll
-      for (int j = 0; j < kRowsMax / 32; ++j) {
-        const int c = 32 * j;
+      for (int j = 0; j < kRowsMax / 64; ++j) {
+        const int c = c0 + 64 * j;
         if (c >= a.bn || n0 + c >= a.g.N) break;
         uint32_t r[32];
         __syncwarp();
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       __syncwarp();
       if (elect_one()) bar_arrive_cluster(map_to_cta(freed + 8 * buf, 0));
     }
-  } else if (warp >= 6) {
+  } else if (warp >= kFirstConverter) {
     // Staged rows are 128 bytes whose 16-byte piece p lies at p ^ (row % 8), and
     // so are w's operand rows.  A step converts half of a staged row, pieces 4h ..
     // 4h + 3.  A thread takes a whole such row of x (eight lanes read eight
@@ -268,7 +272,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     // pieces of rows r and r + 4 (eight banks again) into all eight of an
     // operand row, and the lanes of the second row store their two results in
     // the other order, which again makes eight.
-    const int group = (warp - 6) / kGroupWarps, thread = (int)(threadIdx.x - 6 * 32) % kGroupThreads;
+    const int group = (warp - kFirstConverter) / kGroupWarps;
+    const int thread = (int)(threadIdx.x - kFirstConverter * 32) % kGroupThreads;
     const int lane = thread & 31, j = lane & 3, second = (lane >> 2) & 1;
     const int row0 = (thread >> 5) * 8 + (lane >> 3) + 4 * second;  // of w, + 8 kGroupWarps each time
     const int x_row = (warp & 3) * 32 + lane;
@@ -421,11 +426,11 @@ cudaError_t launch_type(const GemmArgs& g, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-// A tensor map wants rows that start on 16 bytes.
+// A tensor map wants rows that start on 16 bytes, and strides below 2^40.
 bool gemm_i8_takes(int mode, const GemmArgs& g) {
   const int64_t most = (int64_t)1 << 30;
   return mode == kGemmI8 && tc_available() && g.M <= most && g.N <= most && g.K <= most && g.lda % 16 == 0 &&
-         g.ldb % 16 == 0 && ((reinterpret_cast<uintptr_t>(g.a0) | reinterpret_cast<uintptr_t>(g.b0)) & 15u) == 0;
+         g.ldb % 16 == 0 && g.lda < most << 9 && g.ldb < most << 9 && ((reinterpret_cast<uintptr_t>(g.a0) | reinterpret_cast<uintptr_t>(g.b0)) & 15u) == 0;
 }
 
 cudaError_t launch_gemm_i8(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {

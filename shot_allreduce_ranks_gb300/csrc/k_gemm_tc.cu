@@ -370,7 +370,7 @@ bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t 
 }
 
 bool rows_on_16(const void* p, int64_t ld) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && ld < (int64_t)1 << 38;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -385,7 +385,7 @@ bool make_part(TcArgs& a, TcMaps& maps, int which, int dtype, const GemmArgs& g,
   p.steps = (int)ceil_div(g.K, kBK);
   uintptr_t bits = (uintptr_t)g.ldc * 2;
   for (int i = 0; i < outs; ++i) bits |= reinterpret_cast<uintptr_t>(c[i]);
-  p.out_align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  p.out_align = bits % 16 == 0 && rows_on_16(c[0], g.ldc) ? 16 : bits % 4 == 0 ? 4 : 2;
   for (int i = 0; i < outs && p.out_align == 16; ++i)
     if (c[i] && !make_map(&maps.c[c - a.c + i], dtype, c[i], p.M, g.N, g.ldc, p.fold ? 16 : 32, 32)) return false;
   return true;
@@ -508,8 +508,8 @@ cudaError_t grad_type(int dtype, const GemmArgs* dx, const GemmArgs* dw, int num
 
 }  // namespace
 
-// A tensor map wants rows that start on 16 bytes and extents within 32 bits;
-// coordinates are 32-bit.
+// A tensor map wants rows that start on 16 bytes, strides below 2^40 bytes and
+// extents within 32 bits; coordinates are 32-bit.
 bool gemm_tc_takes(int mode, const GemmArgs& g) {
   const int64_t most = (int64_t)1 << 30;
   return mode != kGemmI8 && tc_available() && g.M <= most && g.N <= most && g.K <= most && rows_on_16(g.a0, g.lda) &&

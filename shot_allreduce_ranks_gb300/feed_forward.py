@@ -6,7 +6,8 @@
 and never stored.  Matrices are 2-D CUDA tensors whose rows are contiguous
 (any row stride).  Calls are asynchronous on the current (or given) stream,
 which also owns the outputs that a call allocates, and run on the tensors'
-device.
+device.  torch's differentiation does not record them: the backward passes are
+calls of their own.
 """
 from __future__ import annotations
 
