@@ -25,7 +25,7 @@
 // a cluster whose KS CTAs split k, and the sums are sent to the CTAs' shared
 // memory, quarter of the channels by quarter, and added in the order of the parts.
 //
-// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 273 us, 2,010
+// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 273-283 us, 1,940-2,010
 // TFLOP/s counted as products (a 16-bit library product of 8192^3 reached 1,924);
 // 306 us in a loop under the power limit.  It was 395 us with x in shared memory,
 // 387 with x in tensor memory, 365 with eight operand stages instead of four, 285

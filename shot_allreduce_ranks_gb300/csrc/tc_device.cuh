@@ -266,8 +266,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // Tiles of the output: `group` rows of tiles are walked column by column, so
 // that the tiles in flight at one time form a block whose operands stay in L2.
-// (Eight rows of 256, 8192 tokens x 8192 -> 3584 in loops on one machine: 614 us;
-// four: 634, twelve 625, sixteen 632.)
+// (Eight rows of 256, 8192 tokens x 8192 -> 3584 in loops on one machine:
+// 614 and 619 us in two runs; four: 634, twelve 625, sixteen 632.  Other sizes
+// differ less than their runs do.)
 // 32-bit numbers: a thread that copies or stores finds its next tile by four
 // divisions, which 64-bit ones would make a good part of a short tile's time.
 struct TileWalk {
