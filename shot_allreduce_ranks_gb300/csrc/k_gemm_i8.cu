@@ -25,7 +25,7 @@
 // a cluster whose KS CTAs split k, and the sums are sent to the CTAs' shared
 // memory, quarter of the channels by quarter, and added in the order of the parts.
 //
-// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 273-283 us, 1,940-2,010
+// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 286 us, 1,920
 // TFLOP/s counted as products (a 16-bit library product of 8192^3 reached 1,924);
 // 306 us in a loop under the power limit.  It was 395 us with x in shared memory,
 // 387 with x in tensor memory, 365 with eight operand stages instead of four, 285
@@ -296,9 +296,18 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
         if (row0 + i * 8 * kGroupWarps < rows - 128) load(q[i], 128 + row0 + i * 8 * kGroupWarps, j);
-      // The staged rows are in registers: the next copy need not wait for the operand stage.
-      __syncwarp();
-      if (elect_one()) bar_arrive(taken + 8 * ss);
+      // Once the staged rows are in registers the next copy may come: it need not wait
+      // for the operand stage.  A load that was issued has read nothing yet, and an
+      // arrival can overtake it, so the arrival's address is made of what all lanes
+      // have loaded (blockIdx.y is 0, which the compiler does not know).
+      uint32_t seen = 0;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) seen ^= xq[p].x ^ xq[p].y ^ xq[p].z ^ xq[p].w;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (row0 + i * 8 * kGroupWarps < rows - 128) seen ^= q[i].x ^ q[i].y ^ q[i].z ^ q[i].w;
+      seen = __reduce_or_sync(0xFFFFFFFFu, seen & blockIdx.y);
+      if (elect_one()) bar_arrive(taken + 8 * ss + seen);
       if (!(ok = bar_wait(used + 8 * os, (round & 1) ^ 1, &dead))) break;
       fence_after_sync();
       {

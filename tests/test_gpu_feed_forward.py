@@ -426,6 +426,39 @@ def test_linear_i8_largest_sums(ar, size):
     run_i8(ar, *size, BF16, full=True)
 
 
+@pytest.mark.parametrize("size", [(4096, 8192, 8192), (1030, 8192, 2600), (440, 2048, 5120), (64, 3584, 8192)])
+def test_linear_i8_the_same_bits_every_time(ar, size):
+    """Many launches, half of them beside copies on another stream.  A sum of K products of numbers up to 127 that vary has a
+    standard deviation of 5376 sqrt(K) < 2^19, so that all partial sums fit 24 bits by 30 of them: the sums are
+    exact, and with two products in fp32 and one rounding so are the results' bits."""
+    M, K, N = size
+    g = gen(M + N)
+    x = torch.randint(-127, 128, (M, K), generator=g, device=DEV, dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    sx = torch.rand(M, generator=g, device=DEV) + 0.5
+    sw = (torch.rand(N, generator=g, device=DEV) + 0.5) * (1e-3 / K ** 0.5)
+    want = ((x.double() @ w.double().T).float() * sx[:, None] * sw[None, :]).half()
+    side, room = torch.cuda.Stream(), torch.empty(2, 1 << 26, device=DEV, dtype=torch.uint8)
+    torch.cuda.synchronize()
+    for k in range(80):
+        if k % 2:
+            with torch.cuda.stream(side):
+                for _ in range(1 + k % 5):
+                    room[0].copy_(room[1])
+        assert torch.equal(ar.linear_i8(x, sx, w, sw, dtype=FP16), want), "launch %d" % k
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("size", [(4096, 8192, 3584), (1000, 2056, 520)])
+def test_large_products_have_the_same_bits_every_time(ar, size):
+    M, K, F = size
+    t, ffn = inputs(M, K, F, 3), ar.GatedFFN(M, K, F, dtype=BF16, train=True)
+    first = everything(ar, ffn, t)
+    for _ in range(20):
+        for a, b in zip(first, everything(ar, ffn, t)):
+            assert torch.equal(a, b)
+
+
 # --------------------------------------------------------------------------------------------------- how they are called
 
 def everything(ar, ffn, t, stream=None):
