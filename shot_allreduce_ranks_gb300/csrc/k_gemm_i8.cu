@@ -86,7 +86,6 @@ __device__ __forceinline__ void join_parts(const I8Args& a, uint32_t room, uint3
     uint32_t r[32];
     __syncwarp();
     tmem_load32(r, tmem + ((uint32_t)quarter << 21) + c);
-    tmem_wait_load32(r);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (c + i < M) {
@@ -254,7 +253,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         uint32_t r[32];
         __syncwarp();
         tmem_load32(r, tmem + (lane0 << 16) + buf * kAccStride + c);
-        tmem_wait_load32(r);
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * sm * __shfl_sync(0xFFFFFFFFu, sn[j], i);

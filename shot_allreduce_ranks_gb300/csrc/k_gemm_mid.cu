@@ -145,7 +145,6 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     uint32_t r[32];
     __syncwarp();
     tmem_load32(r, tmem + ((uint32_t)quarter << 21) + c);
-    tmem_wait_load32(r);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (c + i < a.g.M) {

@@ -298,10 +298,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (n0 + c >= part.N) break;
         uint32_t r[32], u[32];
         __syncwarp();
-        tmem_load32(r, acc + c);
-        if (WHAT == kTcGated) tmem_load32(u, acc + cols + c);
-        tmem_wait_load32(r);
-        if (WHAT == kTcGated) tmem_wait_load32(u);
+        if (WHAT == kTcGated)
+          tmem_load32(r, u, acc + c, acc + cols + c);
+        else
+          tmem_load32(r, acc + c);
         // Rows that start on 16 bytes leave through shared memory as boxes of 64-byte
         // rows; a lane storing its own row would touch 32 lines at a time.
         const auto store = [&](int to, const float(&v)[32]) {
