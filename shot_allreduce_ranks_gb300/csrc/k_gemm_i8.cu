@@ -25,14 +25,17 @@
 // a cluster whose KS CTAs split k, and the sums are sent to the CTAs' shared
 // memory, quarter of the channels by quarter, and added in the order of the parts.
 //
-// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 286 us, 1,920
+// Measured on one GB300 (replayed graph): 4096 x 8192 x 8192 282-286 us, 1,920-1,950
 // TFLOP/s counted as products (a 16-bit library product of 8192^3 reached 1,924);
-// 306 us in a loop under the power limit.  It was 395 us with x in shared memory,
-// 387 with x in tensor memory, 365 with eight operand stages instead of four, 285
-// with the arrivals on the pair's barriers ordered at the CTA's scope, 273 with
-// eight instead of four warps storing.  440 x 2048 -> 5120: 13.5 us, of which
-// about 7 are launch, set-up and the last tile.  64 tokens 3584 -> 8192: 13.4 us
-// (16.9 by padded tiles of tokens).
+// 321 us in a loop under the power limit.  Steps on the way, none of which yet
+// waited for a staged row's loads before giving it back, so that rows could be
+// overwritten (waiting costs 3-5%): 395 us with x in shared memory, 387 with x in
+// tensor memory, 365 with eight operand stages instead of four, 285 with the pair's
+// arrivals ordered for shared memory alone (358 now with the cluster's full fence,
+// by two warps that only pass arrivals on), 273 with eight instead of four warps
+// storing.  440 x 2048 -> 5120: 14.2-15.8 us, of which about 7 are launch, set-up
+// and the last tile.  64 tokens 3584 -> 8192: 13.9-15.8 us (16.9 by padded tiles
+// of tokens).
 #include "tc_device.cuh"
 
 namespace ar {
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const uint32_t accs = a.bn <= (int)kAccStride ? 2 : 1;  // accumulators
   const uint32_t part = KS > 1 ? cluster_rank() : 0;       // of k
   const int u0 = (int)((int64_t)a.units * part / KS), u1 = (int)((int64_t)a.units * (part + 1) / KS);
-  const int steps = 2 * (u1 - u0);  // of 64 k
+  const int steps = 2 * (u1 - u0);  // of 64 k, of a tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSS; ++i) {
@@ -175,6 +178,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   pdl_enter();  // nothing before this has touched global memory
   // SWAP: a cluster makes one tile.
   const uint32_t first = blockIdx.x / (CG * KS), stride = SWAP ? 1u << 30 : gridDim.x / CG;
+  const int64_t total = (int64_t)(first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0) * steps;
 
   if (warp == 0) {
     if (elect_one()) {
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         fence_after_sync();
         for (int s = 0; s < steps; ++s, ++it) {
           const uint32_t st = it % kOS;
-          if (!(ok = bar_wait(ready + 8 * st, (it / kOS) & 1, &dead))) break;
+          if (!(ok = bar_wait<CG == 2>(ready + 8 * st, (it / kOS) & 1, &dead))) break;
           fence_after_sync();
           const uint32_t x = tmem + kXCols + st * 32;
           const uint64_t w = operand_desc(operands + st * kOperand, 16, 1024);
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         uint32_t r[32];
         __syncwarp();
         tmem_load32(r, tmem + (lane0 << 16) + buf * kAccStride + c);
-        float v[32];
+            float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * sm * __shfl_sync(0xFFFFFFFFu, sn[j], i);
         store_chunk<E>(a.g.c0, a.g.ldc, m0, n0 + c, a.g.M, a.g.N, v, a.out_align);
@@ -275,7 +279,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int lane = thread & 31, j = lane & 3, second = (lane >> 2) & 1;
     const int row0 = (thread >> 5) * 8 + (lane >> 3) + 4 * second;  // of w, + 8 kGroupWarps each time
     const int x_row = (warp & 3) * 32 + lane;
-    const int64_t total = (int64_t)(first < a.walk.tiles ? (a.walk.tiles - 1 - first) / stride + 1 : 0) * steps;
     bool ok = true;
     int64_t it = group;
     for (; it < total && ok; it += kGroups) {
@@ -340,10 +343,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       fence_async_smem();  // the matrix unit reads through the asynchronous proxy
       __syncwarp();
       if (elect_one()) {
-        if (CG == 2)
+        if (CG == 2) {
+          fence_cluster_smem();  // the pair's first CTA issues, and reads both CTAs' shared memory
           bar_arrive_cluster(map_to_cta(ready + 8 * os, 0));
-        else
+        } else {
           bar_arrive(ready + 8 * os);
+        }
       }
     }
     if (!ok) atomicExch(&g_i8_error, 1u);

@@ -42,18 +42,43 @@ __device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrival on a barrier of any CTA of the cluster.  Ordered at the CTA's scope,
-// which is all that is needed: what it announces lies in this CTA's tensor memory
-// or, behind a proxy fence, in its shared memory, where this SM's own half of the
-// pair's instruction reads it.  (Release at cluster scope took 1,300 clocks.)
+// Arrival on a barrier of any CTA of the cluster that orders no memory between
+// CTAs: enough where it announces that tensor memory has been read (the read was
+// waited for), or behind fence_cluster_smem() for what was written to shared memory.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Orders what this thread did in its CTA's shared memory, and what it has learned
+// of others there, before its next arrivals for every CTA of the cluster.  (All of
+// memory at that scope, as a release does, took 1,300 clocks.)
+__device__ __forceinline__ void fence_cluster_smem() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+
+// CLUSTER: what the arrivals announce was written by other CTAs.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// The same without waiting at all.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
@@ -69,21 +94,23 @@ __device__ __forceinline__ uint64_t now_ns() {
 // waits once one of them has raised *dead.
 constexpr uint64_t kWaitNs = 2000ull * 1000ull * 1000ull;
 
+template <bool CLUSTER>
 static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
   const uint64_t t0 = now_ns();
   for (uint32_t k = 0; k < (1u << 30); ++k) {
-    if (bar_try(bar, parity)) return true;
+    if (bar_try<CLUSTER>(bar, parity)) return true;
     if ((k & 31u) == 31u && (*dead != 0 || now_ns() - t0 > kWaitNs)) break;
   }
   *dead = 1;
   return false;
 }
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
 #pragma unroll 1
   for (int k = 0; k < 16; ++k)
-    if (bar_try(bar, parity)) return true;
-  return bar_wait_slow(bar, parity, dead);
+    if (bar_try<CLUSTER>(bar, parity)) return true;
+  return bar_wait_slow<CLUSTER>(bar, parity, dead);
 }
 
 // The same for what is still under way after a wait gave up.
