@@ -293,8 +293,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int64_t m0 = (((int64_t)tile.m * CG + rank) * 128 + lane0) >> fold;
       const int n0 = tile.n * cols;
       const uint32_t acc = tmem + (lane0 << 16) + buf * 256;
+      // A warp whose rows lie past the last has nothing to store.  It must not go
+      // through the boxes either: their turns below count on a copy for every write.
 #pragma unroll 1
-      for (int c = warp < 6 ? 0 : 32; c < cols; c += 64) {
+      for (int c = warp < 6 ? 0 : 32; c < cols && m0 < part.M; c += 64) {
         if (n0 + c >= part.N) break;
         uint32_t r[32], u[32];
         __syncwarp();
@@ -303,14 +305,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else
           tmem_load32(r, acc + c);
         // Rows that start on 16 bytes leave through shared memory as boxes of 64-byte
-        // rows; a lane storing its own row would touch 32 lines at a time.
+        // rows; a lane storing its own row would touch 32 lines at a time.  Two boxes
+        // take turns, and every write to one is followed by its copy, so the copy that
+        // may still be reading when all but one have is the other box's.
         const auto store = [&](int to, const float(&v)[32]) {
           if (part.out_align < 16) {
             store_chunk<E>(a.c[to], part.ldc, m0, n0 + c, fold ? min(part.M, m0 + 16) : part.M, min(part.N, (int64_t)(n0 + cols)), v, part.out_align);
             return;
           }
           const uint32_t box = boxes + (stored & 1) * 2048, row = box + (uint32_t)lane * 64;
-          if (lane == 0) store_box_wait_read<1>();  // the box's last copy but one has been read
+          if (lane == 0) store_box_wait_read<1>();  // this box's last copy has been read
           __syncwarp();
 #pragma unroll
           for (int p = 0; p < 4; ++p)
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          "r"(E::pack(v[8 * p + 4], v[8 * p + 5])), "r"(E::pack(v[8 * p + 6], v[8 * p + 7])) : "memory");
           fence_async_smem();
           __syncwarp();
-          if (lane == 0 && m0 < part.M) store_box(&maps.c[to], n0 + c, (int)m0, box);
+          if (lane == 0) store_box(&maps.c[to], n0 + c, (int)m0, box);
           ++stored;
         };
         float v[32];
