@@ -343,8 +343,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           if (fold) {
+            // An infinite sum stays as the first parts make it: with an infinite weight
+            // the second's is NaN where nothing was left, or of the other sign.
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += __shfl_down_sync(0xFFFFFFFFu, v[i], 16);
+            for (int i = 0; i < 32; ++i) {
+              const float second = __shfl_down_sync(0xFFFFFFFFu, v[i], 16);
+              v[i] = fabsf(v[i]) < INFINITY ? v[i] + second : v[i];
+            }
           }
           store(which == 0 ? 0 : 1 + tile.z, v);
         }

@@ -12,8 +12,18 @@ struct PackJobs {
   PackJob job[3];
 };
 
-// One matrix's rows, 16 bytes a thread.
-template <int B>
+// Both 16-bit elements of a word, 0 in the place of an infinity or NaN.
+template <class E>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  constexpr uint32_t kExponents = IsBf16<E>::value ? 0x7F807F80u : 0x7C007C00u;
+  return w & ~__vcmpeq2(w & kExponents, kExponents);
+}
+
+// One matrix's rows, 16 bytes a thread.  E, the type of 16-bit elements, matters
+// where rows go to both rows of their token: infinities and NaN go to the first
+// alone, since what a value's rounding left may be 0, or of the other sign, and
+// with an infinity would make NaN of an infinite sum.
+template <int B, class E = F16>
 __device__ __forceinline__ void pack_rows(const PackJob& j) {
   constexpr int G = 16 / B;
   const int64_t per_row = (j.cols + G - 1) / G, total = j.rows * per_row, sources = j.twice ? j.twice : j.rows;
@@ -26,6 +36,8 @@ __device__ __forceinline__ void pack_rows(const PackJob& j) {
     const int64_t source = j.twice ? row / 32 * 16 + row % 16 : row;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (source < sources) v = load_anywhere<B>(begin + (source * j.ld_from + col) * B, (j.cols - col) * B, begin, end);
+    if (B == 2 && j.twice && row % 32 >= 16)
+      v = make_uint4(finite_only<E>(v.x), finite_only<E>(v.y), finite_only<E>(v.z), finite_only<E>(v.w));
     *reinterpret_cast<uint4*>(static_cast<char*>(j.to) + (row * j.ld_to + col) * B) = v;
   }
 }
@@ -60,7 +72,7 @@ __global__ void __launch_bounds__(kGateThreads)
                 int two_parts, const __grid_constant__ PackJobs jobs) {
   pdl_enter();
   if (blockIdx.y > 0) {
-    pack_rows<2>(jobs.job[blockIdx.y - 1]);
+    pack_rows<2, E>(jobs.job[blockIdx.y - 1]);
     return;
   }
   const int64_t total = (two_parts ? (rows + 15) / 16 * 16 : rows) * groups_per_row;

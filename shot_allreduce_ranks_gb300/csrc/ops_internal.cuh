@@ -96,7 +96,7 @@ struct PackJob {
   const void* from;
   void* to;
   int64_t rows, cols, ld_from, ld_to;  // elements
-  int64_t twice;  // 0, or the source's rows, each copied to both rows of its token in two-part rows
+  int64_t twice;  // 0, or the source's rows, each copied to both rows of its token in two-part rows (see pack_rows)
 };
 cudaError_t launch_pack(const PackJob* jobs, int count, int elem_bytes, int num_sms, cudaStream_t s);
 

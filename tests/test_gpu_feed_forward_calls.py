@@ -1,0 +1,60 @@
+"""What the feed-forward operators do with values, handles and tensors at the edges of their contracts."""
+import pytest
+import torch
+
+from shot_allreduce_ranks_gb300 import build
+from tests import ff_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF16, FP16 = torch.bfloat16, torch.float16
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def ar():
+    build.build()
+    import shot_allreduce_ranks_gb300
+    return shot_allreduce_ranks_gb300
+
+
+def normal(g, rows, cols, dtype=BF16, scale=1.0):
+    return (torch.randn(rows, cols, generator=g, device=DEV) * scale).to(dtype)
+
+
+def same_kind(got, want, unknown):
+    """Infinities where the definition has them, with its sign, NaN where it has NaN, numbers elsewhere."""
+    got = got.double()
+    same = torch.where(torch.isfinite(want), torch.isfinite(got), (got == want) | (torch.isnan(got) & torch.isnan(want)))
+    return bool((same | unknown).all())
+
+
+@pytest.mark.parametrize("M", [3, 16, 40, 64, 65, 200])
+@pytest.mark.parametrize("dtype,act", [(BF16, "silu"), (FP16, "gelu")])
+@pytest.mark.parametrize("K,F", [(136, 72), (131, 77)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_gradients_of_operands_that_are_not_finite(ar, M, dtype, act, K, F, bad):
+    """An infinity in x or in a weight makes the sums that it takes part in infinite, not NaN, at any number of
+    tokens."""
+    g = torch.Generator(device=DEV).manual_seed(M)
+    x, wg, wu = normal(g, M, K, dtype), normal(g, F, K, dtype), normal(g, F, K, dtype)
+
+    def away(t):  # no value below 1/8, where a product of three could vanish in 16 bits
+        return torch.where(t.abs() < 0.125, torch.full_like(t, 0.125), t)
+
+    gate, up, dout = (away(normal(g, M, F, dtype)) for _ in range(3))
+    x[M - 1, 5] = bad
+    wg[F - 2, 7] = bad
+    wu[3, K - 1] = bad
+    with ar.GatedFFN(M, K, F, dtype=dtype, activation=act, train=True) as ffn:
+        dx, dwg, dwu = ffn.backward(x, wg, wu, gate, up, dout)
+    f, df, _, edf = ref.activation(gate.double(), act)
+    a, b = dout.double() * up.double() * df, dout.double() * f
+    # where the slope's sign lies within its rounding, or a factor may be 0 in 16 bits, either is right
+    near_a, near_b = (df.abs() <= edf) | (a.abs() <= 2 * ref.TINY[dtype]), b.abs() <= 2 * ref.TINY[dtype]
+    # on the host: the definition's own infinities, summed one by one
+    a, b, xd, wgd, wud = (t.double().cpu() for t in (a, b, x, wg, wu))
+    near_a, near_b, bad_x, bad_g, bad_u = (t.double().cpu() for t in (near_a, near_b, *(~torch.isfinite(t) for t in (x, wg, wu))))
+    for got, want, unknown, what in ((dx, a @ wgd + b @ wud, near_a @ bad_g + near_b @ bad_u, "dx"),
+                                     (dwg, a.T @ xd, near_a.T @ bad_x, "dw_gate"), (dwu, b.T @ xd, near_b.T @ bad_x, "dw_up")):
+        assert not torch.isfinite(want).all() and (unknown == 0).any()
+        assert same_kind(got.cpu(), want, unknown > 0), what
