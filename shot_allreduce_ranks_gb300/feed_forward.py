@@ -4,10 +4,10 @@
 ``linear_i8`` (with ``quantize_rows``) the down projection in 8-bit integers,
 ``dropout`` the step after the sum, its mask drawn from the elements' places
 and never stored.  Matrices are 2-D CUDA tensors whose rows are contiguous
-(any row stride).  Calls are asynchronous on the current (or given) stream,
-which also owns the outputs that a call allocates, and run on the tensors'
-device.  torch's differentiation does not record them: the backward passes are
-calls of their own.
+(any row stride).  Calls are asynchronous on the current (or given) stream of
+the tensors' device, which also owns the outputs that a call allocates; a
+given stream of another device is refused.  torch's differentiation does not
+record them: the backward passes are calls of their own.
 """
 from __future__ import annotations
 
@@ -36,6 +36,13 @@ def _load_ops():
 
 
 _ops = _load_ops()
+
+
+def _current(stream, device):
+    """The context in which `stream` is the current one of `device`, which it has to belong to."""
+    if device is not None and stream.device != device:
+        raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
 
 
 class GatedFFN:
@@ -88,7 +95,7 @@ class GatedFFN:
     def forward(self, x, w_gate, w_up, out=None, gate=None, up=None, save: bool = False, stream=None):
         """``out``; with ``save`` (or given ``gate`` and ``up``) ``(out, gate, up)``."""
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _current(stream, self.device):
                 return self.forward(x, w_gate, w_up, out, gate, up, save)
         return _ops.ffn_forward(self._constants, x, w_gate, w_up, out, gate, up, save)
 
@@ -96,7 +103,7 @@ class GatedFFN:
                  need_dx: bool = True, need_dw: bool = True, stream=None):
         """``(dx, dw_gate, dw_up)`` from the saved ``gate`` and ``up``; None for what is not needed."""
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with _current(stream, self.device):
                 return self.backward(x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, need_dx, need_dw)
         return _ops.ffn_backward(self._constants, x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, need_dx,
                                  need_dw)
@@ -110,7 +117,7 @@ def dropout(x, p: float, seed: int, sequence: int = 0, offset: int = 0, residual
     ``seed`` and ``sequence`` name; equal arguments draw equal masks.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _current(stream, getattr(x, "device", None)):
             return _ops.dropout(x, p, seed, sequence, offset, residual, out)
     return _ops.dropout(x, p, seed, sequence, offset, residual, out)
 
@@ -118,7 +125,7 @@ def dropout(x, p: float, seed: int, sequence: int = 0, offset: int = 0, residual
 def dropout_backward(dy, p: float, seed: int, sequence: int = 0, offset: int = 0, dx=None, stream=None):
     """Gradient of ``dropout`` with respect to x (that of ``residual`` is dy)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _current(stream, getattr(dy, "device", None)):
             return _ops.dropout_backward(dy, p, seed, sequence, offset, dx)
     return _ops.dropout_backward(dy, p, seed, sequence, offset, dx)
 
@@ -129,7 +136,7 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     The rows of a new ``q`` start on 16 bytes, so that ``linear_i8`` reads them as they are.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _current(stream, getattr(x, "device", None)):
             return _ops.quantize_rows(x, q, scale)
     return _ops.quantize_rows(x, q, scale)
 
@@ -140,7 +147,7 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
     if code is None or code == AR_FP32:
         raise ValueError("dtype must be torch.bfloat16 or torch.float16, got %s" % dtype)
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _current(stream, getattr(x, "device", None)):
             return _ops.linear_i8(x, x_scale, w, w_scale, out, code)
     return _ops.linear_i8(x, x_scale, w, w_scale, out, code)
 
