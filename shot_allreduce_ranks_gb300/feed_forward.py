@@ -153,6 +153,10 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
 
 
 def ops_device_status(stream=None) -> int:
-    """AR_OK, or AR_ERR_TIMEOUT if a wait in one of these operators' kernels gave up (clears it)."""
+    """AR_OK, or AR_ERR_TIMEOUT if a wait in one of these operators' kernels gave up (clears it).
+
+    Read on the device of the given stream, or of the current one.
+    """
     s = torch.cuda.current_stream() if stream is None else stream
-    return load().ar_ops_get_device_status(s.cuda_stream)
+    with torch.cuda.device(s.device):
+        return load().ar_ops_get_device_status(s.cuda_stream)

@@ -55,3 +55,11 @@ def test_a_stream_of_another_device_is_refused(ff, monkeypatch, devices):
                  lambda: ff.quantize_rows(x, stream=s), lambda: ff.linear_i8(x, x, x, x, stream=s)):
         with pytest.raises(ValueError, match="stream is on cuda:1"):
             call()
+
+
+def test_the_status_is_read_on_the_streams_device(ff, monkeypatch, devices):
+    read = []
+    lib = SimpleNamespace(ar_ops_get_device_status=lambda s: read.append((devices[0], s)) or 0)
+    monkeypatch.setattr(ff, "load", lambda: lib)
+    assert ff.ops_device_status(on(1)) == 0
+    assert read == [(1, 71)]
