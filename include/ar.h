@@ -480,7 +480,8 @@ typedef struct ar_ffn_ctx* ar_ffn_t;
 ar_status_t ar_ffn_create(size_t max_tokens, size_t hidden, size_t width, int dtype,
                           int activation, int train, ar_ffn_t* out);
 
-/* ar_ffn_destroy -- synchronise the device and free the handle.  NULL is accepted. */
+/* ar_ffn_destroy -- synchronise the device and free the handle.  NULL is
+ * accepted.  Not while a stream is being captured. */
 ar_status_t ar_ffn_destroy(ar_ffn_t h);
 
 /* ar_ffn_forward -- out = act(x Wgate^T) * (x Wup^T), in one kernel.

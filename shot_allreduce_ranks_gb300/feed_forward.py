@@ -45,13 +45,38 @@ def _current(stream, device):
     return torch.cuda.stream(stream)
 
 
+# Freeing a workspace waits for the device, which ends a capture with an error.
+# Handles that are collected during one wait here for the next handle that is made or closed.
+_late = []
+
+
+def _capturing(device) -> bool:
+    """Whether the device's current stream is being captured into a graph."""
+    if torch.cuda.current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _destroy(h, device) -> None:
+    with torch.cuda.device(device):
+        check(load().ar_ffn_destroy(h), "ar_ffn_destroy")
+
+
+def _destroy_late() -> None:
+    while _late and not _capturing(_late[-1][1]):
+        _destroy(*_late.pop())
+
+
 class GatedFFN:
     """One rank's gated feed-forward shard: ``act(x Wgate^T) * (x Wup^T)``.
 
     ``hidden`` is the width of x, ``width`` this rank's rows of both weight
     matrices.  ``train=True`` also allocates the workspace of ``backward`` for
     up to ``max_tokens`` rows; without it ``backward`` is refused.
-    ``backward`` calls share that workspace: order them on one stream.
+    ``backward`` calls share that workspace: order them on one stream.  Freeing
+    it waits for the device: ``close`` is refused while a graph is being
+    captured, and a handle that is collected then is freed later.
     """
 
     def __init__(self, max_tokens: int, hidden: int, width: int, dtype=torch.bfloat16,
@@ -66,6 +91,7 @@ class GatedFFN:
             raise ValueError("dtype must be torch.bfloat16 or torch.float16, got %s" % dtype)
         index = None if device is None else torch.device(device).index
         self.device = torch.device("cuda", torch.cuda.current_device() if index is None else index)
+        _destroy_late()
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
             check(load().ar_ffn_create(self.max_tokens, self.hidden, self.width, _CODES[dtype],
@@ -76,13 +102,18 @@ class GatedFFN:
 
     def close(self) -> None:
         if getattr(self, "_h", None):
-            with torch.cuda.device(self.device):
-                check(load().ar_ffn_destroy(self._h), "ar_ffn_destroy")
-            self._h = self._constants = None
+            if self.train and _capturing(self.device):
+                raise RuntimeError("a GatedFFN with a workspace is not closed while a graph is being captured")
+            h, self._h, self._constants = self._h, None, None
+            _destroy(h, self.device)
+            _destroy_late()
 
     def __del__(self):
         try:
-            self.close()
+            if self.train and self._h and _capturing(self.device):
+                _late.append((self._h, self.device))
+            else:
+                self.close()
         except Exception:
             pass
 

@@ -63,3 +63,33 @@ def test_the_status_is_read_on_the_streams_device(ff, monkeypatch, devices):
     monkeypatch.setattr(ff, "load", lambda: lib)
     assert ff.ops_device_status(on(1)) == 0
     assert read == [(1, 71)]
+
+
+@pytest.fixture
+def destroyed(ff, monkeypatch, devices):
+    calls = []
+    monkeypatch.setattr(ff, "load", lambda: SimpleNamespace(ar_ffn_destroy=lambda h: calls.append((devices[0], h)) or 0))
+    return calls
+
+
+def test_a_handle_dropped_during_a_capture_is_freed_after_it(ff, monkeypatch, destroyed):
+    capturing = [True]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    a, b = handle(ff, 1), handle(ff, 0)
+    del a
+    assert destroyed == []
+    with pytest.raises(RuntimeError, match="captured"):
+        b.close()
+    assert destroyed == [] and b._h == 99
+    capturing[0] = False
+    b.close()
+    assert sorted(destroyed) == [(0, 99), (1, 99)]
+    b.close()
+    assert len(destroyed) == 2
+
+
+def test_a_handle_without_a_workspace_is_freed_at_any_time(ff, monkeypatch, destroyed):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    a = handle(ff, 0, train=False)
+    del a
+    assert destroyed == [(0, 99)]

@@ -1,4 +1,6 @@
 """What the feed-forward operators do with values, handles and tensors at the edges of their contracts."""
+import gc
+
 import pytest
 import torch
 
@@ -58,3 +60,41 @@ def test_gradients_of_operands_that_are_not_finite(ar, M, dtype, act, K, F, bad)
                                      (dwg, a.T @ xd, near_a.T @ bad_x, "dw_gate"), (dwu, b.T @ xd, near_b.T @ bad_x, "dw_up")):
         assert not torch.isfinite(want).all() and (unknown == 0).any()
         assert same_kind(got.cpu(), want, unknown > 0), what
+
+
+def small(ar, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    M, K, F = 40, 64, 72
+    return (M, K, F), (normal(g, M, K), normal(g, F, K), normal(g, F, K), *(normal(g, M, F) for _ in range(3)))
+
+
+def test_a_handle_collected_while_a_graph_is_captured(ar):
+    """Its workspace is freed later: freeing waits for the device, which would end the capture."""
+    (M, K, F), t = small(ar)
+    ffn = ar.GatedFFN(M, K, F, train=True)
+    ffn.backward(*t)
+    torch.cuda.synchronize()
+    graph, x = torch.cuda.CUDAGraph(), torch.ones(8, device=DEV)
+    with torch.cuda.graph(graph):
+        y = x + 1
+        del ffn
+        gc.collect()
+        z = y * 2
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((z == 4).all())
+
+
+def test_a_handle_is_not_closed_while_a_graph_is_captured(ar):
+    """Asked for by name, it is refused before the capture is broken."""
+    (M, K, F), t = small(ar)
+    ffn = ar.GatedFFN(M, K, F, train=True)
+    graph, x = torch.cuda.CUDAGraph(), torch.ones(8, device=DEV)
+    with torch.cuda.graph(graph):
+        y = x + 1
+        with pytest.raises(RuntimeError, match="captured"):
+            ffn.close()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((y == 2).all())
+    ffn.close()
