@@ -481,7 +481,9 @@ ar_status_t ar_ffn_create(size_t max_tokens, size_t hidden, size_t width, int dt
                           int activation, int train, ar_ffn_t* out);
 
 /* ar_ffn_destroy -- synchronise the device and free the handle.  NULL is
- * accepted.  Not while a stream is being captured. */
+ * accepted.  Not while a stream is being captured, nor while a graph that holds
+ * an ar_ffn_backward of the handle may still be launched: the graph keeps the
+ * workspace's address. */
 ar_status_t ar_ffn_destroy(ar_ffn_t h);
 
 /* ar_ffn_forward -- out = act(x Wgate^T) * (x Wup^T), in one kernel.

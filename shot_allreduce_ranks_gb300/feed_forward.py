@@ -76,8 +76,13 @@ class GatedFFN:
     up to ``max_tokens`` rows; without it ``backward`` is refused.
     ``backward`` calls share that workspace: order them on one stream.  Freeing
     it waits for the device: ``close`` is refused while a graph is being
-    captured, and a handle that is collected then is freed later.
+    captured, and a handle that is collected then is freed later.  A graph that
+    holds a ``backward`` holds the workspace's address: such a handle
+    (``captured``) is freed by ``close`` alone, to be called when no such graph
+    is replayed any more, and not by being collected.
     """
+
+    captured = False
 
     def __init__(self, max_tokens: int, hidden: int, width: int, dtype=torch.bfloat16,
                  activation: str = "silu", train: bool = False, device=None):
@@ -110,6 +115,8 @@ class GatedFFN:
 
     def __del__(self):
         try:
+            if self.captured:
+                return
             if self.train and self._h and _capturing(self.device):
                 _late.append((self._h, self.device))
             else:
@@ -136,6 +143,8 @@ class GatedFFN:
         if stream is not None:
             with _current(stream, self.device):
                 return self.backward(x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, need_dx, need_dw)
+        if not self.captured and _capturing(self.device):
+            self.captured = True
         return _ops.ffn_backward(self._constants, x, w_gate, w_up, gate, up, dout, dx, dw_gate, dw_up, need_dx,
                                  need_dw)
 

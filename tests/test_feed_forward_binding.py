@@ -93,3 +93,17 @@ def test_a_handle_without_a_workspace_is_freed_at_any_time(ff, monkeypatch, dest
     a = handle(ff, 0, train=False)
     del a
     assert destroyed == [(0, 99)]
+
+
+def test_a_captured_handle_is_freed_by_close_alone(ff, monkeypatch, destroyed):
+    capturing = [True]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(ff, "_ops", SimpleNamespace(ffn_backward=lambda *a: None))
+    a, b = handle(ff), handle(ff)
+    for h in (a, b):
+        h.backward(*[None] * 6)
+    capturing[0] = False
+    del a
+    assert destroyed == []
+    b.close()
+    assert destroyed == [(0, 99)]

@@ -98,3 +98,25 @@ def test_a_handle_is_not_closed_while_a_graph_is_captured(ar):
     torch.cuda.synchronize()
     assert bool((y == 2).all())
     ffn.close()
+
+
+def test_a_captured_backward_keeps_its_workspace(ar):
+    """The graph holds the workspace's address, so dropping the handle does not free it."""
+    (M, K, F), t = small(ar)
+    ffn = ar.GatedFFN(M, K, F, train=True)
+    want = ffn.backward(*t)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ffn.backward(*t)
+    assert ffn.captured
+    del ffn
+    gc.collect()
+    others = [ar.GatedFFN(M, K, F, train=True) for _ in range(3)]
+    for o in others:
+        o.backward(*t[:5], t[5] * 3)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for o in others:
+        assert not o.captured
+        o.close()
