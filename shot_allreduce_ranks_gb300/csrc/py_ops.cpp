@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_strided.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -63,6 +64,16 @@ const at::Tensor& tensor(PyObject* o, const char* what) {
 int gpu_of(const at::Tensor& t, const char* what) {
   if (!t.is_cuda()) refuse(std::string(what) + " must be a CUDA tensor");
   return t.get_device();
+}
+
+// A result carries no history, so a gradient that the caller's backward pass
+// would have sent to this input is lost: worth a word.
+void no_history(const at::Tensor& t, const char* what) {
+  if (!t.requires_grad() || !c10::GradMode::is_enabled()) return;
+  if (PyErr_WarnFormat(PyExc_UserWarning, 2,
+                       "%s requires grad, but torch's differentiation does not record this operator: its result carries "
+                       "no gradient. Call the operator's backward pass, and this under torch.no_grad().", what) < 0)
+    throw Raised{};
 }
 
 constexpr int64_t kAny = -1;
@@ -238,6 +249,9 @@ PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject* {
     const Ffn f(a[0]);
     FfnInputs in(f, a[1], a[2], a[3], false);
+    no_history(in.x, "x");
+    no_history(in.wg, "w_gate");
+    no_history(in.wu, "w_up");
     int64_t ldo;
     const at::Tensor out = output(a[4], "out", f.type, f.index, in.m, f.width, in.x, &ldo);
     at::Tensor gate, up;
@@ -296,11 +310,13 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const double p = real(a[1]);
     const uint64_t seed = unsigned_word(a[2]), sequence = unsigned_word(a[3]), offset = unsigned_word(a[4]);
     const int64_t ldx = matrix(x, "x", x.scalar_type(), index), rows = x.size(0), cols = x.size(1);
+    no_history(x, "x");
     int64_t ldr = 0, ldo;
     const void* r = nullptr;
     if (a[5] != Py_None) {
       const at::Tensor& t = tensor(a[5], "residual");
       ldr = matrix(t, "residual", x.scalar_type(), index, rows, cols);
+      no_history(t, "residual");
       r = t.data_ptr();
     }
     const at::Tensor out = output(a[6], "out", x.scalar_type(), index, rows, cols, x, &ldo);
@@ -334,6 +350,7 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& x = tensor(a[0], "x");
     const int index = gpu_of(x, "x"), code = type_code(x.scalar_type(), "x", false);
     const int64_t ldx = matrix(x, "x", x.scalar_type(), index), rows = x.size(0), cols = x.size(1);
+    no_history(x, "x");
     int64_t ldq = (cols + 15) / 16 * 16;
     // A new q's rows start on 16 bytes, as the product wants them.
     const at::Tensor q = a[1] != Py_None ? output(a[1], "q", at::kChar, index, rows, cols, x, &ldq)
@@ -365,6 +382,8 @@ PyObject* linear_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ldw = matrix(w, "w", at::kChar, index, kAny, in), cols = w.size(0);
     vector(sx, "x_scale", rows, index);
     vector(sw, "w_scale", cols, index);
+    no_history(sx, "x_scale");
+    no_history(sw, "w_scale");
     const at::ScalarType type = a[4] == Py_None ? type_of((int)integer(a[5])) : tensor(a[4], "out").scalar_type();
     const int code = type_code(type, "dtype", true);
     int64_t ldy;

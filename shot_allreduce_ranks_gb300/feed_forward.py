@@ -7,7 +7,8 @@ and never stored.  Matrices are 2-D CUDA tensors whose rows are contiguous
 (any row stride).  Calls are asynchronous on the current (or given) stream of
 the tensors' device, which also owns the outputs that a call allocates; a
 given stream of another device is refused.  torch's differentiation does not
-record them: the backward passes are calls of their own.
+record them: the backward passes are calls of their own, and a forward pass
+warns where an input requires grad (not under ``torch.no_grad()``).
 """
 from __future__ import annotations
 

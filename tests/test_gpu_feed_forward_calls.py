@@ -1,5 +1,6 @@
 """What the feed-forward operators do with values, handles and tensors at the edges of their contracts."""
 import gc
+import warnings
 
 import pytest
 import torch
@@ -120,3 +121,31 @@ def test_a_captured_backward_keeps_its_workspace(ar):
     for o in others:
         assert not o.captured
         o.close()
+
+
+def test_gradients_are_not_lost_without_a_word(ar):
+    (M, K, F), (x, wg, wu, *_) = small(ar)
+    p = torch.nn.Parameter(wg)
+    w8, s8 = torch.ones(8, F, dtype=torch.int8, device=DEV), torch.ones(8, device=DEV)
+    with ar.GatedFFN(M, K, F) as ffn:
+        with pytest.warns(UserWarning, match="w_gate requires grad"):
+            h = ffn.forward(x, p, wu)
+        assert not h.requires_grad
+        with pytest.warns(UserWarning, match="x requires grad"):
+            ar.dropout(x.clone().requires_grad_(), 0.5, 1)
+        with pytest.warns(UserWarning, match="residual requires grad"):
+            ar.dropout(x, 0.5, 1, residual=x.clone().requires_grad_())
+        with pytest.warns(UserWarning, match="x requires grad"):
+            q, s = ar.quantize_rows(h.clone().requires_grad_())
+        with pytest.warns(UserWarning, match="w_scale requires grad"):
+            ar.linear_i8(q, s, w8, s8.clone().requires_grad_())
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with torch.no_grad():
+                ffn.forward(x, p, wu)
+                ar.dropout(x.clone().requires_grad_(), 0.5, 1)
+            ffn.forward(x, wg, wu)
+            ar.linear_i8(q, s, w8, s8)
+        with warnings.catch_warnings(), pytest.raises(UserWarning):
+            warnings.simplefilter("error")
+            ffn.forward(x, p, wu)
