@@ -3,7 +3,8 @@
 Thin Python binding of libar_gb300.so (C ABI in include/ar.h).  PyTorch only
 provides device memory and streams here; every step of the reduction runs in
 the library's CUDA kernels.  Importing this package does not load the
-library; the first ``AllReduce`` does, and fails loudly if it is not built.
+library; the first ``AllReduce`` or feed-forward call does, and fails loudly
+if it is not built.
 The feed-forward operators that stand around the sum in a tensor-parallel
 layer (``GatedFFN``, ``linear_i8``, ``dropout``) are in ``feed_forward``.
 """

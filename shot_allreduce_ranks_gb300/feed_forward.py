@@ -36,7 +36,16 @@ def _load_ops():
     return module
 
 
-_ops = _load_ops()
+class _NotLoaded:
+    """Stands for the binding until its first call, so that importing names needs no built library."""
+
+    def __getattr__(self, name):
+        global _ops
+        _ops = _load_ops()
+        return getattr(_ops, name)
+
+
+_ops = _NotLoaded()
 
 
 def _current(stream, device):

@@ -1,12 +1,17 @@
 """The feed-forward operators' Python face: streams, devices, handles' lifetimes and imports, with stand-ins for
 the GPU's side."""
 import contextlib
+import os
+import subprocess
+import sys
 from types import SimpleNamespace
 
 import pytest
 import torch
 
 from shot_allreduce_ranks_gb300 import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -107,3 +112,18 @@ def test_a_captured_handle_is_freed_by_close_alone(ff, monkeypatch, destroyed):
     assert destroyed == []
     b.close()
     assert destroyed == [(0, 99)]
+
+
+def test_a_star_import_does_not_need_the_library():
+    code = ("import shot_allreduce_ranks_gb300._lib as lib\n"
+            "lib.PKG = '/nonexistent'\n"
+            "from shot_allreduce_ranks_gb300 import *\n"
+            "assert AllReduce and GatedFFN and dropout\n"
+            "try:\n"
+            "    dropout(None, 0.5, 1)\n"
+            "except RuntimeError as e:\n"
+            "    assert 'not built' in str(e), e\n"
+            "else:\n"
+            "    raise SystemExit('a missing binding went unnoticed')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
