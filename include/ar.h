@@ -447,12 +447,14 @@ ar_status_t ar_allreduce_fused_noalloc(int R, const void* const* d_in_tbl,
  * that the call's _scratch_bytes function gives for the same operands (0 where
  * all rows start on 16 bytes; scratch may then be NULL), owned by the caller
  * and free again when the call has completed.  With scratch NULL such operands
- * take a slower kernel.  (Forward products of up to 32 tokens read any rows as
- * they are and use no scratch.)  All calls are
+ * take a slower kernel.  (Forward products of up to AR_FEW_TOKENS tokens read
+ * any rows as they are and use no scratch.)  All calls are
  * asynchronous on `stream`, allocate nothing, synchronise nothing, and can be
  * captured into a CUDA graph.  Outputs must not overlap inputs or one another
  * unless a call says so.
  */
+#define AR_FEW_TOKENS 32
+
 typedef enum {
   AR_ACT_SILU = 0,      /* v / (1 + exp(-v)) */
   AR_ACT_GELU_TANH = 1  /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */

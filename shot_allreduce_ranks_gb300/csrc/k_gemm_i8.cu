@@ -74,7 +74,7 @@ struct I8Args {
 // then, and from there, scaled, to y.
 template <class E, int KS>
 __device__ __forceinline__ void join_parts(const I8Args& a, uint32_t room, uint32_t tmem, uint32_t done, uint32_t tile,
-                                           uint32_t part, bool any, volatile uint32_t* dead) {
+                                           uint32_t part, volatile uint32_t* dead) {
   constexpr int kHere = 4 / KS;  // quarters that a CTA finishes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, M = (int)a.g.M;
   if (!bar_wait(done, 0, dead) && lane == 0) atomicExch(&g_i8_error, 1u);
@@ -93,8 +93,7 @@ __device__ __forceinline__ void join_parts(const I8Args& a, uint32_t room, uint3
     for (int i = 0; i < 32; ++i)
       if (c + i < M) {
         const uint32_t at = to + (uint32_t)((c + i) * 32 + lane) * 4;
-        // A part of no steps adds nothing (its tensor memory was never written).
-        const float v = any ? __uint_as_float(r[i]) : 0.0f;
+        const float v = __uint_as_float(r[i]);
         if (KS > 1)
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
         else
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         uint32_t r[32];
         __syncwarp();
         tmem_load32(r, tmem + (lane0 << 16) + buf * kAccStride + c);
-            float v[32];
+        float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * sm * __shfl_sync(0xFFFFFFFFu, sn[j], i);
         store_chunk<E>(a.g.c0, a.g.ldc, m0, n0 + c, a.g.M, a.g.N, v, a.out_align);
@@ -361,7 +360,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   }
   __syncwarp();
   if (SWAP) {
-    join_parts<E, KS>(a, operands, tmem, done, first, part, steps > 0, &dead);
+    join_parts<E, KS>(a, operands, tmem, done, first, part, &dead);
   } else {
     fence_before_sync();
     __syncthreads();
@@ -413,7 +412,7 @@ cudaError_t launch_pairs(const GemmArgs& g, int num_sms, cudaStream_t s) {
   return launch<E, 2, false, 1>(a, mx, mw, slots * 2, s);
 }
 
-// Up to 128 tokens: as many parts of k as fill the SMs.
+// Up to 128 tokens: as many parts of k as fill the SMs, none of them empty.
 template <class E>
 cudaError_t launch_swapped(const GemmArgs& g, int num_sms, cudaStream_t s) {
   const int64_t tiles = (g.N + 127) / 128;

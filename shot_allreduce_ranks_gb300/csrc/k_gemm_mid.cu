@@ -149,8 +149,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     for (int i = 0; i < 32; ++i)
       if (c + i < a.g.M) {
         const uint32_t at = to + (uint32_t)((c + i) * 32 + lane) * 4;
-        // A part of no steps adds nothing (its tensor memory was never written).
-        const float v = s1 > s0 ? __uint_as_float(r[i]) : 0.0f;
+        const float v = __uint_as_float(r[i]);
         if (KS > 1)
           store_remote(at, v);
         else
@@ -211,6 +210,7 @@ cudaError_t launch(int dtype, const GemmArgs& g, cudaStream_t s) {
   return launch_op(kernel, dim3((unsigned)(tiles * KS)), kMidThreads, kMidSmem, KS, s, a, mx, mg, mu);
 }
 
+// As many parts of k as fill the SMs, none of them empty.
 template <class E, int ACT>
 cudaError_t launch_split(int dtype, const GemmArgs& g, int num_sms, cudaStream_t s) {
   const int64_t tiles = (g.N + 63) / 64, steps = (g.K + kMidBK - 1) / kMidBK;

@@ -29,7 +29,7 @@ constexpr size_t kMaxSize = (size_t)1 << 30;  // the sizes a handle is made for
 constexpr size_t kTwoPartTokens = 64;
 // Up to this many tokens a forward product reads the weights once, where they
 // are: laying them out first costs two passes more.
-constexpr size_t kFewTokens = 32;
+constexpr size_t kFewTokens = AR_FEW_TOKENS;
 
 bool half_type(int dtype) { return dtype == AR_BF16 || dtype == AR_FP16; }
 bool any_type(int dtype) { return half_type(dtype) || dtype == AR_FP32; }

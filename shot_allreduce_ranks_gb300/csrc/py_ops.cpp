@@ -238,7 +238,7 @@ struct FfnInputs {
     if (matrix(wu, "w_up", f.type, f.index, f.width, f.hidden) != ldw)
       refuse("w_gate and w_up must have the same row stride");
     m = x.size(0);
-    if (m <= 32 && !backward) return;  // read as they are
+    if (m <= AR_FEW_TOKENS && !backward) return;  // read as they are
     if (unaligned(x, ldx, 2) || unaligned(wg, ldw, 2) || unaligned(wu, ldw, 2))
       room = scratch(ar_ffn_scratch_bytes(f.h, x.data_ptr(), ldx, wg.data_ptr(), wu.data_ptr(), ldw, m), x);
   }
