@@ -520,7 +520,10 @@ size_t ar_ffn_scratch_bytes(ar_ffn_t h, const void* x, size_t ldx, const void* w
  * Sums in fp32, outputs rounded once.  dgate and dup are rounded to dtype
  * between the two steps, since they are operands of 16-bit tensor-core
  * products; for at most 64 tokens they are kept as the sum of two numbers of
- * dtype (where rows start on 16 bytes, or scratch is given).  The gradients are written, not added to what the outputs held.
+ * dtype (where rows start on 16 bytes, or scratch is given).  So in AR_FP16 a
+ * value of them below 2^-25 counts as 0, and one above 65504 as infinite: scale
+ * the loss, as for any gradients held in that type.  The gradients are written,
+ * not added to what the outputs held.
  * tokens = 0 writes zeros to dw_gate and dw_up.
  * Errors: AR_ERR_INVALID_ARG (also tokens > max_tokens), AR_ERR_UNSUPPORTED
  * (handle made with train = 0), AR_ERR_CUDA. */
@@ -569,8 +572,10 @@ ar_status_t ar_quantize_rows(const void* x, size_t ldx, int8_t* q, size_t ldq, f
  *   x_scale  one float a token, w_scale  one float an output channel,
  *   y  [tokens, out] of dtype AR_BF16 or AR_FP16, leading dimension ldy.
  * Products are exact and sums are held in fp32: exact while partial sums stay
- * within 2^24 (always for in <= 1024), rounded like any fp32 sum beyond.  The
- * sum is multiplied by x_scale, then by w_scale, and rounded once.
+ * within 2^24 (always for in <= 1024).  Beyond, each addition may round or
+ * truncate to 24 bits: the sum is within `in` times 2^-23 of the sum of the
+ * products' absolute values.  The sum is multiplied by x_scale, then by w_scale,
+ * and rounded once.
  * tokens = 0 returns AR_OK without a launch.
  * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (dtype AR_FP32), AR_ERR_CUDA. */
 ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, const int8_t* w,

@@ -8,9 +8,10 @@
 // a copy draws the same one without an exchange, a rank that holds a block
 // draws its part by `offset`, and the backward pass draws it again.
 //
-// Bound by memory with a residual in 16 bits, 6 bytes an element; without one, by
-// the generator's multiplications (18 wide ones for 4 elements, on the pipe that
-// ran at 77% when there were 20 and unpacking used it too).  Measured on one
+// Bound by memory with a residual in 16 bits, 6 bytes an element; without one,
+// nearest to the generator's multiplications (18 wide ones for 4 elements): their
+// pipe is active 68% of the time, more than any other, and memory 53%; neither is
+// full, nor was that pipe at 77% with 20 of them.  Measured on one
 // GB300 (replayed graph): with residual 16384 x 8192 bf16 121.6 us (6.62 TB/s, 98%
 // of a copy's rate); without 113 us (4.8 TB/s); fp32 without, 680 x 5120 at an odd
 // place 8.8 us; one row of 5120 1.9 us, the launch.  A persistent grid of 5 CTAs

@@ -29,10 +29,12 @@
 //   1,900-1,960 TFLOP/s, tensor pipe active 94% of the time (a library product
 //   of 8192^3 reached 1,924); in a loop the power limit takes the clock from
 //   2,070 to about 1,470 MHz and the time to 560 us;
-//   forward 440 x 5120 -> 1736: 18.3 us, of which about 8 are launch, set-up, the
-//   first copies and the last tile's stores (21.0 with six stages for narrow
-//   tiles too, instead of eight);
-//   gradients 4096 x 8192 -> 3584: 545 us (1,770 TFLOP/s); 512 x 8192 -> 3584: 89
+//   forward 440 x 5120 -> 1736: 18.3 us (21.0 with six stages for narrow tiles too,
+//   instead of eight), on 56 of 76 pairs: 80 steps of 128 columns at about 350
+//   clocks, nearer to the copies' 384 than to the instruction's 256, and 4 us of
+//   launch, set-up and last stores (1280, 2560, 10240 instead of 5120: 7.8, 11.3,
+//   31.1 us);
+//   gradients 4096 x 8192 -> 3584: 545 us (1,770 TFLOP/s); 512 x 8192 -> 3584: 89-90
 //   us (tensor pipe active 60%: the weights' tiles have eight steps each).
 // Measured and left out: clusters of four that share A by multicast (the same
 // time: an SM's own intake binds, and only 36 of 38 such clusters fit).
@@ -116,8 +118,10 @@ struct TcMaps {
 // The j-th tile of slot p (a CTA or a pair) of P: its part and number.  dx's tiles
 // come first, round by round; where its last round leaves slots free, those
 // take `ahead` tiles of the weight gradients each (about as many as fit beside one
-// of dx), and the rest goes round all slots.  Every tile has one slot, fixed by
-// its number.
+// of dx), and the rest goes round all slots.  With fewer tiles than the machine has
+// slots `ahead` is 0: the slots with a tile of dx then take the first tiles of the
+// weights' gradients too, and as many of the last slots get none.  Every tile has
+// one slot, fixed by its number.
 template <int WHAT>
 __device__ __forceinline__ bool job_at(const TcArgs& a, uint32_t p, uint32_t P, uint32_t j, int& part, uint32_t& t) {
   t = p + j * P;
