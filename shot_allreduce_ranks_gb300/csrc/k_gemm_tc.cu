@@ -311,9 +311,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // Rows that start on 16 bytes leave through shared memory as boxes of 64-byte
         // rows; a lane storing its own row would touch 32 lines at a time.  Two boxes
         // take turns, and every write to one is followed by its copy, so the copy that
-        // may still be reading when all but one have is the other box's.
+        // may still be reading when all but one have is the other box's.  The copy
+        // engine writes pieces of 16 bytes, zeros past the last column: a box that
+        // reaches past a row whose end lies inside a piece is stored by lanes.
         const auto store = [&](int to, const float(&v)[32]) {
-          if (part.out_align < 16) {
+          if (part.out_align < 16 || (part.N % 8 != 0 && n0 + c + 32 > part.N)) {
             store_chunk<E>(a.c[to], part.ldc, m0, n0 + c, fold ? min(part.M, m0 + 16) : part.M, min(part.N, (int64_t)(n0 + cols)), v, part.out_align);
             return;
           }

@@ -63,6 +63,52 @@ def test_gradients_of_operands_that_are_not_finite(ar, M, dtype, act, K, F, bad)
         assert same_kind(got.cpu(), want, unknown > 0), what
 
 
+@pytest.mark.parametrize("cols", [1, 2, 3, 5, 7, 9, 12, 15, 30, 33, 34, 67, 71, 100, 131, 257, 715])
+@pytest.mark.parametrize("M", [20, 40, 150, 300])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_nothing_is_written_past_a_row(ar, cols, M, dtype):
+    """Outputs are the first columns of a wider matrix whose rows start on 16 bytes; the others hold a marker."""
+    g = torch.Generator(device=DEV).manual_seed(cols)
+    ld = (cols + 15) // 8 * 8
+
+    def wide(rows):
+        buf = torch.full((rows + 2, ld), 7.0, dtype=dtype, device=DEV)
+        return buf, buf[:rows, :cols]
+
+    def untouched(buf, rows):
+        return bool((buf[:rows, cols:] == 7).all()) and bool((buf[rows:] == 7).all())
+
+    # the columns of a forward product's outputs are the shard's width
+    x, wg, wu = normal(g, M, 72, dtype), normal(g, cols, 72, dtype, 0.1), normal(g, cols, 72, dtype, 0.1)
+    bufs, outs = zip(*(wide(M) for _ in range(3)))
+    with ar.GatedFFN(M, 72, cols, dtype=dtype) as ffn:
+        got = ffn.forward(x, wg, wu, *outs)
+    want, bounds = ref.forward(x, wg, wu, "silu")
+    for a, b, e, what in zip(got, want, bounds, ("out", "gate", "up")):
+        ref.assert_close(a, b, e, what)
+    assert all(untouched(b, M) for b in bufs)
+
+    # those of the gradients its hidden size
+    F = 72
+    x, wg, wu = normal(g, M, cols, dtype), normal(g, F, cols, dtype, 0.1), normal(g, F, cols, dtype, 0.1)
+    gate, up, dout = (normal(g, M, F, dtype) for _ in range(3))
+    bufs, outs = zip(*(wide(rows) for rows in (M, F, F)))
+    with ar.GatedFFN(M, cols, F, dtype=dtype, train=True) as ffn:
+        got = ffn.backward(x, wg, wu, gate, up, dout, *outs)
+    want, bounds = ref.backward(x, wg, wu, gate, up, dout, "silu", two_parts=M <= 64)
+    for a, b, e, what in zip(got, want, bounds, ("dx", "dw_gate", "dw_up")):
+        ref.assert_close(a, b, e, what)
+    assert all(untouched(b, rows) for b, rows in zip(bufs, (M, F, F)))
+
+    # and those of an 8-bit product its channels
+    q, w8 = (torch.randint(-127, 128, (n, 80), generator=g, device=DEV, dtype=torch.int8) for n in (M, cols))
+    buf, out = wide(M)
+    ar.linear_i8(q, torch.ones(M, device=DEV), w8, torch.ones(cols, device=DEV) / 4096, out=out)
+    want = q.double() @ w8.double().T / 4096
+    ref.assert_close(out, want, 0 * want, "linear_i8")
+    assert untouched(buf, M)
+
+
 def small(ar, seed=0):
     g = torch.Generator(device=DEV).manual_seed(seed)
     M, K, F = 40, 64, 72
