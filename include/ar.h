@@ -587,6 +587,84 @@ ar_status_t ar_linear_i8(const int8_t* x, size_t ldx, const float* x_scale, cons
 size_t ar_linear_i8_scratch_bytes(const int8_t* x, size_t ldx, const int8_t* w, size_t ldw,
                                   size_t tokens, size_t in, size_t out);
 
+/* ---- norms and the residual after the sum --------------------------------
+ *
+ * What a layer does with the sum before its next block reads it, in one pass
+ * over the rows.  With N(v) = (v - mu) / sqrt(mean((v - mu)^2) + eps), mu the
+ * row's mean (AR_NORM_LAYER) or 0 (AR_NORM_RMS):
+ *   z = N(x) * (weight_offset + after_weight) + after_bias   the norm after a block
+ *   r = residual_scale * residual + gate * z                 the residual stream
+ *   y = N(r) * (weight_offset + weight) + bias               the norm before the next one
+ * The pages have no counterpart to these calls.
+ */
+typedef enum { AR_NORM_RMS = 0, AR_NORM_LAYER = 1 } ar_norm_kind_t;
+
+typedef struct {
+  int kind;   /* ar_norm_kind_t */
+  int dtype;  /* AR_BF16, AR_FP16 or AR_FP32, of every array of the call */
+  size_t rows, cols;
+  size_t gate_rows;  /* rows of the gate matrix, a divisor of rows: gate row g is of the
+                        rows / gate_rows rows from g * rows / gate_rows on (1: a gate for
+                        each column, rows: for each row, between them for each sequence);
+                        0: no gate */
+  double eps, residual_scale, weight_offset;
+} ar_norm_t;
+
+/* ar_residual_norm --
+ *   x             [rows, cols], leading dimension ldx: the block's output
+ *   residual      NULL (taken as 0), or [rows, cols]
+ *   gate          [gate_rows, cols]; NULL where gate_rows is 0 (taken as 1)
+ *   after_weight  NULL: z = x; else cols values.  after_bias: NULL (0) or cols
+ *                 values; only with after_weight
+ *   weight        NULL: no y; else cols values.  bias likewise
+ *   r, y          [rows, cols]; r may be NULL (not wanted), y is NULL where weight is
+ * Means, sums and products are fp32, the mean square being taken of the
+ * differences from the mean; y is made from the unrounded r; each output is rounded once.
+ * A row's values are its own: an infinity or NaN stays in its row.  In
+ * AR_FP32 squares that overflow make the row's norm 0 or NaN.
+ * r or y may be exactly x or residual (same address and leading dimension);
+ * otherwise outputs overlap nothing.  rows = 0 returns AR_OK without a launch.
+ * Errors: AR_ERR_INVALID_ARG (a NULL that is needed, ld < cols, an odd address,
+ * cols = 0, gate_rows that does not divide rows, eps negative or not finite, neither weight nor
+ * after_weight), AR_ERR_UNSUPPORTED (dtype, kind), AR_ERR_CUDA. */
+ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, const void* residual,
+                             size_t ldres, const void* gate, size_t ldg, const void* after_weight,
+                             const void* after_bias, const void* weight, const void* bias, void* r,
+                             size_t ldr, void* y, size_t ldy, void* stream);
+
+/* ar_residual_norm_backward -- the gradients, given dy and dr, those of y and r:
+ *   g = dr + (gradient of N(r) (weight_offset + weight) + bias with respect to r, at dy)
+ *   dresidual = residual_scale * g,   dgate = sum of g * z over a gate row's rows
+ *   dz = gate * g,                    dx = gradient of z with respect to x, at dz
+ *   dweight = sum over rows of dy * N(r),  dbias = sum of dy
+ *   dafter_weight = sum over rows of dz * N(x),  dafter_bias = sum of dz
+ *   dy   [rows, cols], NULL where weight is
+ *   dr   [rows, cols], or NULL (taken as 0)
+ *   x    the forward pass's; may be NULL where there is neither after_weight nor gate
+ *   r    the forward pass's (its rounded output; x where nothing was added); may be
+ *        NULL where weight is
+ *   dx, dresidual, dgate, dweight, dbias, dafter_weight, dafter_bias
+ *        NULL: not computed.  dgate has the leading dimension lddg.
+ * Statistics are taken again from x and r; sums are fp32, in an order that
+ * depends on the sizes and the device alone; outputs are rounded once and
+ * written, not added to.
+ *   scratch  device memory on 16 bytes, of ar_residual_norm_scratch_bytes(rows,
+ *            cols, how many of dgate, dweight, dbias, dafter_weight and
+ *            dafter_bias are not NULL) bytes; NULL where that is 0
+ * Outputs overlap neither inputs nor one another.
+ * rows = 0 writes zeros to the gradients of the vectors. */
+ar_status_t ar_residual_norm_backward(const ar_norm_t* n, const void* dy, size_t lddy, const void* dr,
+                                      size_t lddr, const void* x, size_t ldx, const void* r, size_t ldr,
+                                      const void* gate, size_t ldg, const void* after_weight,
+                                      const void* after_bias, const void* weight, void* dx, size_t lddx,
+                                      void* dresidual, size_t lddres, void* dgate, size_t lddg,
+                                      void* dweight, void* dbias, void* dafter_weight,
+                                      void* dafter_bias, void* scratch, size_t scratch_bytes,
+                                      void* stream);
+
+/* ar_residual_norm_scratch_bytes -- see ar_residual_norm_backward.  Host-only. */
+size_t ar_residual_norm_scratch_bytes(size_t rows, size_t cols, int vectors);
+
 /* ar_ops_get_device_status -- wait for `stream` to drain, then read and clear
  * the feed-forward operators' error word on the current device: AR_ERR_TIMEOUT
  * if a wait inside one of their tensor-core kernels gave up (two seconds; such

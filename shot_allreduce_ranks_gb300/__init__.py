@@ -17,10 +17,11 @@ from ._lib import (AR_AUTO, AR_BF16, AR_FP16, AR_FP32, AR_FUSED_LL8,  # noqa: F4
                    AR_TWOPHASE, VARIANTS, ArError, ArInfo, check, load)
 
 __all__ = ["AllReduce", "ArError", "GatedFFN", "VARIANTS", "allreduce_fused_noalloc", "dropout",
-           "dropout_backward", "linear_i8", "load", "ops_device_status", "quantize_rows"]
+           "dropout_backward", "linear_i8", "load", "ops_device_status", "quantize_rows", "residual_norm",
+           "residual_norm_backward"]
 
 _FEED_FORWARD = ("GatedFFN", "dropout", "dropout_backward", "linear_i8", "ops_device_status",
-                 "quantize_rows")
+                 "quantize_rows", "residual_norm", "residual_norm_backward")
 
 
 def __getattr__(name):

@@ -30,6 +30,8 @@ VARIANTS = {
 }
 AR_ACT_SILU, AR_ACT_GELU_TANH = 0, 1
 ACTIVATIONS = {"silu": AR_ACT_SILU, "gelu": AR_ACT_GELU_TANH}
+AR_NORM_RMS, AR_NORM_LAYER = 0, 1
+NORMS = {"rms": AR_NORM_RMS, "layer": AR_NORM_LAYER}
 AR_MAX_RANKS = 16
 AR_MAX_PACKET_RANKS = 8
 
@@ -44,6 +46,19 @@ class ArInfo(ctypes.Structure):
         ("fused_max_ctas", ctypes.c_int),
         ("fused_threads", ctypes.c_int),
         ("device", ctypes.c_int),
+    ]
+
+
+class ArNorm(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("rows", ctypes.c_size_t),
+        ("cols", ctypes.c_size_t),
+        ("gate_rows", ctypes.c_size_t),
+        ("eps", ctypes.c_double),
+        ("residual_scale", ctypes.c_double),
+        ("weight_offset", ctypes.c_double),
     ]
 
 
@@ -92,6 +107,12 @@ PROTOTYPES = {
     "ar_quantize_rows": (_ST, [_VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, _I, _VP]),
     "ar_linear_i8": (_ST, [_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _I, _VP, _SZ, _VP]),
     "ar_linear_i8_scratch_bytes": (_SZ, [_VP, _SZ, _VP, _SZ, _SZ, _SZ, _SZ]),
+    "ar_residual_norm": (_ST, [ctypes.POINTER(ArNorm), _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _VP, _VP, _VP,
+                               _VP, _SZ, _VP, _SZ, _VP]),
+    "ar_residual_norm_backward": (_ST, [ctypes.POINTER(ArNorm), _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _SZ,
+                                        _VP, _SZ, _VP, _VP, _VP, _VP, _SZ, _VP, _SZ, _VP, _SZ,
+                                        _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "ar_residual_norm_scratch_bytes": (_SZ, [_SZ, _SZ, _I]),
 }
 
 AR_NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -1,0 +1,131 @@
+// C ABI of a layer's steps around the feed-forward block: argument checks,
+// workspaces and the choice of kernel.  Declarations and contracts are in
+// include/ar.h.
+#include <math.h>
+
+#include "ops_internal.cuh"
+
+namespace {
+
+using namespace ar;  // the entry points' shared checks
+
+constexpr size_t kMaxCols = (size_t)1 << 30;
+
+size_t elem_bytes(int dtype) { return dtype == AR_FP32 ? 4 : 2; }
+
+// What both passes check of the description; rows = 0 is left to the caller.
+ar_status_t check_norm(const ar_norm_t* n, const void* gate, size_t ldg, const void* after_weight,
+                       const void* after_bias, const void* weight) {
+  if (!n) return AR_ERR_INVALID_ARG;
+  if (!any_type(n->dtype) || (n->kind != AR_NORM_RMS && n->kind != AR_NORM_LAYER)) return AR_ERR_UNSUPPORTED;
+  if (n->cols == 0 || n->cols > kMaxCols || n->rows > kMaxElems || !(n->eps >= 0.0) || isinf(n->eps) ||
+      (!weight && !after_weight) || (after_bias && !after_weight))
+    return AR_ERR_INVALID_ARG;
+  const size_t e = elem_bytes(n->dtype);
+  if (misaligned(after_weight, e) || misaligned(after_bias, e) || misaligned(weight, e)) return AR_ERR_INVALID_ARG;
+  if ((gate != nullptr) != (n->gate_rows != 0)) return AR_ERR_INVALID_ARG;
+  if (gate && (n->rows % n->gate_rows || bad_matrix(gate, n->gate_rows, n->cols, ldg) || misaligned(gate, e)))
+    return AR_ERR_INVALID_ARG;
+  return AR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, const void* residual,
+                             size_t ldres, const void* gate, size_t ldg, const void* after_weight,
+                             const void* after_bias, const void* weight, const void* bias, void* r,
+                             size_t ldr, void* y, size_t ldy, void* stream) {
+  if (ar_status_t st = check_norm(n, gate, ldg, after_weight, after_bias, weight)) return st;
+  const size_t rows = n->rows, cols = n->cols, e = elem_bytes(n->dtype);
+  if ((bias && !weight) || misaligned(bias, e)) return AR_ERR_INVALID_ARG;
+  if (rows == 0) return AR_OK;
+  if ((y != nullptr) != (weight != nullptr) || bad_matrix(x, rows, cols, ldx) || misaligned(x, e) ||
+      (residual && (bad_matrix(residual, rows, cols, ldres) || misaligned(residual, e))) ||
+      (r && (bad_matrix(r, rows, cols, ldr) || misaligned(r, e))) ||
+      (y && (bad_matrix(y, rows, cols, ldy) || misaligned(y, e))))
+    return AR_ERR_INVALID_ARG;
+  if (!r && !y) return AR_OK;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  NormArgs a = {};
+  a.x = x, a.residual = residual, a.gate = gate;
+  a.after_weight = after_weight, a.after_bias = after_bias, a.weight = weight, a.bias = bias;
+  a.r = r, a.y = y;
+  a.ldx = (int64_t)ldx, a.ldres = (int64_t)ldres, a.ldg = (int64_t)ldg, a.ldr = (int64_t)ldr, a.ldy = (int64_t)ldy;
+  a.rows = (int64_t)rows, a.cols = (int64_t)cols;
+  a.gate_run = gate ? (int64_t)(rows / n->gate_rows) : (int64_t)rows;
+  a.eps = (float)n->eps, a.alpha = (float)n->residual_scale, a.offset = (float)n->weight_offset;
+  a.layer = n->kind == AR_NORM_LAYER;
+  return cuda_status(launch_norm(n->dtype, a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ar_residual_norm_scratch_bytes(size_t rows, size_t cols, int vectors) {
+  if (vectors <= 0 || cols > kMaxCols) return 0;
+  const size_t parts = rows < (size_t)kNormMaxCtas ? rows : (size_t)kNormMaxCtas;
+  return (size_t)vectors * parts * cols * sizeof(float);
+}
+
+ar_status_t ar_residual_norm_backward(const ar_norm_t* n, const void* dy, size_t lddy, const void* dr,
+                                      size_t lddr, const void* x, size_t ldx, const void* r, size_t ldr,
+                                      const void* gate, size_t ldg, const void* after_weight,
+                                      const void* after_bias, const void* weight, void* dx, size_t lddx,
+                                      void* dresidual, size_t lddres, void* dgate, size_t lddg,
+                                      void* dweight, void* dbias, void* dafter_weight,
+                                      void* dafter_bias, void* scratch, size_t scratch_bytes,
+                                      void* stream) {
+  if (ar_status_t st = check_norm(n, gate, ldg, after_weight, after_bias, weight)) return st;
+  const size_t rows = n->rows, cols = n->cols, e = elem_bytes(n->dtype);
+  void* const sums[kNormSums] = {dweight, dbias, dafter_weight, dafter_bias, dgate};
+  int vectors = 0;
+  for (void* p : sums) {
+    if (misaligned(p, e)) return AR_ERR_INVALID_ARG;
+    vectors += p != nullptr;
+  }
+  if (((dweight || dbias) && !weight) || ((dafter_weight || dafter_bias) && !after_weight) || (dgate && !gate) ||
+      (dgate && bad_matrix(dgate, n->gate_rows, cols, lddg)))
+    return AR_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    for (int k = 0; k < kNormSums; ++k) {
+      const size_t m = k == kSumGate ? n->gate_rows : 1, ld = k == kSumGate ? lddg : cols;
+      if (sums[k] && cudaMemset2DAsync(sums[k], ld * e, 0, cols * e, m, s) != cudaSuccess) return AR_ERR_CUDA;
+    }
+    return AR_OK;
+  }
+  if ((dy != nullptr) != (weight != nullptr) || (!dy && !dr)) return AR_ERR_INVALID_ARG;
+  if ((dy && (bad_matrix(dy, rows, cols, lddy) || misaligned(dy, e) || bad_matrix(r, rows, cols, ldr) || misaligned(r, e))) ||
+      (dr && (bad_matrix(dr, rows, cols, lddr) || misaligned(dr, e))) ||
+      ((gate || after_weight) && (bad_matrix(x, rows, cols, ldx) || misaligned(x, e))) ||
+      (dx && (bad_matrix(dx, rows, cols, lddx) || misaligned(dx, e))) ||
+      (dresidual && (bad_matrix(dresidual, rows, cols, lddres) || misaligned(dresidual, e))))
+    return AR_ERR_INVALID_ARG;
+  if (vectors && (!scratch || misaligned(scratch, 16) || scratch_bytes < ar_residual_norm_scratch_bytes(rows, cols, vectors)))
+    return AR_ERR_INVALID_ARG;
+  if (!vectors && !dx && !dresidual) return AR_OK;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  NormGradArgs a = {};
+  a.dy = dy, a.dr = dr, a.x = x, a.r = r, a.gate = gate;
+  a.after_weight = after_weight, a.after_bias = after_bias, a.weight = weight;
+  a.dx = dx, a.dresidual = dresidual;
+  const size_t parts = rows < (size_t)kNormMaxCtas ? rows : (size_t)kNormMaxCtas;
+  float* part = static_cast<float*>(scratch);
+  for (int k = 0; k < kNormSums; ++k) {
+    a.sum[k] = sums[k];
+    if (!sums[k]) continue;
+    a.part[k] = part;
+    part += parts * cols;
+  }
+  a.lddy = (int64_t)lddy, a.lddr = (int64_t)lddr, a.ldx = (int64_t)ldx, a.ldr = (int64_t)ldr, a.ldg = (int64_t)ldg;
+  a.lddx = (int64_t)lddx, a.lddres = (int64_t)lddres, a.lddg = (int64_t)lddg;
+  a.rows = (int64_t)rows, a.cols = (int64_t)cols;
+  a.gate_rows = gate ? (int64_t)n->gate_rows : 1;
+  a.gate_run = (int64_t)rows / a.gate_rows;
+  a.eps = (float)n->eps, a.alpha = (float)n->residual_scale, a.offset = (float)n->weight_offset;
+  a.layer = n->kind == AR_NORM_LAYER;
+  return cuda_status(launch_norm_grad(n->dtype, a, sms, s));
+}
+
+}  // extern "C"

@@ -20,8 +20,9 @@ struct ar_ffn_ctx {
 
 namespace {
 
+using namespace ar;  // the entry points' shared checks
+
 constexpr int kMaxDevices = 64;
-constexpr size_t kMaxElems = (size_t)1 << 40;  // of a matrix: more than the memory holds
 constexpr size_t kMaxSize = (size_t)1 << 30;  // the sizes a handle is made for
 // Up to this many tokens the gradients of the pre-activations reach the products
 // in two parts: with few values the rounding of each shows most.  In dx the second
@@ -33,32 +34,6 @@ constexpr size_t kTwoPartTokens = 64;
 // Up to this many tokens a forward product reads the weights once, where they
 // are: laying them out first costs two passes more.
 constexpr size_t kFewTokens = AR_FEW_TOKENS;
-
-bool half_type(int dtype) { return dtype == AR_BF16 || dtype == AR_FP16; }
-bool any_type(int dtype) { return half_type(dtype) || dtype == AR_FP32; }
-
-ar_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? AR_OK : AR_ERR_CUDA; }
-
-// SMs of the current device, looked up once for each.
-ar_status_t current_sms(int* sms) {
-  static int known[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return AR_ERR_CUDA;
-  if (dev >= 0 && dev < kMaxDevices && known[dev] > 0) {
-    *sms = known[dev];
-    return AR_OK;
-  }
-  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return AR_ERR_CUDA;
-  if (dev >= 0 && dev < kMaxDevices) known[dev] = *sms;
-  return AR_OK;
-}
-
-bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
-  return !p || ld < cols || ld > kMaxElems || (ld && rows > kMaxElems / ld);
-}
-
-bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
 // A matrix with its row stride; packed rows take the place of ones that do not
 // start on 16 bytes where the caller gave scratch memory for them.
@@ -161,6 +136,20 @@ ar_status_t dropout_call(const void* x, size_t ldx, const void* res, size_t ldr,
 }
 
 }  // namespace
+
+ar_status_t ar::current_sms(int* sms) {
+  static int known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return AR_ERR_CUDA;
+  if (dev >= 0 && dev < kMaxDevices && known[dev] > 0) {
+    *sms = known[dev];
+    return AR_OK;
+  }
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return AR_ERR_CUDA;
+  if (dev >= 0 && dev < kMaxDevices) known[dev] = *sms;
+  return AR_OK;
+}
 
 bool ar::ops_pdl() {
   static const bool on = [] {

@@ -28,6 +28,19 @@ cudaError_t launch_op(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
 }
 
 // ---------------------------------------------------------------------------
+// Checks that the entry points share.
+constexpr size_t kMaxElems = (size_t)1 << 40;  // of a matrix: more than the memory holds
+
+inline bool half_type(int dtype) { return dtype == AR_BF16 || dtype == AR_FP16; }
+inline bool any_type(int dtype) { return half_type(dtype) || dtype == AR_FP32; }
+inline ar_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? AR_OK : AR_ERR_CUDA; }
+inline bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
+  return !p || ld < cols || ld > kMaxElems || (ld && rows > kMaxElems / ld);
+}
+inline bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+ar_status_t current_sms(int* sms);  // SMs of the current device, looked up once for each
+
+// ---------------------------------------------------------------------------
 // Matrix products.  All of them are C[m, n] = sum_k A(m, k) B(n, k); what
 // differs is which matrices stand for A and B, which of their two axes is
 // contiguous, and what is done with the sum.
@@ -126,6 +139,37 @@ struct DropoutArgs {
   float scale;
 };
 cudaError_t launch_dropout(int dtype, const DropoutArgs& a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Norms and the residual (k_norm.cu).  Absent arrays are null.
+struct NormArgs {
+  const void *x, *residual, *gate, *after_weight, *after_bias, *weight, *bias;
+  void *r, *y;
+  int64_t ldx, ldres, ldg, ldr, ldy;
+  int64_t rows, cols, gate_run;  // gate_run: rows of one gate row
+  float eps, alpha, offset;
+  int layer;
+};
+cudaError_t launch_norm(int dtype, const NormArgs& a, int num_sms, cudaStream_t s);
+
+// The sums over rows that the backward pass makes, in the order of their parts.
+enum NormSum : int { kSumWeight = 0, kSumBias, kSumAfterWeight, kSumAfterBias, kSumGate, kNormSums };
+
+struct NormGradArgs {
+  const void *dy, *dr, *x, *r, *gate, *after_weight, *after_bias, *weight;
+  void *dx, *dresidual;
+  void* sum[kNormSums];    // outputs
+  float* part[kNormSums];  // a row of cols floats for every CTA; null where sum is
+  int64_t lddy, lddr, ldx, ldr, ldg, lddx, lddres, lddg;
+  int64_t rows, cols, gate_rows, gate_run;  // gate_rows is 1 and gate_run is rows where there is no gate
+  // How the rows are dealt out: with `split` CTAs to each gate row (1 or more),
+  // or (split = 0) with several whole gate rows to each of `ctas` CTAs.
+  int64_t ctas, split, chunk;  // chunk: rows of a CTA where split > 0
+  float eps, alpha, offset;
+  int layer;
+};
+constexpr int64_t kNormMaxCtas = 320;  // bounds the parts
+cudaError_t launch_norm_grad(int dtype, NormGradArgs& a, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Activations.  Both are v * sigmoid(s(v)): s(v) = v for SiLU, and for the

@@ -93,10 +93,11 @@ int64_t matrix(const at::Tensor& t, const char* what, at::ScalarType type, int i
   return t.stride(0);
 }
 
-void vector(const at::Tensor& t, const char* what, int64_t n, int index) {
-  if (t.scalar_type() != at::kFloat || !t.is_cuda() || t.get_device() != index || t.dim() != 1 || t.size(0) != n ||
+void vector(const at::Tensor& t, const char* what, int64_t n, int index, at::ScalarType type = at::kFloat) {
+  if (t.scalar_type() != type || !t.is_cuda() || t.get_device() != index || t.dim() != 1 || t.size(0) != n ||
       !t.is_contiguous())
-    refuse(std::string(what) + " must be " + std::to_string(n) + " contiguous float32 values on cuda:" + std::to_string(index));
+    refuse(std::string(what) + " must be " + std::to_string(n) + " contiguous " +
+           (type == at::kFloat ? "float32" : type_name(type)) + " values on cuda:" + std::to_string(index));
 }
 
 at::Tensor fresh(int64_t rows, int64_t cols, at::ScalarType type, const at::Tensor& like) {
@@ -401,6 +402,126 @@ PyObject* linear_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// What a call of the norms has beside its matrices of rows.
+struct Norm {
+  ar_norm_t n;
+  at::ScalarType type;
+  int index;
+  at::Tensor weight, bias, after_weight, after_bias, gate;
+  int64_t ldg = 0;
+
+  // like: a matrix of the call; o: weight, bias, after_weight, after_bias, gate, kind, eps, residual_scale, weight_offset.
+  Norm(const at::Tensor& like, const char* what, PyObject* const* o) {
+    index = gpu_of(like, what);
+    type = like.scalar_type();
+    n.dtype = type_code(type, what, false);
+    if (like.dim() != 2) refuse(std::string(what) + " must be 2-D");
+    n.rows = (size_t)like.size(0), n.cols = (size_t)like.size(1);
+    if (n.cols == 0) refuse(std::string(what) + " must have columns");
+    weight = one(o[0], "weight"), bias = one(o[1], "bias");
+    after_weight = one(o[2], "after_weight"), after_bias = one(o[3], "after_bias");
+    if (!weight.defined() && !after_weight.defined()) refuse("weight or after_weight must be given");
+    if (bias.defined() && !weight.defined()) refuse("bias needs weight");
+    if (after_bias.defined() && !after_weight.defined()) refuse("after_bias needs after_weight");
+    n.gate_rows = 0;
+    if (o[4] != Py_None) {
+      gate = tensor(o[4], "gate");
+      ldg = matrix(gate, "gate", type, index, kAny, (int64_t)n.cols);
+      n.gate_rows = (size_t)gate.size(0);
+      if (n.gate_rows == 0 || n.rows % n.gate_rows)
+        refuse("gate has " + std::to_string(n.gate_rows) + " rows, which do not divide " + std::to_string(n.rows));
+    }
+    n.kind = (int)integer(o[5]);
+    n.eps = real(o[6]), n.residual_scale = real(o[7]), n.weight_offset = real(o[8]);
+    if (!(n.eps >= 0.0) || n.eps > 3e38) refuse("eps must be finite and not negative");
+  }
+  at::Tensor one(PyObject* o, const char* what) const {
+    if (o == Py_None) return at::Tensor();
+    const at::Tensor& t = tensor(o, what);
+    vector(t, what, (int64_t)n.cols, index, type);
+    return t;
+  }
+  // A matrix of rows, or null.
+  at::Tensor rows(PyObject* o, const char* what, int64_t* ld) const {
+    *ld = 0;
+    if (o == Py_None) return at::Tensor();
+    const at::Tensor& t = tensor(o, what);
+    *ld = matrix(t, what, type, index, (int64_t)n.rows, (int64_t)n.cols);
+    return t;
+  }
+};
+
+// (x, residual, weight, bias, after_weight, after_bias, gate, kind, eps, residual_scale, weight_offset, r, y)
+PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 13, [&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[0], "x");
+    const Norm p(x, "x", a + 2);
+    int64_t ldx, ldres, ldr = 0, ldy = 0;
+    p.rows(a[0], "x", &ldx);
+    const at::Tensor residual = p.rows(a[1], "residual", &ldres);
+    no_history(x, "x");
+    if (residual.defined()) no_history(residual, "residual");
+    if (p.weight.defined()) no_history(p.weight, "weight");
+    if (p.bias.defined()) no_history(p.bias, "bias");
+    if (p.after_weight.defined()) no_history(p.after_weight, "after_weight");
+    if (p.after_bias.defined()) no_history(p.after_bias, "after_bias");
+    if (p.gate.defined()) no_history(p.gate, "gate");
+    const int64_t m = (int64_t)p.n.rows, n = (int64_t)p.n.cols;
+    at::Tensor r, y;
+    // Where nothing is added to x and nothing multiplies it, r would be x.
+    if (residual.defined() || p.gate.defined() || p.after_weight.defined() || a[11] != Py_None)
+      r = output(a[11], "r", p.type, p.index, m, n, x, &ldr);
+    if (p.weight.defined())
+      y = output(a[12], "y", p.type, p.index, m, n, x, &ldy);
+    else if (a[12] != Py_None)
+      refuse("y needs weight");
+    call("ar_residual_norm", p.index, [&](void* s) {
+      return ar_residual_norm(&p.n, x.data_ptr(), ldx, address(residual), ldres, address(p.gate), p.ldg, address(p.after_weight),
+                              address(p.after_bias), address(p.weight), address(p.bias), address(r), ldr, address(y), ldy, s);
+    });
+    return tuple_of(r, y);
+  });
+}
+
+// (dy, dr, x, r, weight, bias, after_weight, after_bias, gate, kind, eps, residual_scale, weight_offset, need_dresidual)
+PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 14, [&]() -> PyObject* {
+    const at::Tensor& first = a[0] != Py_None ? tensor(a[0], "dy") : tensor(a[1], "dr");
+    const Norm p(first, a[0] != Py_None ? "dy" : "dr", a + 4);
+    const int64_t m = (int64_t)p.n.rows, n = (int64_t)p.n.cols;
+    int64_t lddy, lddr, ldx, ldr;
+    const at::Tensor dy = p.rows(a[0], "dy", &lddy), dr = p.rows(a[1], "dr", &lddr), x = p.rows(a[2], "x", &ldx);
+    at::Tensor r = p.rows(a[3], "r", &ldr);
+    const bool branch = p.gate.defined() || p.after_weight.defined();
+    if (dy.defined() != p.weight.defined()) refuse("dy and weight are given together");
+    if (branch && !x.defined()) refuse("a gate or after_weight needs x");
+    const bool added = r.defined();
+    if (p.weight.defined() && !added) {
+      if (branch || !x.defined()) refuse("weight needs r");
+      r = x, ldr = ldx;  // nothing was added
+    }
+    const at::Tensor& like = first;
+    const at::Tensor dx = fresh(m, n, p.type, like);
+    at::Tensor dres;
+    // The gradient of the residual is that of x where nothing stands between them.
+    const bool same = !branch && p.n.residual_scale == 1.0;
+    const bool need = added && PyObject_IsTrue(a[13]);
+    if (need && !same) dres = fresh(m, n, p.type, like);
+    const auto param = [&](const at::Tensor& t) { return t.defined() ? at::empty({n}, like.options()) : at::Tensor(); };
+    const at::Tensor dw = param(p.weight), db = param(p.bias), daw = param(p.after_weight), dab = param(p.after_bias);
+    const at::Tensor dgate = p.gate.defined() ? fresh((int64_t)p.n.gate_rows, n, p.type, like) : at::Tensor();
+    const int vectors = dw.defined() + db.defined() + daw.defined() + dab.defined() + dgate.defined();
+    const at::Tensor room = scratch(ar_residual_norm_scratch_bytes(p.n.rows, p.n.cols, vectors), like);
+    call("ar_residual_norm_backward", p.index, [&](void* s) {
+      return ar_residual_norm_backward(&p.n, address(dy), lddy, address(dr), lddr, address(x), ldx, address(r), ldr,
+                                       address(p.gate), p.ldg, address(p.after_weight), address(p.after_bias), address(p.weight),
+                                       address(dx), n, address(dres), n, address(dgate), n, address(dw), address(db), address(daw),
+                                       address(dab), address(room), bytes_of(room), s);
+    });
+    return tuple_of(dx, need && same ? dx : dres, dw, db, daw, dab, dgate);
+  });
+}
+
 // (check): what raises for a status that is not AR_OK.
 PyObject* set_check(PyObject*, PyObject* f) {
   Py_XSETREF(g_check, Py_NewRef(f));
@@ -414,6 +535,8 @@ PyMethodDef methods[] = {AR_FAST(ffn_forward),
                          AR_FAST(dropout_backward),
                          AR_FAST(quantize_rows),
                          AR_FAST(linear_i8),
+                         AR_FAST(residual_norm),
+                         AR_FAST(residual_norm_backward),
                          {"set_check", set_check, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", "Feed-forward operators: see feed_forward.", -1, methods};

@@ -18,7 +18,7 @@ import os
 
 import torch
 
-from ._lib import ACTIVATIONS, AR_BF16, AR_FP16, AR_FP32, PKG, check, load
+from ._lib import ACTIVATIONS, AR_BF16, AR_FP16, AR_FP32, NORMS, PKG, check, load
 
 _CODES = {torch.bfloat16: AR_BF16, torch.float16: AR_FP16, torch.float32: AR_FP32}
 
@@ -200,6 +200,59 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
         with _current(stream, getattr(x, "device", None)):
             return _ops.linear_i8(x, x_scale, w, w_scale, out, code)
     return _ops.linear_i8(x, x_scale, w, w_scale, out, code)
+
+
+def _kind(kind: str) -> int:
+    if kind not in NORMS:
+        raise ValueError("kind must be one of %s" % ", ".join(sorted(NORMS)))
+    return NORMS[kind]
+
+
+def residual_norm(x, residual=None, weight=None, bias=None, after_weight=None, after_bias=None, gate=None,
+                  kind: str = "rms", eps: float = 1e-6, residual_scale: float = 1.0, weight_offset: float = 0.0,
+                  r=None, y=None, stream=None):
+    """``(r, y)``: the norm after a block, its gate, the residual and the norm before the next block, in one pass.
+
+    With ``norm(v)`` the rows over the root of their mean square (``kind="rms"``),
+    or less their mean over their standard deviation (``"layer"``)::
+
+        z = norm(x) * (weight_offset + after_weight) + after_bias      x itself without after_weight
+        r = residual_scale * residual + gate * z
+        y = norm(r) * (weight_offset + weight) + bias                  None without weight
+
+    ``gate`` is a matrix whose row g is for the rows / gate rows rows from
+    g * rows / gate rows on: one row for all, one a sequence, or one a token.
+    Without residual, gate and after_weight r would be x and None is
+    returned for it.  ``r`` and ``y`` may be given, and be x or the residual.
+    """
+    k = _kind(kind)
+    if stream is not None:
+        with _current(stream, getattr(x, "device", None)):
+            return _ops.residual_norm(x, residual, weight, bias, after_weight, after_bias, gate, k, eps, residual_scale,
+                                      weight_offset, r, y)
+    return _ops.residual_norm(x, residual, weight, bias, after_weight, after_bias, gate, k, eps, residual_scale,
+                              weight_offset, r, y)
+
+
+def residual_norm_backward(dy, dr, x, r, weight=None, bias=None, after_weight=None, after_bias=None, gate=None,
+                           kind: str = "rms", eps: float = 1e-6, residual_scale: float = 1.0,
+                           weight_offset: float = 0.0, need_dresidual: bool = True, stream=None):
+    """``(dx, dresidual, dweight, dbias, dafter_weight, dafter_bias, dgate)`` from the gradients of y and r.
+
+    ``dr`` None counts as 0; ``dy`` is None where there was no weight.  ``x`` and
+    ``r`` are the forward pass's: x may be None without gate and after_weight, r
+    is None where nothing was added to x (then there is no dresidual).
+    What was not given has None for its gradient.  Where neither a gate, nor
+    after_weight, nor a scale stands between them, dx and dresidual are equal and one
+    tensor is returned for both.
+    """
+    k = _kind(kind)
+    if stream is not None:
+        with _current(stream, getattr(dr if dy is None else dy, "device", None)):
+            return _ops.residual_norm_backward(dy, dr, x, r, weight, bias, after_weight, after_bias, gate, k, eps,
+                                               residual_scale, weight_offset, need_dresidual)
+    return _ops.residual_norm_backward(dy, dr, x, r, weight, bias, after_weight, after_bias, gate, k, eps,
+                                       residual_scale, weight_offset, need_dresidual)
 
 
 def ops_device_status(stream=None) -> int:
