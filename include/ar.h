@@ -665,6 +665,61 @@ ar_status_t ar_residual_norm_backward(const ar_norm_t* n, const void* dy, size_t
 /* ar_residual_norm_scratch_bytes -- see ar_residual_norm_backward.  Host-only. */
 size_t ar_residual_norm_scratch_bytes(size_t rows, size_t cols, int vectors);
 
+/* ---- a layer of gated experts for a few tokens ----------------------------
+ *
+ * A mixture-of-experts layer in serving: every token is sent to its top_k
+ * experts, each a gated feed-forward block as above with a down projection, and
+ * their outputs are summed by weight.  A rank may hold a part of the experts (or
+ * of every expert's inner width); the ranks' partial outputs are what
+ * ar_allreduce sums.  The pages have no counterpart to it.
+ */
+#define AR_MAX_EXPERTS 1024
+#define AR_MAX_TOP_K 16
+
+typedef struct {
+  int dtype;         /* AR_BF16 or AR_FP16, of x, the weights and out */
+  int logits_dtype;  /* AR_BF16, AR_FP16 or AR_FP32 */
+  int activation;    /* ar_activation_t */
+  int experts;       /* of the whole layer: columns of the logits, 1 .. AR_MAX_EXPERTS */
+  int first_expert;  /* this rank holds experts first_expert .. */
+  int local_experts; /* .. first_expert + local_experts - 1 */
+  int top_k;         /* 1 .. the smaller of experts and AR_MAX_TOP_K */
+  int normalize;     /* non-zero: a token's weights are made to sum to 1 */
+  size_t hidden;     /* columns of x and of out (K) */
+  size_t width;      /* rows of an expert's gate and up projections (F) */
+} ar_moe_t;
+
+/* ar_moe_ffn --
+ *   x              [tokens, hidden], leading dimension ldx
+ *   logits         [tokens, experts], ldl: the router's
+ *   w_gate, w_up   [local_experts, width, hidden]: rows ldw, experts esw elements apart
+ *   w_down         [local_experts, hidden, width]: ldd, esd
+ *   out            [tokens, hidden], ldo
+ *   expert, weight NULL, or [tokens, top_k] without gaps: receive the routing
+ * A token's experts are those of its top_k highest logits, the highest first
+ * and equal ones by the lowest index; weight j is exp(logit_j) over the sum of
+ * all experts' exp, or (normalize) of the chosen ones'.  An expert whose logit is
+ * -infinity is never chosen: where fewer remain, expert is -1 and weight 0.  A
+ * row with a NaN or +infinity has NaN weights.  With e = expert[t, j]:
+ *   h   = act(x[t] Wgate_e^T) * (x[t] Wup_e^T)
+ *   out[t] = sum over the j whose e this rank holds of weight[t, j] * (h Wdown_e^T)
+ * and zeros where it holds none.  Sums, the activation and the weighting are fp32; h is rounded
+ * to dtype between the two products, out once.  Each matrix of an expert with tokens is read
+ * once for every AR_FEW_TOKENS tokens (more are taken in runs of that many).
+ *   scratch  device memory on 16 bytes, ar_moe_scratch_bytes of it, not shared
+ *            with a call that may run at the same time
+ * tokens = 0 returns AR_OK without a launch.  Asynchronous on `stream`; out
+ * overlaps no input.  Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (a dtype),
+ * AR_ERR_CUDA. */
+ar_status_t ar_moe_ffn(const ar_moe_t* m, const void* x, size_t ldx, const void* logits, size_t ldl,
+                       const void* w_gate, const void* w_up, size_t ldw, size_t esw,
+                       const void* w_down, size_t ldd, size_t esd, void* out, size_t ldo,
+                       int32_t* expert, float* weight, size_t tokens, void* scratch,
+                       size_t scratch_bytes, void* stream);
+
+/* ar_moe_scratch_bytes -- see ar_moe_ffn; 0 for what it refuses.  Host-only. */
+size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens);
+
 /* ar_ops_get_device_status -- wait for `stream` to drain, then read and clear
  * the feed-forward operators' error word on the current device: AR_ERR_TIMEOUT
  * if a wait inside one of their tensor-core kernels gave up (two seconds; such

@@ -62,6 +62,14 @@ class ArNorm(ctypes.Structure):
     ]
 
 
+class ArMoe(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("dtype", "logits_dtype", "activation", "experts", "first_expert",
+                                                  "local_experts", "top_k", "normalize")] + [
+        ("hidden", ctypes.c_size_t),
+        ("width", ctypes.c_size_t),
+    ]
+
+
 _H = ctypes.c_void_p
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
@@ -113,6 +121,9 @@ PROTOTYPES = {
                                         _VP, _SZ, _VP, _VP, _VP, _VP, _SZ, _VP, _SZ, _VP, _SZ,
                                         _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "ar_residual_norm_scratch_bytes": (_SZ, [_SZ, _SZ, _I]),
+    "ar_moe_ffn": (_ST, [ctypes.POINTER(ArMoe), _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, _SZ, _VP, _SZ, _SZ,
+                         _VP, _SZ, _VP, _VP, _SZ, _VP, _SZ, _VP]),
+    "ar_moe_scratch_bytes": (_SZ, [ctypes.POINTER(ArMoe), _SZ]),
 }
 
 AR_NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -29,9 +29,68 @@ ar_status_t check_norm(const ar_norm_t* n, const void* gate, size_t ldg, const v
   return AR_OK;
 }
 
+// Experts' matrices, es elements from one to the next (0: all the same).
+bool bad_stack(const void* p, size_t count, size_t rows, size_t cols, size_t ld, size_t es) {
+  return bad_matrix(p, rows, cols, ld) || misaligned(p, 2) || es > kMaxElems || (es && count > kMaxElems / es);
+}
+
+size_t moe_ldh(const ar_moe_t* m) { return (m->width + 7) / 8 * 8; }
+
+ar_status_t check_moe(const ar_moe_t* m) {
+  if (!m) return AR_ERR_INVALID_ARG;
+  if (!half_type(m->dtype) || !any_type(m->logits_dtype)) return AR_ERR_UNSUPPORTED;
+  if ((m->activation != AR_ACT_SILU && m->activation != AR_ACT_GELU_TANH) || m->experts < 1 ||
+      m->experts > AR_MAX_EXPERTS || m->local_experts < 1 || m->local_experts > m->experts || m->first_expert < 0 ||
+      m->first_expert > m->experts - m->local_experts || m->top_k < 1 || m->top_k > AR_MAX_TOP_K ||
+      m->top_k > m->experts || m->hidden < 1 || m->hidden > kMaxCols || m->width < 1 || m->width > kMaxCols)
+    return AR_ERR_INVALID_ARG;
+  return AR_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens) {
+  if (check_moe(m)) return 0;
+  return (tokens < AR_FEW_TOKENS ? tokens : AR_FEW_TOKENS) * (size_t)m->top_k * moe_ldh(m) * 2;
+}
+
+ar_status_t ar_moe_ffn(const ar_moe_t* m, const void* x, size_t ldx, const void* logits, size_t ldl,
+                       const void* w_gate, const void* w_up, size_t ldw, size_t esw,
+                       const void* w_down, size_t ldd, size_t esd, void* out, size_t ldo,
+                       int32_t* expert, float* weight, size_t tokens, void* scratch,
+                       size_t scratch_bytes, void* stream) {
+  if (ar_status_t st = check_moe(m)) return st;
+  if (tokens == 0) return AR_OK;
+  const size_t K = m->hidden, F = m->width, le = elem_bytes(m->logits_dtype), n = (size_t)m->local_experts;
+  if (bad_matrix(x, tokens, K, ldx) || misaligned(x, 2) || bad_matrix(logits, tokens, (size_t)m->experts, ldl) ||
+      misaligned(logits, le) || bad_stack(w_gate, n, F, K, ldw, esw) || bad_stack(w_up, n, F, K, ldw, esw) ||
+      bad_stack(w_down, n, K, F, ldd, esd) || bad_matrix(out, tokens, K, ldo) || misaligned(out, 2) ||
+      misaligned(expert, 4) || misaligned(weight, 4) || !scratch || misaligned(scratch, 16) ||
+      scratch_bytes < ar_moe_scratch_bytes(m, tokens))
+    return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  MoeArgs a = {};
+  a.w_gate = w_gate, a.w_up = w_up, a.w_down = w_down, a.h = scratch;
+  a.ldx = (int64_t)ldx, a.ldl = (int64_t)ldl, a.ldw = (int64_t)ldw, a.esw = (int64_t)esw;
+  a.ldd = (int64_t)ldd, a.esd = (int64_t)esd, a.ldh = (int64_t)moe_ldh(m), a.ldo = (int64_t)ldo;
+  a.hidden = (int64_t)K, a.width = (int64_t)F;
+  a.experts = m->experts, a.first = m->first_expert, a.local = m->local_experts;
+  a.top_k = m->top_k, a.normalize = m->normalize != 0, a.logits_dtype = m->logits_dtype;
+  for (size_t t = 0; t < tokens; t += AR_FEW_TOKENS) {
+    a.tokens = (int)(tokens - t < AR_FEW_TOKENS ? tokens - t : AR_FEW_TOKENS);
+    a.x = static_cast<const char*>(x) + t * ldx * 2;
+    a.logits = static_cast<const char*>(logits) + t * ldl * le;
+    a.out = static_cast<char*>(out) + t * ldo * 2;
+    a.out_expert = expert ? expert + t * (size_t)m->top_k : nullptr;
+    a.out_weight = weight ? weight + t * (size_t)m->top_k : nullptr;
+    const cudaError_t e = launch_moe(m->dtype, m->activation, a, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return AR_ERR_CUDA;
+  }
+  return AR_OK;
+}
 
 ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, const void* residual,
                              size_t ldres, const void* gate, size_t ldg, const void* after_weight,

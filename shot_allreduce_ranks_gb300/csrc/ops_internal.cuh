@@ -172,6 +172,19 @@ constexpr int64_t kNormMaxCtas = 320;  // bounds the parts
 cudaError_t launch_norm_grad(int dtype, NormGradArgs& a, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// Gated feed-forward experts for at most AR_FEW_TOKENS tokens (k_moe.cu).
+struct MoeArgs {
+  const void *x, *logits, *w_gate, *w_up, *w_down;
+  void *h, *out;  // h: row t * top_k + j for choice j of token t, rows on 16 bytes
+  int32_t* out_expert;
+  float* out_weight;  // of the routing, or null
+  int64_t ldx, ldl, ldw, esw, ldd, esd, ldh, ldo;  // es: elements from one expert's matrix to the next
+  int64_t hidden, width;
+  int tokens, experts, first, local, top_k, normalize, logits_dtype;
+};
+cudaError_t launch_moe(int dtype, int act, const MoeArgs& m, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // Activations.  Both are v * sigmoid(s(v)): s(v) = v for SiLU, and for the
 // tanh form of GELU s(v) = 2 sqrt(2/pi) (v + 0.044715 v^3), because
 // (1 + tanh t) / 2 = sigmoid(2 t).  __expf and __fdividef are good to a few

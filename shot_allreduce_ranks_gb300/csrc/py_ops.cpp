@@ -522,6 +522,71 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count
   });
 }
 
+// Experts' matrices: row and expert strides.
+const at::Tensor& stack(PyObject* o, const char* what, at::ScalarType type, int index, int64_t count, int64_t rows, int64_t cols,
+                        int64_t* ld, int64_t* es) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.dim() != 3 || t.scalar_type() != type || !t.is_cuda() || t.get_device() != index)
+    refuse(std::string(what) + " must be a 3-D " + type_name(type) + " tensor on cuda:" + std::to_string(index));
+  const int64_t want[3] = {count, rows, cols};
+  for (int i = 0; i < 3; ++i)
+    if (want[i] != kAny && t.size(i) != want[i])
+      refuse(std::string(what) + " has size " + std::to_string(t.size(i)) + " in dimension " + std::to_string(i) + ", wanted " +
+             std::to_string(want[i]));
+  if (t.numel() == 0) refuse(std::string(what) + " is empty");
+  if (t.size(2) > 1 && t.stride(2) != 1) refuse(std::string(what) + " must have contiguous rows");
+  *ld = t.size(1) > 1 ? t.stride(1) : t.size(2);
+  if (*ld < t.size(2)) refuse(std::string(what) + " has overlapping rows");
+  *es = t.size(0) > 1 ? t.stride(0) : 0;
+  return t;
+}
+
+// (x, logits, w_gate, w_up, w_down, top_k, activation, normalize, first_expert, out, routing)
+PyObject* moe_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const at::Tensor &x = tensor(a[0], "x"), &logits = tensor(a[1], "logits");
+    const int index = gpu_of(x, "x");
+    ar_moe_t m = {};
+    m.dtype = type_code(x.scalar_type(), "x", true);
+    m.logits_dtype = type_code(logits.scalar_type(), "logits", false);
+    const int64_t ldx = matrix(x, "x", x.scalar_type(), index), rows = x.size(0), K = x.size(1);
+    const int64_t ldl = matrix(logits, "logits", logits.scalar_type(), index, rows);
+    int64_t ldw, esw, ldu, esu, ldd, esd, ldo;
+    const at::Tensor& wg = stack(a[2], "w_gate", x.scalar_type(), index, kAny, kAny, K, &ldw, &esw);
+    const int64_t local = wg.size(0), F = wg.size(1);
+    const at::Tensor& wu = stack(a[3], "w_up", x.scalar_type(), index, local, F, K, &ldu, &esu);
+    if (ldu != ldw || esu != esw) refuse("w_gate and w_up must have the same strides");
+    const at::Tensor& wd = stack(a[4], "w_down", x.scalar_type(), index, local, K, F, &ldd, &esd);
+    for (int i = 0; i < 5; ++i) {
+      static const char* const names[] = {"x", "logits", "w_gate", "w_up", "w_down"};
+      no_history(tensor(a[i], names[i]), names[i]);
+    }
+    const int64_t experts = logits.size(1), top_k = integer(a[5]), first = integer(a[8]);
+    if (experts < 1 || experts > AR_MAX_EXPERTS) refuse("logits must have 1 to " + std::to_string(AR_MAX_EXPERTS) + " columns");
+    if (first < 0 || first > experts - local)
+      refuse("experts " + std::to_string(first) + " to " + std::to_string(first + local - 1) + " are not among the " +
+             std::to_string(experts) + " of the logits");
+    if (top_k < 1 || top_k > experts || top_k > AR_MAX_TOP_K)
+      refuse("top_k must be in 1 to " + std::to_string(experts < AR_MAX_TOP_K ? experts : (int64_t)AR_MAX_TOP_K));
+    m.activation = (int)integer(a[6]), m.normalize = PyObject_IsTrue(a[7]);
+    m.experts = (int)experts, m.first_expert = (int)first, m.local_experts = (int)local, m.top_k = (int)top_k;
+    m.hidden = (size_t)K, m.width = (size_t)F;
+    const at::Tensor out = output(a[9], "out", x.scalar_type(), index, rows, K, x, &ldo);
+    at::Tensor expert, weight;
+    if (PyObject_IsTrue(a[10])) {
+      expert = at::empty({rows, top_k}, x.options().dtype(at::kInt));
+      weight = at::empty({rows, top_k}, x.options().dtype(at::kFloat));
+    }
+    const at::Tensor room = scratch(ar_moe_scratch_bytes(&m, (size_t)rows), x);
+    call("ar_moe_ffn", index, [&](void* s) {
+      return ar_moe_ffn(&m, x.data_ptr(), ldx, logits.data_ptr(), ldl, wg.data_ptr(), wu.data_ptr(), ldw, esw, wd.data_ptr(), ldd,
+                        esd, out.data_ptr(), ldo, static_cast<int32_t*>(address(expert)), static_cast<float*>(address(weight)),
+                        (size_t)rows, address(room), bytes_of(room), s);
+    });
+    return expert.defined() ? tuple_of(out, expert, weight) : THPVariable_Wrap(out);
+  });
+}
+
 // (check): what raises for a status that is not AR_OK.
 PyObject* set_check(PyObject*, PyObject* f) {
   Py_XSETREF(g_check, Py_NewRef(f));
@@ -535,6 +600,7 @@ PyMethodDef methods[] = {AR_FAST(ffn_forward),
                          AR_FAST(dropout_backward),
                          AR_FAST(quantize_rows),
                          AR_FAST(linear_i8),
+                         AR_FAST(moe_ffn),
                          AR_FAST(residual_norm),
                          AR_FAST(residual_norm_backward),
                          {"set_check", set_check, METH_O, nullptr},

@@ -202,6 +202,32 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
     return _ops.linear_i8(x, x_scale, w, w_scale, out, code)
 
 
+def moe_ffn(x, logits, w_gate, w_up, w_down, top_k: int, activation: str = "silu", normalize: bool = True,
+            first_expert: int = 0, out=None, routing: bool = False, stream=None):
+    """A layer of gated experts for a few tokens; with ``routing`` ``(out, expert, weight)``.
+
+    Token t goes to the experts of its ``top_k`` highest ``logits`` (equal ones by the
+    lowest index), weighted by their softmax over all experts or, with
+    ``normalize``, over the chosen ones::
+
+        out[t] = sum_j weight[t, j] * ((act(x[t] Wgate_e^T) * (x[t] Wup_e^T)) Wdown_e^T),   e = expert[t, j]
+
+    ``w_gate`` and ``w_up`` are experts x width x hidden, ``w_down`` experts x
+    hidden x width.  They may be a part of the layer's experts, from
+    ``first_expert`` on, or of their width: the ranks' outputs are then summed.  A logit of
+    -infinity is never chosen (expert -1, weight 0, where fewer remain).  Each
+    matrix in use is read once for every 32 tokens.
+    """
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
+    if stream is not None:
+        with _current(stream, getattr(x, "device", None)):
+            return _ops.moe_ffn(x, logits, w_gate, w_up, w_down, top_k, ACTIVATIONS[activation], normalize, first_expert,
+                                out, routing)
+    return _ops.moe_ffn(x, logits, w_gate, w_up, w_down, top_k, ACTIVATIONS[activation], normalize, first_expert, out,
+                        routing)
+
+
 def _kind(kind: str) -> int:
     if kind not in NORMS:
         raise ValueError("kind must be one of %s" % ", ".join(sorted(NORMS)))

@@ -127,3 +127,53 @@ class Norm:
             g, eg = t, et
         out["dx"] = (g, eg)
         return out
+
+
+def routing(logits, top_k, normalize):
+    """(experts, weights in 64 bits, relative bound on the weights) by the definition, on the host."""
+    z = logits.double().cpu()
+    T, n = z.shape
+    expert = torch.full((T, top_k), -1, dtype=torch.int32)
+    weight = torch.zeros((T, top_k), dtype=torch.float64)
+    bound = torch.zeros((T, 1), dtype=torch.float64)
+    for t in range(T):
+        def place(e):
+            v = float(z[t, e])
+            return (0, 0.0, e) if v != v else (1, -v, e)
+
+        best = [e for e in sorted(range(n), key=place)[:top_k] if float(z[t, e]) != -float("inf")]
+        if not best:
+            continue
+        expert[t, :len(best)] = torch.tensor(best, dtype=torch.int32)
+        d = z[t, best] - z[t, best[0]]
+        p = torch.exp(d)
+        weight[t, :len(best)] = p / (p.sum() if normalize else torch.exp(z[t] - z[t, best[0]]).sum())
+        # the difference's rounding moves the exponential by |d| E, which is itself good to 2 units (4 E); as much again
+        # for the sum, whose terms count by their size (d e^d <= 1/e each), its additions, and the division
+        bound[t] = (2 * d.abs().nan_to_num(0, 0, 0).max() + 16 + n / 32 + 10) * E
+    return expert, weight, bound
+
+
+def moe(x, logits, w_gate, w_up, w_down, top_k, activation="silu", normalize=True, first_expert=0):
+    """(out, its bound without the final rounding, experts, weights, the weights' bound)"""
+    from tests import ff_reference as ff
+    u, tiny = ff.U[x.dtype], ff.TINY[x.dtype]
+    expert, weight, rel = routing(logits, top_k, normalize)
+    K, F = x.shape[1], w_gate.shape[1]
+    out = torch.zeros(x.shape, dtype=torch.float64, device=x.device)
+    bound, size = torch.zeros_like(out), torch.zeros_like(out)
+    for e in range(w_gate.shape[0]):
+        t, j = torch.nonzero(expert == first_expert + e, as_tuple=True)
+        if not len(t):
+            continue
+        w, ew = weight[t, j].to(x.device)[:, None], (weight[t, j] * rel[t, 0]).to(x.device)[:, None]
+        t = t.to(x.device)
+        (h, _, _), (eh, _, _) = ff.forward(x[t], w_gate[e], w_up[e], activation)
+        eh = eh + u * (h.abs() + eh) + tiny
+        d = w_down[e].double()
+        part, epart = h @ d.T, (eh + F * ff.E32 * (h.abs() + eh)) @ d.abs().T
+        out[t] += w * part
+        bound[t] += w * epart + ew * (part.abs() + epart)
+        size[t] += w * (part.abs() + epart)
+    # the weighted pieces are added one by one: at most a piece for every 64 inner columns of a token's experts
+    return out, bound + (top_k * (F / 64 + 1) + 10) * E * size, expert, weight, weight * rel
