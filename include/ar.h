@@ -665,6 +665,68 @@ ar_status_t ar_residual_norm_backward(const ar_norm_t* n, const void* dy, size_t
 /* ar_residual_norm_scratch_bytes -- see ar_residual_norm_backward.  Host-only. */
 size_t ar_residual_norm_scratch_bytes(size_t rows, size_t cols, int vectors);
 
+/* ---- products with 4-bit weights ------------------------------------------
+ *
+ *   y[m, n] = sum_k x[m, k] * scale[n, k / group] * (q[n, k] - zero[n, k / group])
+ * with q and zero whole numbers in 0 .. 15 (zero is 8 where there are none), a
+ * scale of the activations' type for each channel and group of k, for a few
+ * tokens in serving.  The weights are laid out once, when they are loaded: by
+ * ar_pack_i4 from whole numbers a row, or by ar_quantize_i4 from a matrix.  The
+ * pages have no counterpart to them.
+ *
+ * group is 32, 64 or 128; the last group of a row may be short.  The laid-out
+ * arrays are device memory on 16 bytes that the caller owns: `data` and `scale`, and
+ * `zero` where there are zero points, of the sizes that ar_i4_sizes gives.
+ * Their order is the library's own.
+ */
+/* ar_i4_sizes -- *data_bytes, and *scales: how many scales (16 bits each) and how many zero
+ * points (a byte each) the layout of `out` channels of `in` weights holds.  Host-only.
+ * Errors: AR_ERR_INVALID_ARG (a size of 0 or above 2^30, another group, NULL). */
+ar_status_t ar_i4_sizes(size_t out, size_t in, int group, size_t* data_bytes, size_t* scales);
+
+/* ar_pack_i4 -- lays out
+ *   q      [out, in] bytes, of which the low four bits count; leading dimension ldq
+ *   scale  [out, ceil(in / group)], 16 bits each; lds
+ *   zero   NULL, or like scale, a byte each, of which the low four bits count; ldz
+ * into data, packed_scale and packed_zero (NULL where zero is).  Asynchronous. */
+ar_status_t ar_pack_i4(const uint8_t* q, size_t ldq, const void* scale, size_t lds, const uint8_t* zero,
+                       size_t ldz, size_t out, size_t in, int group, void* data, void* packed_scale,
+                       void* packed_zero, void* stream);
+
+/* ar_quantize_i4 -- lays out w [out, in] of dtype (AR_BF16, AR_FP16), each group by itself:
+ *   without zero points  scale = max |w| / 7,  q = rint(w / scale) + 8 in 1 .. 15
+ *   with zero points     scale = max(w, 0) / 15 - min(w, 0) / 15,
+ *                        zero = rint(-min / scale),  q = rint(w / scale) + zero in 0 .. 15
+ * in IEEE fp32, the scale rounded to dtype before it divides, results past either end
+ * taken as that end.  A group of zeros has scale 0; one that holds an
+ * infinity or a NaN has scale NaN.
+ *   packed_zero  NULL: without zero points
+ *   scratch      ar_quantize_i4_scratch_bytes of device memory on 16 bytes, free
+ *                again when the call has completed */
+ar_status_t ar_quantize_i4(const void* w, size_t ldw, size_t out, size_t in, int group, int dtype,
+                           void* data, void* packed_scale, void* packed_zero, void* scratch,
+                           size_t scratch_bytes, void* stream);
+size_t ar_quantize_i4_scratch_bytes(size_t out, size_t in, int group);
+
+/* ar_dequantize_i4 -- w[n, k] = scale * (q - zero), multiplied in fp32 and
+ * rounded once to dtype: [out, in], leading dimension ldw (for a product of many tokens). */
+ar_status_t ar_dequantize_i4(const void* data, const void* packed_scale, const void* packed_zero,
+                             size_t out, size_t in, int group, int dtype, void* w, size_t ldw,
+                             void* stream);
+
+/* ar_linear_i4 -- the product above.
+ *   x  [tokens, in] of dtype AR_BF16 or AR_FP16 (that of the scales), ldx
+ *   y  [tokens, out] of dtype, ldy
+ *   packed_zero  NULL: every zero is 8
+ * q - zero is exact; a group's products are summed in fp32, multiplied by its
+ * scale in fp32 and added; y is rounded once.  The weights are read once for
+ * every AR_FEW_TOKENS tokens; tokens is at most 32 * 65535.
+ * tokens = 0 returns AR_OK without a launch.  Asynchronous; needs no scratch.
+ * Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (dtype), AR_ERR_CUDA. */
+ar_status_t ar_linear_i4(const void* x, size_t ldx, const void* data, const void* packed_scale,
+                         const void* packed_zero, void* y, size_t ldy, size_t tokens, size_t in,
+                         size_t out, int group, int dtype, void* stream);
+
 /* ---- a layer of gated experts for a few tokens ----------------------------
  *
  * A mixture-of-experts layer in serving: every token is sent to its top_k

@@ -16,12 +16,13 @@ from ._lib import (AR_AUTO, AR_BF16, AR_FP16, AR_FP32, AR_FUSED_LL8,  # noqa: F4
                    AR_MAX_PACKET_RANKS, AR_MAX_RANKS, AR_ONESHOT_FANOUT, AR_ONESHOT_PULL,
                    AR_TWOPHASE, VARIANTS, ArError, ArInfo, check, load)
 
-__all__ = ["AllReduce", "ArError", "GatedFFN", "VARIANTS", "allreduce_fused_noalloc", "dropout",
-           "dropout_backward", "linear_i8", "load", "moe_ffn", "ops_device_status", "quantize_rows", "residual_norm",
-           "residual_norm_backward"]
+__all__ = ["AllReduce", "ArError", "GatedFFN", "Int4Weight", "VARIANTS", "allreduce_fused_noalloc", "dropout",
+           "dropout_backward", "linear_i4", "linear_i8", "load", "moe_ffn", "ops_device_status", "pack_i4",
+           "quantize_i4", "quantize_rows", "residual_norm", "residual_norm_backward"]
 
-_FEED_FORWARD = ("GatedFFN", "dropout", "dropout_backward", "linear_i8", "moe_ffn", "ops_device_status",
-                 "quantize_rows", "residual_norm", "residual_norm_backward")
+_FEED_FORWARD = ("GatedFFN", "Int4Weight", "dropout", "dropout_backward", "linear_i4", "linear_i8", "moe_ffn",
+                 "ops_device_status", "pack_i4", "quantize_i4", "quantize_rows", "residual_norm",
+                 "residual_norm_backward")
 
 
 def __getattr__(name):

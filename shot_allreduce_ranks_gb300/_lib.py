@@ -121,6 +121,12 @@ PROTOTYPES = {
                                         _VP, _SZ, _VP, _VP, _VP, _VP, _SZ, _VP, _SZ, _VP, _SZ,
                                         _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "ar_residual_norm_scratch_bytes": (_SZ, [_SZ, _SZ, _I]),
+    "ar_i4_sizes": (_ST, [_SZ, _SZ, _I, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
+    "ar_pack_i4": (_ST, [_VP, _SZ, _VP, _SZ, _VP, _SZ, _SZ, _SZ, _I, _VP, _VP, _VP, _VP]),
+    "ar_quantize_i4": (_ST, [_VP, _SZ, _SZ, _SZ, _I, _I, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "ar_quantize_i4_scratch_bytes": (_SZ, [_SZ, _SZ, _I]),
+    "ar_dequantize_i4": (_ST, [_VP, _VP, _VP, _SZ, _SZ, _I, _I, _VP, _SZ, _VP]),
+    "ar_linear_i4": (_ST, [_VP, _SZ, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _I, _I, _VP]),
     "ar_moe_ffn": (_ST, [ctypes.POINTER(ArMoe), _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, _SZ, _VP, _SZ, _SZ,
                          _VP, _SZ, _VP, _VP, _SZ, _VP, _SZ, _VP]),
     "ar_moe_scratch_bytes": (_SZ, [ctypes.POINTER(ArMoe), _SZ]),

@@ -34,6 +34,16 @@ bool bad_stack(const void* p, size_t count, size_t rows, size_t cols, size_t ld,
   return bad_matrix(p, rows, cols, ld) || misaligned(p, 2) || es > kMaxElems || (es && count > kMaxElems / es);
 }
 
+bool bad_i4(size_t out, size_t in, int group) {
+  return out < 1 || out > kMaxCols || in < 1 || in > kMaxCols || (group != 32 && group != 64 && group != 128);
+}
+size_t i4_groups(size_t in, int group) { return (in + (size_t)group - 1) / (size_t)group; }
+size_t i4_spans(size_t in, int group) { return i4_groups(in, i4_span(group)); }
+// The laid-out arrays of a call.
+bool bad_i4_arrays(const void* data, const void* scale, const void* zero) {
+  return !data || !scale || misaligned(data, 16) || misaligned(scale, 16) || misaligned(zero, 16);
+}
+
 size_t moe_ldh(const ar_moe_t* m) { return (m->width + 7) / 8 * 8; }
 
 ar_status_t check_moe(const ar_moe_t* m) {
@@ -50,6 +60,91 @@ ar_status_t check_moe(const ar_moe_t* m) {
 }  // namespace
 
 extern "C" {
+
+ar_status_t ar_i4_sizes(size_t out, size_t in, int group, size_t* data_bytes, size_t* scales) {
+  if (bad_i4(out, in, group) || !data_bytes || !scales) return AR_ERR_INVALID_ARG;
+  const size_t tiles = (out + 15) / 16, span = (size_t)i4_span(group), spans = i4_spans(in, group);
+  *data_bytes = tiles * spans * span * 8;
+  *scales = tiles * spans * 16 * (span / (size_t)group);
+  return AR_OK;
+}
+
+ar_status_t ar_pack_i4(const uint8_t* q, size_t ldq, const void* scale, size_t lds, const uint8_t* zero,
+                       size_t ldz, size_t out, size_t in, int group, void* data, void* packed_scale,
+                       void* packed_zero, void* stream) {
+  if (bad_i4(out, in, group)) return AR_ERR_INVALID_ARG;
+  const size_t groups = i4_groups(in, group);
+  if (bad_i4_arrays(data, packed_scale, packed_zero) || (zero != nullptr) != (packed_zero != nullptr) ||
+      bad_matrix(q, out, in, ldq) || bad_matrix(scale, out, groups, lds) || misaligned(scale, 2) ||
+      (zero && bad_matrix(zero, out, groups, ldz)))
+    return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  I4Pack a = {};
+  a.q = q, a.row_scale = static_cast<const uint16_t*>(scale), a.row_zero = zero;
+  a.data = static_cast<uint4*>(data), a.scale = static_cast<uint16_t*>(packed_scale), a.zero = static_cast<uint8_t*>(packed_zero);
+  a.ldq = (int64_t)ldq, a.lds = (int64_t)lds, a.ldz = (int64_t)ldz, a.N = (int64_t)out, a.K = (int64_t)in;
+  a.spans = (int64_t)i4_spans(in, group), a.group = group;
+  return cuda_status(launch_pack_i4(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ar_quantize_i4_scratch_bytes(size_t out, size_t in, int group) {
+  if (bad_i4(out, in, group)) return 0;
+  return out * i4_groups(in, group) * 3 + out * in;
+}
+
+ar_status_t ar_quantize_i4(const void* w, size_t ldw, size_t out, size_t in, int group, int dtype,
+                           void* data, void* packed_scale, void* packed_zero, void* scratch,
+                           size_t scratch_bytes, void* stream) {
+  if (!half_type(dtype)) return AR_ERR_UNSUPPORTED;
+  if (bad_i4(out, in, group) || bad_i4_arrays(data, packed_scale, packed_zero) || bad_matrix(w, out, in, ldw) ||
+      misaligned(w, 2) || !scratch || misaligned(scratch, 16) || scratch_bytes < ar_quantize_i4_scratch_bytes(out, in, group))
+    return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  const size_t groups = i4_groups(in, group);
+  I4Quantize a = {};
+  a.w = w, a.row_scale = static_cast<uint16_t*>(scratch);
+  uint8_t* const zero = static_cast<uint8_t*>(scratch) + out * groups * 2;
+  a.row_zero = packed_zero ? zero : nullptr;
+  a.q = zero + out * groups;
+  a.ldw = (int64_t)ldw, a.N = (int64_t)out, a.K = (int64_t)in, a.group = group;
+  const cudaError_t e = launch_quantize_i4(dtype, a, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return AR_ERR_CUDA;
+  return ar_pack_i4(a.q, in, a.row_scale, groups, a.row_zero, groups, out, in, group, data, packed_scale, packed_zero, stream);
+}
+
+ar_status_t ar_dequantize_i4(const void* data, const void* packed_scale, const void* packed_zero,
+                             size_t out, size_t in, int group, int dtype, void* w, size_t ldw,
+                             void* stream) {
+  if (!half_type(dtype)) return AR_ERR_UNSUPPORTED;
+  if (bad_i4(out, in, group) || bad_i4_arrays(data, packed_scale, packed_zero) || bad_matrix(w, out, in, ldw) || misaligned(w, 2))
+    return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
+  I4Unpack a = {};
+  a.data = static_cast<const uint32_t*>(data), a.scale = static_cast<const uint16_t*>(packed_scale);
+  a.zero = static_cast<const uint8_t*>(packed_zero);
+  a.w = w, a.ldw = (int64_t)ldw, a.N = (int64_t)out, a.K = (int64_t)in;
+  a.spans = (int64_t)i4_spans(in, group), a.group = group;
+  return cuda_status(launch_unpack_i4(dtype, a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+ar_status_t ar_linear_i4(const void* x, size_t ldx, const void* data, const void* packed_scale,
+                         const void* packed_zero, void* y, size_t ldy, size_t tokens, size_t in,
+                         size_t out, int group, int dtype, void* stream) {
+  if (!half_type(dtype)) return AR_ERR_UNSUPPORTED;
+  if (bad_i4(out, in, group) || tokens > (size_t)32 * 65535) return AR_ERR_INVALID_ARG;
+  if (tokens == 0) return AR_OK;
+  if (bad_i4_arrays(data, packed_scale, packed_zero) || bad_matrix(x, tokens, in, ldx) || misaligned(x, 2) ||
+      bad_matrix(y, tokens, out, ldy) || misaligned(y, 2))
+    return AR_ERR_INVALID_ARG;
+  I4Args a = {};
+  a.x = x, a.data = data, a.scale = packed_scale, a.zero = static_cast<const uint8_t*>(packed_zero), a.y = y;
+  a.ldx = (int64_t)ldx, a.ldy = (int64_t)ldy, a.M = (int64_t)tokens, a.N = (int64_t)out, a.K = (int64_t)in;
+  a.spans = (int64_t)i4_spans(in, group);
+  return cuda_status(launch_linear_i4(dtype, group, a, static_cast<cudaStream_t>(stream)));
+}
 
 size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens) {
   if (check_moe(m)) return 0;

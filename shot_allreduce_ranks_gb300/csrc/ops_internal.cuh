@@ -172,6 +172,49 @@ constexpr int64_t kNormMaxCtas = 320;  // bounds the parts
 cudaError_t launch_norm_grad(int dtype, NormGradArgs& a, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// 4-bit weights (k_i4.cu).  spans: runs of max(group, 64) along k.
+struct I4Args {
+  const void *x, *data, *scale;
+  const uint8_t* zero;  // or null: 8
+  void* y;
+  int64_t ldx, ldy, M, N, K, spans;
+};
+cudaError_t launch_linear_i4(int dtype, int group, const I4Args& a, cudaStream_t s);
+int i4_span(int group);
+
+struct I4Pack {
+  const uint8_t* q;
+  const uint16_t* row_scale;  // 16 bits of either type
+  const uint8_t* row_zero;
+  uint4* data;
+  uint16_t* scale;
+  uint8_t* zero;
+  int64_t ldq, lds, ldz, N, K, spans;
+  int group;
+};
+cudaError_t launch_pack_i4(const I4Pack& a, int num_sms, cudaStream_t s);
+
+struct I4Quantize {
+  const void* w;
+  uint8_t* q;
+  uint16_t* row_scale;
+  uint8_t* row_zero;  // null: symmetric
+  int64_t ldw, N, K;
+  int group;
+};
+cudaError_t launch_quantize_i4(int dtype, const I4Quantize& a, int num_sms, cudaStream_t s);
+
+struct I4Unpack {
+  const uint32_t* data;
+  const uint16_t* scale;
+  const uint8_t* zero;
+  void* w;
+  int64_t ldw, N, K, spans;
+  int group;
+};
+cudaError_t launch_unpack_i4(int dtype, const I4Unpack& a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // Gated feed-forward experts for at most AR_FEW_TOKENS tokens (k_moe.cu).
 struct MoeArgs {
   const void *x, *logits, *w_gate, *w_up, *w_down;

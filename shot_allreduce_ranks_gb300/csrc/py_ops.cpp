@@ -39,6 +39,7 @@ std::string type_name(at::ScalarType t) {
     case at::kHalf: return "torch.float16";
     case at::kFloat: return "torch.float32";
     case at::kChar: return "torch.int8";
+    case at::kByte: return "torch.uint8";
     default: return c10::toString(t);
   }
 }
@@ -522,6 +523,121 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count
   });
 }
 
+// An Int4Weight's constants: data, scale, zero or None, out, in, group.
+struct Packed {
+  at::Tensor data, scale, zero;
+  int64_t out, in;
+  int group, index, code;
+  at::ScalarType type;
+  explicit Packed(PyObject* o) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 6) {
+      PyErr_SetString(PyExc_TypeError, "expected an Int4Weight's six constants");
+      throw Raised{};
+    }
+    data = tensor(PyTuple_GET_ITEM(o, 0), "data"), scale = tensor(PyTuple_GET_ITEM(o, 1), "scale");
+    if (PyTuple_GET_ITEM(o, 2) != Py_None) zero = tensor(PyTuple_GET_ITEM(o, 2), "zero");
+    out = integer(PyTuple_GET_ITEM(o, 3)), in = integer(PyTuple_GET_ITEM(o, 4)), group = (int)integer(PyTuple_GET_ITEM(o, 5));
+    index = gpu_of(data, "data"), type = scale.scalar_type(), code = type_code(type, "scale", true);
+    size_t bytes = 0, scales = 0;
+    if (ar_i4_sizes((size_t)out, (size_t)in, group, &bytes, &scales) != AR_OK) refuse("an Int4Weight of no matrix's size");
+    array(data, "data", at::kByte, bytes);
+    array(scale, "scale", type, scales);
+    if (zero.defined()) array(zero, "zero", at::kByte, scales);
+  }
+  void array(const at::Tensor& t, const char* what, at::ScalarType want, size_t count) const {
+    if (t.scalar_type() != want || !t.is_cuda() || t.get_device() != index || !t.is_contiguous() || (size_t)t.numel() != count)
+      refuse(std::string("the weight's ") + what + " must be " + std::to_string(count) + " contiguous " + type_name(want) +
+             " values on cuda:" + std::to_string(index));
+  }
+  // New arrays for a layout.
+  Packed(int64_t out_, int64_t in_, int group_, bool zeros, at::ScalarType type_, const at::Tensor& like)
+      : out(out_), in(in_), group(group_), index(like.get_device()), type(type_) {
+    if (group != 32 && group != 64 && group != 128) refuse("group must be 32, 64 or 128");
+    size_t bytes = 0, scales = 0;
+    if (ar_i4_sizes((size_t)out, (size_t)in, group, &bytes, &scales) != AR_OK)
+      refuse("weights must have 1 to 2^30 rows and columns, got " + std::to_string(out) + " x " + std::to_string(in));
+    code = type_code(type, "scale", true);
+    data = at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
+    scale = at::empty({(int64_t)scales}, like.options().dtype(type));
+    if (zeros) zero = at::empty({(int64_t)scales}, like.options().dtype(at::kByte));
+  }
+};
+
+// (q, scale, zero, group): data, scale, zero
+PyObject* pack_i4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    const at::Tensor &q = tensor(a[0], "q"), &scale = tensor(a[1], "scale");
+    const int index = gpu_of(q, "q"), group = (int)integer(a[3]);
+    if (group != 32 && group != 64 && group != 128) refuse("group must be 32, 64 or 128");
+    const int64_t ldq = matrix(q, "q", at::kByte, index), rows = q.size(0), cols = q.size(1), groups = (cols + group - 1) / group;
+    const at::ScalarType type = scale.scalar_type();
+    type_code(type, "scale", true);
+    const int64_t lds = matrix(scale, "scale", type, index, rows, groups);
+    int64_t ldz = 0;
+    at::Tensor zero;
+    if (a[2] != Py_None) {
+      zero = tensor(a[2], "zero");
+      ldz = matrix(zero, "zero", at::kByte, index, rows, groups);
+    }
+    no_history(scale, "scale");
+    const Packed p(rows, cols, group, zero.defined(), type, q);
+    call("ar_pack_i4", index, [&](void* s) {
+      return ar_pack_i4(static_cast<const uint8_t*>(q.data_ptr()), ldq, scale.data_ptr(), lds, static_cast<const uint8_t*>(address(zero)),
+                        ldz, rows, cols, group, p.data.data_ptr(), p.scale.data_ptr(), address(p.zero), s);
+    });
+    return tuple_of(p.data, p.scale, p.zero);
+  });
+}
+
+// (w, group, whether zero points): data, scale, zero
+PyObject* quantize_i4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    const at::Tensor& w = tensor(a[0], "w");
+    const int index = gpu_of(w, "w");
+    const at::ScalarType type = w.scalar_type();
+    const int code = type_code(type, "w", true);
+    const int64_t ldw = matrix(w, "w", type, index), rows = w.size(0), cols = w.size(1);
+    no_history(w, "w");
+    const Packed p(rows, cols, (int)integer(a[1]), PyObject_IsTrue(a[2]), type, w);
+    const at::Tensor room = scratch(ar_quantize_i4_scratch_bytes(rows, cols, p.group), w);
+    call("ar_quantize_i4", index, [&](void* s) {
+      return ar_quantize_i4(w.data_ptr(), ldw, rows, cols, p.group, code, p.data.data_ptr(), p.scale.data_ptr(), address(p.zero),
+                            address(room), bytes_of(room), s);
+    });
+    return tuple_of(p.data, p.scale, p.zero);
+  });
+}
+
+// (constants, out)
+PyObject* dequantize_i4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 2, [&]() -> PyObject* {
+    const Packed p(a[0]);
+    int64_t ldw;
+    const at::Tensor w = output(a[1], "out", p.type, p.index, p.out, p.in, p.scale, &ldw);
+    call("ar_dequantize_i4", p.index, [&](void* s) {
+      return ar_dequantize_i4(p.data.data_ptr(), p.scale.data_ptr(), address(p.zero), p.out, p.in, p.group, p.code, w.data_ptr(), ldw, s);
+    });
+    return THPVariable_Wrap(w);
+  });
+}
+
+// (x, constants, out)
+PyObject* linear_i4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    const Packed p(a[1]);
+    const at::Tensor& x = tensor(a[0], "x");
+    const int64_t ldx = matrix(x, "x", p.type, p.index, kAny, p.in), rows = x.size(0);
+    no_history(x, "x");
+    int64_t ldy;
+    const at::Tensor y = output(a[2], "out", p.type, p.index, rows, p.out, x, &ldy);
+    call("ar_linear_i4", p.index, [&](void* s) {
+      return ar_linear_i4(x.data_ptr(), ldx, p.data.data_ptr(), p.scale.data_ptr(), address(p.zero), y.data_ptr(), ldy, rows, p.in,
+                          p.out, p.group, p.code, s);
+    });
+    return THPVariable_Wrap(y);
+  });
+}
+
 // Experts' matrices: row and expert strides.
 const at::Tensor& stack(PyObject* o, const char* what, at::ScalarType type, int index, int64_t count, int64_t rows, int64_t cols,
                         int64_t* ld, int64_t* es) {
@@ -600,6 +716,10 @@ PyMethodDef methods[] = {AR_FAST(ffn_forward),
                          AR_FAST(dropout_backward),
                          AR_FAST(quantize_rows),
                          AR_FAST(linear_i8),
+                         AR_FAST(pack_i4),
+                         AR_FAST(quantize_i4),
+                         AR_FAST(dequantize_i4),
+                         AR_FAST(linear_i4),
                          AR_FAST(moe_ffn),
                          AR_FAST(residual_norm),
                          AR_FAST(residual_norm_backward),

@@ -202,6 +202,60 @@ def linear_i8(x, x_scale, w, w_scale, out=None, dtype=torch.bfloat16, stream=Non
     return _ops.linear_i8(x, x_scale, w, w_scale, out, code)
 
 
+class Int4Weight:
+    """A matrix of 4-bit weights as ``linear_i4`` reads it: made by ``pack_i4`` or ``quantize_i4``.
+
+    ``shape`` is that of the matrix, ``dtype`` that of the scales and of the
+    activations that it multiplies.  ``data``, ``scale`` and ``zero`` (or None) are the
+    laid-out arrays; their order is the library's own.
+    """
+
+    def __init__(self, data, scale, zero, shape, group: int):
+        self.data, self.scale, self.zero = data, scale, zero
+        self.shape, self.group, self.dtype, self.device = tuple(shape), int(group), scale.dtype, data.device
+        self._constants = (data, scale, zero, *self.shape, self.group)
+
+    def dequantize(self, out=None, stream=None):
+        """The matrix that the weights stand for, rounded to ``dtype`` (for a product of many tokens)."""
+        if stream is not None:
+            with _current(stream, self.device):
+                return _ops.dequantize_i4(self._constants, out)
+        return _ops.dequantize_i4(self._constants, out)
+
+    def __repr__(self):
+        return "Int4Weight(%d x %d, group=%d, dtype=%s, zero=%s)" % (*self.shape, self.group, self.dtype, self.zero is not None)
+
+
+def pack_i4(q, scale, zero=None, group: int = 128, stream=None) -> Int4Weight:
+    """Lays out 4-bit weights: ``scale[n, k // group] * (q[n, k] - zero[n, k // group])``.
+
+    ``q`` and ``zero`` are uint8 matrices of which the low four bits count, zero 8 where it
+    is None; ``scale`` is in bfloat16 or float16.  ``group`` is 32, 64 or 128.
+    """
+    if stream is not None:
+        with _current(stream, getattr(q, "device", None)):
+            return pack_i4(q, scale, zero, group)
+    return Int4Weight(*_ops.pack_i4(q, scale, zero, group), q.shape, group)
+
+
+def quantize_i4(w, group: int = 128, zero: bool = False, stream=None) -> Int4Weight:
+    """A matrix of weights in 4 bits, each group of a row by itself: symmetric, or with zero points."""
+    if stream is not None:
+        with _current(stream, getattr(w, "device", None)):
+            return quantize_i4(w, group, zero)
+    return Int4Weight(*_ops.quantize_i4(w, group, zero), w.shape, group)
+
+
+def linear_i4(x, weight: Int4Weight, out=None, stream=None):
+    """``x W^T`` with 4-bit weights, for a few tokens: the weights are read once for every 32 rows of x."""
+    if not isinstance(weight, Int4Weight):
+        raise TypeError("weight must be an Int4Weight, got %s" % type(weight).__name__)
+    if stream is not None:
+        with _current(stream, getattr(x, "device", None)):
+            return _ops.linear_i4(x, weight._constants, out)
+    return _ops.linear_i4(x, weight._constants, out)
+
+
 def moe_ffn(x, logits, w_gate, w_up, w_down, top_k: int, activation: str = "silu", normalize: bool = True,
             first_expert: int = 0, out=None, routing: bool = False, stream=None):
     """A layer of gated experts for a few tokens; with ``routing`` ``(out, expert, weight)``.

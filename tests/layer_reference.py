@@ -177,3 +177,31 @@ def moe(x, logits, w_gate, w_up, w_down, top_k, activation="silu", normalize=Tru
         size[t] += w * (part.abs() + epart)
     # the weighted pieces are added one by one: at most a piece for every 64 inner columns of a token's experts
     return out, bound + (top_k * (F / 64 + 1) + 10) * E * size, expert, weight, weight * rel
+
+
+def quantize_i4(w, group, zero):
+    """(q, scale, zero point or None) by the definition: IEEE fp32, the scale rounded to 16 bits before it divides."""
+    N, K = w.shape
+    groups = -(-K // group)
+    v = torch.zeros((N, groups * group), device=w.device)
+    v[:, :K] = w.float()
+    v = v.view(N, groups, group)
+    seven, fifteen = torch.tensor(7.0, device=w.device), torch.tensor(15.0, device=w.device)
+    high, low = v.amax(2).clamp_min(0), v.amin(2).clamp_max(0)
+    want = high / fifteen - low / fifteen if zero else torch.maximum(high, -low) / seven
+    bad = ~torch.isfinite(v).all(2)
+    scale = torch.where(bad, float("nan"), want).to(w.dtype)
+    none = (scale == 0) | bad
+    by = torch.where(none, 1.0, scale.float())
+    z = torch.where(none, 0.0, torch.round(-low / by).clamp_max(15)) if zero else torch.full_like(by, 8.0)
+    q = (torch.round(v / by[:, :, None]) + z[:, :, None]).clamp(0.0 if zero else 1.0, 15.0)
+    q = torch.where(none[:, :, None], z[:, :, None].clamp_min(0.0 if zero else 1.0), q)
+    return q.reshape(N, -1)[:, :K].to(torch.uint8), scale, z.to(torch.uint8) if zero else None
+
+
+def weights_i4(q, scale, zero, group):
+    """The weights in 64 bits."""
+    def spread(t):
+        return t.double().repeat_interleave(group, 1)[:, :q.shape[1]]
+
+    return (q.double() - (8.0 if zero is None else spread(zero))) * spread(scale)
