@@ -216,9 +216,8 @@ ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, cons
 }
 
 size_t ar_residual_norm_scratch_bytes(size_t rows, size_t cols, int vectors) {
-  if (vectors <= 0 || cols > kMaxCols) return 0;
-  const size_t parts = rows < (size_t)kNormMaxCtas ? rows : (size_t)kNormMaxCtas;
-  return (size_t)vectors * parts * cols * sizeof(float);
+  if (vectors <= 0 || rows > kMaxElems || cols > kMaxCols) return 0;
+  return (size_t)vectors * (size_t)norm_parts((int64_t)rows, (int64_t)cols) * cols * sizeof(float);
 }
 
 ar_status_t ar_residual_norm_backward(const ar_norm_t* n, const void* dy, size_t lddy, const void* dr,
@@ -264,7 +263,7 @@ ar_status_t ar_residual_norm_backward(const ar_norm_t* n, const void* dy, size_t
   a.dy = dy, a.dr = dr, a.x = x, a.r = r, a.gate = gate;
   a.after_weight = after_weight, a.after_bias = after_bias, a.weight = weight;
   a.dx = dx, a.dresidual = dresidual;
-  const size_t parts = rows < (size_t)kNormMaxCtas ? rows : (size_t)kNormMaxCtas;
+  const size_t parts = (size_t)norm_parts((int64_t)rows, (int64_t)cols);
   float* part = static_cast<float*>(scratch);
   for (int k = 0; k < kNormSums; ++k) {
     a.sum[k] = sums[k];

@@ -168,7 +168,10 @@ struct NormGradArgs {
   float eps, alpha, offset;
   int layer;
 };
-constexpr int64_t kNormMaxCtas = 320;  // bounds the parts
+// CTAs of the backward pass at most, a row of the parts each: SMs times the CTAs
+// that an SM holds, where the rows are no fewer.
+constexpr int64_t kMostSms = 160;
+int64_t norm_parts(int64_t rows, int64_t cols);
 cudaError_t launch_norm_grad(int dtype, NormGradArgs& a, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

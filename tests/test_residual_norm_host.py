@@ -66,7 +66,8 @@ def test_backward_refuses(lib, kw, want):
 def test_scratch_bytes(lib):
     f = lib.ar_residual_norm_scratch_bytes
     assert f(4, 8, 0) == 0 and f(4, 8, 1) == 128 and f(0, 8, 3) == 0
-    assert f(10 ** 6, 100, 5) == 5 * 320 * 400
+    # a row of parts for every CTA, of which there are no more than rows
+    assert f(10 ** 6, 100, 5) == 5 * 640 * 400 and f(10 ** 6, 8192, 1) == 320 * 8192 * 4 and f(100, 20000, 2) == 2 * 100 * 80000
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
