@@ -25,9 +25,9 @@ OPS = os.path.join(PKG, "_ops.so")
 SOURCES = ["ar_api.cu", "k_oneshot.cu", "k_oneshot_bulk.cu", "k_twophase.cu", "k_fused_ll8.cu",
            "k_rs_ag.cu", "op_api.cu", "k_gemm_any.cu", "k_gemm_tc.cu",
            "k_gemm_mid.cu", "k_gemm_i8.cu", "k_gemm_few.cu", "k_rows.cu", "k_dropout.cu",
-           "layer_api.cu", "k_norm.cu", "k_moe.cu", "k_i4.cu"]
+           "layer_api.cu", "k_norm.cu", "k_norm_grad.cu", "k_moe.cu", "k_i4.cu"]
 HEADERS = [os.path.join(CSRC, "ar_internal.cuh"), os.path.join(CSRC, "ops_internal.cuh"),
-           os.path.join(CSRC, "tc_device.cuh"),
+           os.path.join(CSRC, "tc_device.cuh"), os.path.join(CSRC, "norm_device.cuh"),
            os.path.join(INCLUDE, "ar.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -10,6 +10,7 @@
 // for two instructions are 16 contiguous bytes.  An instruction's k lie
 // within one group of 32 or more, so the group's scale multiplies the fp32 sums and never
 // a weight: q - zero is exact in 16 bits.
+#include <stdlib.h>
 #include "ops_internal.cuh"
 
 namespace ar {
@@ -44,113 +45,168 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t zero_lo, uint32_t ze
   for (int i = 0; i < 4; ++i) f[i] = less<E>(biased<E>(w >> (4 * i) & 0x000F000Fu), i & 1 ? zero_hi : zero_lo);
 }
 
-// Sixteen channels for up to 8 NB tokens a CTA; its warps take turns at the spans
+// 16 bytes of a token's row at byte k, of which `left` are there.
+template <bool VEC>
+__device__ __forceinline__ uint4 row_piece(const char* row, int64_t k, int64_t left) {
+  if (VEC && left >= 16) return *reinterpret_cast<const uint4*>(row + k);
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (2 * i < left) w[i / 2] |= ld_elem<2>(row + k + 2 * i) << (16 * (i % 2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A span's weights of one tile, and its scales and zero points.
+template <int GROUP, bool ZERO>
+struct Span {
+  static constexpr int kPer = groups_in(GROUP), kTiles = span_of(GROUP) / 64;
+  uint4 w[kTiles];
+  uint32_t scale[kPer], zero[kPer];
+
+  // The pointers are those of the lane in the tile.
+  __device__ __forceinline__ void load(const uint4* data, const uint16_t* scales, const uint8_t* zeros, int64_t s) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const uint4* p = data + (s * kTiles + i) * 32;
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "l"(p));
+    }
+    if (kPer == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales + s * 8 * kPer * 2));
+      scale[0] = v.x, scale[kPer - 1] = v.y;
+      if (ZERO) {
+        const uint32_t z = __ldg(reinterpret_cast<const uint32_t*>(zeros + s * 8 * kPer * 2));
+        zero[0] = z & 0xFFFFu, zero[kPer - 1] = z >> 16;
+      }
+    } else {
+      scale[0] = __ldg(reinterpret_cast<const uint32_t*>(scales + s * 8 * kPer * 2));
+      if (ZERO) zero[0] = __ldg(reinterpret_cast<const uint16_t*>(zeros + s * 8 * kPer * 2));
+    }
+  }
+
+  // acc += the span's products with x, pieces p of tile i for 8 NB tokens.
+  template <class E, int NB>
+  __device__ __forceinline__ void multiply(float (&acc)[NB][4], const uint4 (&x)[kTiles][2][NB]) const {
+    float sum[NB][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int g = kPer == 2 ? h / 2 : 0;
+        const bool first = GROUP == 32 ? h % 2 == 0 : i == 0 && h == 0, last = GROUP == 32 ? h % 2 == 1 : i == kTiles - 1 && h == 3;
+        const uint32_t zl = ZERO ? zero[g] & 0xFFu : 8u, zh = ZERO ? zero[g] >> 8 : 8u;
+        uint32_t f[4];
+        unpack<E>(words[h], biased<E>(zl * 0x10001u), biased<E>(zh * 0x10001u), f);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const uint4& v = x[i][h / 2][j];
+          const uint32_t y[2] = {h % 2 ? v.z : v.x, h % 2 ? v.w : v.y};
+          if (first) sum[j][0] = sum[j][1] = sum[j][2] = sum[j][3] = 0.0f;
+          mma_16816<E>(sum[j], f, y);
+        }
+        if (last) {
+          const float lo = E::lo(scale[g]), hi = E::hi(scale[g]);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            acc[j][0] = __fmaf_rn(lo, sum[j][0], acc[j][0]);
+            acc[j][1] = __fmaf_rn(lo, sum[j][1], acc[j][1]);
+            acc[j][2] = __fmaf_rn(hi, sum[j][2], acc[j][2]);
+            acc[j][3] = __fmaf_rn(hi, sum[j][3], acc[j][3]);
+          }
+        }
+      }
+    }
+  }
+};
+
+// R tiles of sixteen channels for up to 8 NB tokens a CTA; its warps take turns at the spans
 // along k, and their sums are joined in a fixed order.
-template <class E, int GROUP, bool ZERO, int NB, bool VEC>
+template <class E, int GROUP, bool ZERO, int NB, int R, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_linear_i4(I4Args a) {
   constexpr int kSpan = span_of(GROUP), kPer = groups_in(GROUP), kTiles = kSpan / 64;
-  constexpr int U = NB > 2 ? 1 : 4 / kTiles;  // spans in flight
+  constexpr int U = NB > 2 ? 1 : 2 / kTiles;  // spans in flight
   __shared__ float4 part[kWarps][NB][32];
   pdl_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 32, M = min(a.M - m0, (int64_t)32);
-  const int64_t spans = a.spans, bytes = a.K * 2;
-  const uint4* data = reinterpret_cast<const uint4*>(a.data) + (int64_t)blockIdx.x * spans * kTiles * 32 + lane;
-  const uint16_t* scale = static_cast<const uint16_t*>(a.scale) + ((int64_t)blockIdx.x * spans * 8 + g8) * kPer * 2;
-  const uint8_t* zero = a.zero + ((int64_t)blockIdx.x * spans * 8 + g8) * kPer * 2;
-  const char *begin = static_cast<const char*>(a.x), *end = begin + ((a.M - 1) * a.ldx + a.K) * 2;
+  const int64_t m0 = (int64_t)blockIdx.y * 32, M = min(a.M - m0, (int64_t)32), spans = a.spans, bytes = a.K * 2;
+  const int64_t tiles = (a.N + 15) / 16, tile0 = (int64_t)blockIdx.x * R;
+  const uint4* data[R];
+  const uint16_t* scales[R];
+  const uint8_t* zeros[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {  // a tile past the last is read as the last, and dropped
+    const int64_t t = min(tile0 + r, tiles - 1);
+    data[r] = reinterpret_cast<const uint4*>(a.data) + t * spans * kTiles * 32 + lane;
+    scales[r] = static_cast<const uint16_t*>(a.scale) + (t * spans * 8 + g8) * kPer * 2;
+    zeros[r] = a.zero + (t * spans * 8 + g8) * kPer * 2;
+  }
+  // A token past the last is read as the last: its column of the results is dropped.
   const char* xs[NB];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) xs[j] = 8 * j + g8 < M ? begin + (m0 + 8 * j + g8) * a.ldx * 2 : nullptr;
+  for (int j = 0; j < NB; ++j)
+    xs[j] = static_cast<const char*>(a.x) + (m0 + min((int64_t)(8 * j + g8), M - 1)) * a.ldx * 2 + 16 * t4;
 
-  float acc[NB][4] = {};
-  for (int64_t s0 = (int64_t)warp * U; s0 < spans; s0 += kWarps * U) {
-    uint4 w[U][kTiles], x[U][kTiles][2][NB];
-    uint32_t sc[U][kPer], zp[U][kPer];
+  float acc[R][NB][4] = {};
+  Span<GROUP, ZERO> span[U][R];
+  uint4 x[U][kTiles][2][NB];
+  const int64_t whole = bytes / (kSpan * 2);  // spans that x has all of
+  int64_t s = (int64_t)warp * U;
+  for (; s + U <= whole; s += kWarps * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t s = s0 + u < spans ? s0 + u : spans - 1;
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) w[u][i] = __ldg(data + (s * kTiles + i) * 32);
-      if (kPer == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(scale + s * 8 * kPer * 2));
-        sc[u][0] = v.x, sc[u][kPer - 1] = v.y;
-      } else {
-        sc[u][0] = __ldg(reinterpret_cast<const uint32_t*>(scale + s * 8 * kPer * 2));
-      }
-      if (s0 + u >= spans) sc[u][0] = sc[u][kPer - 1] = 0;
-      if (ZERO) {
-        if (kPer == 2) {
-          const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(zero + s * 8 * kPer * 2));
-          zp[u][0] = v & 0xFFFFu, zp[u][kPer - 1] = v >> 16;
-        } else {
-          zp[u][0] = __ldg(reinterpret_cast<const uint16_t*>(zero + s * 8 * kPer * 2));
-        }
-      }
+      for (int r = 0; r < R; ++r) span[u][r].load(data[r], scales[r], zeros[r], s + u);
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            // a span past the last one counts nothing
-            const int64_t k = (s0 + u) * kSpan * 2 + 128 * i + 64 * p + 16 * t4;
-            x[u][i][p][j] = !xs[j]                     ? make_uint4(0, 0, 0, 0)
-                            : VEC && bytes - k >= 16 ? *reinterpret_cast<const uint4*>(xs[j] + k)
-                                                     : load_anywhere<2>(xs[j] + k, bytes - k, begin, end);
-          }
+          for (int j = 0; j < NB; ++j) x[u][i][p][j] = row_piece<VEC>(xs[j], (s + u) * kSpan * 2 + 128 * i + 64 * p, 16);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float sum[NB][4];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const uint32_t words[4] = {w[u][i].x, w[u][i].y, w[u][i].z, w[u][i].w};
+      for (int r = 0; r < R; ++r) span[u][r].template multiply<E, NB>(acc[r], x[u]);
+  }
+  for (int u = 0; u < U && s + u < spans; ++u) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int g = kPer == 2 ? h / 2 : 0;
-          const bool first = GROUP == 32 ? h % 2 == 0 : i == 0 && h == 0, last = GROUP == 32 ? h % 2 == 1 : i == kTiles - 1 && h == 3;
-          const uint32_t zl = ZERO ? zp[u][g] & 0xFFu : 8u, zh = ZERO ? zp[u][g] >> 8 : 8u;
-          uint32_t f[4];
-          unpack<E>(words[h], biased<E>(zl * 0x10001u), biased<E>(zh * 0x10001u), f);
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const uint4& v = x[u][i][h / 2][j];
-            const uint32_t y[2] = {h % 2 ? v.z : v.x, h % 2 ? v.w : v.y};
-            if (first) sum[j][0] = sum[j][1] = sum[j][2] = sum[j][3] = 0.0f;
-            mma_16816<E>(sum[j], f, y);
-          }
-          if (last) {
-            const float lo = E::lo(sc[u][g]), hi = E::hi(sc[u][g]);
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              acc[j][0] = __fmaf_rn(lo, sum[j][0], acc[j][0]);
-              acc[j][1] = __fmaf_rn(lo, sum[j][1], acc[j][1]);
-              acc[j][2] = __fmaf_rn(hi, sum[j][2], acc[j][2]);
-              acc[j][3] = __fmaf_rn(hi, sum[j][3], acc[j][3]);
-            }
-          }
+        for (int j = 0; j < NB; ++j) {
+          const int64_t k = (s + u) * kSpan * 2 + 128 * i + 64 * p;
+          x[0][i][p][j] = row_piece<VEC>(xs[j], k, bytes - k - 16 * t4);
         }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      span[0][r].load(data[r], scales[r], zeros[r], s + u);
+      span[0][r].template multiply<E, NB>(acc[r], x[0]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NB; ++j) part[warp][j][lane] = make_float4(acc[r][j][0], acc[r][j][1], acc[r][j][2], acc[r][j][3]);
+    __syncthreads();
+    if (warp >= NB) continue;
+    float v[4] = {};
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const float4 p = part[i][warp][lane];
+      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t m = 8 * warp + 2 * t4 + c, n = (tile0 + r) * 16 + g8 + 8 * h;
+        if (m < M && n < a.N) static_cast<uint16_t*>(a.y)[(m0 + m) * a.ldy + n] = (uint16_t)E::from_f32(v[2 * h + c]);
       }
-    }
   }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) part[warp][j][lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-  __syncthreads();
-  if (warp >= NB) return;
-  float v[4] = {};
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const float4 p = part[i][warp][lane];
-    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-  }
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t m = 8 * warp + 2 * t4 + c, n = n0 + g8 + 8 * r;
-      if (m < M && n < a.N) static_cast<uint16_t*>(a.y)[(m0 + m) * a.ldy + n] = (uint16_t)E::from_f32(v[2 * r + c]);
-    }
 }
 
 // One lane's 16 bytes of a tile; get(n, k): the whole number at channel n and k.
@@ -259,11 +315,12 @@ cudaError_t linear(const I4Args& a, cudaStream_t s) {
   const int64_t tiles = (a.N + 15) / 16, runs = (a.M + 31) / 32;
   if (tiles > 0x7FFFFFFF || runs > 65535) return cudaErrorInvalidConfiguration;
   const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx % 8 == 0;
-#define AR_I4_TOKENS(VEC) \
-  (a.M <= 8 ? k_linear_i4<E, GROUP, ZERO, 1, VEC> : a.M <= 16 ? k_linear_i4<E, GROUP, ZERO, 2, VEC> : k_linear_i4<E, GROUP, ZERO, 4, VEC>)
-  auto* k = vec ? AR_I4_TOKENS(true) : AR_I4_TOKENS(false);
+  static const int force = getenv("I4_R") ? atoi(getenv("I4_R")) : 1;
+#define AR_I4_TOKENS(R, VEC) \
+  (a.M <= 8 ? k_linear_i4<E, GROUP, ZERO, 1, R, VEC> : a.M <= 16 ? k_linear_i4<E, GROUP, ZERO, 2, R, VEC> : k_linear_i4<E, GROUP, ZERO, 4, R, VEC>)
+  auto* k = force == 2 ? (vec ? AR_I4_TOKENS(2, true) : AR_I4_TOKENS(2, false)) : (vec ? AR_I4_TOKENS(1, true) : AR_I4_TOKENS(1, false));
 #undef AR_I4_TOKENS
-  return launch_op(k, dim3((unsigned)tiles, (unsigned)runs), kThreads, 0, 1, s, a);
+  return launch_op(k, dim3((unsigned)((tiles + force - 1) / force), (unsigned)runs), kThreads, 0, 1, s, a);
 }
 
 template <class E>

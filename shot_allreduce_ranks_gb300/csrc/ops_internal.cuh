@@ -165,6 +165,7 @@ struct NormGradArgs {
   // How the rows are dealt out: with `split` CTAs to each gate row (1 or more),
   // or (split = 0) with several whole gate rows to each of `ctas` CTAs.
   int64_t ctas, split, chunk;  // chunk: rows of a CTA where split > 0
+  int sums_at;  // bytes of shared memory before the sums that are kept there
   float eps, alpha, offset;
   int layer;
 };
