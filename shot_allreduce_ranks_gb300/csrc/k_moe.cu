@@ -2,15 +2,20 @@
 // include/ar.h), in two kernels: the gated products of the experts that have
 // tokens, then the down products summed over each token's experts.
 //
-// Each used expert's matrices are read once, and memory bounds both kernels.  A
-// CTA finds the routing for itself from the logits: a few hundred
-// instructions, against a kernel of its own and its launch.
+// Each used expert's matrices are read once, and memory bounds both kernels: one
+// CTA an SM walks over its part of the matrices, and each of its warps copies the
+// next pieces of its own (kStages - 1 of 2 KB: 128 KB an SM in flight) into shared memory
+// while it multiplies.  A lane copies just the 16 bytes that it will use, so
+// a warp waits for nothing but its own copies.  A CTA finds the routing for itself from the
+// logits: a few hundred instructions, against a kernel of its own and its launch.
+#include <type_traits>
+
 #include "ops_internal.cuh"
 
 namespace ar {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32, kTokens = AR_FEW_TOKENS, kTop = AR_MAX_TOP_K;
+constexpr int kWarps = 16, kThreads = kWarps * 32, kTokens = AR_FEW_TOKENS, kTop = AR_MAX_TOP_K;
 
 // Logits in an order of whole numbers: NaN first, then by value, -0 as 0; what
 // cannot be chosen (-infinity) is kNever or less.
@@ -152,11 +157,6 @@ __device__ __forceinline__ void route(const MoeArgs& m, char* smem, bool write) 
   __syncthreads();
 }
 
-template <bool VEC>
-__device__ __forceinline__ uint4 weights16(const char* p, int64_t left, const char* begin, const char* end) {
-  if (VEC && left >= 16) return ld_v4_stream(p);
-  return load_anywhere<2>(p, left, begin, end);
-}
 // 16 bytes of an operand that other CTAs of the SM read too.
 template <bool VEC>
 __device__ __forceinline__ uint4 tokens16(const char* p, int64_t left, const char* begin, const char* end) {
@@ -164,6 +164,44 @@ __device__ __forceinline__ uint4 tokens16(const char* p, int64_t left, const cha
   return load_anywhere<2>(p, left, begin, end);
 }
 
+// The pieces of 64 k (two steps of 32) of sixteen rows that a warp copies ahead:
+// lane 4 g + t has rows g and g + 8 at k = 8 t .. 8 t + 7 of each step.
+constexpr int kStages = 5, kSteps = 2, kPieceBytes = 128, kRingBytes = kWarps * kStages * kSteps * 2 * 512;
+
+struct Ring {
+  char* mine;  // this lane's place in its warp's ring
+  __device__ __forceinline__ explicit Ring(char* smem)
+      : mine(smem + (threadIdx.x >> 5) * kStages * kSteps * 2 * 512 + (threadIdx.x & 31) * 16) {}
+  __device__ __forceinline__ char* at(int stage, int step, int row) const { return mine + ((stage * kSteps + step) * 2 + row) * 512; }
+
+  // Rows a and b (this lane's) at byte k of `bytes`; what lies past a row's end is zeros.
+  template <bool VEC>
+  __device__ __forceinline__ void fetch(int stage, const char* a, const char* b, int64_t k, int64_t bytes, const char* begin_a,
+                                        const char* begin_b, int64_t extent) const {
+    const int t4 = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int64_t at_k = k + 64 * i + 16 * t4, left = bytes - at_k;
+      if (VEC) {
+        const int n = left >= 16 ? 16 : left > 0 ? (int)left : 0;
+        copy(at(stage, i, 0), n ? a + at_k : a, n);
+        copy(at(stage, i, 1), n ? b + at_k : b, n);
+      } else {
+        *reinterpret_cast<uint4*>(at(stage, i, 0)) = load_anywhere<2>(a + at_k, left, begin_a, begin_a + extent);
+        *reinterpret_cast<uint4*>(at(stage, i, 1)) = load_anywhere<2>(b + at_k, left, begin_b, begin_b + extent);
+      }
+    }
+  }
+  static __device__ __forceinline__ void copy(char* to, const char* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
+};
+
+// Sums of a step: the rows of mma.sync are the sixteen, its columns eight tokens; which k
+// an instruction's k slots stand for is free as long as both operands agree.
 template <class E, int NB>
 __device__ __forceinline__ void multiply(float (&acc)[NB][4], const uint4& a, const uint4& b, const uint4 (&x)[NB]) {
   const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
@@ -179,192 +217,322 @@ __device__ __forceinline__ void multiply(float (&acc)[NB][4], const uint4& a, co
   }
 }
 
-// Eight rows of one expert's gate and of its up projection for its tokens, 8 NB at
-// most: the rows of mma.sync are the gate's and the up projection's, its
-// columns the tokens; a lane loads 16 contiguous bytes of its rows and its token
-// (which k an instruction's k slots stand for is free as long as they agree).
-// The warps take turns along k.
-template <class E, int ACT, int NB, bool VEC>
-__device__ __forceinline__ void gated_rows(const MoeArgs& m, const RouteTables& tab, int place, int64_t f0,
-                                           uint8_t* list, float4 (*part)[4][32]) {
-  constexpr int U = NB > 2 ? 2 : 4;
+// An item: eight rows of one expert's gate and the same of its up projection, whose
+// sums of one output land in one lane.  The warps take turns at the pieces along k, and
+// their sums are joined in a fixed order.
+template <class E, int ACT, bool VEC>
+__global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
+  extern __shared__ __align__(16) char smem[];
+  pdl_enter();
+  char* const tables_at = smem + kRingBytes;
+  const Ring ring(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
-  const int e = tab.number[place];
-  const uint32_t tokens = tab.tokens[e];
-  const int count = __popc(tokens);
-  if (tokens >> lane & 1) list[__popc(tokens & ((1u << lane) - 1))] = (uint8_t)lane;
-  __syncwarp();
-  const int64_t f = min(f0 + g8, m.width - 1), bytes = m.hidden * 2;
+  // The down kernel's counts of finished parts.
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (m.hidden + 15) / 16; i += (int64_t)gridDim.x * kThreads) m.done[i] = 0;
+  route(m, tables_at, blockIdx.x == 0);
+  const RouteTables tab = tables(tables_at, m.local);
+  float4* const part = reinterpret_cast<float4*>(tables_at + (route_bytes(m.local, (int64_t)m.tokens * m.top_k) + 15) / 16 * 16);
+  __shared__ uint8_t lists[kWarps][kTokens];
+  uint8_t* const list = lists[warp];
+
+  const int strips = (int)((m.width + 7) / 8);
+  const int64_t items = (int64_t)reinterpret_cast<const Routes*>(tables_at)->active * strips, bytes = m.hidden * 2;
+  const int turns = (int)((bytes + kWarps * kPieceBytes - 1) / (kWarps * kPieceBytes));
   const char *bg = static_cast<const char*>(m.w_gate), *bu = static_cast<const char*>(m.w_up), *bx = static_cast<const char*>(m.x);
   const int64_t extent = ((m.local - 1) * m.esw + (m.width - 1) * m.ldw + m.hidden) * 2;
-  const char *wg = bg + (e * m.esw + f * m.ldw) * 2, *wu = bu + (e * m.esw + f * m.ldw) * 2;
   const char* ex = bx + ((m.tokens - 1) * m.ldx + m.hidden) * 2;
-  const char* xs[NB];
-#pragma unroll
-  for (int j = 0; j < NB; ++j) xs[j] = 8 * j + g8 < count ? bx + list[8 * j + g8] * m.ldx * 2 : nullptr;
-  float acc[NB][4] = {};
-  for (int64_t at = (int64_t)warp * 64 * U; at < bytes; at += kWarps * 64 * U) {
-    uint4 a[U], b[U], x[U][NB];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t k = at + 64 * i + 16 * t4;
-      a[i] = weights16<VEC>(wg + k, bytes - k, bg, bg + extent);
-      b[i] = weights16<VEC>(wu + k, bytes - k, bu, bu + extent);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) x[i][j] = xs[j] ? tokens16<VEC>(xs[j] + k, bytes - k, bx, ex) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) multiply<E, NB>(acc, a[i], b[i], x[i]);
-  }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) part[warp][j][lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-  __syncthreads();
-  if (warp < NB) {
-    float v[4] = {};
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 p = part[w][warp][lane];
-      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int i = 8 * warp + 2 * t4 + c;
-      if (i >= count) continue;
-      const int t = list[i];
-      const int64_t row = t * m.top_k + tab.choice[place * kTokens + t];
-      // The row's end, up to a whole group, is read with it: zeros.
-      const float h = f0 + g8 < m.width ? act_value<ACT>(v[c]) * v[c + 2] : 0.0f;
-      static_cast<uint16_t*>(m.h)[row * m.ldh + f0 + g8] = (uint16_t)E::from_f32(h);
-    }
-  }
-  __syncthreads();
-}
 
-template <class E, int ACT, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_moe_gated(MoeArgs m) {
-  extern __shared__ __align__(16) char smem[];
-  __shared__ float4 part[kWarps][4][32];
-  __shared__ uint8_t lists[kWarps][kTokens];
-  pdl_enter();
-  route(m, smem, blockIdx.x == 0);
-  const RouteTables tab = tables(smem, m.local);
-  const int64_t strips = (m.width + 7) / 8, items = reinterpret_cast<const Routes*>(smem)->active * strips;
-  uint8_t* list = lists[threadIdx.x >> 5];
-  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-    const int place = (int)(i / strips), count = __popc(tab.tokens[tab.number[place]]);
-    const int64_t f0 = i % strips * 8;
-    if (count <= 8)
-      gated_rows<E, ACT, 1, VEC>(m, tab, place, f0, list, part);
-    else if (count <= 16)
-      gated_rows<E, ACT, 2, VEC>(m, tab, place, f0, list, part);
-    else
-      gated_rows<E, ACT, 4, VEC>(m, tab, place, f0, list, part);
-  }
-}
+  // What is copied next: turn next_turn of item next, rows at wg and wu.
+  int64_t next = blockIdx.x;
+  int next_turn = 0;
+  const char *wg = nullptr, *wu = nullptr;
+  const auto fetch = [&](int stage) {
+    if (next < items) {
+      if (next_turn == 0) {
+        const int place = (int)(next / strips), e = tab.number[place];
+        const int64_t f = min((next - (int64_t)place * strips) * 8 + g8, m.width - 1), at = (e * m.esw + f * m.ldw) * 2;
+        wg = bg + at, wu = bu + at;
+      }
+      const int64_t k = (int64_t)(next_turn * kWarps + warp) * kPieceBytes;
+      if (k < bytes) ring.fetch<VEC>(stage, wg, wu, k, bytes, bg, bu, extent);
+      if (++next_turn == turns) next_turn = 0, next += gridDim.x;
+    }
+    Ring::commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
-// Sixteen output columns for all tokens (8 NB at most): the warps take turns at
-// pieces of 128 of the experts' inner columns; each piece's sums are weighted and
-// added in fp32, in a fixed order.
-template <class E, int NB, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_moe_down(MoeArgs m) {
-  extern __shared__ __align__(16) char smem[];
-  __shared__ float4 part[kWarps][NB][32];
-  constexpr int U = NB > 2 ? 2 : 4;
-  pdl_enter();
-  route(m, smem, false);
-  const Routes& s = *reinterpret_cast<const Routes*>(smem);
-  const RouteTables tab = tables(smem, m.local);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, bytes = m.width * 2;
-  const int64_t ra = min(n0 + g8, m.hidden - 1), rb = min(n0 + g8 + 8, m.hidden - 1);
-  const char *bd = static_cast<const char*>(m.w_down), *ed = bd + ((m.local - 1) * m.esd + (m.hidden - 1) * m.ldd + m.width) * 2;
-  const char* h = static_cast<const char*>(m.h);
-  const int pieces = (int)((bytes + 64 * U - 1) / (64 * U)), units = s.active * pieces;
-  float total[NB][4] = {};
-  for (int u = warp; u < units; u += kWarps) {
-    const int place = u / pieces, e = tab.number[place];
+  int stage = 0;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int place = (int)(item / strips), e = tab.number[place];
+    const int64_t f0 = (item - (int64_t)place * strips) * 8;
     const uint32_t tokens = tab.tokens[e];
-    const int64_t at = (int64_t)(u % pieces) * 64 * U;
-    const char *wa = bd + (e * m.esd + ra * m.ldd) * 2, *wb = bd + (e * m.esd + rb * m.ldd) * 2;
-    uint4 a[U], b[U], x[U][NB];
+    const int count = __popc(tokens);
+    __syncwarp();
+    if (tokens >> lane & 1) list[__popc(tokens & ((1u << lane) - 1))] = (uint8_t)lane;
+    __syncwarp();
+    const auto run = [&](auto blocks) {
+      constexpr int NB = decltype(blocks)::value;
+      const char* xs[NB];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t k = at + 64 * i + 16 * t4;
-      a[i] = weights16<VEC>(wa + k, bytes - k, bd, ed);
-      b[i] = weights16<VEC>(wb + k, bytes - k, bd, ed);
-    }
+      for (int j = 0; j < NB; ++j) xs[j] = 8 * j + g8 < count ? bx + list[8 * j + g8] * m.ldx * 2 : nullptr;
+      float acc[NB][4] = {};
+      for (int turn = 0; turn < turns; ++turn) {
+        fetch(stage == 0 ? kStages - 1 : stage - 1);
+        const int64_t k0 = (int64_t)(turn * kWarps + warp) * kPieceBytes + 16 * t4;
+        uint4 x[kSteps][NB];
+        if (k0 - 16 * t4 < bytes) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int t = 8 * j + g8;
-      const bool has = tokens >> t & 1;
-      const char* row = h + (has ? t * m.top_k + tab.choice[place * kTokens + t] : 0) * m.ldh * 2;
+          for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t k = at + 64 * i + 16 * t4;
-        // rows of h start on 16 bytes and end in zeros
-        x[i][j] = has && k < bytes ? *reinterpret_cast<const uint4*>(row + k) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < NB; ++j)
+              x[i][j] = xs[j] ? tokens16<VEC>(xs[j] + k0 + 64 * i, bytes - k0 - 64 * i, bx, ex) : make_uint4(0, 0, 0, 0);
+          Ring::wait();
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+            multiply<E, NB>(acc, *reinterpret_cast<const uint4*>(ring.at(stage, i, 0)), *reinterpret_cast<const uint4*>(ring.at(stage, i, 1)), x[i]);
+        }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
       }
-    }
-    float acc[NB][4] = {};
 #pragma unroll
-    for (int i = 0; i < U; ++i) multiply<E, NB>(acc, a[i], b[i], x[i]);
+      for (int j = 0; j < NB; ++j) part[(warp * NB + j) * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+      __syncthreads();
+      if (warp < NB) {
+        float v[4] = {};
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 p = part[(w * NB + warp) * 32 + lane];
+          v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+        }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int t = 8 * j + 2 * t4 + c;
-        if (!(tokens >> t & 1)) continue;  // 0 times an infinite weight would be NaN
-        const float w = s.weight[t][tab.choice[place * kTokens + t]];
-        total[j][c] = __fmaf_rn(w, acc[j][c], total[j][c]);
-        total[j][c + 2] = __fmaf_rn(w, acc[j][c + 2], total[j][c + 2]);
+        for (int c = 0; c < 2; ++c) {
+          const int i = 8 * warp + 2 * t4 + c;
+          if (i >= count) continue;
+          const int t = list[i];
+          const int64_t row = t * m.top_k + tab.choice[place * kTokens + t];
+          // The row's end, up to a whole group, is read with it: zeros.
+          const float h = f0 + g8 < m.width ? act_value<ACT>(v[c]) * v[c + 2] : 0.0f;
+          static_cast<uint16_t*>(m.h)[row * m.ldh + f0 + g8] = (uint16_t)E::from_f32(h);
+        }
       }
+      __syncthreads();
+    };
+    if (count <= 8)
+      run(std::integral_constant<int, 1>());
+    else if (count <= 16)
+      run(std::integral_constant<int, 2>());
+    else
+      run(std::integral_constant<int, 4>());
   }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) part[warp][j][lane] = make_float4(total[j][0], total[j][1], total[j][2], total[j][3]);
-  __syncthreads();
-  if (warp >= NB) return;
-  float v[4] = {};
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float4 p = part[w][warp][lane];
-    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-  }
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t t = 8 * warp + 2 * t4 + c, n = n0 + g8 + 8 * r;
-      if (t < m.tokens && n < m.hidden) static_cast<uint16_t*>(m.out)[t * m.ldo + n] = (uint16_t)E::from_f32(v[2 * r + c]);
-    }
 }
 
-template <class E, int ACT, bool VEC>
-cudaError_t moe(const MoeArgs& m, int num_sms, cudaStream_t s) {
-  const int64_t pairs = m.tokens * m.top_k, most = m.local < pairs ? m.local : pairs;
-  const int64_t strips = (m.width + 7) / 8, tiles = (m.hidden + 15) / 16;
-  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const size_t smem = route_bytes(m.local, pairs);
-  const int64_t items = most * strips, slots = (int64_t)num_sms * 3;
-  cudaError_t e = launch_op(k_moe_gated<E, ACT, VEC>, dim3((unsigned)(items < slots ? items : slots)), kThreads, smem, 1, s, m);
-  if (e != cudaSuccess) return e;
-  auto* k = m.tokens <= 8 ? k_moe_down<E, 1, VEC> : m.tokens <= 16 ? k_moe_down<E, 2, VEC> : k_moe_down<E, 4, VEC>;
-  return launch_op(k, dim3((unsigned)tiles), kThreads, smem, 1, s, m);
+// Sixteen output columns are a tile, for which there are as many units as pieces
+// of 64 of the used experts' inner columns.  All tiles' units are dealt out evenly in one
+// row, so that every SM reads as much; a CTA's part of a tile is shared out among its
+// warps in runs.  A run's sums of one expert's tokens (eight at a time) are weighted and
+// added to the warp's own sums in fp32, and those are joined in the warps' order.  A tile that
+// lies on several CTAs is left in parts, which the CTA that finishes last
+// adds in their order: nothing is waited for, and every call gives the same bits.
+template <class E, bool VEC>
+__global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
+  extern __shared__ __align__(16) char smem[];
+  char* const tables_at = smem + kRingBytes;
+  const Ring ring(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  // The kernel before this one, which made h, has itself waited for what came before
+  // it: the logits and the weights may be read before it ends.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  route(m, tables_at, false);
+  const Routes& s = *reinterpret_cast<const Routes*>(tables_at);
+  const RouteTables tab = tables(tables_at, m.local);
+  // sums[warp][token][16], 17 apart against bank conflicts
+  float* const sums = reinterpret_cast<float*>(tables_at + (route_bytes(m.local, (int64_t)m.tokens * m.top_k) + 15) / 16 * 16);
+  __shared__ uint8_t lists[kWarps][kTokens];
+  __shared__ int finished;
+  uint8_t* const list = lists[warp];
+  const int entries = m.tokens * 17;
+  float* const own = sums + warp * entries;
+
+  const int64_t tiles = (m.hidden + 15) / 16, bytes = m.width * 2;
+  const int pieces = (int)((bytes + kPieceBytes - 1) / kPieceBytes), units = s.active * pieces;
+  const int64_t total = tiles * units;
+  const int G = (int)min((int64_t)gridDim.x, total);  // CTAs that have a part, none of it empty
+  const char* bd = static_cast<const char*>(m.w_down);
+  const int64_t extent = ((m.local - 1) * m.esd + (m.hidden - 1) * m.ldd + m.width) * 2;
+  const char* h = static_cast<const char*>(m.h);
+
+  if (units == 0) {  // no token has an expert here
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < m.tokens * m.hidden; i += (int64_t)gridDim.x * kThreads)
+      static_cast<uint16_t*>(m.out)[i / m.hidden * m.ldo + i % m.hidden] = 0;
+    return;
+  }
+  // This CTA's part of the row of units, and this warp's run of a tile's.
+  const int64_t cta = min((int)blockIdx.x, G), begin = cta * total / G, end = min(cta + 1, (int64_t)G) * total / G;
+  struct Run {
+    int64_t tile, pos;  // pos: where the CTA's part of the tile begins
+    int u0, u1;         // that part
+    int at, stop;       // this warp's run
+  };
+  const auto run_at = [&](int64_t pos) {
+    Run r;
+    r.pos = pos, r.tile = pos / units, r.u0 = (int)(pos - r.tile * units);
+    r.u1 = (int)min((int64_t)units, r.u0 + (end - pos));
+    const int n = r.u1 - r.u0, each = (n + kWarps - 1) / kWarps;
+    r.at = r.u0 + min(warp * each, n), r.stop = r.u0 + min((warp + 1) * each, n);
+    return r;
+  };
+  Run next = begin < end ? run_at(begin) : Run{0, end, 0, 0, 0, 0};
+  const auto fetch = [&](int stage) {
+    while (next.at >= next.stop && next.pos < end) {
+      const int64_t pos = next.pos + (next.u1 - next.u0);
+      if (pos >= end) {
+        next.pos = end;
+        break;
+      }
+      next = run_at(pos);
+    }
+    if (next.pos < end) {
+      const int place = next.at / pieces, e = tab.number[place];
+      const int64_t n0 = next.tile * 16, ra = min(n0 + g8, m.hidden - 1), rb = min(n0 + g8 + 8, m.hidden - 1);
+      const char* we = bd + e * m.esd * 2;
+      ring.fetch<VEC>(stage, we + ra * m.ldd * 2, we + rb * m.ldd * 2, (int64_t)(next.at - place * pieces) * kPieceBytes, bytes, bd, bd, extent);
+      ++next.at;
+    }
+    Ring::commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  int stage = 0;
+  for (int64_t pos = begin; pos < end;) {
+    const Run r = run_at(pos);
+    for (int i = lane; i < entries; i += 32) own[i] = 0.0f;
+    int u = r.at;
+    while (u < r.stop) {
+      const int place = u / pieces, until = min(r.stop, (place + 1) * pieces);
+      const uint32_t tokens = tab.tokens[tab.number[place]];
+      const int count = __popc(tokens);
+      __syncwarp();
+      if (tokens >> lane & 1) list[__popc(tokens & ((1u << lane) - 1))] = (uint8_t)lane;
+      __syncwarp();
+      const auto run = [&](auto blocks) {
+        constexpr int NB = decltype(blocks)::value;
+        const char* xs[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int t = 8 * j + g8 < count ? list[8 * j + g8] : -1;
+          xs[j] = t < 0 ? nullptr : h + (int64_t)(t * m.top_k + tab.choice[place * kTokens + t]) * m.ldh * 2;
+        }
+        float acc[NB][4] = {};
+        for (; u < until; ++u) {
+          fetch(stage == 0 ? kStages - 1 : stage - 1);
+          const int64_t k0 = (int64_t)(u - place * pieces) * kPieceBytes + 16 * t4;
+          uint4 x[kSteps][NB];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)  // rows of h start on 16 bytes and end in zeros
+              x[i][j] = xs[j] && k0 + 64 * i < bytes ? *reinterpret_cast<const uint4*>(xs[j] + k0 + 64 * i) : make_uint4(0, 0, 0, 0);
+          Ring::wait();
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+            multiply<E, NB>(acc, *reinterpret_cast<const uint4*>(ring.at(stage, i, 0)), *reinterpret_cast<const uint4*>(ring.at(stage, i, 1)), x[i]);
+          stage = stage == kStages - 1 ? 0 : stage + 1;
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int i = 8 * j + 2 * t4 + c;
+            if (i >= count) continue;
+            const int t = list[i];
+            const float w = s.weight[t][tab.choice[place * kTokens + t]];
+            own[t * 17 + g8] = __fmaf_rn(w, acc[j][c], own[t * 17 + g8]);
+            own[t * 17 + g8 + 8] = __fmaf_rn(w, acc[j][c + 2], own[t * 17 + g8 + 8]);
+          }
+      };
+      if (count <= 8)
+        run(std::integral_constant<int, 1>());
+      else if (count <= 16)
+        run(std::integral_constant<int, 2>());
+      else
+        run(std::integral_constant<int, 4>());
+    }
+    __syncthreads();
+    const bool whole = r.u0 == 0 && r.u1 == units;
+    float* const mine = m.parts + ((int64_t)blockIdx.x * 2 + (r.u0 == 0)) * kTokens * 16;
+    for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += sums[w * entries + i / 16 * 17 + i % 16];
+      const int64_t n = r.tile * 16 + i % 16;
+      if (!whole)
+        mine[i] = v;
+      else if (n < m.hidden)
+        static_cast<uint16_t*>(m.out)[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+    }
+    if (!whole) {
+      // CTA c has unit p of the row where c is the last whose part begins at or before p.
+      const int64_t p0 = r.tile * units, p1 = p0 + units - 1;
+      const int c0 = (int)(((p0 + 1) * G - 1) / total), c1 = (int)(((p1 + 1) * G - 1) / total);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) finished = atomicAdd(&m.done[r.tile], 1u) == (uint32_t)(c1 - c0);
+      __syncthreads();
+      if (finished) {
+        __threadfence();
+        for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
+          float v = 0.0f;
+          for (int c = c0; c <= c1; ++c) v += __ldcg(m.parts + ((int64_t)c * 2 + (c == c0)) * kTokens * 16 + i);
+          const int64_t n = r.tile * 16 + i % 16;
+          if (n < m.hidden) static_cast<uint16_t*>(m.out)[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+        }
+      }
+    }
+    __syncthreads();
+    pos += r.u1 - r.u0;
+  }
 }
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <class E, int ACT>
-cudaError_t moe_align(const MoeArgs& m, int num_sms, cudaStream_t s) {
-  const bool vec = ((reinterpret_cast<uintptr_t>(m.x) | reinterpret_cast<uintptr_t>(m.w_gate) | reinterpret_cast<uintptr_t>(m.w_up) |
-                     reinterpret_cast<uintptr_t>(m.w_down)) & 15u) == 0 &&
-                   (m.ldx | m.ldw | m.esw | m.ldd | m.esd) % 8 == 0;
-  return vec ? moe<E, ACT, true>(m, num_sms, s) : moe<E, ACT, false>(m, num_sms, s);
+cudaError_t moe(const MoeArgs& m, int num_sms, cudaStream_t s) {
+  const int64_t pairs = (int64_t)m.tokens * m.top_k, most = m.local < pairs ? m.local : pairs, strips = (m.width + 7) / 8;
+  const size_t tables = (route_bytes(m.local, pairs) + 15) / 16 * 16;
+  const size_t blocks = m.tokens <= 8 ? 1 : m.tokens <= 16 ? 2 : 4;
+  const size_t gated = kRingBytes + tables + kWarps * blocks * 512, down = kRingBytes + tables + (size_t)kWarps * m.tokens * 17 * 4;
+  const bool vec = on16(m.x) && on16(m.w_gate) && on16(m.w_up) && (m.ldx | m.ldw | m.esw) % 8 == 0;
+  auto* k = vec ? k_moe_gated<E, ACT, true> : k_moe_gated<E, ACT, false>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gated);
+  if (e != cudaSuccess) return e;
+  const int64_t slots = num_sms < kMostSms ? num_sms : kMostSms, items = most * strips;
+  e = launch_op(k, dim3((unsigned)(items < slots ? items : slots)), kThreads, gated, 1, s, m);
+  if (e != cudaSuccess) return e;
+  auto* d = on16(m.w_down) && (m.ldd | m.esd) % 8 == 0 ? k_moe_down<E, true> : k_moe_down<E, false>;
+  e = cudaFuncSetAttribute(d, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)down);
+  if (e != cudaSuccess) return e;
+  return launch_op(d, dim3((unsigned)slots), kThreads, down, 1, s, m);
 }
 
 }  // namespace
 
+size_t moe_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t hidden, MoeArgs* m, char* base) {
+  const size_t ldh = (size_t)(width + 7) / 8 * 8, t = tokens < kTokens ? tokens : kTokens;
+  const size_t h = (t * top_k * ldh * 2 + 15) / 16 * 16, done = ((size_t)(hidden + 15) / 16 * 4 + 15) / 16 * 16;
+  if (m) {
+    m->h = base, m->ldh = (int64_t)ldh;
+    m->done = reinterpret_cast<uint32_t*>(base + h);
+    m->parts = reinterpret_cast<float*>(base + h + done);
+  }
+  return h + done + (size_t)kMostSms * 2 * kTokens * 16 * 4;
+}
+
 cudaError_t launch_moe(int dtype, int act, const MoeArgs& m, int num_sms, cudaStream_t s) {
-  if (dtype == AR_BF16)
-    return act == AR_ACT_SILU ? moe_align<Bf16, AR_ACT_SILU>(m, num_sms, s) : moe_align<Bf16, AR_ACT_GELU_TANH>(m, num_sms, s);
-  return act == AR_ACT_SILU ? moe_align<F16, AR_ACT_SILU>(m, num_sms, s) : moe_align<F16, AR_ACT_GELU_TANH>(m, num_sms, s);
+  if (dtype == AR_BF16) return act == AR_ACT_SILU ? moe<Bf16, AR_ACT_SILU>(m, num_sms, s) : moe<Bf16, AR_ACT_GELU_TANH>(m, num_sms, s);
+  return act == AR_ACT_SILU ? moe<F16, AR_ACT_SILU>(m, num_sms, s) : moe<F16, AR_ACT_GELU_TANH>(m, num_sms, s);
 }
 
 }  // namespace ar

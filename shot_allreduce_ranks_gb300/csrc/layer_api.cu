@@ -9,7 +9,7 @@ namespace {
 
 using namespace ar;  // the entry points' shared checks
 
-constexpr size_t kMaxCols = (size_t)1 << 30;
+constexpr size_t kMaxCols = (size_t)1 << 30, kMaxInner = (size_t)1 << 22;
 
 size_t elem_bytes(int dtype) { return dtype == AR_FP32 ? 4 : 2; }
 
@@ -44,15 +44,13 @@ bool bad_i4_arrays(const void* data, const void* scale, const void* zero) {
   return !data || !scale || misaligned(data, 16) || misaligned(scale, 16) || misaligned(zero, 16);
 }
 
-size_t moe_ldh(const ar_moe_t* m) { return (m->width + 7) / 8 * 8; }
-
 ar_status_t check_moe(const ar_moe_t* m) {
   if (!m) return AR_ERR_INVALID_ARG;
   if (!half_type(m->dtype) || !any_type(m->logits_dtype)) return AR_ERR_UNSUPPORTED;
   if ((m->activation != AR_ACT_SILU && m->activation != AR_ACT_GELU_TANH) || m->experts < 1 ||
       m->experts > AR_MAX_EXPERTS || m->local_experts < 1 || m->local_experts > m->experts || m->first_expert < 0 ||
       m->first_expert > m->experts - m->local_experts || m->top_k < 1 || m->top_k > AR_MAX_TOP_K ||
-      m->top_k > m->experts || m->hidden < 1 || m->hidden > kMaxCols || m->width < 1 || m->width > kMaxCols)
+      m->top_k > m->experts || m->hidden < 1 || m->hidden > kMaxInner || m->width < 1 || m->width > kMaxInner)
     return AR_ERR_INVALID_ARG;
   return AR_OK;
 }
@@ -139,16 +137,18 @@ ar_status_t ar_linear_i4(const void* x, size_t ldx, const void* data, const void
   if (bad_i4_arrays(data, packed_scale, packed_zero) || bad_matrix(x, tokens, in, ldx) || misaligned(x, 2) ||
       bad_matrix(y, tokens, out, ldy) || misaligned(y, 2))
     return AR_ERR_INVALID_ARG;
+  int sms = 0;
+  if (ar_status_t st = current_sms(&sms)) return st;
   I4Args a = {};
   a.x = x, a.data = data, a.scale = packed_scale, a.zero = static_cast<const uint8_t*>(packed_zero), a.y = y;
   a.ldx = (int64_t)ldx, a.ldy = (int64_t)ldy, a.M = (int64_t)tokens, a.N = (int64_t)out, a.K = (int64_t)in;
   a.spans = (int64_t)i4_spans(in, group);
-  return cuda_status(launch_linear_i4(dtype, group, a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_linear_i4(dtype, group, a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens) {
   if (check_moe(m)) return 0;
-  return (tokens < AR_FEW_TOKENS ? tokens : AR_FEW_TOKENS) * (size_t)m->top_k * moe_ldh(m) * 2;
+  return tokens ? moe_scratch((int64_t)(tokens < AR_FEW_TOKENS ? tokens : AR_FEW_TOKENS), m->top_k, (int64_t)m->width, (int64_t)m->hidden, nullptr, nullptr) : 0;
 }
 
 ar_status_t ar_moe_ffn(const ar_moe_t* m, const void* x, size_t ldx, const void* logits, size_t ldl,
@@ -168,9 +168,10 @@ ar_status_t ar_moe_ffn(const ar_moe_t* m, const void* x, size_t ldx, const void*
   int sms = 0;
   if (ar_status_t st = current_sms(&sms)) return st;
   MoeArgs a = {};
-  a.w_gate = w_gate, a.w_up = w_up, a.w_down = w_down, a.h = scratch;
+  a.w_gate = w_gate, a.w_up = w_up, a.w_down = w_down;
+  moe_scratch((int64_t)(tokens < AR_FEW_TOKENS ? tokens : AR_FEW_TOKENS), m->top_k, (int64_t)m->width, (int64_t)m->hidden, &a, static_cast<char*>(scratch));
   a.ldx = (int64_t)ldx, a.ldl = (int64_t)ldl, a.ldw = (int64_t)ldw, a.esw = (int64_t)esw;
-  a.ldd = (int64_t)ldd, a.esd = (int64_t)esd, a.ldh = (int64_t)moe_ldh(m), a.ldo = (int64_t)ldo;
+  a.ldd = (int64_t)ldd, a.esd = (int64_t)esd, a.ldo = (int64_t)ldo;
   a.hidden = (int64_t)K, a.width = (int64_t)F;
   a.experts = m->experts, a.first = m->first_expert, a.local = m->local_experts;
   a.top_k = m->top_k, a.normalize = m->normalize != 0, a.logits_dtype = m->logits_dtype;

@@ -38,6 +38,7 @@ inline bool bad_matrix(const void* p, size_t rows, size_t cols, size_t ld) {
   return !p || ld < cols || ld > kMaxElems || (ld && rows > kMaxElems / ld);
 }
 inline bool misaligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+constexpr int64_t kMostSms = 160;  // bounds scratch memory that is sized without a device
 ar_status_t current_sms(int* sms);  // SMs of the current device, looked up once for each
 
 // ---------------------------------------------------------------------------
@@ -171,7 +172,6 @@ struct NormGradArgs {
 };
 // CTAs of the backward pass at most, a row of the parts each: SMs times the CTAs
 // that an SM holds, where the rows are no fewer.
-constexpr int64_t kMostSms = 160;
 int64_t norm_parts(int64_t rows, int64_t cols);
 cudaError_t launch_norm_grad(int dtype, NormGradArgs& a, int num_sms, cudaStream_t s);
 
@@ -183,7 +183,7 @@ struct I4Args {
   void* y;
   int64_t ldx, ldy, M, N, K, spans;
 };
-cudaError_t launch_linear_i4(int dtype, int group, const I4Args& a, cudaStream_t s);
+cudaError_t launch_linear_i4(int dtype, int group, const I4Args& a, int num_sms, cudaStream_t s);
 int i4_span(int group);
 
 struct I4Pack {
@@ -222,13 +222,17 @@ cudaError_t launch_unpack_i4(int dtype, const I4Unpack& a, int num_sms, cudaStre
 // Gated feed-forward experts for at most AR_FEW_TOKENS tokens (k_moe.cu).
 struct MoeArgs {
   const void *x, *logits, *w_gate, *w_up, *w_down;
-  void *h, *out;  // h: row t * top_k + j for choice j of token t, rows on 16 bytes
+  void *h, *out;   // h: row t * top_k + j for choice j of token t, rows on 16 bytes
+  uint32_t* done;  // of each 16 columns of out: the parts that are there
+  float* parts;    // two for every CTA, [AR_FEW_TOKENS][16]
   int32_t* out_expert;
   float* out_weight;  // of the routing, or null
   int64_t ldx, ldl, ldw, esw, ldd, esd, ldh, ldo;  // es: elements from one expert's matrix to the next
   int64_t hidden, width;
   int tokens, experts, first, local, top_k, normalize, logits_dtype;
 };
+// The scratch memory's size, and (m not null) its pieces in place.
+size_t moe_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t hidden, MoeArgs* m, char* base);
 cudaError_t launch_moe(int dtype, int act, const MoeArgs& m, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

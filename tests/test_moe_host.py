@@ -18,7 +18,7 @@ def lib():
 
 DESCRIPTION = dict(dtype=0, logits_dtype=2, activation=0, experts=8, first_expert=2, local_experts=4, top_k=3, normalize=1, hidden=16, width=12)
 CALL = dict(x=16, ldx=16, logits=16, ldl=8, wg=16, wu=16, ldw=16, esw=192, wd=16, ldd=12, esd=192, out=16, ldo=16, expert=16,
-            weight=16, tokens=5, scratch=16, bytes=5 * 3 * 16 * 2)
+            weight=16, tokens=5, scratch=16, bytes=480 + 16 + 160 * 2 * 32 * 16 * 4)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -30,7 +30,7 @@ CALL = dict(x=16, ldx=16, logits=16, ldl=8, wg=16, wu=16, ldw=16, esw=192, wd=16
     (dict(ldl=7), INVALID), (dict(wg=None), INVALID), (dict(wu=17), INVALID), (dict(ldw=15), INVALID), (dict(wd=None), INVALID),
     (dict(ldd=11), INVALID), (dict(esd=1 << 41), INVALID), (dict(out=None), INVALID), (dict(out=17), INVALID), (dict(ldo=15), INVALID),
     (dict(expert=18), INVALID), (dict(weight=18), INVALID), (dict(scratch=None), INVALID), (dict(scratch=24), INVALID),
-    (dict(bytes=5 * 3 * 16 * 2 - 1), INVALID), (dict(tokens=0, x=None, out=None, scratch=None), OK)])
+    (dict(bytes=480 + 15 + 160 * 4096), INVALID), (dict(tokens=0, x=None, out=None, scratch=None), OK)])
 def test_refuses(lib, kw, want):
     d, a = dict(DESCRIPTION), dict(CALL)
     for k, v in kw.items():
@@ -43,7 +43,10 @@ def test_scratch_bytes(lib):
     def f(tokens, **k):
         return lib.ar_moe_scratch_bytes(ctypes.byref(_lib.ArMoe(*dict(DESCRIPTION, **k).values())), tokens)
 
-    assert f(5) == 480 and f(1000) == 32 * 3 * 16 * 2 and f(5, width=17) == 5 * 3 * 24 * 2 and f(0) == 0
+    # the experts' inner rows, a count for every 16 columns of the result, and what is left of them in parts
+    parts = 160 * 2 * 32 * 16 * 4
+    assert f(5) == 480 + 16 + parts and f(1000) == 32 * 3 * 16 * 2 + 16 + parts and f(0) == 0
+    assert f(5, width=17) == 5 * 3 * 24 * 2 + 16 + parts and f(5, hidden=81) == 480 + 32 + parts
     assert f(5, top_k=9) == 0 and lib.ar_moe_scratch_bytes(None, 5) == 0
 
 
