@@ -166,37 +166,74 @@ __device__ __forceinline__ uint4 tokens16(const char* p, int64_t left, const cha
 
 // The pieces of 64 k (two steps of 32) of sixteen rows that a warp copies ahead:
 // lane 4 g + t has rows g and g + 8 at k = 8 t .. 8 t + 7 of each step.
-constexpr int kStages = 5, kSteps = 2, kPieceBytes = 128, kRingBytes = kWarps * kStages * kSteps * 2 * 512;
+constexpr int kStages = 3, kSteps = 2, kPieceBytes = 128, kStageBytes = kSteps * 2 * 512, kRingBytes = kWarps * kStages * kStageBytes;
+
+__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_some(uint32_t to, const char* from, int bytes) {  // the rest of the 16 is zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
+// What a warp copies next: `more` pieces of this lane's rows, now at a and b (its 16 bytes of the
+// first step), of which `left` bytes remain from the piece's begin on.
+struct Feed {
+  const char *a, *b;
+  int left, more;
+};
 
 struct Ring {
-  char* mine;  // this lane's place in its warp's ring
+  uint32_t mine;  // this lane's place in its warp's ring
+  int stage;      // the one that is used next
   __device__ __forceinline__ explicit Ring(char* smem)
-      : mine(smem + (threadIdx.x >> 5) * kStages * kSteps * 2 * 512 + (threadIdx.x & 31) * 16) {}
-  __device__ __forceinline__ char* at(int stage, int step, int row) const { return mine + ((stage * kSteps + step) * 2 + row) * 512; }
-
-  // Rows a and b (this lane's) at byte k of `bytes`; what lies past a row's end is zeros.
-  template <bool VEC>
-  __device__ __forceinline__ void fetch(int stage, const char* a, const char* b, int64_t k, int64_t bytes, const char* begin_a,
-                                        const char* begin_b, int64_t extent) const {
-    const int t4 = threadIdx.x & 3;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int64_t at_k = k + 64 * i + 16 * t4, left = bytes - at_k;
-      if (VEC) {
-        const int n = left >= 16 ? 16 : left > 0 ? (int)left : 0;
-        copy(at(stage, i, 0), n ? a + at_k : a, n);
-        copy(at(stage, i, 1), n ? b + at_k : b, n);
-      } else {
-        *reinterpret_cast<uint4*>(at(stage, i, 0)) = load_anywhere<2>(a + at_k, left, begin_a, begin_a + extent);
-        *reinterpret_cast<uint4*>(at(stage, i, 1)) = load_anywhere<2>(b + at_k, left, begin_b, begin_b + extent);
-      }
-    }
-  }
-  static __device__ __forceinline__ void copy(char* to, const char* from, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes)
+      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kStages * kStageBytes + (threadIdx.x & 31) * 16), stage(0) {}
+  __device__ __forceinline__ uint4 row(int step, int r) const {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(mine + stage * kStageBytes + (step * 2 + r) * 512)
                  : "memory");
+    return v;
   }
-  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void put(uint32_t to, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  }
+  __device__ __forceinline__ void advance() { stage = stage == kStages - 1 ? 0 : stage + 1; }
+
+  // The next piece to the stage that is `ahead` of the one used next; the matrices' ends bound what is read where
+  // rows begin anywhere.  What lies past a row's end is zeros.
+  template <bool VEC>
+  __device__ __forceinline__ void fetch(int ahead, Feed& f, const char* begin_a, const char* begin_b, int64_t extent) const {
+    if (f.more > 0) {
+      const int to_stage = stage + ahead < kStages ? stage + ahead : stage + ahead - kStages;
+      const uint32_t at = mine + to_stage * kStageBytes;
+      if (VEC) {
+        if (f.left >= kPieceBytes) {
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            copy16(at + i * 1024, f.a + 64 * i);
+            copy16(at + i * 1024 + 512, f.b + 64 * i);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int left = f.left - 64 * i - 16 * (int)(threadIdx.x & 3), n = left >= 16 ? 16 : left > 0 ? left : 0;
+            copy_some(at + i * 1024, n ? f.a + 64 * i : begin_a, n);
+            copy_some(at + i * 1024 + 512, n ? f.b + 64 * i : begin_b, n);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int left = f.left - 64 * i - 16 * (int)(threadIdx.x & 3);
+          put(at + i * 1024, load_anywhere<2>(f.a + 64 * i, left, begin_a, begin_a + extent));
+          put(at + i * 1024 + 512, load_anywhere<2>(f.b + 64 * i, left, begin_b, begin_b + extent));
+        }
+      }
+      f.a += kPieceBytes, f.b += kPieceBytes, f.left -= kPieceBytes, --f.more;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
 };
 
@@ -217,105 +254,124 @@ __device__ __forceinline__ void multiply(float (&acc)[NB][4], const uint4& a, co
   }
 }
 
+// Which of n runs, run r being r * total / n to (r + 1) * total / n, has unit p.
+__device__ __forceinline__ int run_of(int p, int total, int n) { return (int)(((int64_t)(p + 1) * n - 1) / total); }
+__device__ __forceinline__ int run_begin(int r, int total, int n) { return (int)((int64_t)r * total / n); }
+
 // An item: eight rows of one expert's gate and the same of its up projection, whose
-// sums of one output land in one lane.  The warps take turns at the pieces along k, and
-// their sums are joined in a fixed order.
+// sums of one output land in one lane.  A CTA has as many items as the others; their pieces along k, one
+// item's behind the other's, are dealt out evenly to its warps.  A warp finishes the
+// items that are its own; those that lie on several warps are joined once, at the end,
+// in the warps' order.
 template <class E, int ACT, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
   extern __shared__ __align__(16) char smem[];
   pdl_enter();
   char* const tables_at = smem + kRingBytes;
-  const Ring ring(smem);
+  Ring ring(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   // The down kernel's counts of finished parts.
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (m.hidden + 15) / 16; i += (int64_t)gridDim.x * kThreads) m.done[i] = 0;
   route(m, tables_at, blockIdx.x == 0);
   const RouteTables tab = tables(tables_at, m.local);
+  // Sums of the items that a warp has a part of: that which begins before it, and that which ends behind it.
+  const int blocks = m.tokens <= 8 ? 1 : m.tokens <= 16 ? 2 : 4;
   float4* const part = reinterpret_cast<float4*>(tables_at + (route_bytes(m.local, (int64_t)m.tokens * m.top_k) + 15) / 16 * 16);
+  const auto part_at = [&](int w, int which) { return part + (w * 2 + which) * blocks * 32 + lane; };
   __shared__ uint8_t lists[kWarps][kTokens];
   uint8_t* const list = lists[warp];
 
   const int strips = (int)((m.width + 7) / 8);
-  const int64_t items = (int64_t)reinterpret_cast<const Routes*>(tables_at)->active * strips, bytes = m.hidden * 2;
-  const int turns = (int)((bytes + kWarps * kPieceBytes - 1) / (kWarps * kPieceBytes));
+  const int items = reinterpret_cast<const Routes*>(tables_at)->active * strips, bytes = (int)m.hidden * 2;
+  const int pieces = (bytes + kPieceBytes - 1) / kPieceBytes;
+  const int item0 = run_begin(blockIdx.x, items, gridDim.x), total = (run_begin(blockIdx.x + 1, items, gridDim.x) - item0) * pieces;
+  if (total == 0) return;
+  const int runs = min(kWarps, total), first = run_begin(min(warp, runs), total, runs), last = run_begin(min(warp + 1, runs), total, runs);
   const char *bg = static_cast<const char*>(m.w_gate), *bu = static_cast<const char*>(m.w_up), *bx = static_cast<const char*>(m.x);
   const int64_t extent = ((m.local - 1) * m.esw + (m.width - 1) * m.ldw + m.hidden) * 2;
   const char* ex = bx + ((m.tokens - 1) * m.ldx + m.hidden) * 2;
 
-  // What is copied next: turn next_turn of item next, rows at wg and wu.
-  int64_t next = blockIdx.x;
-  int next_turn = 0;
-  const char *wg = nullptr, *wu = nullptr;
-  const auto fetch = [&](int stage) {
-    if (next < items) {
-      if (next_turn == 0) {
-        const int place = (int)(next / strips), e = tab.number[place];
-        const int64_t f = min((next - (int64_t)place * strips) * 8 + g8, m.width - 1), at = (e * m.esw + f * m.ldw) * 2;
-        wg = bg + at, wu = bu + at;
-      }
-      const int64_t k = (int64_t)(next_turn * kWarps + warp) * kPieceBytes;
-      if (k < bytes) ring.fetch<VEC>(stage, wg, wu, k, bytes, bg, bu, extent);
-      if (++next_turn == turns) next_turn = 0, next += gridDim.x;
+  Feed feed = {nullptr, nullptr, 0, 0};
+  int fed = first;  // pieces before this one have been given to `feed`
+  const auto fetch = [&](int ahead) {
+    if (feed.more == 0 && fed < last) {
+      const int q = fed / pieces, p = fed - q * pieces, place = (item0 + q) / strips;
+      const int64_t f = min((int64_t)(item0 + q - place * strips) * 8 + g8, m.width - 1);
+      const int64_t at = (tab.number[place] * m.esw + f * m.ldw) * 2 + p * kPieceBytes + 16 * t4;
+      feed = {bg + at, bu + at, bytes - p * kPieceBytes, min(pieces - p, last - fed)};
+      fed += feed.more;
     }
-    Ring::commit();
+    ring.fetch<VEC>(ahead, feed, bg, bu, extent);
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
-  int stage = 0;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int place = (int)(item / strips), e = tab.number[place];
-    const int64_t f0 = (item - (int64_t)place * strips) * 8;
-    const uint32_t tokens = tab.tokens[e];
-    const int count = __popc(tokens);
+  // An item's expert, its tokens in `list`, their number.
+  const auto open = [&](int item, int& place) {
+    place = item / strips;
+    const uint32_t tokens = tab.tokens[tab.number[place]];
     __syncwarp();
     if (tokens >> lane & 1) list[__popc(tokens & ((1u << lane) - 1))] = (uint8_t)lane;
     __syncwarp();
-    const auto run = [&](auto blocks) {
-      constexpr int NB = decltype(blocks)::value;
+    return __popc(tokens);
+  };
+  const auto finish = [&](int item, int place, int count, int j, const float4& v) {
+    const int f = (item - place * strips) * 8 + g8;
+    const float sums[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int i = 8 * j + 2 * t4 + c;
+      if (i >= count) continue;
+      const int t = list[i];
+      const int64_t row = t * m.top_k + tab.choice[place * kTokens + t];
+      // The row's end, up to a whole group, is read with it: zeros.
+      const float h = f < m.width ? act_value<ACT>(sums[c]) * sums[c + 2] : 0.0f;
+      static_cast<uint16_t*>(m.h)[row * m.ldh + f] = (uint16_t)E::from_f32(h);
+    }
+  };
+
+  for (int pos = first; pos < last;) {
+    const int q = pos / pieces, p0 = pos - q * pieces, p1 = min(pieces, p0 + (last - pos));
+    int place;
+    const int count = open(item0 + q, place);
+    const auto run = [&](auto number) {
+      constexpr int NB = decltype(number)::value;
+      // A token past the last is read as the last: its column of the sums is dropped.
       const char* xs[NB];
 #pragma unroll
-      for (int j = 0; j < NB; ++j) xs[j] = 8 * j + g8 < count ? bx + list[8 * j + g8] * m.ldx * 2 : nullptr;
+      for (int j = 0; j < NB; ++j) xs[j] = bx + list[min(8 * j + g8, count - 1)] * m.ldx * 2 + p0 * kPieceBytes + 16 * t4;
       float acc[NB][4] = {};
-      for (int turn = 0; turn < turns; ++turn) {
-        fetch(stage == 0 ? kStages - 1 : stage - 1);
-        const int64_t k0 = (int64_t)(turn * kWarps + warp) * kPieceBytes + 16 * t4;
+      const auto step = [&](auto whole, int left) {
         uint4 x[kSteps][NB];
-        if (k0 - 16 * t4 < bytes) {
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-              x[i][j] = xs[j] ? tokens16<VEC>(xs[j] + k0 + 64 * i, bytes - k0 - 64 * i, bx, ex) : make_uint4(0, 0, 0, 0);
-          Ring::wait();
+          for (int j = 0; j < NB; ++j)
+            x[i][j] = tokens16<VEC>(xs[j] + 64 * i, decltype(whole)::value && VEC ? 16 : left - 64 * i - 16 * t4, bx, ex);
+        fetch(kStages - 1);
+        Ring::wait();
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i)
-            multiply<E, NB>(acc, *reinterpret_cast<const uint4*>(ring.at(stage, i, 0)), *reinterpret_cast<const uint4*>(ring.at(stage, i, 1)), x[i]);
-        }
-        stage = stage == kStages - 1 ? 0 : stage + 1;
+        for (int i = 0; i < kSteps; ++i) multiply<E, NB>(acc, ring.row(i, 0), ring.row(i, 1), x[i]);
+        ring.advance();
+#pragma unroll
+        for (int j = 0; j < NB; ++j) xs[j] += kPieceBytes;
+      };
+      const int whole = min(p1, bytes / kPieceBytes);
+      int p = p0;
+      for (; p < whole; ++p) {
+        step(std::true_type(), bytes - p * kPieceBytes);
+      }
+      for (; p < p1; ++p) {
+        step(std::false_type(), bytes - p * kPieceBytes);
       }
 #pragma unroll
-      for (int j = 0; j < NB; ++j) part[(warp * NB + j) * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-      __syncthreads();
-      if (warp < NB) {
-        float v[4] = {};
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4 p = part[(w * NB + warp) * 32 + lane];
-          v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int i = 8 * warp + 2 * t4 + c;
-          if (i >= count) continue;
-          const int t = list[i];
-          const int64_t row = t * m.top_k + tab.choice[place * kTokens + t];
-          // The row's end, up to a whole group, is read with it: zeros.
-          const float h = f0 + g8 < m.width ? act_value<ACT>(v[c]) * v[c + 2] : 0.0f;
-          static_cast<uint16_t*>(m.h)[row * m.ldh + f0 + g8] = (uint16_t)E::from_f32(h);
-        }
+      for (int j = 0; j < NB; ++j) {
+        const float4 v = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        if (p1 - p0 == pieces)
+          finish(item0 + q, place, count, j, v);
+        else
+          part_at(warp, p0 == 0)[j * 32] = v;
       }
-      __syncthreads();
     };
     if (count <= 8)
       run(std::integral_constant<int, 1>());
@@ -323,21 +379,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
       run(std::integral_constant<int, 2>());
     else
       run(std::integral_constant<int, 4>());
+    pos += p1 - p0;
+  }
+  __syncthreads();
+  // An item that this warp begins and does not end.
+  const int q = (last - 1) / pieces;
+  if (warp < runs && last % pieces != 0 && q * pieces >= first) {
+    const int until = run_of(q * pieces + pieces - 1, total, runs);
+    int place;
+    const int count = open(item0 + q, place);
+    for (int j = 0; 8 * j < count; ++j) {
+      float4 v = part_at(warp, 1)[j * 32];
+      for (int w = warp + 1; w <= until; ++w) {
+        const float4 t = part_at(w, 0)[j * 32];
+        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+      }
+      finish(item0 + q, place, count, j, v);
+    }
   }
 }
 
 // Sixteen output columns are a tile, for which there are as many units as pieces
 // of 64 of the used experts' inner columns.  All tiles' units are dealt out evenly in one
-// row, so that every SM reads as much; a CTA's part of a tile is shared out among its
-// warps in runs.  A run's sums of one expert's tokens (eight at a time) are weighted and
-// added to the warp's own sums in fp32, and those are joined in the warps' order.  A tile that
-// lies on several CTAs is left in parts, which the CTA that finishes last
+// row, first to the CTAs, then to a CTA's warps, so that every SM reads as much.  A
+// warp's sums of one expert's tokens (eight at a time) are weighted and added to its
+// sums of the tile in fp32, and those are joined at the end, in the warps' order.  A
+// tile that lies on several CTAs is left in parts, which the CTA that finishes last
 // adds in their order: nothing is waited for, and every call gives the same bits.
 template <class E, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   extern __shared__ __align__(16) char smem[];
   char* const tables_at = smem + kRingBytes;
-  const Ring ring(smem);
+  Ring ring(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   // The kernel before this one, which made h, has itself waited for what came before
   // it: the logits and the weights may be read before it ends.
@@ -345,154 +418,162 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   route(m, tables_at, false);
   const Routes& s = *reinterpret_cast<const Routes*>(tables_at);
   const RouteTables tab = tables(tables_at, m.local);
-  // sums[warp][token][16], 17 apart against bank conflicts
-  float* const sums = reinterpret_cast<float*>(tables_at + (route_bytes(m.local, (int64_t)m.tokens * m.top_k) + 15) / 16 * 16);
   __shared__ uint8_t lists[kWarps][kTokens];
-  __shared__ int finished;
+  __shared__ int finished[2];
   uint8_t* const list = lists[warp];
+  // A warp's sums of the tile that begins before its run, and of that which ends behind it (or, whole, of
+  // any between): [token][16], 17 apart against bank conflicts.
+  float* const sums = reinterpret_cast<float*>(tables_at + (route_bytes(m.local, (int64_t)m.tokens * m.top_k) + 15) / 16 * 16);
   const int entries = m.tokens * 17;
-  float* const own = sums + warp * entries;
+  const auto sums_of = [&](int w, int which) { return sums + (w * 2 + which) * entries; };
 
-  const int64_t tiles = (m.hidden + 15) / 16, bytes = m.width * 2;
-  const int pieces = (int)((bytes + kPieceBytes - 1) / kPieceBytes), units = s.active * pieces;
-  const int64_t total = tiles * units;
-  const int G = (int)min((int64_t)gridDim.x, total);  // CTAs that have a part, none of it empty
+  const int tiles = (int)((m.hidden + 15) / 16), bytes = (int)m.width * 2, pieces = (bytes + kPieceBytes - 1) / kPieceBytes;
+  const int units = s.active * pieces, total = tiles * units, G = min((int)gridDim.x, total);  // G CTAs have a part, none of it empty
   const char* bd = static_cast<const char*>(m.w_down);
   const int64_t extent = ((m.local - 1) * m.esd + (m.hidden - 1) * m.ldd + m.width) * 2;
   const char* h = static_cast<const char*>(m.h);
+  uint16_t* const out = static_cast<uint16_t*>(m.out);
 
   if (units == 0) {  // no token has an expert here
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < m.tokens * m.hidden; i += (int64_t)gridDim.x * kThreads)
-      static_cast<uint16_t*>(m.out)[i / m.hidden * m.ldo + i % m.hidden] = 0;
+      out[i / m.hidden * m.ldo + i % m.hidden] = 0;
     return;
   }
-  // This CTA's part of the row of units, and this warp's run of a tile's.
-  const int64_t cta = min((int)blockIdx.x, G), begin = cta * total / G, end = min(cta + 1, (int64_t)G) * total / G;
-  struct Run {
-    int64_t tile, pos;  // pos: where the CTA's part of the tile begins
-    int u0, u1;         // that part
-    int at, stop;       // this warp's run
-  };
-  const auto run_at = [&](int64_t pos) {
-    Run r;
-    r.pos = pos, r.tile = pos / units, r.u0 = (int)(pos - r.tile * units);
-    r.u1 = (int)min((int64_t)units, r.u0 + (end - pos));
-    const int n = r.u1 - r.u0, each = (n + kWarps - 1) / kWarps;
-    r.at = r.u0 + min(warp * each, n), r.stop = r.u0 + min((warp + 1) * each, n);
-    return r;
-  };
-  Run next = begin < end ? run_at(begin) : Run{0, end, 0, 0, 0, 0};
-  const auto fetch = [&](int stage) {
-    while (next.at >= next.stop && next.pos < end) {
-      const int64_t pos = next.pos + (next.u1 - next.u0);
-      if (pos >= end) {
-        next.pos = end;
-        break;
-      }
-      next = run_at(pos);
+  if ((int)blockIdx.x >= G) return;
+  const int begin = run_begin(blockIdx.x, total, G), end = run_begin(blockIdx.x + 1, total, G), mine = end - begin;
+  const int runs = min(kWarps, mine);
+  const auto begin_of = [&](int w) { return begin + run_begin(min(w, runs), mine, runs); };
+  const int first = begin_of(warp), last = begin_of(warp + 1);
+
+  Feed feed = {nullptr, nullptr, 0, 0};
+  int fed = first;  // units before this one have been given to `feed`
+  const auto fetch = [&](int ahead) {
+    if (feed.more == 0 && fed < last) {
+      const int tile = fed / units, u = fed - tile * units, place = u / pieces, p = u - place * pieces;
+      const int64_t n0 = (int64_t)tile * 16, ra = min(n0 + g8, m.hidden - 1), rb = min(n0 + g8 + 8, m.hidden - 1);
+      const char* from = bd + tab.number[place] * m.esd * 2 + (int64_t)p * kPieceBytes + 16 * t4;
+      feed = {from + ra * m.ldd * 2, from + rb * m.ldd * 2, bytes - p * kPieceBytes, min(pieces - p, last - fed)};
+      fed += feed.more;
     }
-    if (next.pos < end) {
-      const int place = next.at / pieces, e = tab.number[place];
-      const int64_t n0 = next.tile * 16, ra = min(n0 + g8, m.hidden - 1), rb = min(n0 + g8 + 8, m.hidden - 1);
-      const char* we = bd + e * m.esd * 2;
-      ring.fetch<VEC>(stage, we + ra * m.ldd * 2, we + rb * m.ldd * 2, (int64_t)(next.at - place * pieces) * kPieceBytes, bytes, bd, bd, extent);
-      ++next.at;
-    }
-    Ring::commit();
+    ring.fetch<VEC>(ahead, feed, bd, bd, extent);
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  for (int i = lane; i < 2 * entries; i += 32) sums_of(warp, 0)[i] = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  int stage = 0;
-  for (int64_t pos = begin; pos < end;) {
-    const Run r = run_at(pos);
-    for (int i = lane; i < entries; i += 32) own[i] = 0.0f;
-    int u = r.at;
-    while (u < r.stop) {
-      const int place = u / pieces, until = min(r.stop, (place + 1) * pieces);
-      const uint32_t tokens = tab.tokens[tab.number[place]];
-      const int count = __popc(tokens);
-      __syncwarp();
-      if (tokens >> lane & 1) list[__popc(tokens & ((1u << lane) - 1))] = (uint8_t)lane;
-      __syncwarp();
-      const auto run = [&](auto blocks) {
-        constexpr int NB = decltype(blocks)::value;
-        const char* xs[NB];
+  for (int pos = first; pos < last;) {
+    // One expert's units of a tile.
+    const int tile = pos / units, u0 = pos - tile * units, place = u0 / pieces, p0 = u0 - place * pieces, p1 = min(pieces, p0 + (last - pos));
+    float* const own = sums_of(warp, tile * units >= first);
+    const uint32_t tokens = tab.tokens[tab.number[place]];
+    const int count = __popc(tokens);
+    __syncwarp();
+    if (tokens >> lane & 1) list[__popc(tokens & ((1u << lane) - 1))] = (uint8_t)lane;
+    __syncwarp();
+    const auto run = [&](auto blocks) {
+      constexpr int NB = decltype(blocks)::value;
+      // A token past the last is read as the last: its column of the sums is dropped.
+      const char* xs[NB];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const int t = 8 * j + g8 < count ? list[8 * j + g8] : -1;
-          xs[j] = t < 0 ? nullptr : h + (int64_t)(t * m.top_k + tab.choice[place * kTokens + t]) * m.ldh * 2;
-        }
-        float acc[NB][4] = {};
-        for (; u < until; ++u) {
-          fetch(stage == 0 ? kStages - 1 : stage - 1);
-          const int64_t k0 = (int64_t)(u - place * pieces) * kPieceBytes + 16 * t4;
-          uint4 x[kSteps][NB];
+      for (int j = 0; j < NB; ++j) {
+        const int t = list[min(8 * j + g8, count - 1)];
+        xs[j] = h + (int64_t)(t * m.top_k + tab.choice[place * kTokens + t]) * m.ldh * 2 + p0 * kPieceBytes + 16 * t4;
+      }
+      float acc[NB][4] = {};
+      for (int p = p0; p < p1; ++p) {
+        uint4 x[kSteps][NB];
+        const int left = bytes - p * kPieceBytes - 16 * t4;
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i)
+        for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)  // rows of h start on 16 bytes and end in zeros
-              x[i][j] = xs[j] && k0 + 64 * i < bytes ? *reinterpret_cast<const uint4*>(xs[j] + k0 + 64 * i) : make_uint4(0, 0, 0, 0);
-          Ring::wait();
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i)
-            multiply<E, NB>(acc, *reinterpret_cast<const uint4*>(ring.at(stage, i, 0)), *reinterpret_cast<const uint4*>(ring.at(stage, i, 1)), x[i]);
-          stage = stage == kStages - 1 ? 0 : stage + 1;
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int i = 8 * j + 2 * t4 + c;
-            if (i >= count) continue;
-            const int t = list[i];
-            const float w = s.weight[t][tab.choice[place * kTokens + t]];
-            own[t * 17 + g8] = __fmaf_rn(w, acc[j][c], own[t * 17 + g8]);
-            own[t * 17 + g8 + 8] = __fmaf_rn(w, acc[j][c + 2], own[t * 17 + g8 + 8]);
+          for (int j = 0; j < NB; ++j) {  // rows of h start on 16 bytes and end in zeros
+            x[i][j] = make_uint4(0, 0, 0, 0);
+            if (left > 64 * i) x[i][j] = *reinterpret_cast<const uint4*>(xs[j] + 64 * i);
           }
-      };
-      if (count <= 8)
-        run(std::integral_constant<int, 1>());
-      else if (count <= 16)
-        run(std::integral_constant<int, 2>());
-      else
-        run(std::integral_constant<int, 4>());
-    }
-    __syncthreads();
-    const bool whole = r.u0 == 0 && r.u1 == units;
-    float* const mine = m.parts + ((int64_t)blockIdx.x * 2 + (r.u0 == 0)) * kTokens * 16;
-    for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
-      float v = 0.0f;
+        fetch(kStages - 1);
+        Ring::wait();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += sums[w * entries + i / 16 * 17 + i % 16];
-      const int64_t n = r.tile * 16 + i % 16;
-      if (!whole)
-        mine[i] = v;
-      else if (n < m.hidden)
-        static_cast<uint16_t*>(m.out)[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
-    }
-    if (!whole) {
-      // CTA c has unit p of the row where c is the last whose part begins at or before p.
-      const int64_t p0 = r.tile * units, p1 = p0 + units - 1;
-      const int c0 = (int)(((p0 + 1) * G - 1) / total), c1 = (int)(((p1 + 1) * G - 1) / total);
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) finished = atomicAdd(&m.done[r.tile], 1u) == (uint32_t)(c1 - c0);
-      __syncthreads();
-      if (finished) {
-        __threadfence();
-        for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
-          float v = 0.0f;
-          for (int c = c0; c <= c1; ++c) v += __ldcg(m.parts + ((int64_t)c * 2 + (c == c0)) * kTokens * 16 + i);
-          const int64_t n = r.tile * 16 + i % 16;
-          if (n < m.hidden) static_cast<uint16_t*>(m.out)[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+        for (int i = 0; i < kSteps; ++i) multiply<E, NB>(acc, ring.row(i, 0), ring.row(i, 1), x[i]);
+        ring.advance();
+#pragma unroll
+        for (int j = 0; j < NB; ++j) xs[j] += kPieceBytes;
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int i = 8 * j + 2 * t4 + c;
+          if (i >= count) continue;
+          const int t = list[i];
+          const float w = s.weight[t][tab.choice[place * kTokens + t]];
+          own[t * 17 + g8] = __fmaf_rn(w, acc[j][c], own[t * 17 + g8]);
+          own[t * 17 + g8 + 8] = __fmaf_rn(w, acc[j][c + 2], own[t * 17 + g8 + 8]);
         }
+    };
+    if (count <= 8)
+      run(std::integral_constant<int, 1>());
+    else if (count <= 16)
+      run(std::integral_constant<int, 2>());
+    else
+      run(std::integral_constant<int, 4>());
+    pos += p1 - p0;
+    if (tile * units >= first && pos == (tile + 1) * units) {  // the whole tile was this warp's
+      __syncwarp();
+      for (int i = lane; i < m.tokens * 16; i += 32) {
+        const int64_t n = (int64_t)tile * 16 + i % 16;
+        if (n < m.hidden) out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(own[i / 16 * 17 + i % 16]);
+        own[i / 16 * 17 + i % 16] = 0.0f;
       }
     }
-    __syncthreads();
-    pos += r.u1 - r.u0;
+  }
+  __syncthreads();
+
+  // The tiles that lie on several warps; of those, the CTA's first and last may lie on several CTAs.
+  const int tile0 = begin / units, tile1 = (end - 1) / units;
+  const auto part_of = [&](int cta, int tile) {  // a CTA's first tile that it did not begin, or the one that it began
+    return m.parts + ((int64_t)cta * 2 + (tile * units >= run_begin(cta, total, G))) * kTokens * 16;
+  };
+  for (int tile = tile0; tile <= tile1; ++tile) {
+    const int from = max(tile * units, begin), to = min((tile + 1) * units, end);
+    const int w0 = run_of(from - begin, mine, runs), w1 = run_of(to - 1 - begin, mine, runs);
+    const bool whole = from == tile * units && to == (tile + 1) * units;
+    if (w0 == w1 && whole) continue;  // done above
+    for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
+      float v = 0.0f;
+      for (int w = w0; w <= w1; ++w) v += sums_of(w, tile * units >= begin_of(w))[i / 16 * 17 + i % 16];
+      const int64_t n = (int64_t)tile * 16 + i % 16;
+      if (!whole)
+        part_of(blockIdx.x, tile)[i] = v;
+      else if (n < m.hidden)
+        out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+    }
+  }
+  if (tile0 * units == begin && (tile1 + 1) * units == end) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    const int tile = threadIdx.x ? tile1 : tile0;
+    const bool is_split = tile * units < begin || (tile + 1) * units > end;
+    finished[threadIdx.x] = 0;
+    if (is_split && (threadIdx.x == 0 || tile1 != tile0)) {
+      const int c0 = run_of(tile * units, total, G), c1 = run_of((tile + 1) * units - 1, total, G);
+      finished[threadIdx.x] = atomicAdd(&m.done[tile], 1u) == (uint32_t)(c1 - c0);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!finished[k]) continue;
+    __threadfence();
+    const int tile = k ? tile1 : tile0, c0 = run_of(tile * units, total, G), c1 = run_of((tile + 1) * units - 1, total, G);
+    for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
+      float v = 0.0f;
+      for (int c = c0; c <= c1; ++c) v += __ldcg(part_of(c, tile) + i);
+      const int64_t n = (int64_t)tile * 16 + i % 16;
+      if (n < m.hidden) out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+    }
   }
 }
 
@@ -503,12 +584,14 @@ cudaError_t moe(const MoeArgs& m, int num_sms, cudaStream_t s) {
   const int64_t pairs = (int64_t)m.tokens * m.top_k, most = m.local < pairs ? m.local : pairs, strips = (m.width + 7) / 8;
   const size_t tables = (route_bytes(m.local, pairs) + 15) / 16 * 16;
   const size_t blocks = m.tokens <= 8 ? 1 : m.tokens <= 16 ? 2 : 4;
-  const size_t gated = kRingBytes + tables + kWarps * blocks * 512, down = kRingBytes + tables + (size_t)kWarps * m.tokens * 17 * 4;
+  const size_t gated = kRingBytes + tables + kWarps * 2 * blocks * 512, down = kRingBytes + tables + (size_t)kWarps * 2 * m.tokens * 17 * 4;
   const bool vec = on16(m.x) && on16(m.w_gate) && on16(m.w_up) && (m.ldx | m.ldw | m.esw) % 8 == 0;
   auto* k = vec ? k_moe_gated<E, ACT, true> : k_moe_gated<E, ACT, false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gated);
   if (e != cudaSuccess) return e;
+  // The kernels count pieces in 32 bits.
   const int64_t slots = num_sms < kMostSms ? num_sms : kMostSms, items = most * strips;
+  if (items * ((m.hidden + 63) / 64) >> 31 || most * ((m.width + 63) / 64) * ((m.hidden + 15) / 16) >> 31) return cudaErrorInvalidConfiguration;
   e = launch_op(k, dim3((unsigned)(items < slots ? items : slots)), kThreads, gated, 1, s, m);
   if (e != cudaSuccess) return e;
   auto* d = on16(m.w_down) && (m.ldd | m.esd) % 8 == 0 ? k_moe_down<E, true> : k_moe_down<E, false>;
