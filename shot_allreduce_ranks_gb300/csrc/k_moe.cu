@@ -35,44 +35,45 @@ struct Routes {
   int expert[kTokens][kTop];  // -1: none
   int active;                 // local experts that have tokens
 };
-// Behind it: for each local expert the tokens that it has (a bit each) and its
-// place among the active ones; for each active one its number; and which of a
-// token's choices it is.
+// Behind it: for each local expert the tokens that it has (a bit each); for each active
+// one its number, and which of a token's choices it is.
 struct RouteTables {
   uint32_t* tokens;
-  uint16_t* place;
   uint16_t* number;
   uint8_t* choice;  // [active][32]
 };
 __host__ __device__ constexpr size_t route_bytes(int64_t local, int64_t pairs) {
-  return (sizeof(Routes) + 15) / 16 * 16 + (size_t)local * 8 + (size_t)(local < pairs ? local : pairs) * kTokens;
+  return (sizeof(Routes) + 15) / 16 * 16 + (size_t)local * 6 + (size_t)(local < pairs ? local : pairs) * kTokens;
 }
 __device__ __forceinline__ RouteTables tables(char* smem, int local) {
   RouteTables t;
   t.tokens = reinterpret_cast<uint32_t*>(smem + (sizeof(Routes) + 15) / 16 * 16);
-  t.place = reinterpret_cast<uint16_t*>(t.tokens + local);
-  t.number = t.place + local;
+  t.number = reinterpret_cast<uint16_t*>(t.tokens + local);
   t.choice = reinterpret_cast<uint8_t*>(t.number + local);
   return t;
 }
 
-__device__ __forceinline__ float logit(const MoeArgs& m, int64_t t, int e) {
+// A logit's bits as they are stored, and its value.
+__device__ __forceinline__ uint32_t logit_bits(const MoeArgs& m, int t, int e) {
   const char* p = static_cast<const char*>(m.logits);
   const int64_t i = t * m.ldl + e;
-  return m.logits_dtype == AR_FP32   ? __uint_as_float(ld_elem<4>(p + 4 * i))
-         : m.logits_dtype == AR_BF16 ? Bf16::to_f32(ld_elem<2>(p + 2 * i))
-                                     : F16::to_f32(ld_elem<2>(p + 2 * i));
+  return m.logits_dtype == AR_FP32 ? ld_elem<4>(p + 4 * i) : ld_elem<2>(p + 2 * i);
+}
+__device__ __forceinline__ float logit_value(const MoeArgs& m, uint32_t bits) {
+  return m.logits_dtype == AR_FP32 ? __uint_as_float(bits) : m.logits_dtype == AR_BF16 ? Bf16::to_f32(bits) : F16::to_f32(bits);
 }
 
-// One token's choices by one warp: lane j gets the j-th (its order and expert).
-// R > 0: up to 32 R experts, held in registers; 0: any number, read again for every choice.
+// A token's choices by one warp: lane j gets the j-th (its order and expert); lanes' parts of the sum of all experts'
+// exponentials in `total` where that is wanted.
+// R > 0: up to 32 R experts, whose bits are in `raw`; 0: any number, read again for every choice.
 template <int R>
-__device__ __forceinline__ void choose(const MoeArgs& m, int64_t t, int lane, uint32_t& mine, int& expert, float& total) {
+__device__ __forceinline__ void choose(const MoeArgs& m, int t, int lane, const uint32_t (&raw)[R ? R : 1], uint32_t& mine, int& expert,
+                                       float& total) {
   constexpr int N = R ? R : 1;
   uint32_t o[N];
   if (R)
 #pragma unroll
-    for (int r = 0; r < N; ++r) o[r] = 32 * r + lane < m.experts ? order_of(logit(m, t, 32 * r + lane)) : 0;
+    for (int r = 0; r < N; ++r) o[r] = 32 * r + lane < m.experts ? order_of(logit_value(m, raw[r])) : 0;
   mine = 0, expert = -1;
   uint32_t last = 0xFFFFFFFFu;  // the choice before: nothing before it comes again
   int last_e = -1;
@@ -85,7 +86,7 @@ __device__ __forceinline__ void choose(const MoeArgs& m, int64_t t, int lane, ui
         if (o[r] > best) best = o[r], e = 32 * r + lane;
     } else {
       for (int i = lane; i < m.experts; i += 32) {
-        const uint32_t v = order_of(logit(m, t, i));
+        const uint32_t v = order_of(logit_value(m, logit_bits(m, t, i)));
         if (v > best && (v < last || (v == last && i > last_e))) best = v, e = i;
       }
     }
@@ -100,28 +101,38 @@ __device__ __forceinline__ void choose(const MoeArgs& m, int64_t t, int lane, ui
     last = top, last_e = e;
   }
   total = 0.0f;
-  const float first = value_of(__shfl_sync(0xFFFFFFFFu, mine, 0));
-  if (!m.normalize)
-    for (int i = lane; i < m.experts; i += 32) total += expf(logit(m, t, i) - first);
+  if (!m.normalize) {
+    const float first = value_of(__shfl_sync(0xFFFFFFFFu, mine, 0));
+    if (R) {
+#pragma unroll
+      for (int r = 0; r < N; ++r)
+        if (32 * r + lane < m.experts) total += expf(logit_value(m, raw[r]) - first);
+    } else {
+      for (int i = lane; i < m.experts; i += 32) total += expf(logit_value(m, logit_bits(m, t, i)) - first);
+    }
+  }
 }
 
-// write: this CTA also stores the routing for the caller.
-__device__ __forceinline__ void route(const MoeArgs& m, char* smem, bool write) {
-  Routes& s = *reinterpret_cast<Routes*>(smem);
-  const RouteTables tab = tables(smem, m.local);
+// The choices of a warp's tokens; all of a token's logits are loaded at once, the next token's before this one's choices.
+template <int R>
+__device__ __forceinline__ void choose_all(const MoeArgs& m, Routes& s, const RouteTables& tab, bool write) {
+  constexpr int N = R ? R : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t raw[N], next[N];
+  const auto load = [&](int t, uint32_t(&v)[N]) {
+    if (R)
+#pragma unroll
+      for (int r = 0; r < N; ++r) v[r] = t < m.tokens && 32 * r + lane < m.experts ? logit_bits(m, t, 32 * r + lane) : 0;
+  };
+  load(warp, raw);
   for (int e = threadIdx.x; e < m.local; e += kThreads) tab.tokens[e] = 0;
   __syncthreads();
   for (int t = warp; t < m.tokens; t += kWarps) {
+    load(t + kWarps, next);
     uint32_t mine;
     int expert;
     float total;
-    if (m.experts <= 64)
-      choose<2>(m, t, lane, mine, expert, total);
-    else if (m.experts <= 256)
-      choose<8>(m, t, lane, mine, expert, total);
-    else
-      choose<0>(m, t, lane, mine, expert, total);
+    choose<R>(m, t, lane, raw, mine, expert, total);
     const float first = value_of(__shfl_sync(0xFFFFFFFFu, mine, 0));
     float p = expert >= 0 ? expf(value_of(mine) - first) : 0.0f;
     if (m.normalize) total = p;
@@ -136,24 +147,42 @@ __device__ __forceinline__ void route(const MoeArgs& m, char* smem, bool write) 
       if (write && m.out_expert) m.out_expert[t * m.top_k + lane] = expert;
       if (write && m.out_weight) m.out_weight[t * m.top_k + lane] = p;
     }
+#pragma unroll
+    for (int r = 0; r < N; ++r) raw[r] = next[r];
   }
+}
+
+// The routing by a whole CTA; write: it also stores it for the caller.
+__device__ __forceinline__ void route(const MoeArgs& m, char* smem, bool write) {
+  Routes& s = *reinterpret_cast<Routes*>(smem);
+  const RouteTables tab = tables(smem, m.local);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (m.experts <= 64)
+    choose_all<2>(m, s, tab, write);
+  else if (m.experts <= 256)
+    choose_all<8>(m, s, tab, write);
+  else
+    choose_all<0>(m, s, tab, write);
   __syncthreads();
-  if (warp == 0) {
-    int count = 0;
-    for (int base = 0; base < m.local; base += 32) {
-      const int e = base + lane;
-      const uint32_t with = __ballot_sync(0xFFFFFFFFu, e < m.local && tab.tokens[e] != 0);
+  // Every warp counts the active experts for itself, and stores its share of the tables.
+  int count = 0;
+  for (int base = 0; base < m.local; base += 32) {
+    const int e = base + lane;
+    const uint32_t tokens = e < m.local ? tab.tokens[e] : 0, with = __ballot_sync(0xFFFFFFFFu, tokens != 0);
+    if (base / 32 % kWarps == warp && tokens) {
       const int at = count + __popc(with & ((1u << lane) - 1));
-      if (with >> lane & 1) tab.place[e] = (uint16_t)at, tab.number[at] = (uint16_t)e;
-      count += __popc(with);
+      tab.number[at] = (uint16_t)e;
+      // Which of its choices this expert is for each token.
+      for (uint32_t left = tokens; left; left &= left - 1) {
+        const int t = __ffs(left) - 1;
+        int j = 0;
+        while (s.expert[t][j] != m.first + e) ++j;
+        tab.choice[at * kTokens + t] = (uint8_t)j;
+      }
     }
-    if (lane == 0) s.active = count;
+    count += __popc(with);
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < m.tokens * m.top_k; i += kThreads) {
-    const int t = i / m.top_k, j = i % m.top_k, e = s.expert[t][j] - m.first;
-    if (s.expert[t][j] >= 0 && e >= 0 && e < m.local) tab.choice[tab.place[e] * kTokens + t] = (uint8_t)j;
-  }
+  if (threadIdx.x == 0) s.active = count;
   __syncthreads();
 }
 
@@ -255,8 +284,12 @@ __device__ __forceinline__ void multiply(float (&acc)[NB][4], const uint4& a, co
 }
 
 // Which of n runs, run r being r * total / n to (r + 1) * total / n, has unit p.
-__device__ __forceinline__ int run_of(int p, int total, int n) { return (int)(((int64_t)(p + 1) * n - 1) / total); }
-__device__ __forceinline__ int run_begin(int r, int total, int n) { return (int)((int64_t)r * total / n); }
+__device__ __forceinline__ int ratio(int a, int b, int minus, int by) {  // (a * b - minus) / by; 64-bit divisions take four times as long
+  const uint64_t v = (uint64_t)a * (uint32_t)b - minus;
+  return v >> 32 ? (int)(v / (uint32_t)by) : (int)((uint32_t)v / (uint32_t)by);
+}
+__device__ __forceinline__ int run_of(int p, int total, int n) { return ratio(p + 1, n, 1, total); }
+__device__ __forceinline__ int run_begin(int r, int total, int n) { return ratio(r, total, 0, n); }
 
 // An item: eight rows of one expert's gate and the same of its up projection, whose
 // sums of one output land in one lane.  A CTA has as many items as the others; their pieces along k, one
@@ -443,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   if ((int)blockIdx.x >= G) return;
   const int begin = run_begin(blockIdx.x, total, G), end = run_begin(blockIdx.x + 1, total, G), mine = end - begin;
   const int runs = min(kWarps, mine);
-  const auto begin_of = [&](int w) { return begin + run_begin(min(w, runs), mine, runs); };
-  const int first = begin_of(warp), last = begin_of(warp + 1);
+  __shared__ int begins[kWarps + 1];  // of the warps' runs
+  const int first = begin + run_begin(min(warp, runs), mine, runs), last = begin + run_begin(min(warp + 1, runs), mine, runs);
+  if (lane == 0) begins[warp] = first, begins[warp + 1] = last;  // neighbours store the same
 
   Feed feed = {nullptr, nullptr, 0, 0};
   int fed = first;  // units before this one have been given to `feed`
@@ -532,20 +566,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
 
   // The tiles that lie on several warps; of those, the CTA's first and last may lie on several CTAs.
   const int tile0 = begin / units, tile1 = (end - 1) / units;
-  const auto part_of = [&](int cta, int tile) {  // a CTA's first tile that it did not begin, or the one that it began
-    return m.parts + ((int64_t)cta * 2 + (tile * units >= run_begin(cta, total, G))) * kTokens * 16;
-  };
+  const auto part_of = [&](int cta, bool begun) { return m.parts + ((int64_t)cta * 2 + begun) * kTokens * 16; };
   for (int tile = tile0; tile <= tile1; ++tile) {
     const int from = max(tile * units, begin), to = min((tile + 1) * units, end);
-    const int w0 = run_of(from - begin, mine, runs), w1 = run_of(to - 1 - begin, mine, runs);
+    int w0 = 0, w1 = 0;  // the warps that have its first and last unit here
+    for (int w = 1; w < runs; ++w) w0 += begins[w] <= from, w1 += begins[w] < to;
     const bool whole = from == tile * units && to == (tile + 1) * units;
     if (w0 == w1 && whole) continue;  // done above
     for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
-      float v = 0.0f;
-      for (int w = w0; w <= w1; ++w) v += sums_of(w, tile * units >= begin_of(w))[i / 16 * 17 + i % 16];
+      const int at = i / 16 * 17 + i % 16;
+      float v = sums_of(w0, tile * units >= begins[w0])[at];
+      for (int w = w0 + 1; w <= w1; ++w) v += sums_of(w, 0)[at];
       const int64_t n = (int64_t)tile * 16 + i % 16;
       if (!whole)
-        part_of(blockIdx.x, tile)[i] = v;
+        part_of(blockIdx.x, tile * units >= begin)[i] = v;
       else if (n < m.hidden)
         out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
     }
@@ -569,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
     __threadfence();
     const int tile = k ? tile1 : tile0, c0 = run_of(tile * units, total, G), c1 = run_of((tile + 1) * units - 1, total, G);
     for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
-      float v = 0.0f;
-      for (int c = c0; c <= c1; ++c) v += __ldcg(part_of(c, tile) + i);
+      float v = __ldcg(part_of(c0, true) + i);
+      for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(part_of(c, false) + i);
       const int64_t n = (int64_t)tile * 16 + i % 16;
       if (n < m.hidden) out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
     }
