@@ -35,20 +35,23 @@ struct Routes {
   int expert[kTokens][kTop];  // -1: none
   int active;                 // local experts that have tokens
 };
-// Behind it: for each local expert the tokens that it has (a bit each); for each active
-// one its number, and which of a token's choices it is.
+// Behind it: for each local expert the tokens that it has (a bit each) and its
+// place among the active ones; for each active one its number; and which of a
+// token's choices it is.
 struct RouteTables {
   uint32_t* tokens;
+  uint16_t* place;
   uint16_t* number;
   uint8_t* choice;  // [active][32]
 };
 __host__ __device__ constexpr size_t route_bytes(int64_t local, int64_t pairs) {
-  return (sizeof(Routes) + 15) / 16 * 16 + (size_t)local * 6 + (size_t)(local < pairs ? local : pairs) * kTokens;
+  return (sizeof(Routes) + 15) / 16 * 16 + (size_t)local * 8 + (size_t)(local < pairs ? local : pairs) * kTokens;
 }
 __device__ __forceinline__ RouteTables tables(char* smem, int local) {
   RouteTables t;
   t.tokens = reinterpret_cast<uint32_t*>(smem + (sizeof(Routes) + 15) / 16 * 16);
-  t.number = reinterpret_cast<uint16_t*>(t.tokens + local);
+  t.place = reinterpret_cast<uint16_t*>(t.tokens + local);
+  t.number = t.place + local;
   t.choice = reinterpret_cast<uint8_t*>(t.number + local);
   return t;
 }
@@ -164,25 +167,25 @@ __device__ __forceinline__ void route(const MoeArgs& m, char* smem, bool write) 
   else
     choose_all<0>(m, s, tab, write);
   __syncthreads();
-  // Every warp counts the active experts for itself, and stores its share of the tables.
+  // Every warp counts the active experts for itself, and stores its share of them.
   int count = 0;
   for (int base = 0; base < m.local; base += 32) {
     const int e = base + lane;
-    const uint32_t tokens = e < m.local ? tab.tokens[e] : 0, with = __ballot_sync(0xFFFFFFFFu, tokens != 0);
-    if (base / 32 % kWarps == warp && tokens) {
+    const uint32_t with = __ballot_sync(0xFFFFFFFFu, e < m.local && tab.tokens[e] != 0);
+    if (base / 32 % kWarps == warp && with >> lane & 1) {
       const int at = count + __popc(with & ((1u << lane) - 1));
-      tab.number[at] = (uint16_t)e;
-      // Which of its choices this expert is for each token.
-      for (uint32_t left = tokens; left; left &= left - 1) {
-        const int t = __ffs(left) - 1;
-        int j = 0;
-        while (s.expert[t][j] != m.first + e) ++j;
-        tab.choice[at * kTokens + t] = (uint8_t)j;
-      }
+      tab.place[e] = (uint16_t)at, tab.number[at] = (uint16_t)e;
     }
     count += __popc(with);
   }
   if (threadIdx.x == 0) s.active = count;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kTokens * m.top_k; i += kThreads) {
+    const int t = i % kTokens, j = i / kTokens;
+    if (t >= m.tokens) continue;
+    const int e = s.expert[t][j] - m.first;
+    if (s.expert[t][j] >= 0 && e >= 0 && e < m.local) tab.choice[tab.place[e] * kTokens + t] = (uint8_t)j;
+  }
   __syncthreads();
 }
 
@@ -197,8 +200,10 @@ __device__ __forceinline__ uint4 tokens16(const char* p, int64_t left, const cha
 // lane 4 g + t has rows g and g + 8 at k = 8 t .. 8 t + 7 of each step.
 constexpr int kStages = 3, kSteps = 2, kPieceBytes = 128, kStageBytes = kSteps * 2 * 512, kRingBytes = kWarps * kStages * kStageBytes;
 
-__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+// Weights stream through L2 once: they are the first to leave it, or they would drive out the
+// tokens and the kernels' own code, whose misses then go to memory.
+__device__ __forceinline__ void copy16(uint32_t to, const char* from, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void copy_some(uint32_t to, const char* from, int bytes) {  // the rest of the 16 is zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
@@ -214,8 +219,10 @@ struct Feed {
 struct Ring {
   uint32_t mine;  // this lane's place in its warp's ring
   int stage;      // the one that is used next
+  uint64_t policy;
   __device__ __forceinline__ explicit Ring(char* smem)
-      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kStages * kStageBytes + (threadIdx.x & 31) * 16), stage(0) {}
+      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kStages * kStageBytes + (threadIdx.x & 31) * 16), stage(0),
+        policy(l2_policy_evict_first()) {}
   __device__ __forceinline__ uint4 row(int step, int r) const {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -240,8 +247,8 @@ struct Ring {
         if (f.left >= kPieceBytes) {
 #pragma unroll
           for (int i = 0; i < kSteps; ++i) {
-            copy16(at + i * 1024, f.a + 64 * i);
-            copy16(at + i * 1024 + 512, f.b + 64 * i);
+            copy16(at + i * 1024, f.a + 64 * i, policy);
+            copy16(at + i * 1024 + 512, f.b + 64 * i, policy);
           }
         } else {
 #pragma unroll
