@@ -200,10 +200,8 @@ __device__ __forceinline__ uint4 tokens16(const char* p, int64_t left, const cha
 // lane 4 g + t has rows g and g + 8 at k = 8 t .. 8 t + 7 of each step.
 constexpr int kStages = 3, kSteps = 2, kPieceBytes = 128, kStageBytes = kSteps * 2 * 512, kRingBytes = kWarps * kStages * kStageBytes;
 
-// Weights stream through L2 once: they are the first to leave it, or they would drive out the
-// tokens and the kernels' own code, whose misses then go to memory.
-__device__ __forceinline__ void copy16(uint32_t to, const char* from, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
+__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy_some(uint32_t to, const char* from, int bytes) {  // the rest of the 16 is zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
@@ -219,10 +217,8 @@ struct Feed {
 struct Ring {
   uint32_t mine;  // this lane's place in its warp's ring
   int stage;      // the one that is used next
-  uint64_t policy;
   __device__ __forceinline__ explicit Ring(char* smem)
-      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kStages * kStageBytes + (threadIdx.x & 31) * 16), stage(0),
-        policy(l2_policy_evict_first()) {}
+      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kStages * kStageBytes + (threadIdx.x & 31) * 16), stage(0) {}
   __device__ __forceinline__ uint4 row(int step, int r) const {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -247,8 +243,8 @@ struct Ring {
         if (f.left >= kPieceBytes) {
 #pragma unroll
           for (int i = 0; i < kSteps; ++i) {
-            copy16(at + i * 1024, f.a + 64 * i, policy);
-            copy16(at + i * 1024 + 512, f.b + 64 * i, policy);
+            copy16(at + i * 1024, f.a + 64 * i);
+            copy16(at + i * 1024 + 512, f.b + 64 * i);
           }
         } else {
 #pragma unroll
@@ -290,13 +286,14 @@ __device__ __forceinline__ void multiply(float (&acc)[NB][4], const uint4& a, co
   }
 }
 
-// Which of n runs, run r being r * total / n to (r + 1) * total / n, has unit p.
-__device__ __forceinline__ int ratio(int a, int b, int minus, int by) {  // (a * b - minus) / by; 64-bit divisions take four times as long
-  const uint64_t v = (uint64_t)a * (uint32_t)b - minus;
-  return v >> 32 ? (int)(v / (uint32_t)by) : (int)((uint32_t)v / (uint32_t)by);
+// The first of `total` that share r has of n even ones: total / n each, and one more for the first total % n.
+__device__ __forceinline__ int share(int r, int total, int n) { return r * (total / n) + min(r, total % n); }
+__device__ __forceinline__ int warp_share(int w, int total) { return share(w, total, kWarps); }
+// Which share has number p.
+__device__ __forceinline__ int share_of(int p, int total, int n) {
+  const int each = total / n, longer = total % n;
+  return p < longer * (each + 1) ? p / (each + 1) : longer + (p - longer * (each + 1)) / max(each, 1);
 }
-__device__ __forceinline__ int run_of(int p, int total, int n) { return ratio(p + 1, n, 1, total); }
-__device__ __forceinline__ int run_begin(int r, int total, int n) { return ratio(r, total, 0, n); }
 
 // An item: eight rows of one expert's gate and the same of its up projection, whose
 // sums of one output land in one lane.  A CTA has as many items as the others; their pieces along k, one
@@ -321,12 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
   __shared__ uint8_t lists[kWarps][kTokens];
   uint8_t* const list = lists[warp];
 
-  const int strips = (int)((m.width + 7) / 8);
-  const int items = reinterpret_cast<const Routes*>(tables_at)->active * strips, bytes = (int)m.hidden * 2;
-  const int pieces = (bytes + kPieceBytes - 1) / kPieceBytes;
-  const int item0 = run_begin(blockIdx.x, items, gridDim.x), total = (run_begin(blockIdx.x + 1, items, gridDim.x) - item0) * pieces;
+  const int strips = (int)((m.width + 7) / 8), bytes = (int)m.hidden * 2, pieces = (bytes + kPieceBytes - 1) / kPieceBytes;
+  const int items = reinterpret_cast<const Routes*>(tables_at)->active * strips;
+  const int item0 = share(blockIdx.x, items, (int)gridDim.x), total = (share(blockIdx.x + 1, items, (int)gridDim.x) - item0) * pieces;
   if (total == 0) return;
-  const int runs = min(kWarps, total), first = run_begin(min(warp, runs), total, runs), last = run_begin(min(warp + 1, runs), total, runs);
+  const int first = warp_share(warp, total), last = warp_share(warp + 1, total);
   const char *bg = static_cast<const char*>(m.w_gate), *bu = static_cast<const char*>(m.w_up), *bx = static_cast<const char*>(m.x);
   const int64_t extent = ((m.local - 1) * m.esw + (m.width - 1) * m.ldw + m.hidden) * 2;
   const char* ex = bx + ((m.tokens - 1) * m.ldx + m.hidden) * 2;
@@ -343,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
     }
     ring.fetch<VEC>(ahead, feed, bg, bu, extent);
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
   // An item's expert, its tokens in `list`, their number.
@@ -423,9 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
   }
   __syncthreads();
   // An item that this warp begins and does not end.
-  const int q = (last - 1) / pieces;
-  if (warp < runs && last % pieces != 0 && q * pieces >= first) {
-    const int until = run_of(q * pieces + pieces - 1, total, runs);
+  const int q = max(last - 1, 0) / pieces, end = q * pieces + pieces;
+  if (first < last && last < end && q * pieces >= first) {
+    // the last warp that has a part of it
+    const int until = __popc(__ballot_sync(0xFFFFFFFFu, lane < kWarps && warp_share(lane, total) < end)) - 1;
     int place;
     const int count = open(item0 + q, place);
     for (int j = 0; 8 * j < count; ++j) {
@@ -467,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   const int entries = m.tokens * 17;
   const auto sums_of = [&](int w, int which) { return sums + (w * 2 + which) * entries; };
 
-  const int tiles = (int)((m.hidden + 15) / 16), bytes = (int)m.width * 2, pieces = (bytes + kPieceBytes - 1) / kPieceBytes;
-  const int units = s.active * pieces, total = tiles * units, G = min((int)gridDim.x, total);  // G CTAs have a part, none of it empty
+  const int tiles = (int)((m.hidden + 15) / 16), bytes = (int)m.width * 2, pieces = (bytes + kPieceBytes - 1) / kPieceBytes, active = s.active;
+  const int units = active * pieces, total = tiles * units;
   const char* bd = static_cast<const char*>(m.w_down);
   const int64_t extent = ((m.local - 1) * m.esd + (m.hidden - 1) * m.ldd + m.width) * 2;
   const char* h = static_cast<const char*>(m.h);
@@ -480,18 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
       out[i / m.hidden * m.ldo + i % m.hidden] = 0;
     return;
   }
-  if ((int)blockIdx.x >= G) return;
-  const int begin = run_begin(blockIdx.x, total, G), end = run_begin(blockIdx.x + 1, total, G), mine = end - begin;
-  const int runs = min(kWarps, mine);
-  __shared__ int begins[kWarps + 1];  // of the warps' runs
-  const int first = begin + run_begin(min(warp, runs), mine, runs), last = begin + run_begin(min(warp + 1, runs), mine, runs);
-  if (lane == 0) begins[warp] = first, begins[warp + 1] = last;  // neighbours store the same
+  const int begin = share(blockIdx.x, total, (int)gridDim.x), mine = share(blockIdx.x + 1, total, (int)gridDim.x) - begin, end = begin + mine;
+  if (mine == 0) return;
+  const auto begin_of = [&](int w) { return begin + warp_share(w, mine); };
+  const int first = begin_of(warp), last = begin_of(warp + 1);
 
   Feed feed = {nullptr, nullptr, 0, 0};
   int fed = first;  // units before this one have been given to `feed`
   const auto fetch = [&](int ahead) {
     if (feed.more == 0 && fed < last) {
-      const int tile = fed / units, u = fed - tile * units, place = u / pieces, p = u - place * pieces;
+      const int q = fed / pieces, p = fed - q * pieces, tile = q / active, place = q - tile * active;
       const int64_t n0 = (int64_t)tile * 16, ra = min(n0 + g8, m.hidden - 1), rb = min(n0 + g8 + 8, m.hidden - 1);
       const char* from = bd + tab.number[place] * m.esd * 2 + (int64_t)p * kPieceBytes + 16 * t4;
       feed = {from + ra * m.ldd * 2, from + rb * m.ldd * 2, bytes - p * kPieceBytes, min(pieces - p, last - fed)};
@@ -499,14 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
     }
     ring.fetch<VEC>(ahead, feed, bd, bd, extent);
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
   for (int i = lane; i < 2 * entries; i += 32) sums_of(warp, 0)[i] = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   for (int pos = first; pos < last;) {
     // One expert's units of a tile.
-    const int tile = pos / units, u0 = pos - tile * units, place = u0 / pieces, p0 = u0 - place * pieces, p1 = min(pieces, p0 + (last - pos));
+    const int q = pos / pieces, p0 = pos - q * pieces, tile = q / active, place = q - tile * active, p1 = min(pieces, p0 + (last - pos));
     float* const own = sums_of(warp, tile * units >= first);
     const uint32_t tokens = tab.tokens[tab.number[place]];
     const int count = __popc(tokens);
@@ -569,26 +564,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
       }
     }
   }
-  __syncthreads();
-
-  // The tiles that lie on several warps; of those, the CTA's first and last may lie on several CTAs.
+  // The tiles that lie on several warps are named by the first warp that has a part: the CTA's first, where another
+  // CTA began it, and the one that a warp begins and does not end.
+  __shared__ int split[kWarps + 1][2];  // tile (-1: none), its last warp
   const int tile0 = begin / units, tile1 = (end - 1) / units;
+  const auto name = [&](int at, int tile, bool there) {
+    const int until = __popc(__ballot_sync(0xFFFFFFFFu, lane < kWarps && begin_of(lane) < min((tile + 1) * units, end))) - 1;
+    if (lane == 0) split[at][0] = there ? tile : -1, split[at][1] = until;
+  };
+  if (warp == 0) name(kWarps, tile0, tile0 * units < begin);
+  const int my_last = max(last - 1, 0) / units;
+  name(warp, my_last, first < last && my_last * units >= first && last < (my_last + 1) * units);
+  __syncthreads();
   const auto part_of = [&](int cta, bool begun) { return m.parts + ((int64_t)cta * 2 + begun) * kTokens * 16; };
-  for (int tile = tile0; tile <= tile1; ++tile) {
-    const int from = max(tile * units, begin), to = min((tile + 1) * units, end);
-    int w0 = 0, w1 = 0;  // the warps that have its first and last unit here
-    for (int w = 1; w < runs; ++w) w0 += begins[w] <= from, w1 += begins[w] < to;
-    const bool whole = from == tile * units && to == (tile + 1) * units;
-    if (w0 == w1 && whole) continue;  // done above
+  const auto store = [&](int tile, int i, float v) {
+    const int64_t n = (int64_t)tile * 16 + i % 16;
+    if (n < m.hidden) out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+  };
+#pragma unroll 1
+  for (int k = 0; k <= kWarps; ++k) {
+    const int tile = split[k][0], until = split[k][1], w0 = k % kWarps;
+    if (tile < 0) continue;
+    const bool whole = k < kWarps && (tile + 1) * units <= end;
     for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
       const int at = i / 16 * 17 + i % 16;
-      float v = sums_of(w0, tile * units >= begins[w0])[at];
-      for (int w = w0 + 1; w <= w1; ++w) v += sums_of(w, 0)[at];
-      const int64_t n = (int64_t)tile * 16 + i % 16;
-      if (!whole)
-        part_of(blockIdx.x, tile * units >= begin)[i] = v;
-      else if (n < m.hidden)
-        out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+      float v = sums_of(w0, k < kWarps)[at];
+      for (int w = w0 + 1; w <= until; ++w) v += sums_of(w, 0)[at];
+      if (whole)
+        store(tile, i, v);
+      else
+        part_of(blockIdx.x, k < kWarps)[i] = v;
     }
   }
   if (tile0 * units == begin && (tile1 + 1) * units == end) return;
@@ -596,24 +601,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   __syncthreads();
   if (threadIdx.x < 2) {
     const int tile = threadIdx.x ? tile1 : tile0;
-    const bool is_split = tile * units < begin || (tile + 1) * units > end;
-    finished[threadIdx.x] = 0;
-    if (is_split && (threadIdx.x == 0 || tile1 != tile0)) {
-      const int c0 = run_of(tile * units, total, G), c1 = run_of((tile + 1) * units - 1, total, G);
-      finished[threadIdx.x] = atomicAdd(&m.done[tile], 1u) == (uint32_t)(c1 - c0);
+    finished[threadIdx.x] = -1;
+    if ((tile * units < begin || (tile + 1) * units > end) && (threadIdx.x == 0 || tile1 != tile0)) {
+      const int c0 = share_of(tile * units, total, (int)gridDim.x), c1 = share_of((tile + 1) * units - 1, total, (int)gridDim.x);
+      if (atomicAdd(&m.done[tile], 1u) == (uint32_t)(c1 - c0)) finished[threadIdx.x] = c0 << 16 | c1;
     }
   }
   __syncthreads();
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    if (!finished[k]) continue;
+    if (finished[k] < 0) continue;
     __threadfence();
-    const int tile = k ? tile1 : tile0, c0 = run_of(tile * units, total, G), c1 = run_of((tile + 1) * units - 1, total, G);
+    const int tile = k ? tile1 : tile0, c0 = finished[k] >> 16, c1 = finished[k] & 0xFFFF;
     for (int i = threadIdx.x; i < m.tokens * 16; i += kThreads) {
       float v = __ldcg(part_of(c0, true) + i);
       for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(part_of(c, false) + i);
-      const int64_t n = (int64_t)tile * 16 + i % 16;
-      if (n < m.hidden) out[i / 16 * m.ldo + n] = (uint16_t)E::from_f32(v);
+      store(tile, i, v);
     }
   }
 }
