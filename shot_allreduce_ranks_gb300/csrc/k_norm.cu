@@ -74,23 +74,23 @@ __device__ __forceinline__ Stats stats_of(const C& c, const float (&v)[N], int l
 }
 
 // One row, x in v and the residual in q: r and y are stored.  room holds four rows.
-template <class E, int N, bool VEC, bool WARP>
-__device__ __forceinline__ void norm_row(const NormArgs& a, const Columns<E, N, VEC>& c, int64_t row, float (&v)[N], const float (&q)[N],
+template <class E, int N, Layout L, bool WARP>
+__device__ __forceinline__ void norm_row(const NormArgs& a, const Columns<E, N, L>& c, int64_t row, float (&v)[N], const float (&q)[N],
                                          float (*room)[32]) {
   float w[N];
   if (a.after_weight) {
-    c.load_shared(a.after_weight, 0, w);
+    c.load_shared(a.after_weight, 0, a.cols, w);
     const Stats s = stats_of<WARP>(c, v, a.layer, a.eps, room);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = (v[i] - s.mean) * s.factor * (a.offset + w[i]);
     if (a.after_bias) {
-      c.load_shared(a.after_bias, 0, w);
+      c.load_shared(a.after_bias, 0, a.cols, w);
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += w[i];
     }
   }
   if (a.gate) {
-    c.load_shared(a.gate, row / a.gate_run * a.ldg, w);
+    c.load_shared(a.gate, row / a.gate_run * a.ldg, a.gate_extent, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] *= w[i];
   }
@@ -98,7 +98,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Columns<E, N, 
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = __fmaf_rn(a.alpha, q[i], v[i]);
   }
-  if (a.weight) c.load_shared(a.weight, 0, w);
+  if (a.weight) c.load_shared(a.weight, 0, a.cols, w);
   if (a.r) c.store(a.r, row * a.ldr, v);
   if (!a.weight) return;
   // Columns past the last hold what biases left there, which the norm must not see.
@@ -108,7 +108,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Columns<E, N, 
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = (v[i] - s.mean) * s.factor * (a.offset + w[i]);
   if (a.bias) {
-    c.load_shared(a.bias, 0, w);
+    c.load_shared(a.bias, 0, a.cols, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += w[i];
   }
@@ -116,17 +116,17 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Columns<E, N, 
 }
 
 // A row a CTA, or (WARP) a row a warp, read once and held in registers, N columns a thread.
-template <class E, int N, bool VEC, bool WARP>
+template <class E, int N, Layout L, bool WARP>
 __global__ void __launch_bounds__(1024) k_norm_rows(NormArgs a) {
   __shared__ float room[4][32];
   pdl_enter();
   const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   if (WARP && row >= a.rows) return;
-  const Columns<E, N, VEC> c = {WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.cols};
+  const Columns<E, N, L> c = {WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.cols};
   float v[N], q[N];
-  c.load(a.x, row * a.ldx, v);
-  if (a.residual) c.load(a.residual, row * a.ldres, q);
-  norm_row<E, N, VEC, WARP>(a, c, row, v, q, room);
+  c.load(a.x, row * a.ldx, (a.rows - 1) * a.ldx + a.cols, v);
+  if (a.residual) c.load(a.residual, row * a.ldres, (a.rows - 1) * a.ldres + a.cols, q);
+  norm_row<E, N, L, WARP>(a, c, row, v, q, room);
 }
 
 // Many rows: a CTA (or warp) takes every gridDim-th and copies the next ones into shared
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(1024) k_norm_stream(NormArgs a) {
   constexpr int G = E::kGroup, kPieces = N / G;
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const Columns<E, N, true> c = {WARP ? lane : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.cols};
+  const Columns<E, N, kAligned> c = {WARP ? lane : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.cols};
   const int64_t first = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : (int64_t)gridDim.x;
   // Piece p of matrix m of a stage, one thread's after the other's.
@@ -181,20 +181,20 @@ __global__ void __launch_bounds__(1024) k_norm_stream(NormArgs a) {
       }
     }
     // The next row's sums go to the other half of the room: a warp may be a row ahead.
-    norm_row<E, N, true, WARP>(a, c, row, v, q, room + 4 * parity);
+    norm_row<E, N, kAligned, WARP>(a, c, row, v, q, room + 4 * parity);
     parity ^= 1;
     stage = stage == kStages - 1 ? 0 : stage + 1;
   }
 }
 
-template <class E, int N, bool VEC>
+template <class E, int N, Layout L>
 cudaError_t norm_rows(const NormArgs& a, cudaStream_t s) {
   const int64_t threads = (a.cols + 32 * N - 1) / (32 * N) * 32;
   if (threads == 32) {
     const int64_t grid = (a.rows + 3) / 4;
-    return launch_op(k_norm_rows<E, N, VEC, true>, dim3((unsigned)grid), 128, 0, 1, s, a);
+    return launch_op(k_norm_rows<E, N, L, true>, dim3((unsigned)grid), 128, 0, 1, s, a);
   }
-  return launch_op(k_norm_rows<E, N, VEC, false>, dim3((unsigned)a.rows), (int)threads, 0, 1, s, a);
+  return launch_op(k_norm_rows<E, N, L, false>, dim3((unsigned)a.rows), (int)threads, 0, 1, s, a);
 }
 
 template <class E>
@@ -219,17 +219,18 @@ cudaError_t norm(const NormArgs& a, int num_sms, cudaStream_t s) {
     const int64_t most = (int64_t)num_sms * 8;
     return launch_op(k_norm_any<E>, dim3((unsigned)(a.rows < most ? a.rows : most)), kAnyThreads, 0, 1, s, a);
   }
-  // Eight columns a thread where no SM gets a second row (1 x 5120 bf16 2.3 us, sixteen 2.7)
-  // or rows start anywhere (1001 x 1031 fp16 5.0, sixteen 6.7); above, sixteen, whose
-  // loads in flight keep fp32 at the copy rate (8192 x 8192: 154 us, copied ahead 179); 16-bit rows of half the
-  // bytes are copied ahead from three rows an SM on (440 x 8192 bf16 6.4 us,
+  // Rows that start anywhere: 16-bit ones by shifted pieces, fp32 by elements (8192 x 4095 bf16 108 and 110 us,
+  // 2048 x 5121 fp32 73 and 50).
+  constexpr Layout kAny = E::kBytes == 2 ? kShifted : kElements;
+  if (!vec) return a.cols <= 8192 ? norm_rows<E, 8, kAny>(a, s) : norm_rows<E, 16, kAny>(a, s);
+  // Eight columns a thread where no SM gets a second row (1 x 5120 bf16 2.3 us, sixteen 2.7);
+  // above, sixteen, whose loads in flight keep fp32 at the copy rate (8192 x 8192: 154 us, copied ahead 179);
+  // 16-bit rows of half the bytes are copied ahead from three rows an SM on (440 x 8192 bf16 6.4 us,
   // copied ahead 7.1; 1000 x 8192 16.1 and 14.5; 16384 x 8192 232 and 177).
-  if (!vec || (a.rows <= num_sms && a.cols <= 8192))
-    return a.cols <= 8192 ? vec ? norm_rows<E, 8, true>(a, s) : norm_rows<E, 8, false>(a, s)
-                          : vec ? norm_rows<E, 16, true>(a, s) : norm_rows<E, 16, false>(a, s);
+  if (a.rows <= num_sms && a.cols <= 8192) return norm_rows<E, 8, kAligned>(a, s);
   if constexpr (E::kBytes == 2)
     if (a.rows > 3 * (int64_t)num_sms) return norm_stream<E>(a, num_sms, s);
-  return norm_rows<E, 16, true>(a, s);
+  return norm_rows<E, 16, kAligned>(a, s);
 }
 
 }  // namespace

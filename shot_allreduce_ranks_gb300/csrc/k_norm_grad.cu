@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
   __shared__ float rooms[MAXT > kGroupThreads ? 1 : 4][2][8][32];  // groups of one warp use none
   pdl_enter();
   const int groups = (int)blockDim.x / T, group = (int)threadIdx.x / T;
-  const Columns<E, N, VEC> c = {(int)threadIdx.x - group * T, T, (int)a.cols};
+  const Columns<E, N, VEC ? kAligned : kShifted> c = {(int)threadIdx.x - group * T, T, (int)a.cols};
   const float inv = 1.0f / (float)a.cols;
   int64_t first, last, step;
   if (a.split) {
@@ -178,66 +178,29 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
   const bool has_weight = !FULL || a.weight;  // one of the two norms is there
   const void* const mats[4] = {a.dy, a.dr, has_weight ? a.r : nullptr, FULL ? a.x : nullptr};
   const int64_t lds[4] = {a.lddy, a.lddr, a.ldr, a.ldx};
-  // This thread's pieces of a row: where they begin, how many bytes are there,
-  // and its place in a stage of shared memory.
-  int begin[kPieces], left[kPieces];
-#pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
-    left[p] = min(max(c.cols - c.at(p * G), 0), G) * E::kBytes;
-    begin[p] = left[p] ? c.at(p * G) * E::kBytes : 0;
-  }
-  const int plane = (int)blockDim.x * 16, stage_bytes = kMats * kPieces * plane;
-  const char* mine = smem + threadIdx.x * 16;
+  const Staged<E, N, VEC> rows = {c};
+  const int mat_bytes = rows.bytes(T), stage_bytes = kMats * mat_bytes;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + group * stages * stage_bytes;
+  const auto row_of = [&](int m, int64_t row) { return static_cast<const char*>(mats[m]) + row * (lds[m] * E::kBytes); };
   const auto fetch = [&](int64_t row, int stage) {
     if (row < last) {
-      const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine) + stage * stage_bytes;
 #pragma unroll
-      for (int m = 0; m < kMats; ++m) {
-        if (!mats[m]) continue;
-        const char* from = static_cast<const char*>(mats[m]) + row * (lds[m] * E::kBytes);
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) copy_async16(to + (m * kPieces + p) * plane, from + begin[p], left[p]);
-      }
+      for (int m = 0; m < kMats; ++m)
+        if (mats[m])
+          rows.fetch(mine + stage * stage_bytes + m * mat_bytes, row_of(m, row), row_of(m, 0),
+                     VEC ? nullptr : row_of(m, a.rows - 1) + a.cols * E::kBytes);
     }
     copies_commit();
   };
   // The row's part of matrix m in v.
   const auto get = [&](int m, int64_t row, int stage, float(&v)[N]) {
-    if (VEC) {
-      const char* from = mine + stage * stage_bytes + m * kPieces * plane;
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        Acc<E> x;
-        x.set(*reinterpret_cast<const uint4*>(from + p * plane));
-#pragma unroll
-        for (int k = 0; k < G; ++k) v[p * G + k] = x.v[k];
-      }
-    } else {
-      c.load(mats[m], row * lds[m], v);
-    }
-  };
-  const auto put_row = [&](void* out, int64_t first_elem, const float(&v)[N]) {
-    if (!VEC) {
-      c.store(out, first_elem, v);
-      return;
-    }
-    char* to = static_cast<char*>(out) + first_elem * E::kBytes;
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      Acc<E> x;
-#pragma unroll
-      for (int k = 0; k < G; ++k) x.v[k] = v[p * G + k];
-      if (left[p] == 16)
-        st_v4_stream(to + begin[p], x.round());
-      else if (left[p])
-        store_group<E>(to + begin[p], 0, x.round(), left[p] / E::kBytes, false);
-    }
+    rows.read(mine + stage * stage_bytes + m * mat_bytes, VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(row_of(m, row)) & 15u), v);
   };
 
   // The weight stays in registers where no other vector takes turns with it.
   float w[N];
   if constexpr (!FULL) {
-    c.load_shared(a.weight, 0, w);
+    c.load_shared(a.weight, 0, a.cols, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] += a.offset;  // past the last column dy is 0
   }
@@ -266,21 +229,42 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
     }
   };
   if constexpr (ALL) clear(kSumAfterWeight), clear(kSumAfterBias), clear(kSumGate);
-  if (VEC)
-    for (int i = 0; i < stages - 1; ++i) fetch(first + i * step, i);
+  const auto meet = [&] {
+    if (T == 32)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
+  };
+  const auto wait_but = [](int later) {  // for all copies but the latest `later` groups
+    if (later == 3)
+      copies_wait<3>();
+    else if (later == 2)
+      copies_wait<2>();
+    else if (later == 1)
+      copies_wait<1>();
+    else
+      copies_wait<0>();
+  };
+  for (int i = 0; i < stages - 1; ++i) fetch(first + i * step, i);
   int stage = 0, parity = 0;
   for (int64_t row = first; row < last; row += step) {
+    const int64_t ahead = row + (stages - 1) * step;
+    const int refilled = stage == 0 ? stages - 1 : stage - 1;
     if (VEC) {
-      const int to = stage == 0 ? stages - 1 : stage - 1;
-      fetch(row + (stages - 1) * step, to);
-      if (stages == 4)
-        copies_wait<3>();
-      else if (stages == 3)
-        copies_wait<2>();
-      else if (stages == 2)
-        copies_wait<1>();
-      else
-        copies_wait<0>();
+      fetch(ahead, refilled);
+      wait_but(stages - 1);
+    } else {
+      // Neighbours read each other's copies: a stage is refilled once all have left its row.
+      if (stages == 1) {
+        meet();
+        fetch(ahead, refilled);
+        wait_but(0);
+        meet();
+      } else {
+        wait_but(stages - 2);
+        meet();
+        fetch(ahead, refilled);
+      }
     }
     float(*room)[32] = rooms[group][parity];
     float r[N], d[N];
@@ -289,7 +273,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
       get(kR, row, stage, r);
       get(kDy, row, stage, d);
       if constexpr (FULL) {
-        c.load_shared(a.weight, 0, w);
+        c.load_shared(a.weight, 0, a.cols, w);
 #pragma unroll
         for (int i = 0; i < N; ++i) w[i] += a.offset;
       }
@@ -342,12 +326,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
       }
     }
     // What a thread of a large CTA has no registers for it reads again.
-    constexpr bool kAgain = VEC && FULL && MAXT > 512;
+    constexpr bool kAgain = FULL && MAXT > 512;
     if constexpr (kAgain) {
       if (has_weight) {
         get(kR, row, stage, r);
         get(kDy, row, stage, d);
-        c.load_shared(a.weight, 0, w);
+        c.load_shared(a.weight, 0, a.cols, w);
 #pragma unroll
         for (int i = 0; i < N; ++i) w[i] += a.offset;
       }
@@ -371,7 +355,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
     if (a.dresidual) {
 #pragma unroll
       for (int i = 0; i < N; ++i) r[i] = a.alpha * g[i];
-      put_row(a.dresidual, row * a.lddres, r);
+      c.store(a.dresidual, row * a.lddres, r);
     }
     if constexpr (kAgain) get(kX, row, stage, x);
     if constexpr (ALL) {
@@ -379,9 +363,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
       if (a.gate) {
         float v[N];
         if (a.after_weight) {
-          c.load_shared(a.after_weight, 0, w);
+          c.load_shared(a.after_weight, 0, a.cols, w);
           if (a.after_bias)
-            c.load_shared(a.after_bias, 0, d);
+            c.load_shared(a.after_bias, 0, a.cols, d);
           else
 #pragma unroll
             for (int i = 0; i < N; ++i) d[i] = 0.0f;
@@ -397,14 +381,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
           if (a.sum[kSumGate]) c.store(a.sum[kSumGate], gate_row * a.lddg, v);
           clear(kSumGate);
         }
-        c.load_shared(a.gate, gate_row * a.ldg, w);
+        c.load_shared(a.gate, gate_row * a.ldg, (a.gate_rows - 1) * a.ldg + a.cols, w);
 #pragma unroll
         for (int i = 0; i < N; ++i) g[i] *= w[i];
       }
     }
     if constexpr (FULL) {
       if (a.after_weight) {
-        c.load_shared(a.after_weight, 0, w);
+        c.load_shared(a.after_weight, 0, a.cols, w);
         float s[2] = {}, v[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -432,13 +416,13 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
           g[i] = xfactor * __fmaf_rn(LAYER ? xmean - x[i] : -x[i], xfactor * n1, LAYER ? __fmaf_rn(g[i], w[i], -n0) : g[i] * w[i]);
       }
     }
-    if (a.dx) put_row(a.dx, row * a.lddx, g);
+    if (a.dx) c.store(a.dx, row * a.lddx, g);
     parity ^= 1;
     stage = stage == stages - 1 ? 0 : stage + 1;
   }
 
   // The groups' sums are joined in their order, through shared memory, and stored as the CTA's part.
-  if (VEC) copies_wait<0>();
+  copies_wait<0>();
   float* sum = reinterpret_cast<float*>(smem);
   const auto finish = [&](int k, const float(&v)[N]) {
     if (!a.sum[k] || (k == kSumGate && !a.split)) return;
@@ -521,9 +505,9 @@ cudaError_t norm_grad_rows_kind(NormGradArgs& a, int num_sms, cudaStream_t s) {
   const int T = row_threads(a.cols, N), cta = T < kGroupThreads ? T * row_groups(T) : T;
   // 64 registers a thread, or 128 with a branch up to 512 threads; as many stages as fit beside one another.
   const int per_sm = cta > 512 || (BRANCH && cta > 256) ? 1 : BRANCH ? 512 / cta : 1024 / cta;
-  const int64_t stage = (int64_t)kMats * N * E::kBytes * cta, sums = ALL ? (int64_t)3 * N * 4 * cta : 0;
+  const int64_t stage = (int64_t)kMats * Staged<E, N, VEC>::bytes(T) * (cta / T), sums = ALL ? (int64_t)3 * N * 4 * cta : 0;
   const int64_t room = (228 * 1024) / per_sm - 1024 - (cta > kGroupThreads ? 2048 : 8192) - sums;
-  const int stages = !VEC ? 0 : room >= 4 * stage ? 4 : room >= 3 * stage ? 3 : room >= 2 * stage ? 2 : 1;
+  const int stages = room >= 4 * stage ? 4 : room >= 3 * stage ? 3 : room >= 2 * stage ? 2 : 1;
   int64_t smem = stages * stage;
   // The groups' sums are joined at the front, where no thread's sums may lie yet.
   if (smem < a.cols * 4 && cta > T) smem = a.cols * 4;

@@ -211,6 +211,7 @@ ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, cons
   a.ldx = (int64_t)ldx, a.ldres = (int64_t)ldres, a.ldg = (int64_t)ldg, a.ldr = (int64_t)ldr, a.ldy = (int64_t)ldy;
   a.rows = (int64_t)rows, a.cols = (int64_t)cols;
   a.gate_run = gate ? (int64_t)(rows / n->gate_rows) : (int64_t)rows;
+  a.gate_extent = gate ? (int64_t)((n->gate_rows - 1) * ldg + cols) : 0;
   a.eps = (float)n->eps, a.alpha = (float)n->residual_scale, a.offset = (float)n->weight_offset;
   a.layer = n->kind == AR_NORM_LAYER;
   return cuda_status(launch_norm(n->dtype, a, sms, static_cast<cudaStream_t>(stream)));

@@ -148,6 +148,7 @@ struct NormArgs {
   void *r, *y;
   int64_t ldx, ldres, ldg, ldr, ldy;
   int64_t rows, cols, gate_run;  // gate_run: rows of one gate row
+  int64_t gate_extent;           // elements from the gate's first to behind its last
   float eps, alpha, offset;
   int layer;
 };
@@ -297,7 +298,7 @@ __device__ __forceinline__ uint4 load_anywhere(const char* p, int64_t left, cons
 #pragma unroll
   for (int i = 0; i < 16 / B; ++i)
     if (i * B < left) {
-      const uint32_t v = B == 2 ? ld_elem<2>(p + 2 * i) : *reinterpret_cast<const uint8_t*>(p + i);
+      const uint32_t v = B == 1 ? *reinterpret_cast<const uint8_t*>(p + i) : ld_elem<B == 1 ? 2 : B>(p + B * i);
       w[i * B / 4] |= v << (8 * (i * B % 4));
     }
   return make_uint4(w[0], w[1], w[2], w[3]);
