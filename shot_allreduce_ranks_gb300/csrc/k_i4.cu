@@ -10,7 +10,6 @@
 // for two instructions are 16 contiguous bytes.  An instruction's k lie
 // within one group of 32 or more, so the group's scale multiplies the fp32 sums and never
 // a weight: q - zero is exact in 16 bits.
-#include <stdlib.h>
 #include "ops_internal.cuh"
 
 namespace ar {
@@ -121,43 +120,42 @@ struct Span {
   }
 };
 
-// R tiles of sixteen channels for up to 8 NB tokens a CTA; its warps take turns at the spans
+// A tile of sixteen channels for up to 8 NB tokens a CTA; its warps take turns at the spans
 // along k, and their sums are joined in a fixed order.
-template <class E, int GROUP, bool ZERO, int NB, int R, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_linear_i4(I4Args a) {
+//
+// With few tokens what bounds it is first the integer pipe, which unpacks a weight in
+// 7/8 of an instruction (two logical operations and three shifts for every four), then the loads in flight: three CTAs
+// an SM, each warp with four pieces of 512 bytes, were the fastest of 2 to 8 pieces and 1 to 5 CTAs. 8192 -> 16384 in groups of 128 (69
+// MB): one token 17.9 us (57% of the copy rate; without unpacking it would be 16), 8 tokens 18.6; 16 tokens 26.5 and 32 47, where
+// what is read of x from L1 passes what is read of the weights. Weights copied ahead
+// by a persistent CTA with x in shared memory took 21.7 us.
+template <class E, int GROUP, bool ZERO, int NB, bool VEC>
+__global__ void __launch_bounds__(kThreads, NB > 2 ? 2 : 3) k_linear_i4(I4Args a) {
   constexpr int kSpan = span_of(GROUP), kPer = groups_in(GROUP), kTiles = kSpan / 64;
-  constexpr int U = NB > 2 ? 1 : 2 / kTiles;  // spans in flight
+  constexpr int U = NB == 1 ? 4 / kTiles : NB == 2 ? 2 / kTiles : 1;  // spans in flight
   __shared__ float4 part[kWarps][NB][32];
   pdl_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   const int64_t m0 = (int64_t)blockIdx.y * 32, M = min(a.M - m0, (int64_t)32), spans = a.spans, bytes = a.K * 2;
-  const int64_t tiles = (a.N + 15) / 16, tile0 = (int64_t)blockIdx.x * R;
-  const uint4* data[R];
-  const uint16_t* scales[R];
-  const uint8_t* zeros[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {  // a tile past the last is read as the last, and dropped
-    const int64_t t = min(tile0 + r, tiles - 1);
-    data[r] = reinterpret_cast<const uint4*>(a.data) + t * spans * kTiles * 32 + lane;
-    scales[r] = static_cast<const uint16_t*>(a.scale) + (t * spans * 8 + g8) * kPer * 2;
-    zeros[r] = a.zero + (t * spans * 8 + g8) * kPer * 2;
-  }
+  const int64_t tile = blockIdx.x;
+  const uint4* data = reinterpret_cast<const uint4*>(a.data) + tile * spans * kTiles * 32 + lane;
+  const uint16_t* scales = static_cast<const uint16_t*>(a.scale) + (tile * spans * 8 + g8) * kPer * 2;
+  const uint8_t* zeros = ZERO ? a.zero + (tile * spans * 8 + g8) * kPer * 2 : nullptr;
   // A token past the last is read as the last: its column of the results is dropped.
   const char* xs[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
     xs[j] = static_cast<const char*>(a.x) + (m0 + min((int64_t)(8 * j + g8), M - 1)) * a.ldx * 2 + 16 * t4;
 
-  float acc[R][NB][4] = {};
-  Span<GROUP, ZERO> span[U][R];
+  float acc[NB][4] = {};
+  Span<GROUP, ZERO> span[U];
   uint4 x[U][kTiles][2][NB];
   const int64_t whole = bytes / (kSpan * 2);  // spans that x has all of
   int64_t s = (int64_t)warp * U;
   for (; s + U <= whole; s += kWarps * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) span[u][r].load(data[r], scales[r], zeros[r], s + u);
+      span[u].load(data, scales, zeros, s + u);
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -166,9 +164,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_i4(I4Args a) {
           for (int j = 0; j < NB; ++j) x[u][i][p][j] = row_piece<VEC>(xs[j], (s + u) * kSpan * 2 + 128 * i + 64 * p, 16);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < R; ++r) span[u][r].template multiply<E, NB>(acc[r], x[u]);
+    for (int u = 0; u < U; ++u) span[u].template multiply<E, NB>(acc, x[u]);
   }
   for (int u = 0; u < U && s + u < spans; ++u) {
 #pragma unroll
@@ -180,126 +176,26 @@ __global__ void __launch_bounds__(kThreads) k_linear_i4(I4Args a) {
           const int64_t k = (s + u) * kSpan * 2 + 128 * i + 64 * p;
           x[0][i][p][j] = row_piece<VEC>(xs[j], k, bytes - k - 16 * t4);
         }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      span[0][r].load(data[r], scales[r], zeros[r], s + u);
-      span[0][r].template multiply<E, NB>(acc[r], x[0]);
-    }
+    span[0].load(data, scales, zeros, s + u);
+    span[0].template multiply<E, NB>(acc, x[0]);
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (r) __syncthreads();
-#pragma unroll
-    for (int j = 0; j < NB; ++j) part[warp][j][lane] = make_float4(acc[r][j][0], acc[r][j][1], acc[r][j][2], acc[r][j][3]);
-    __syncthreads();
-    if (warp >= NB) continue;
-    float v[4] = {};
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const float4 p = part[i][warp][lane];
-      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t m = 8 * warp + 2 * t4 + c, n = (tile0 + r) * 16 + g8 + 8 * h;
-        if (m < M && n < a.N) static_cast<uint16_t*>(a.y)[(m0 + m) * a.ldy + n] = (uint16_t)E::from_f32(v[2 * h + c]);
-      }
-  }
-}
-
-// Many channels, tokens whose rows of x fit in shared memory: a CTA walks over tiles, every warp with the
-// same KW * 64 k of each (`passes` such places, where k is longer), so that x is
-// laid out once, and as soon as a register of weights has been used the next tile's are
-// loaded into it: loads are in flight while products are made and sums joined.
-template <int NB>
-constexpr int kWalkThreads = NB == 1 ? 1024 : 768;
-
-template <class E, int GROUP, bool ZERO, int NB, int KW>
-__global__ void __launch_bounds__(kWalkThreads<NB>) k_linear_i4_walk(I4Args a, int passes, int ldx) {
-  constexpr int kSpan = span_of(GROUP), kPer = groups_in(GROUP), kTiles = kSpan / 64, kSpans = KW / kTiles;
-  extern __shared__ __align__(16) char smem[];
-  pdl_enter();
-  const int warps = (int)blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
-  const int spans = (int)a.spans, M = (int)a.M;
-  const int64_t tiles = (a.N + 15) / 16;
-  float4* part = reinterpret_cast<float4*>(smem + (int64_t)M * ldx);  // [2][warps][NB][32]
-
-  Span<GROUP, ZERO> now[kSpans];
-  // The spans of a tile's pass that are this warp's.
-  const auto load = [&](int i, int64_t tile, int pass) {
-    const int s = (pass * warps + warp) * kSpans + i;
-    if (tile < tiles && s < spans) {
-      now[i].load(reinterpret_cast<const uint4*>(a.data) + tile * spans * kTiles * 32 + lane,
-                  static_cast<const uint16_t*>(a.scale) + (tile * spans * 8 + g8) * kPer * 2,
-                  a.zero + (tile * spans * 8 + g8) * kPer * 2, s);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < kSpans; ++i) load(i, blockIdx.x, 0);
-
-  // x, each row up to a whole span with zeros behind.
-  const int pieces = spans * kSpan / 8;
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx % 8 == 0;
-  for (int i = threadIdx.x; i < M * pieces; i += (int)blockDim.x) {
-    const int m = i / pieces, k = i % pieces * 16;
-    const char* row = static_cast<const char*>(a.x) + m * a.ldx * 2;
-    *reinterpret_cast<uint4*>(smem + m * ldx + k) = vec ? row_piece<true>(row, k, a.K * 2 - k) : row_piece<false>(row, k, a.K * 2 - k);
-  }
+  for (int j = 0; j < NB; ++j) part[warp][j][lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
   __syncthreads();
-  const char* xs[NB];
+  if (warp >= NB) return;
+  float v[4] = {};
 #pragma unroll
-  for (int j = 0; j < NB; ++j) xs[j] = smem + min(8 * j + g8, M - 1) * ldx + 16 * t4;
-
-  float acc[NB][4] = {};
-  int pass = 0, side = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles;) {
-    const bool last = pass == passes - 1;
-    const int64_t next_tile = last ? tile + gridDim.x : tile;
-    const int next_pass = last ? 0 : pass + 1;
-#pragma unroll
-    for (int i = 0; i < kSpans; ++i) {
-      const int s = (pass * warps + warp) * kSpans + i;
-      if (s < spans) {
-        uint4 x[kTiles][2][NB];
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int j = 0; j < NB; ++j) x[t][p][j] = *reinterpret_cast<const uint4*>(xs[j] + s * kSpan * 2 + 128 * t + 64 * p);
-        now[i].template multiply<E, NB>(acc, x);
-      }
-      load(i, next_tile, next_pass);
-    }
-    if (last) {
-      float4* const mine = part + (side * warps + warp) * NB * 32;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        mine[j * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-      }
-      __syncthreads();
-      for (int b = warp; b < NB; b += warps) {
-        float v[4] = {};
-#pragma unroll 4
-        for (int i = 0; i < warps; ++i) {
-          const float4 q = part[((side * warps + i) * NB + b) * 32 + lane];
-          v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t m = 8 * b + 2 * t4 + c, n = tile * 16 + g8 + 8 * h;
-            if (m < M && n < a.N) static_cast<uint16_t*>(a.y)[m * a.ldy + n] = (uint16_t)E::from_f32(v[2 * h + c]);
-          }
-      }
-      side ^= 1;  // the other half is written next: what is read here is done by the barrier after that
-    }
-    tile = next_tile, pass = next_pass;
+  for (int i = 0; i < kWarps; ++i) {
+    const float4 p = part[i][warp][lane];
+    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
   }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t m = 8 * warp + 2 * t4 + c, n = tile * 16 + g8 + 8 * h;
+      if (m < M && n < a.N) static_cast<uint16_t*>(a.y)[(m0 + m) * a.ldy + n] = (uint16_t)E::from_f32(v[2 * h + c]);
+    }
 }
 
 // One lane's 16 bytes of a tile; get(n, k): the whole number at channel n and k.
@@ -404,40 +300,22 @@ unsigned grid_for(int64_t items, int64_t per, int num_sms) {
 }
 
 template <class E, int GROUP, bool ZERO>
-cudaError_t linear(const I4Args& a, int num_sms, cudaStream_t s) {
+cudaError_t linear(const I4Args& a, cudaStream_t s) {
   const int64_t tiles = (a.N + 15) / 16, runs = (a.M + 31) / 32;
-  if (tiles > 0x7FFFFFFF || runs > 65535) return cudaErrorInvalidConfiguration;
   const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx % 8 == 0;
-  static const int force = getenv("I4_R") ? atoi(getenv("I4_R")) : 1;
-  static const int walk = getenv("I4_WALK") ? atoi(getenv("I4_WALK")) : 4;
-  if (walk && a.M <= 16) {
-    const int NB = a.M <= 8 ? 1 : 2, KW = walk, ks = KW / (span_of(GROUP) / 64), most = NB == 1 ? 32 : 24;
-    const int64_t need = (a.spans + ks - 1) / ks, passes = (need + most - 1) / most, warps = (need + passes - 1) / passes;
-    const int64_t ldx = a.spans * span_of(GROUP) * 2 + 64, smem = a.M * ldx + 2 * warps * NB * 512;
-    if (smem <= 200 * 1024) {
-      int64_t per_sm = most / warps;
-      if (per_sm * (smem + 1024) > 228 * 1024) per_sm = 228 * 1024 / (smem + 1024);
-      const int64_t grid = tiles < per_sm * num_sms ? tiles : per_sm * num_sms;
-      auto* k = KW == 4 ? (NB == 1 ? k_linear_i4_walk<E, GROUP, ZERO, 1, 4> : k_linear_i4_walk<E, GROUP, ZERO, 2, 4>)
-                        : (NB == 1 ? k_linear_i4_walk<E, GROUP, ZERO, 1, 2> : k_linear_i4_walk<E, GROUP, ZERO, 2, 2>);
-      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-      return launch_op(k, dim3((unsigned)grid), (int)warps * 32, (size_t)smem, 1, s, a, (int)passes, (int)ldx);
-    }
-  }
-#define AR_I4_TOKENS(R, VEC) \
-  (a.M <= 8 ? k_linear_i4<E, GROUP, ZERO, 1, R, VEC> : a.M <= 16 ? k_linear_i4<E, GROUP, ZERO, 2, R, VEC> : k_linear_i4<E, GROUP, ZERO, 4, R, VEC>)
-  auto* k = force == 2 ? (vec ? AR_I4_TOKENS(2, true) : AR_I4_TOKENS(2, false)) : (vec ? AR_I4_TOKENS(1, true) : AR_I4_TOKENS(1, false));
+#define AR_I4_TOKENS(VEC) \
+  (a.M <= 8 ? k_linear_i4<E, GROUP, ZERO, 1, VEC> : a.M <= 16 ? k_linear_i4<E, GROUP, ZERO, 2, VEC> : k_linear_i4<E, GROUP, ZERO, 4, VEC>)
+  auto* k = vec ? AR_I4_TOKENS(true) : AR_I4_TOKENS(false);
 #undef AR_I4_TOKENS
-  return launch_op(k, dim3((unsigned)((tiles + force - 1) / force), (unsigned)runs), kThreads, 0, 1, s, a);
+  return launch_op(k, dim3((unsigned)tiles, (unsigned)runs), kThreads, 0, 1, s, a);
 }
 
 template <class E>
-cudaError_t linear_group(const I4Args& a, int group, int num_sms, cudaStream_t s) {
+cudaError_t linear_group(const I4Args& a, int group, cudaStream_t s) {
   switch (group) {
-    case 32: return a.zero ? linear<E, 32, true>(a, num_sms, s) : linear<E, 32, false>(a, num_sms, s);
-    case 64: return a.zero ? linear<E, 64, true>(a, num_sms, s) : linear<E, 64, false>(a, num_sms, s);
-    default: return a.zero ? linear<E, 128, true>(a, num_sms, s) : linear<E, 128, false>(a, num_sms, s);
+    case 32: return a.zero ? linear<E, 32, true>(a, s) : linear<E, 32, false>(a, s);
+    case 64: return a.zero ? linear<E, 64, true>(a, s) : linear<E, 64, false>(a, s);
+    default: return a.zero ? linear<E, 128, true>(a, s) : linear<E, 128, false>(a, s);
   }
 }
 
@@ -445,8 +323,8 @@ cudaError_t linear_group(const I4Args& a, int group, int num_sms, cudaStream_t s
 
 int i4_span(int group) { return span_of(group); }
 
-cudaError_t launch_linear_i4(int dtype, int group, const I4Args& a, int num_sms, cudaStream_t s) {
-  return dtype == AR_BF16 ? linear_group<Bf16>(a, group, num_sms, s) : linear_group<F16>(a, group, num_sms, s);
+cudaError_t launch_linear_i4(int dtype, int group, const I4Args& a, cudaStream_t s) {
+  return dtype == AR_BF16 ? linear_group<Bf16>(a, group, s) : linear_group<F16>(a, group, s);
 }
 
 cudaError_t launch_pack_i4(const I4Pack& a, int num_sms, cudaStream_t s) {

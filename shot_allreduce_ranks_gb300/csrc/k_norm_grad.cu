@@ -433,10 +433,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
       for (int i = 0; i < N; ++i) {
         if (!c.has(i)) continue;
         const float t = q ? sum[c.at(i)] + v[i] : v[i];
-        if (q == groups - 1)
-          a.part[k][(int64_t)blockIdx.x * a.cols + c.at(i)] = t;
-        else
+        if (q < groups - 1)
           sum[c.at(i)] = t;
+        else if (a.direct)
+          put<E>(a.sum[k], c.at(i), t);
+        else
+          a.part[k][(int64_t)blockIdx.x * a.cols + c.at(i)] = t;
       }
     }
   };
@@ -515,7 +517,11 @@ cudaError_t norm_grad_rows_kind(NormGradArgs& a, int num_sms, cudaStream_t s) {
   smem = a.sums_at + sums;
   int64_t want = (int64_t)per_sm * num_sms;
   const int64_t most = norm_parts(a.rows, a.cols);
-  deal(a, want < most ? want : most);
+  if (want > most) want = most;
+  // A CTA that takes two rows a group costs less than joining two CTAs' parts (a launch, 3 us).
+  if (a.gate_rows == 1 && a.rows <= 2 * (cta / T)) want = 1;
+  deal(a, want);
+  a.direct = a.ctas == 1;
   const auto go = [&](auto* k) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     return e != cudaSuccess ? e : launch_op(k, dim3((unsigned)a.ctas), cta, (size_t)smem, 1, s, a, T, stages);
@@ -567,6 +573,7 @@ cudaError_t norm_grad(NormGradArgs& a, int num_sms, cudaStream_t s) {
   int64_t deepest = 1;
   for (int k = 0; k < kNormSums; ++k) {
     if (!a.sum[k] || (k == kSumGate && !a.split)) continue;  // those gates are whole already
+    if (a.direct) continue;
     const bool gate = k == kSumGate;
     j.part[n] = a.part[k], j.sum[n] = a.sum[k];
     j.count[n] = gate ? a.split : a.ctas, j.rows[n] = gate ? a.gate_rows : 1, j.ld[n] = gate ? a.lddg : 0;

@@ -137,13 +137,11 @@ ar_status_t ar_linear_i4(const void* x, size_t ldx, const void* data, const void
   if (bad_i4_arrays(data, packed_scale, packed_zero) || bad_matrix(x, tokens, in, ldx) || misaligned(x, 2) ||
       bad_matrix(y, tokens, out, ldy) || misaligned(y, 2))
     return AR_ERR_INVALID_ARG;
-  int sms = 0;
-  if (ar_status_t st = current_sms(&sms)) return st;
   I4Args a = {};
   a.x = x, a.data = data, a.scale = packed_scale, a.zero = static_cast<const uint8_t*>(packed_zero), a.y = y;
   a.ldx = (int64_t)ldx, a.ldy = (int64_t)ldy, a.M = (int64_t)tokens, a.N = (int64_t)out, a.K = (int64_t)in;
   a.spans = (int64_t)i4_spans(in, group);
-  return cuda_status(launch_linear_i4(dtype, group, a, sms, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_linear_i4(dtype, group, a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens) {

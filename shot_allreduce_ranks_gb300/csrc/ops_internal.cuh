@@ -168,6 +168,7 @@ struct NormGradArgs {
   // or (split = 0) with several whole gate rows to each of `ctas` CTAs.
   int64_t ctas, split, chunk;  // chunk: rows of a CTA where split > 0
   int sums_at;  // bytes of shared memory before the sums that are kept there
+  int direct;   // the one CTA writes the sums itself: there are no parts to join
   float eps, alpha, offset;
   int layer;
 };
@@ -184,7 +185,7 @@ struct I4Args {
   void* y;
   int64_t ldx, ldy, M, N, K, spans;
 };
-cudaError_t launch_linear_i4(int dtype, int group, const I4Args& a, int num_sms, cudaStream_t s);
+cudaError_t launch_linear_i4(int dtype, int group, const I4Args& a, cudaStream_t s);
 int i4_span(int group);
 
 struct I4Pack {
