@@ -748,7 +748,8 @@ typedef struct {
   int top_k;         /* 1 .. the smaller of experts and AR_MAX_TOP_K */
   int normalize;     /* non-zero: a token's weights are made to sum to 1 */
   size_t hidden;     /* columns of x and of out (K), at most 2^22 */
-  size_t width;      /* rows of an expert's gate and up projections (F), at most 2^22 */
+  size_t width;      /* rows of an expert's gate and up projections (F), at most 2^22;
+                        local_experts * hidden * width below 2^40 */
 } ar_moe_t;
 
 /* ar_moe_ffn --

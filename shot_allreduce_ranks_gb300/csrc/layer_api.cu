@@ -52,7 +52,9 @@ ar_status_t check_moe(const ar_moe_t* m) {
       m->first_expert > m->experts - m->local_experts || m->top_k < 1 || m->top_k > AR_MAX_TOP_K ||
       m->top_k > m->experts || m->hidden < 1 || m->hidden > kMaxInner || m->width < 1 || m->width > kMaxInner)
     return AR_ERR_INVALID_ARG;
-  return AR_OK;
+  // The kernels count a layer's pieces (16 rows of 64) in 32 bits: 2^31 of them are 4 TB of weights.
+  const size_t most = (size_t)m->local_experts, pieces = ((m->width + 63) / 64) * ((m->hidden + 63) / 64) * 8;
+  return most * pieces >> 31 ? AR_ERR_INVALID_ARG : AR_OK;
 }
 
 }  // namespace
