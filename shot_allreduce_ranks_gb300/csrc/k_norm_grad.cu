@@ -1,5 +1,13 @@
 // Gradients of the norms before and after a block, its gate and the residual
-// (formulas in include/ar.h).
+// (formulas in include/ar.h): every matrix is read and written once.  With hat = N(r) and
+// d = dy (offset + weight), the gradient of the norm is factor (d - mean d - hat mean(d hat)), the first
+// mean 0 for the mean square, whose two sums, of r^2 and of d r, are therefore one joint sum.
+//
+// Measured on one GB300: 8192 x 8192 bf16 105 us (537 MB: 75% of the copy rate; the instructions for a row bind),
+// 8192 x 4096 62, 4096 x 8192 fp32 88 (90%), 440 x 5120 12.2, one row 5.0. With a norm after the block 8192 x 4096
+// 103, and 8192 x 8192 317: a thread of 1,024 has too few registers and reads vectors and rows again. 680 x
+// 5120 fp32 with every part 50 (floor 12), likewise: 640 threads of 96 registers spill, and shared memory holds one
+// row ahead. 8192 x 1031 fp16 with a mean and biases 74.
 #include "norm_device.cuh"
 
 namespace ar {
@@ -90,6 +98,8 @@ __global__ void __launch_bounds__(kAnyThreads) k_norm_grad_any(NormGradArgs a) {
 
 // ---------------------------------------------------------------------------
 // Gradients of rows that T threads hold in registers and shared memory.
+//
+// (A kernel for any row, which read it again for every statistic, took 1,238 us at 8192 x 8192.)
 //
 // The columns' sums over rows stay in a thread's registers while its CTA walks
 // its rows; a CTA of short rows has several groups of T threads, each with rows of
@@ -246,6 +256,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
       copies_wait<0>();
   };
   for (int i = 0; i < stages - 1; ++i) fetch(first + i * step, i);
+  // The gate's row that a row is of, and where that one's rows end: all of a CTA's rows are of one gate row, or they follow one another.
+  int64_t gate_row = 0, gate_end = 0;
+  if (ALL && a.gate) gate_row = first / a.gate_run, gate_end = (gate_row + 1) * a.gate_run;
   int stage = 0, parity = 0;
   for (int64_t row = first; row < last; row += step) {
     const int64_t ahead = row + (stages - 1) * step;
@@ -326,7 +339,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
       }
     }
     // What a thread of a large CTA has no registers for it reads again.
-    constexpr bool kAgain = FULL && MAXT > 512;
+    constexpr bool kAgain = FULL && MAXT > 640;
     if constexpr (kAgain) {
       if (has_weight) {
         get(kR, row, stage, r);
@@ -359,7 +372,6 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
     }
     if constexpr (kAgain) get(kX, row, stage, x);
     if constexpr (ALL) {
-      const int64_t gate_row = a.gate ? row / a.gate_run : 0;
       if (a.gate) {
         float v[N];
         if (a.after_weight) {
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
           for (int i = 0; i < N; ++i) v[i] = g[i] * x[i];
         }
         add(kSumGate, v);
-        if (!a.split && (row + 1) % a.gate_run == 0) {
+        if (!a.split && row + 1 == gate_end) {
           total(kSumGate, v);
           if (a.sum[kSumGate]) c.store(a.sum[kSumGate], gate_row * a.lddg, v);
           clear(kSumGate);
@@ -384,6 +396,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
         c.load_shared(a.gate, gate_row * a.ldg, (a.gate_rows - 1) * a.ldg + a.cols, w);
 #pragma unroll
         for (int i = 0; i < N; ++i) g[i] *= w[i];
+        if (!a.split && row + 1 == gate_end) ++gate_row, gate_end += a.gate_run;
       }
     }
     if constexpr (FULL) {
@@ -530,7 +543,7 @@ cudaError_t norm_grad_rows_kind(NormGradArgs& a, int num_sms, cudaStream_t s) {
     if (cta <= 256) return go(k_norm_grad_rows<E, N, 256, BRANCH ? 2 : 4, VEC, LAYER, BRANCH, BIAS>);
     if (cta <= 512) return go(k_norm_grad_rows<E, N, 512, BRANCH ? 1 : 2, VEC, LAYER, BRANCH, BIAS>);
     if constexpr (BRANCH != kNothing)
-      if (cta <= 768) return go(k_norm_grad_rows<E, N, 768, 1, VEC, LAYER, BRANCH, BIAS>);
+      if (cta <= 640) return go(k_norm_grad_rows<E, N, 640, 1, VEC, LAYER, BRANCH, BIAS>);
   }
   return go(k_norm_grad_rows<E, N, 1024, 1, VEC, LAYER, BRANCH, BIAS>);
 }

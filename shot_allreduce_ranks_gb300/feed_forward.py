@@ -3,7 +3,9 @@
 ``GatedFFN`` is one rank's shard of the gated projections with its gradients,
 ``linear_i8`` (with ``quantize_rows``) the down projection in 8-bit integers,
 ``dropout`` the step after the sum, its mask drawn from the elements' places
-and never stored.  Matrices are 2-D CUDA tensors whose rows are contiguous
+and never stored; ``residual_norm`` the norms before and after a block with its
+gate and the residual, ``linear_i4`` products of a few tokens with 4-bit weights,
+``moe_ffn`` a layer of gated experts for a few tokens.  Matrices are 2-D CUDA tensors whose rows are contiguous
 (any row stride).  Calls are asynchronous on the current (or given) stream of
 the tensors' device, which also owns the outputs that a call allocates; a
 given stream of another device is refused.  torch's differentiation does not
