@@ -4,10 +4,10 @@
 // mean 0 for the mean square, whose two sums, of r^2 and of d r, are therefore one joint sum.
 //
 // Measured on one GB300: 8192 x 8192 bf16 105 us (537 MB: 75% of the copy rate; the instructions for a row bind),
-// 8192 x 4096 62, 4096 x 8192 fp32 88 (90%), 440 x 5120 12.2, one row 5.0. With a norm after the block 8192 x 4096
+// 8192 x 4096 60, 4096 x 8192 fp32 87 (91%), 440 x 5120 11.7, one row 5.0. With a norm after the block 8192 x 4096
 // 103, and 8192 x 8192 317: a thread of 1,024 has too few registers and reads vectors and rows again. 680 x
 // 5120 fp32 with every part 50 (floor 12), likewise: 640 threads of 96 registers spill, and shared memory holds one
-// row ahead. 8192 x 1031 fp16 with a mean and biases 74.
+// row ahead. 8192 x 1031 bf16 with a mean and biases 71.
 #include "norm_device.cuh"
 
 namespace ar {
@@ -105,8 +105,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_norm_grad_any(NormGradArgs a) {
 // its rows; a CTA of short rows has several groups of T threads, each with rows of
 // its own.  A row's statistics and the two means that the gradient wants come out of one
 // joint sum (mean square) or two (differences from the mean), and one more for the norm
-// after the block.  VEC: the next row is copied to shared memory meanwhile; a
-// thread reads what it copied itself.
+// after the block.  The next rows are copied to shared memory meanwhile, one to three of them.
 constexpr int kGroupThreads = 256;  // of a CTA of short rows
 
 __host__ __device__ constexpr int row_threads(int64_t cols, int n) { return (int)((cols + 32 * n - 1) / (32 * n) * 32); }
@@ -475,7 +474,7 @@ struct JoinArgs {
   int64_t count[kNormSums], rows[kNormSums], ld[kNormSums];  // parts of an output row; output rows
   int64_t cols;
 };
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 
 template <class E>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_norm_join(JoinArgs a) {

@@ -4,7 +4,7 @@ may be off, for the tests.
 Bounds are first-order sums of the roundings on the way, E = 2^-24 being half a step of fp32 relative to the value.  A
 sum over a row is made by at least 32 threads (256 above 2,048 columns), each adding its own elements one by one, and
 joined by at most 10 further additions, so a partial sum passes through at most depth(cols) roundings.  A sum over rows
-is made by up to 200 CTAs or more, each over its own rows, and their parts by eight warps one by one.
+is made by up to 200 CTAs or more, each over its own rows, and their parts by sixteen warps one by one.
 """
 import torch
 
