@@ -766,10 +766,13 @@ typedef struct {
  * row with a NaN or +infinity has NaN weights.  With e = expert[t, j]:
  *   h   = act(x[t] Wgate_e^T) * (x[t] Wup_e^T)
  *   out[t] = sum over the j whose e this rank holds of weight[t, j] * (h Wdown_e^T)
- * and zeros where it holds none.  Sums, the activation and the weighting are fp32; h is rounded
- * to dtype between the two products, out once.  Each matrix of an expert with tokens is read
+ * and zeros where it holds none.  Sums, the activation and the weighting are fp32, out is rounded
+ * once.  Between the two products h is held in dtype: as the sum of two numbers where scratch has
+ * ar_moe_two_part_scratch_bytes, whose error is below that of out's rounding, or else rounded to
+ * one, which makes the result's error 1.4 times that of its own rounding.  In AR_FP16 an |h| of
+ * 65,520 or more is an infinity either way.  Each matrix of an expert with tokens is read
  * once for every AR_FEW_TOKENS tokens (more are taken in runs of that many).
- *   scratch  device memory on 16 bytes, ar_moe_scratch_bytes of it, not shared
+ *   scratch  device memory on 16 bytes, at least ar_moe_scratch_bytes of it, not shared
  *            with a call that may run at the same time
  * tokens = 0 returns AR_OK without a launch.  Asynchronous on `stream`; out
  * overlaps no input.  Errors: AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED (a dtype),
@@ -780,8 +783,10 @@ ar_status_t ar_moe_ffn(const ar_moe_t* m, const void* x, size_t ldx, const void*
                        int32_t* expert, float* weight, size_t tokens, void* scratch,
                        size_t scratch_bytes, void* stream);
 
-/* ar_moe_scratch_bytes -- see ar_moe_ffn; 0 for what it refuses.  Host-only. */
+/* ar_moe_scratch_bytes, ar_moe_two_part_scratch_bytes -- see ar_moe_ffn; 0 for what it refuses.
+ * Host-only. */
 size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens);
+size_t ar_moe_two_part_scratch_bytes(const ar_moe_t* m, size_t tokens);
 
 /* ar_ops_get_device_status -- wait for `stream` to drain, then read and clear
  * the feed-forward operators' error word on the current device: AR_ERR_TIMEOUT

@@ -130,6 +130,7 @@ PROTOTYPES = {
     "ar_moe_ffn": (_ST, [ctypes.POINTER(ArMoe), _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, _SZ, _VP, _SZ, _SZ,
                          _VP, _SZ, _VP, _VP, _SZ, _VP, _SZ, _VP]),
     "ar_moe_scratch_bytes": (_SZ, [ctypes.POINTER(ArMoe), _SZ]),
+    "ar_moe_two_part_scratch_bytes": (_SZ, [ctypes.POINTER(ArMoe), _SZ]),
 }
 
 AR_NOALLOC_SCRATCH_BYTES = 32 << 20

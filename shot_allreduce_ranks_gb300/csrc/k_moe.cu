@@ -9,8 +9,8 @@
 // a warp waits for nothing but its own copies.  A CTA finds the routing for itself from the
 // logits: a few hundred instructions, against a kernel of its own and its launch.
 //
-// Measured on one GB300: 32 tokens through 8 of 64 experts 2048 -> 1024 155-163 us (794 MB: 72-76% of the copy
-// rate), 1 token through 4 of 32 experts 5120 -> 1736 48.5 (213 MB: 65%), 9 tokens on half of 16 experts 2048 -> 1032 27.5 (71
+// Measured on one GB300: 32 tokens through 8 of 64 experts 2048 -> 1024 166 us (794 MB: 70% of the copy
+// rate), 1 token through 4 of 32 experts 5120 -> 1736 49.8 (213 MB: 63%), 9 tokens on half of 16 experts 2048 -> 1032 28 (71
 // MB). While it runs each loop reads at the copy rate (77 us for 520 MB, 20 for 142); what is left is the
 // routing (2.3 us at one token, 4.2 at 32), the first pieces' way (1.7), the joining of sums (2
 // to 5) and the start of the second kernel, whose registers leave no room beside the first's. Eight warps with
@@ -369,7 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
       const int64_t row = t * m.top_k + tab.choice[place * kTokens + t];
       // The row's end, up to a whole group, is read with it: zeros.
       const float h = f < m.width ? act_value<ACT>(sums[c]) * sums[c + 2] : 0.0f;
-      static_cast<uint16_t*>(m.h)[row * m.ldh + f] = (uint16_t)E::from_f32(h);
+      const uint32_t rounded = E::from_f32(h);
+      static_cast<uint16_t*>(m.h)[row * m.ldh + f] = (uint16_t)rounded;
+      // What the rounding left goes to the second product beside it, so that 16 (bfloat16) or 22 (float16) bits of h
+      // reach the result; an infinity has nothing left, for a NaN beside it would spoil an infinite sum.
+      if (m.h_rest) {
+        const float there = E::to_f32(rounded);
+        static_cast<uint16_t*>(m.h_rest)[row * m.ldh + f] = fabsf(there) < INFINITY ? (uint16_t)E::from_f32(h - there) : (uint16_t)0;
+      }
     }
   };
 
@@ -450,7 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_gated(MoeArgs m) {
 // sums of the tile in fp32, and those are joined at the end, in the warps' order.  A
 // tile that lies on several CTAs is left in parts, which the CTA that finishes last
 // adds in their order: nothing is waited for, and every call gives the same bits.
-template <class E, bool VEC>
+//
+// TWO: h is the sum of two numbers, each of which meets the weights in registers; one call of 1 token 49.8 us (with h
+// rounded to one 49.0), of 32 tokens 167 (161), of 32 through 8 experts 56 (50).
+template <class E, bool VEC, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   extern __shared__ __align__(16) char smem[];
   char* const tables_at = smem + kRingBytes;
@@ -476,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   const char* bd = static_cast<const char*>(m.w_down);
   const int64_t extent = ((m.local - 1) * m.esd + (m.hidden - 1) * m.ldd + m.width) * 2;
   const char* h = static_cast<const char*>(m.h);
+  const int64_t to_rest = static_cast<const char*>(m.h_rest) - h;  // where TWO
   uint16_t* const out = static_cast<uint16_t*>(m.out);
 
   if (units == 0) {  // no token has an expert here
@@ -517,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
     __syncwarp();
     const auto run = [&](auto blocks) {
       constexpr int NB = decltype(blocks)::value;
+      constexpr bool EARLY = TWO && NB <= 2;  // four blocks leave no registers to load both parts ahead
       // A token past the last is read as the last: its column of the sums is dropped.
       const char* xs[NB];
 #pragma unroll
@@ -526,19 +538,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
       }
       float acc[NB][4] = {};
       for (int p = p0; p < p1; ++p) {
-        uint4 x[kSteps][NB];
+        uint4 x[kSteps][NB], rest[EARLY ? kSteps : 1][NB];
         const int left = bytes - p * kPieceBytes - 16 * t4;
+        const auto load = [&](uint4(&v)[NB], int i, int64_t from) {  // rows of h start on 16 bytes and end in zeros
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-          for (int j = 0; j < NB; ++j) {  // rows of h start on 16 bytes and end in zeros
-            x[i][j] = make_uint4(0, 0, 0, 0);
-            if (left > 64 * i) x[i][j] = *reinterpret_cast<const uint4*>(xs[j] + 64 * i);
+          for (int j = 0; j < NB; ++j) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (left > 64 * i) v[j] = *reinterpret_cast<const uint4*>(xs[j] + from + 64 * i);
           }
+        };
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          load(x[i], i, 0);
+          if (EARLY) load(rest[EARLY ? i : 0], i, to_rest);
+        }
         fetch(kStages - 1);
         Ring::wait();
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) multiply<E, NB>(acc, ring.row(i, 0), ring.row(i, 1), x[i]);
+        for (int i = 0; i < kSteps; ++i) {
+          if (TWO && !EARLY) load(rest[0], i, to_rest);
+          const uint4 a = ring.row(i, 0), b = ring.row(i, 1);
+          multiply<E, NB>(acc, a, b, x[i]);
+          if (TWO) multiply<E, NB>(acc, a, b, rest[EARLY ? i : 0]);
+        }
         ring.advance();
 #pragma unroll
         for (int j = 0; j < NB; ++j) xs[j] += kPieceBytes;
@@ -645,7 +667,9 @@ cudaError_t moe(const MoeArgs& m, int num_sms, cudaStream_t s) {
   if (items * ((m.hidden + 63) / 64) >> 31 || most * ((m.width + 63) / 64) * ((m.hidden + 15) / 16) >> 31) return cudaErrorInvalidConfiguration;
   e = launch_op(k, dim3((unsigned)(items < slots ? items : slots)), kThreads, gated, 1, s, m);
   if (e != cudaSuccess) return e;
-  auto* d = on16(m.w_down) && (m.ldd | m.esd) % 8 == 0 ? k_moe_down<E, true> : k_moe_down<E, false>;
+  const bool vec_down = on16(m.w_down) && (m.ldd | m.esd) % 8 == 0;
+  auto* d = m.h_rest ? (vec_down ? k_moe_down<E, true, true> : k_moe_down<E, false, true>)
+                     : (vec_down ? k_moe_down<E, true, false> : k_moe_down<E, false, false>);
   e = cudaFuncSetAttribute(d, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)down);
   if (e != cudaSuccess) return e;
   return launch_op(d, dim3((unsigned)slots), kThreads, down, 1, s, m);
@@ -653,15 +677,17 @@ cudaError_t moe(const MoeArgs& m, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-size_t moe_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t hidden, MoeArgs* m, char* base) {
+size_t moe_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t hidden, bool two_parts, MoeArgs* m, char* base) {
   const size_t ldh = (size_t)(width + 7) / 8 * 8, t = tokens < kTokens ? tokens : kTokens;
   const size_t h = (t * top_k * ldh * 2 + 15) / 16 * 16, done = ((size_t)(hidden + 15) / 16 * 4 + 15) / 16 * 16;
+  const size_t all = h + done + (size_t)kMostSms * 2 * kTokens * 16 * 4;
   if (m) {
     m->h = base, m->ldh = (int64_t)ldh;
     m->done = reinterpret_cast<uint32_t*>(base + h);
     m->parts = reinterpret_cast<float*>(base + h + done);
+    m->h_rest = two_parts ? base + all : nullptr;
   }
-  return h + done + (size_t)kMostSms * 2 * kTokens * 16 * 4;
+  return two_parts ? all + h : all;
 }
 
 cudaError_t launch_moe(int dtype, int act, const MoeArgs& m, int num_sms, cudaStream_t s) {

@@ -57,6 +57,12 @@ ar_status_t check_moe(const ar_moe_t* m) {
   return most * pieces >> 31 ? AR_ERR_INVALID_ARG : AR_OK;
 }
 
+size_t moe_bytes(const ar_moe_t* m, size_t tokens, bool two_parts, MoeArgs* a = nullptr, void* base = nullptr) {
+  if (check_moe(m) || tokens == 0) return 0;
+  const size_t run = tokens < AR_FEW_TOKENS ? tokens : AR_FEW_TOKENS;
+  return moe_scratch((int64_t)run, m->top_k, (int64_t)m->width, (int64_t)m->hidden, two_parts, a, static_cast<char*>(base));
+}
+
 }  // namespace
 
 extern "C" {
@@ -146,10 +152,8 @@ ar_status_t ar_linear_i4(const void* x, size_t ldx, const void* data, const void
   return cuda_status(launch_linear_i4(dtype, group, a, static_cast<cudaStream_t>(stream)));
 }
 
-size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens) {
-  if (check_moe(m)) return 0;
-  return tokens ? moe_scratch((int64_t)(tokens < AR_FEW_TOKENS ? tokens : AR_FEW_TOKENS), m->top_k, (int64_t)m->width, (int64_t)m->hidden, nullptr, nullptr) : 0;
-}
+size_t ar_moe_scratch_bytes(const ar_moe_t* m, size_t tokens) { return moe_bytes(m, tokens, false); }
+size_t ar_moe_two_part_scratch_bytes(const ar_moe_t* m, size_t tokens) { return moe_bytes(m, tokens, true); }
 
 ar_status_t ar_moe_ffn(const ar_moe_t* m, const void* x, size_t ldx, const void* logits, size_t ldl,
                        const void* w_gate, const void* w_up, size_t ldw, size_t esw,
@@ -169,7 +173,7 @@ ar_status_t ar_moe_ffn(const ar_moe_t* m, const void* x, size_t ldx, const void*
   if (ar_status_t st = current_sms(&sms)) return st;
   MoeArgs a = {};
   a.w_gate = w_gate, a.w_up = w_up, a.w_down = w_down;
-  moe_scratch((int64_t)(tokens < AR_FEW_TOKENS ? tokens : AR_FEW_TOKENS), m->top_k, (int64_t)m->width, (int64_t)m->hidden, &a, static_cast<char*>(scratch));
+  moe_bytes(m, tokens, scratch_bytes >= moe_bytes(m, tokens, true), &a, scratch);
   a.ldx = (int64_t)ldx, a.ldl = (int64_t)ldl, a.ldw = (int64_t)ldw, a.esw = (int64_t)esw;
   a.ldd = (int64_t)ldd, a.esd = (int64_t)esd, a.ldo = (int64_t)ldo;
   a.hidden = (int64_t)K, a.width = (int64_t)F;

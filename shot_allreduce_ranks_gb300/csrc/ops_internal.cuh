@@ -225,6 +225,7 @@ cudaError_t launch_unpack_i4(int dtype, const I4Unpack& a, int num_sms, cudaStre
 struct MoeArgs {
   const void *x, *logits, *w_gate, *w_up, *w_down;
   void *h, *out;   // h: row t * top_k + j for choice j of token t, rows on 16 bytes
+  void* h_rest;    // like h: what h's rounding left; null where h is one number of 16 bits
   uint32_t* done;  // of each 16 columns of out: the parts that are there
   float* parts;    // two for every CTA, [AR_FEW_TOKENS][16]
   int32_t* out_expert;
@@ -233,8 +234,8 @@ struct MoeArgs {
   int64_t hidden, width;
   int tokens, experts, first, local, top_k, normalize, logits_dtype;
 };
-// The scratch memory's size, and (m not null) its pieces in place.
-size_t moe_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t hidden, MoeArgs* m, char* base);
+// The scratch memory's size, and (m not null) its pieces in place; two_parts: with h_rest, behind all else.
+size_t moe_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t hidden, bool two_parts, MoeArgs* m, char* base);
 cudaError_t launch_moe(int dtype, int act, const MoeArgs& m, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

@@ -693,7 +693,7 @@ PyObject* moe_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
       expert = at::empty({rows, top_k}, x.options().dtype(at::kInt));
       weight = at::empty({rows, top_k}, x.options().dtype(at::kFloat));
     }
-    const at::Tensor room = scratch(ar_moe_scratch_bytes(&m, (size_t)rows), x);
+    const at::Tensor room = scratch(ar_moe_two_part_scratch_bytes(&m, (size_t)rows), x);
     call("ar_moe_ffn", index, [&](void* s) {
       return ar_moe_ffn(&m, x.data_ptr(), ldx, logits.data_ptr(), ldl, wg.data_ptr(), wu.data_ptr(), ldw, esw, wd.data_ptr(), ldd,
                         esd, out.data_ptr(), ldo, static_cast<int32_t*>(address(expert)), static_cast<float*>(address(weight)),
