@@ -659,20 +659,19 @@ cudaError_t moe(const MoeArgs& m, int num_sms, cudaStream_t s) {
   const size_t blocks = m.tokens <= 8 ? 1 : m.tokens <= 16 ? 2 : 4;
   const size_t gated = kRingBytes + tables + kWarps * 2 * blocks * 512, down = kRingBytes + tables + (size_t)kWarps * 2 * m.tokens * 17 * 4;
   const bool vec = on16(m.x) && on16(m.w_gate) && on16(m.w_up) && (m.ldx | m.ldw | m.esw) % 8 == 0;
-  auto* k = vec ? k_moe_gated<E, ACT, true> : k_moe_gated<E, ACT, false>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gated);
-  if (e != cudaSuccess) return e;
   // The kernels count pieces in 32 bits.
   const int64_t slots = num_sms < kMostSms ? num_sms : kMostSms, items = most * strips;
   if (items * ((m.hidden + 63) / 64) >> 31 || most * ((m.width + 63) / 64) * ((m.hidden + 15) / 16) >> 31) return cudaErrorInvalidConfiguration;
-  e = launch_op(k, dim3((unsigned)(items < slots ? items : slots)), kThreads, gated, 1, s, m);
+  const dim3 grid((unsigned)(items < slots ? items : slots)), all((unsigned)slots);
+  const cudaError_t e = vec ? launch_raised<k_moe_gated<E, ACT, true>>(grid, kThreads, gated, s, m)
+                            : launch_raised<k_moe_gated<E, ACT, false>>(grid, kThreads, gated, s, m);
   if (e != cudaSuccess) return e;
   const bool vec_down = on16(m.w_down) && (m.ldd | m.esd) % 8 == 0;
-  auto* d = m.h_rest ? (vec_down ? k_moe_down<E, true, true> : k_moe_down<E, false, true>)
-                     : (vec_down ? k_moe_down<E, true, false> : k_moe_down<E, false, false>);
-  e = cudaFuncSetAttribute(d, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)down);
-  if (e != cudaSuccess) return e;
-  return launch_op(d, dim3((unsigned)slots), kThreads, down, 1, s, m);
+  if (m.h_rest)
+    return vec_down ? launch_raised<k_moe_down<E, true, true>>(all, kThreads, down, s, m)
+                    : launch_raised<k_moe_down<E, false, true>>(all, kThreads, down, s, m);
+  return vec_down ? launch_raised<k_moe_down<E, true, false>>(all, kThreads, down, s, m)
+                  : launch_raised<k_moe_down<E, false, false>>(all, kThreads, down, s, m);
 }
 
 }  // namespace

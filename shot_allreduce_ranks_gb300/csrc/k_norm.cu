@@ -211,11 +211,10 @@ cudaError_t norm_stream(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int64_t threads = (a.cols + 32 * N - 1) / (32 * N) * 32;
   const int cta = threads == 32 ? 128 : (int)threads, rows = threads == 32 ? 4 : 1;
   const size_t smem = (size_t)kStages * 2 * N * E::kBytes * cta;
-  auto* k = threads == 32 ? k_norm_stream<E, N, true> : k_norm_stream<E, N, false>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = (a.rows + rows - 1) / rows, most = 1024 / cta * (int64_t)num_sms;
-  return launch_op(k, dim3((unsigned)(grid < most ? grid : most)), cta, smem, 1, s, a);
+  const int64_t want = (a.rows + rows - 1) / rows, most = 1024 / cta * (int64_t)num_sms;
+  const dim3 grid((unsigned)(want < most ? want : most));
+  return threads == 32 ? launch_raised<k_norm_stream<E, N, true>>(grid, cta, smem, s, a)
+                       : launch_raised<k_norm_stream<E, N, false>>(grid, cta, smem, s, a);
 }
 
 template <class E>

@@ -534,17 +534,16 @@ cudaError_t norm_grad_rows_kind(NormGradArgs& a, int num_sms, cudaStream_t s) {
   if (a.gate_rows == 1 && a.rows <= 2 * (cta / T)) want = 1;
   deal(a, want);
   a.direct = a.ctas == 1;
-  const auto go = [&](auto* k) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    return e != cudaSuccess ? e : launch_op(k, dim3((unsigned)a.ctas), cta, (size_t)smem, 1, s, a, T, stages);
-  };
+  const dim3 grid((unsigned)a.ctas);
+#define AR_GRAD_ROWS(MAXT, MINB) launch_raised<k_norm_grad_rows<E, N, MAXT, MINB, VEC, LAYER, BRANCH, BIAS>>(grid, cta, (size_t)smem, s, a, T, stages)
   if constexpr (N == 8) {
-    if (cta <= 256) return go(k_norm_grad_rows<E, N, 256, BRANCH ? 2 : 4, VEC, LAYER, BRANCH, BIAS>);
-    if (cta <= 512) return go(k_norm_grad_rows<E, N, 512, BRANCH ? 1 : 2, VEC, LAYER, BRANCH, BIAS>);
+    if (cta <= 256) return AR_GRAD_ROWS(256, (BRANCH ? 2 : 4));
+    if (cta <= 512) return AR_GRAD_ROWS(512, (BRANCH ? 1 : 2));
     if constexpr (BRANCH != kNothing)
-      if (cta <= 640) return go(k_norm_grad_rows<E, N, 640, 1, VEC, LAYER, BRANCH, BIAS>);
+      if (cta <= 640) return AR_GRAD_ROWS(640, 1);
   }
-  return go(k_norm_grad_rows<E, N, 1024, 1, VEC, LAYER, BRANCH, BIAS>);
+  return AR_GRAD_ROWS(1024, 1);
+#undef AR_GRAD_ROWS
 }
 
 template <class E, int N, bool VEC, int BRANCH, bool BIAS>

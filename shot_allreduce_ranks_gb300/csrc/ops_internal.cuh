@@ -3,6 +3,8 @@
 // Their entry points and contracts are in include/ar.h.
 #pragma once
 
+#include <atomic>
+
 #include "ar_internal.cuh"
 
 namespace ar {
@@ -25,6 +27,27 @@ cudaError_t launch_op(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
     a.val.clusterDim.y = a.val.clusterDim.z = 1;
   }
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// The same for a kernel whose dynamic shared memory changes from call to call and may pass 48 KB.  The limit is
+// state of the kernel on the device, which calls from other host threads share: it is raised to all that
+// a block can have, once for each device, and never set to a call's own size.
+template <auto K, class... A>
+cudaError_t launch_raised(dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  static std::atomic<bool> raised[64];  // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes own;
+    int most = 0;
+    e = cudaFuncGetAttributes(&own, K);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)own.sharedSizeBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) raised[dev].store(true, std::memory_order_release);
+  }
+  return launch_op(K, grid, threads, smem, 1, s, args...);
 }
 
 // ---------------------------------------------------------------------------
