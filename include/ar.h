@@ -646,8 +646,9 @@ ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, cons
  *   dx, dresidual, dgate, dweight, dbias, dafter_weight, dafter_bias
  *        NULL: not computed.  dgate has the leading dimension lddg.
  * Statistics are taken again from x and r; sums are fp32, in an order that
- * depends on the sizes and the device alone; outputs are rounded once and
- * written, not added to.
+ * depends on the sizes, the device, which arrays are given and whether those that
+ * are read or written start their rows on 16 bytes, and on nothing else: a call
+ * repeated gives the same bits; outputs are rounded once and written, not added to.
  *   scratch  device memory on 16 bytes, of ar_residual_norm_scratch_bytes(rows,
  *            cols, how many of dgate, dweight, dbias, dafter_weight and
  *            dafter_bias are not NULL) bytes; NULL where that is 0

@@ -266,8 +266,9 @@ ar_status_t ar_residual_norm_backward(const ar_norm_t* n, const void* dy, size_t
   int sms = 0;
   if (ar_status_t st = current_sms(&sms)) return st;
   NormGradArgs a = {};
-  a.dy = dy, a.dr = dr, a.x = x, a.r = r, a.gate = gate;
-  a.after_weight = after_weight, a.after_bias = after_bias, a.weight = weight;
+  // What is not read has no say in how the rows are read.
+  a.dy = dy, a.dr = dr, a.x = gate || after_weight ? x : nullptr, a.r = weight ? r : nullptr, a.gate = gate;
+  a.after_weight = after_weight, a.after_bias = gate ? after_bias : nullptr, a.weight = weight;
   a.dx = dx, a.dresidual = dresidual;
   const size_t parts = (size_t)norm_parts((int64_t)rows, (int64_t)cols);
   float* part = static_cast<float*>(scratch);
