@@ -622,9 +622,9 @@ typedef struct {
  * differences from the mean; y is made from the unrounded r; each output is rounded once.
  * A row's values are its own: an infinity or NaN stays in its row.  In
  * AR_FP32 squares that overflow make the row's norm 0 or NaN.
- * r or y may be exactly x or residual (same address and leading dimension);
- * otherwise outputs overlap nothing.  rows = 0 returns AR_OK without a launch.
- * Errors: AR_ERR_INVALID_ARG (a NULL that is needed, ld < cols, an odd address,
+ * r or y may be exactly x or residual (same address and leading dimension), not both the
+ * same one; otherwise outputs overlap nothing.  rows = 0 returns AR_OK without a launch.
+ * Errors: AR_ERR_INVALID_ARG (a NULL that is needed, ld < cols, an odd address, r = y,
  * cols = 0, gate_rows that does not divide rows, eps negative or not finite, neither weight nor
  * after_weight), AR_ERR_UNSUPPORTED (dtype, kind), AR_ERR_CUDA. */
 ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, const void* residual,

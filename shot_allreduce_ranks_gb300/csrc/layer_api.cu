@@ -203,7 +203,7 @@ ar_status_t ar_residual_norm(const ar_norm_t* n, const void* x, size_t ldx, cons
   if ((y != nullptr) != (weight != nullptr) || bad_matrix(x, rows, cols, ldx) || misaligned(x, e) ||
       (residual && (bad_matrix(residual, rows, cols, ldres) || misaligned(residual, e))) ||
       (r && (bad_matrix(r, rows, cols, ldr) || misaligned(r, e))) ||
-      (y && (bad_matrix(y, rows, cols, ldy) || misaligned(y, e))))
+      (y && (bad_matrix(y, rows, cols, ldy) || misaligned(y, e))) || (r && r == y))
     return AR_ERR_INVALID_ARG;
   if (!r && !y) return AR_OK;
   int sms = 0;

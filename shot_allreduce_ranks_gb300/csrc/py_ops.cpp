@@ -476,6 +476,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
       y = output(a[12], "y", p.type, p.index, m, n, x, &ldy);
     else if (a[12] != Py_None)
       refuse("y needs weight");
+    if (m && r.defined() && y.defined() && r.data_ptr() == y.data_ptr()) refuse("r and y must be two tensors");
     call("ar_residual_norm", p.index, [&](void* s) {
       return ar_residual_norm(&p.n, x.data_ptr(), ldx, address(residual), ldres, address(p.gate), p.ldg, address(p.after_weight),
                               address(p.after_bias), address(p.weight), address(p.bias), address(r), ldr, address(y), ldy, s);

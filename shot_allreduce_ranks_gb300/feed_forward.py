@@ -305,7 +305,7 @@ def residual_norm(x, residual=None, weight=None, bias=None, after_weight=None, a
     ``gate`` is a matrix whose row g is for the rows / gate rows rows from
     g * rows / gate rows on: one row for all, one a sequence, or one a token.
     Without residual, gate and after_weight r would be x and None is
-    returned for it.  ``r`` and ``y`` may be given, and be x or the residual.
+    returned for it.  ``r`` and ``y`` may be given, and be x and the residual (either way).
     """
     k = _kind(kind)
     if stream is not None:

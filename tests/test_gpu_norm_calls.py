@@ -43,3 +43,15 @@ def test_arrays_that_are_not_read_change_nothing(ar, rows, cols):
     want = ar.residual_norm_backward(None, dr, x, None, None, None, w, b)
     got = ar.residual_norm_backward(None, dr, x, None, None, None, w, off_16(b))
     assert all(torch.equal(got[i], want[i]) for i in (0, 4, 5))
+
+
+def test_r_and_y_are_two_tensors(ar):
+    x, res, w = normal(1, 6, 40), normal(2, 6, 40), normal(3, 40)
+    keep = x.clone()
+    with pytest.raises(ValueError, match="r and y"):
+        ar.residual_norm(x, res, w, r=x, y=x)
+    assert torch.equal(x, keep)
+    both = torch.empty(6, 80, dtype=BF16, device=DEV)
+    r, y = ar.residual_norm(x, res, w, r=both[:, :40], y=both[:, 40:])
+    want = ar.residual_norm(x, res, w)
+    assert torch.equal(r, want[0]) and torch.equal(y, want[1])
