@@ -337,8 +337,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_norm_grad_rows(NormGradArgs a, i
         if (a.after_weight) xfactor = rsqrtf(__fmaf_rn(s[2], inv, a.eps));
       }
     }
-    // What a thread of a large CTA has no registers for it reads again.
-    constexpr bool kAgain = FULL && MAXT > 640;
+    // What a thread of a large CTA has no registers for it reads again: with 80 of them where a gate or biases take
+    // more (4096 x 6144 bf16 197 us, kept 206; after the block alone 92, kept 89), with 64 always.
+    constexpr bool kAgain = FULL && MAXT > (ALL ? 640 : 768);
     if constexpr (kAgain) {
       if (has_weight) {
         get(kR, row, stage, r);
@@ -539,8 +540,14 @@ cudaError_t norm_grad_rows_kind(NormGradArgs& a, int num_sms, cudaStream_t s) {
   if constexpr (N == 8) {
     if (cta <= 256) return AR_GRAD_ROWS(256, (BRANCH ? 2 : 4));
     if (cta <= 512) return AR_GRAD_ROWS(512, (BRANCH ? 1 : 2));
-    if constexpr (BRANCH != kNothing)
+    // A scheduler's registers are shared by its warps: five of them (up to 640 threads) have 96 each, six (768) 80, eight 64.
+    // With a branch, 680 x 5120 fp32 with every part takes 51 us of 96 registers and 58 of 80, 680 x 6144 66 of 80 and
+    // 73 of 64; with a norm after the block alone 27 and 30, 33 and 43, and 4096 x 6144 bf16 89 and 140. (Seven warps
+    // with 72: 680 x 7168 79 and 84, 4096 x 7168 bf16 139 and 160; not built.)
+    if constexpr (BRANCH != kNothing) {
       if (cta <= 640) return AR_GRAD_ROWS(640, 1);
+      if (cta <= 768) return AR_GRAD_ROWS(768, 1);
+    }
   }
   return AR_GRAD_ROWS(1024, 1);
 #undef AR_GRAD_ROWS
