@@ -659,9 +659,8 @@ cudaError_t moe(const MoeArgs& m, int num_sms, cudaStream_t s) {
   const size_t blocks = m.tokens <= 8 ? 1 : m.tokens <= 16 ? 2 : 4;
   const size_t gated = kRingBytes + tables + kWarps * 2 * blocks * 512, down = kRingBytes + tables + (size_t)kWarps * 2 * m.tokens * 17 * 4;
   const bool vec = on16(m.x) && on16(m.w_gate) && on16(m.w_up) && (m.ldx | m.ldw | m.esw) % 8 == 0;
-  // The kernels count pieces in 32 bits.
+  // The kernels count items and units in 32 bits; the entry point refuses sizes beyond that.
   const int64_t slots = num_sms < kMostSms ? num_sms : kMostSms, items = most * strips;
-  if (items * ((m.hidden + 63) / 64) >> 31 || most * ((m.width + 63) / 64) * ((m.hidden + 15) / 16) >> 31) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(items < slots ? items : slots)), all((unsigned)slots);
   const cudaError_t e = vec ? launch_raised<k_moe_gated<E, ACT, true>>(grid, kThreads, gated, s, m)
                             : launch_raised<k_moe_gated<E, ACT, false>>(grid, kThreads, gated, s, m);
