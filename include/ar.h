@@ -49,7 +49,8 @@
  *     page's NumProcs >= NPeers limitation cannot arise); the kernel is
  *     pipelined over rounds so that its packets stay in L2.
  *
- * Threading: a handle may be used from one host thread at a time.  Calls on
+ * Threading: the operators that take no handle may be called from several host
+ * threads at once.  A handle may be used from one host thread at a time.  Calls on
  * one handle must be ordered on one stream (one call in flight), because a
  * handle owns one packet scratch region and one epoch; use one handle per
  * concurrent stream.  (The one-shot region of "Add HIP-graph capture
@@ -620,8 +621,9 @@ typedef struct {
  *   r, y          [rows, cols]; r may be NULL (not wanted), y is NULL where weight is
  * Means, sums and products are fp32, the mean square being taken of the
  * differences from the mean; y is made from the unrounded r; each output is rounded once.
- * A row's values are its own: an infinity or NaN stays in its row.  In
- * AR_FP32 squares that overflow make the row's norm 0 or NaN.
+ * A row's values are its own: an infinity or NaN stays in its row.  Squares
+ * are fp32: those that overflow (values from 10^19 on, in AR_FP32 and AR_BF16) make the
+ * row's norm 0 or NaN, and a row whose squares all vanish is scaled by 1 / sqrt(eps).
  * r or y may be exactly x or residual (same address and leading dimension), not both the
  * same one; otherwise outputs overlap nothing.  rows = 0 returns AR_OK without a launch.
  * Errors: AR_ERR_INVALID_ARG (a NULL that is needed, ld < cols, an odd address, r = y,

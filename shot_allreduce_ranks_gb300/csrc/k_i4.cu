@@ -123,12 +123,13 @@ struct Span {
 // A tile of sixteen channels for up to 8 NB tokens a CTA; its warps take turns at the spans
 // along k, and their sums are joined in a fixed order.
 //
-// With few tokens what bounds it is first the integer pipe, which unpacks a weight in
-// 7/8 of an instruction (two logical operations and three shifts for every four), then the loads in flight: three CTAs
-// an SM, each warp with four pieces of 512 bytes, were the fastest of 2 to 8 pieces and 1 to 5 CTAs. 8192 -> 16384 in groups of 128 (69
-// MB): one token 17.9 us (57% of the copy rate; without unpacking it would be 16), 8 tokens 18.6; 16 tokens 26.5 and 32 47, where
-// what is read of x from L1 passes what is read of the weights. Weights copied ahead
-// by a persistent CTA with x in shared memory took 21.7 us.
+// With few tokens the loads in flight bound it: a warp has four pieces of 512 bytes under way and none while it
+// multiplies.  Three CTAs an SM with four pieces a warp were the fastest of 2 to 8 pieces and 1 to 5 CTAs.  Unpacking, 7/8 of an
+// integer instruction a weight (four logical operations and three shifts for every eight), costs at most 2 us of the 17.5, and the
+// integer pipe is 54% active; CTAs that are no multiple of the 456 on the device at once cost 0.7 (2 rounds of them 15.2 us, 2.25
+// 17.5, 3 21.7).  With more tokens it is x, of which every CTA reads all through L1: 32 bytes for a block of eight tokens beside 16 of
+// weights.  8192 -> 16384 in groups of 128 (69 MB): one token 17.5 us (58% of the copy rate), 8 tokens 18.4, 13 25.8, 32 47.6, 64
+// (weights twice) 82.6.  Weights copied ahead by a persistent CTA with x in shared memory took 21.7 us for one token.
 template <class E, int GROUP, bool ZERO, int NB, bool VEC>
 __global__ void __launch_bounds__(kThreads, NB > 2 ? 2 : 3) k_linear_i4(I4Args a) {
   constexpr int kSpan = span_of(GROUP), kPer = groups_in(GROUP), kTiles = kSpan / 64;

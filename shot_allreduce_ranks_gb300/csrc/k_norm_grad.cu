@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kAnyThreads) k_norm_grad_any(NormGradArgs a) {
 // its rows; a CTA of short rows has several groups of T threads, each with rows of
 // its own.  A row's statistics and the two means that the gradient wants come out of one
 // joint sum (mean square) or two (differences from the mean), and one more for the norm
-// after the block.  The next rows are copied to shared memory meanwhile, one to three of them.
+// after the block.  The next rows are copied to shared memory meanwhile, as many as fit beside a row's own: one to three, or none
+// (8,192 columns of fp32 with a gate or biases).
 constexpr int kGroupThreads = 256;  // of a CTA of short rows
 
 __host__ __device__ constexpr int row_threads(int64_t cols, int n) { return (int)((cols + 32 * n - 1) / (32 * n) * 32); }

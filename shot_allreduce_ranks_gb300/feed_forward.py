@@ -271,8 +271,9 @@ def moe_ffn(x, logits, w_gate, w_up, w_down, top_k: int, activation: str = "silu
     ``w_gate`` and ``w_up`` are experts x width x hidden, ``w_down`` experts x
     hidden x width.  They may be a part of the layer's experts, from
     ``first_expert`` on, or of their width: the ranks' outputs are then summed.  A logit of
-    -infinity is never chosen (expert -1, weight 0, where fewer remain).  Each
-    matrix in use is read once for every 32 tokens.
+    -infinity is never chosen (expert -1, weight 0, where fewer remain).  What is between the
+    two products is held as the sum of two numbers of x's type, so that its rounding does not show
+    (in float16 it becomes an infinity from 65,520 on).  Each matrix in use is read once for every 32 tokens.
     """
     if activation not in ACTIVATIONS:
         raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
@@ -323,8 +324,9 @@ def residual_norm_backward(dy, dr, x, r, weight=None, bias=None, after_weight=No
 
     ``dr`` None counts as 0; ``dy`` is None where there was no weight.  ``x`` and
     ``r`` are the forward pass's: x may be None without gate and after_weight, r
-    is None where nothing was added to x (then there is no dresidual).
-    What was not given has None for its gradient.  Where neither a gate, nor
+    is None where the forward pass gave None.  A weight, bias or gate that was not given has None for its gradient;
+    dresidual is None without r and where ``need_dresidual`` is False (the call cannot see whether there was a
+    residual: without one, say so, and a matrix is not written).  Where neither a gate, nor
     after_weight, nor a scale stands between them, dx and dresidual are equal and one
     tensor is returned for both.
     """
