@@ -9,7 +9,7 @@
 // a warp waits for nothing but its own copies.  A CTA finds the routing for itself from the
 // logits: a few hundred instructions, against a kernel of its own and its launch.
 //
-// Measured on one GB300: 32 tokens through 8 of 64 experts 2048 -> 1024 166 us (794 MB: 70% of the copy
+// Measured on one GB300: 32 tokens through 8 of 64 experts 2048 -> 1024 160-167 us (794 MB: 70-73% of the copy
 // rate), 1 token through 4 of 32 experts 5120 -> 1736 49.8 (213 MB: 63%), 9 tokens on half of 16 experts 2048 -> 1032 28 (71
 // MB). While it runs each loop reads at the copy rate (77 us for 520 MB, 20 for 142); what is left is the
 // routing (2.3 us at one token, 4.2 at 32), the first pieces' way (1.7), the joining of sums (2
