@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_down(MoeArgs m) {
   const char* bd = static_cast<const char*>(m.w_down);
   const int64_t extent = ((m.local - 1) * m.esd + (m.hidden - 1) * m.ldd + m.width) * 2;
   const char* h = static_cast<const char*>(m.h);
-  const int64_t to_rest = static_cast<const char*>(m.h_rest) - h;  // where TWO
+  const int64_t to_rest = TWO ? static_cast<const char*>(m.h_rest) - h : 0;
   uint16_t* const out = static_cast<uint16_t*>(m.out);
 
   if (units == 0) {  // no token has an expert here

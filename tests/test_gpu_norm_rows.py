@@ -98,7 +98,7 @@ def test_plain_fp32(ar, rows, cols, kind):
 
 # The branch: 256, 512 and then each number of threads from 512 on at which a thread has other registers.
 @pytest.mark.parametrize("rows,cols", [(1500, 2048), (900, 4096), (700, 5120), (700, 5376), (700, 5384), (700, 6144), (700, 6152), (700, 8192),
-                                       (900, 2045), (700, 5119), (700, 5383), (700, 6143), (700, 6145)])
+                                       (900, 2045), (700, 5119), (700, 5383), (700, 6143), (700, 6145), (700, 8191)])
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("parts", [dict(after=True), dict(after=True, bias=True, gates=1, kind="layer", scale=0.7, offset=1.0),
                                    dict(after=True, before=False, kind="layer"), dict(gates=2, residual=False)])
